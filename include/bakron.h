@@ -346,6 +346,104 @@ bakron_status bakron_quantize_noalloc(const float* W, int64_t m, int64_t n,
                                       const float* scale, int qmin, int qmax,
                                       float* V, int8_t* codes, void* stream);
 
+/* ------------------------------------------------ quantised layers in use
+ *
+ * The calls below run the layers that the solver has quantised: products
+ * with the packed codes, and the layer norm in front of them with its
+ * gradients.
+ * They differ from the solver's calls in two points:
+ *  - activations are fp32, bf16 or fp16 (bakron_dtype; one type per call),
+ *    still dense, row-major and contiguous, at any address that is a multiple
+ *    of the element size;
+ *  - except for bakron_pack and bakron_unpack, which synchronise like the
+ *    solver's calls, they only enqueue: the status covers the arguments and
+ *    the launches, and there is no device status to wait for, because no
+ *    value of the data is an error (NaN and Inf propagate as in the
+ *    formulas).  They can be captured into a CUDA graph.  A bounded device
+ *    wait that runs out, which no input causes, is kept for
+ *    bakron_async_status.
+ * All sums are held in fp32.  A result does not depend on the run: the same
+ * inputs give the same bits. */
+typedef enum { BAKRON_F32 = 0, BAKRON_BF16 = 1, BAKRON_F16 = 2 } bakron_dtype;
+
+/* Synchronises `stream` and returns the first error that the enqueue-only
+ * calls below left on the current device since the last call
+ * (BAKRON_ERR_TIMEOUT, then the outputs of the calls since are unspecified),
+ * or BAKRON_OK; the record is cleared. */
+bakron_status bakron_async_status(void* stream);
+
+/* `count` packed matrices of one shape (the experts of a layer; 1 for a
+ * single layer).  The value of entry (i, j) of a matrix is
+ * s_ik (c_ij - z_ik), k = j / group, as in bakron_quantize_grid. */
+typedef struct {
+  int64_t count, m, n;
+  int64_t group;      /* columns per scale; 0 or >= n: one scale per row,
+                         otherwise a multiple of 32 */
+  int qmin;           /* code of the stored nibble 0 */
+  int has_zero;       /* 1: zero points are stored, 0: they are all 0 */
+  const void* data;   /* device, 16-byte aligned, written by bakron_pack */
+  size_t bytes;       /* size of data, at least bakron_pack_size */
+} bakron_packed;
+
+/* bakron_pack: lays codes (count x m x n int8, every code in [qmin, qmax],
+ * qmax - qmin <= 15, -128 <= qmin) and their grid (scale and zero: count x m
+ * x groups, zero nullable) out for the products below, 4 bits a code, in
+ * `data` (device, 16-byte aligned, at least bakron_pack_size bytes).  Scales
+ * keep their fp32 value; zero points are integers in [qmin, qmax] and take
+ * one byte.  A code or a zero point outside the range returns
+ * BAKRON_ERR_CODE_RANGE, a scale that is not positive and finite
+ * BAKRON_ERR_NONFINITE.  m, n and count are at most 2^20, and the codes at
+ * most 2^38.
+ * Layout of data, with mp = m rounded up to 16, np = n rounded up to 128 and
+ * groups = ceil(n / group):
+ *   256 bytes            status word of the packing, otherwise unused;
+ *   codes, count mp np / 2 bytes: blocks of 8 rows x 128 columns (512 bytes)
+ *     in row-major order of blocks; inside a block row by row, 64 bytes each;
+ *     word 4 t + s (32 bits; s, t = 0..3) of a row holds columns 32 s + 8 t
+ *     .. + 7, the even ones (0, 2, 4, 6) in bits 0..15 and the odd ones in
+ *     bits 16..31; a nibble is c - qmin;
+ *   scales, count groups mp floats, group by group (0 on the padding rows);
+ *   with zero points: count groups mp bytes z - qmin, likewise; the region
+ *     ends on a multiple of 16 bytes. */
+bakron_status bakron_pack_size(int64_t count, int64_t m, int64_t n, int64_t group, int has_zero,
+                               size_t* bytes);
+bakron_status bakron_pack(const int8_t* codes, const float* scale, const float* zero,
+                          int64_t count, int64_t m, int64_t n, int64_t group, int qmin, int qmax,
+                          void* data, size_t data_bytes, void* stream);
+/* V (count x m x n fp32, device) of the packed matrices: the bits that the
+ * solver returned for the same codes and grid. */
+bakron_status bakron_unpack(const bakron_packed* w, float* V, void* stream);
+
+/* Y = X V^T for one packed matrix (w->count 1): X is T x n, Y is T x m, both
+ * of type dtype; Y is rounded once from the fp32 sum.  T >= 0.  The sum
+ * over a group (or over 128 columns of a longer one) is formed from the
+ * integers c - z and scaled afterwards, so an intermediate value exceeds the
+ * final one by up to 1 / scale: activations above about 1e34 overflow.
+ * ws: device, 256-byte aligned, bakron_linear_workspace_size bytes (may be 0
+ * bytes; ws is then ignored). */
+bakron_status bakron_linear_workspace_size(const bakron_packed* w, int64_t T, int dtype,
+                                           size_t* bytes);
+bakron_status bakron_linear(const void* X, int64_t T, int dtype, const bakron_packed* w, void* Y,
+                            void* ws, size_t ws_bytes, void* stream);
+/* Layer norm over the rows of X (T x d; d <= 2^20): with mu and var the mean and
+ * the biased variance of a row and r = 1 / sqrt(var + eps),
+ *   Y = (X - mu) r gamma + beta.
+ * gamma, beta: d floats each, nullable (1 and 0).  mean, rstd: T floats each
+ * (mu and r), nullable; the gradient needs them.  eps >= 0. */
+bakron_status bakron_layernorm(const void* X, int64_t T, int64_t d, int dtype, const float* gamma,
+                               const float* beta, float eps, void* Y, float* mean, float* rstd,
+                               void* stream);
+/* Gradients of bakron_layernorm: with h = (X - mu) r and a = dY gamma,
+ *   dX = r (a - mean(a) - h mean(a h)),  dgamma = sum_t dY h,  dbeta = sum_t dY.
+ * dX has dY's type; dgamma and dbeta are d floats each, nullable (both or
+ * none).  T = 0 writes zeros to them.  ws: device, 256-byte aligned,
+ * bakron_layernorm_grad_workspace_size bytes. */
+bakron_status bakron_layernorm_grad_workspace_size(int64_t T, int64_t d, size_t* bytes);
+bakron_status bakron_layernorm_grad(const void* dY, const void* X, int64_t T, int64_t d, int dtype,
+                                    const float* gamma, const float* mean, const float* rstd,
+                                    void* dX, float* dgamma, float* dbeta, void* ws,
+                                    size_t ws_bytes, void* stream);
+
 /* Measurement utilities (not part of the solve).
  * bakron_fma_probe: enqueues `blocks` CTAs of 256 threads on `stream`, each
  * thread running 8 independent chains of 16 * iters fp32 fused multiply-adds

@@ -27,9 +27,13 @@ EXPORTS = ["bakron_default_opts", "bakron_status_string", "bakron_version", "bak
            "bakron_quantize_noalloc", "bakron_factors_workspace_size", "bakron_factors",
            "bakron_grid_params", "bakron_quantize_grid", "bakron_batch_workspace_size",
            "bakron_quantize_batch", "bakron_schedule_export", "bakron_fma_probe", "bakron_sm_count",
-           "bakron_plan_size", "bakron_plan_init"]
+           "bakron_plan_size", "bakron_plan_init", "bakron_async_status", "bakron_pack_size",
+           "bakron_pack", "bakron_unpack", "bakron_linear_workspace_size", "bakron_linear",
+           "bakron_layernorm", "bakron_layernorm_grad_workspace_size",
+           "bakron_layernorm_grad"]
 FACTORS_KFAC = 0
 FACTORS_SHAMPOO = 1
+F32, BF16, F16 = 0, 1, 2      # bakron_dtype
 
 
 class PhaseTimes(ctypes.Structure):
@@ -55,6 +59,12 @@ class Problem(ctypes.Structure):
                 ("zero", ctypes.c_void_p), ("group", ctypes.c_int64), ("qmin", ctypes.c_int),
                 ("qmax", ctypes.c_int), ("V", ctypes.c_void_p), ("codes", ctypes.c_void_p),
                 ("status", ctypes.c_int)]
+
+
+class Packed(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("m", ctypes.c_int64), ("n", ctypes.c_int64),
+                ("group", ctypes.c_int64), ("qmin", ctypes.c_int), ("has_zero", ctypes.c_int),
+                ("data", ctypes.c_void_p), ("bytes", ctypes.c_size_t)]
 
 
 class BakronError(RuntimeError):
@@ -106,12 +116,25 @@ def lib():
     L.bakron_plan_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
     L.bakron_plan_init.argtypes = [i64, i64, vp, sz, vp]
     L.bakron_sm_count.restype = ctypes.c_int
+    pk, f32 = ctypes.POINTER(Packed), ctypes.c_float
+    L.bakron_async_status.argtypes = [vp]
+    L.bakron_pack_size.argtypes = [i64, i64, i64, i64, ctypes.c_int, ctypes.POINTER(sz)]
+    L.bakron_pack.argtypes = [vp, vp, vp, i64, i64, i64, i64, ctypes.c_int, ctypes.c_int, vp, sz, vp]
+    L.bakron_unpack.argtypes = [pk, vp, vp]
+    L.bakron_linear_workspace_size.argtypes = [pk, i64, ctypes.c_int, ctypes.POINTER(sz)]
+    L.bakron_linear.argtypes = [vp, i64, ctypes.c_int, pk, vp, vp, sz, vp]
+    L.bakron_layernorm.argtypes = [vp, i64, i64, ctypes.c_int, vp, vp, f32, vp, vp, vp, vp]
+    L.bakron_layernorm_grad_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.bakron_layernorm_grad.argtypes = [vp, vp, i64, i64, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     for f in ("bakron_schedule_export", "bakron_workspace_size", "bakron_prepare_workspace_size", "bakron_rowscale",
               "bakron_prepare", "bakron_quantize", "bakron_quantize_antidiag",
               "bakron_quantize_noalloc", "bakron_factors_workspace_size", "bakron_factors",
               "bakron_grid_params", "bakron_quantize_grid", "bakron_batch_workspace_size",
               "bakron_quantize_batch", "bakron_fma_probe", "bakron_plan_size",
-              "bakron_plan_init"):
+              "bakron_plan_init", "bakron_async_status", "bakron_pack_size", "bakron_pack",
+              "bakron_unpack", "bakron_linear_workspace_size", "bakron_linear",
+              "bakron_layernorm",
+              "bakron_layernorm_grad_workspace_size", "bakron_layernorm_grad"):
         getattr(L, f).restype = ctypes.c_int
     _LIB = L
     return L
@@ -488,6 +511,207 @@ def bakron_factors(X=None, G=None, mode=FACTORS_KFAC, want_A=True, want_B=True, 
         ctypes.c_void_p(ws.data_ptr()), size.value, _stream(stream))
     _check(st, "bakron_factors")
     return A, B
+
+
+# ------------------------------------------------ quantised layers in use
+#
+# These calls only enqueue (bakron_pack and bakron_unpack excepted) on
+# ``stream``, or on the current stream.  Tensors allocated here belong to the
+# current stream as far as PyTorch's allocator knows; a caller who passes
+# another stream passes ``out`` and ``workspace`` too, or keeps the two
+# streams ordered.
+
+
+def _act(t, name, cols=None):
+    """Checks an activation matrix; returns (rows, columns, bakron_dtype)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    dt = t.dtype
+    code = BF16 if dt == torch.bfloat16 else F16 if dt == torch.float16 else F32 if dt == torch.float32 else -1
+    if code < 0:
+        raise ValueError("%s must be float32, bfloat16 or float16, got %s" % (name, dt))
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError("%s must have shape (tokens, %s), got %s"
+                         % (name, "columns" if cols is None else cols, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.shape[0], t.shape[1], code
+
+
+def _out(out, like, shape, name):
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    _dev(out, like.dtype, shape, name)
+    if out.device != like.device:
+        raise ValueError("%s must be on %s" % (name, like.device))
+    return out
+
+
+def _vec(t, n, like, name):
+    """Device address of a float32 vector of n elements, or None."""
+    if t is None:
+        return None
+    if t.device != like.device:
+        raise ValueError("%s must be on %s" % (name, like.device))
+    return _dev(t, _torch().float32, (n,), name)
+
+
+class PackedWeight:
+    """4-bit codes and their grid in the layout of the products (bakron_pack):
+    ``count`` matrices of m x n.  ``data`` is the device buffer."""
+
+    def __init__(self, data, count, m, n, group, qmin, has_zero):
+        self.data, self.count, self.m, self.n, self.group = data, count, m, n, group
+        self.qmin, self.has_zero = qmin, has_zero
+        self.desc = Packed(count, m, n, group, qmin, 1 if has_zero else 0, data.data_ptr(), data.numel())
+        self.ref = ctypes.byref(self.desc)
+        self.device = data.device
+        self._ws = {}
+
+    def _check(self, like, name):
+        if like.device != self.device:
+            raise ValueError("%s must be on %s, the weight's device" % (name, self.device))
+
+    def unpack(self, stream=None):
+        """V, float32: (m, n), or (count, m, n) for several matrices."""
+        return bakron_unpack(self, stream=stream)
+
+
+def bakron_pack(codes, scale, qmin, qmax, zero=None, group=None, stream=None):
+    """Packs codes (m, n) or (count, m, n), int8 in [qmin, qmax] with
+    qmax - qmin <= 15, on a grid as bakron_grid_params returns it: scale and
+    zero (m, groups) or (count, m, groups); a scale of one group may be (m,).
+    Returns a PackedWeight."""
+    torch = _torch()
+    if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
+        raise ValueError("codes must be a tensor of shape (m, n) or (count, m, n)")
+    lead = tuple(codes.shape[:-1])
+    m, n = codes.shape[-2:]
+    count = codes.shape[0] if codes.dim() == 3 else 1
+    ng = grid_groups(n, group)
+    shape = lead if ng == 1 and isinstance(scale, torch.Tensor) and scale.dim() == len(lead) else lead + (ng,)
+    size = ctypes.c_size_t(0)
+    _check(lib().bakron_pack_size(count, m, n, int(group or 0), 0 if zero is None else 1, ctypes.byref(size)),
+           "bakron_pack_size")
+    args = (_dev(codes, torch.int8, lead + (n,), "codes"), _dev(scale, torch.float32, shape, "scale"),
+            None if zero is None else _dev(zero, torch.float32, zero.shape if zero.shape == lead and ng == 1
+                                           else lead + (ng,), "zero"))
+    data = torch.empty(size.value, dtype=torch.uint8, device=codes.device)
+    _check(lib().bakron_pack(*args, count, m, n, int(group or 0), int(qmin), int(qmax),
+                             ctypes.c_void_p(data.data_ptr()), size.value, _stream(stream)), "bakron_pack")
+    return PackedWeight(data, count, m, n, int(group or 0), int(qmin), zero is not None)
+
+
+def bakron_unpack(w, stream=None):
+    """V (float32) of a PackedWeight: the values the solver returned."""
+    torch = _torch()
+    V = torch.empty((w.count, w.m, w.n), dtype=torch.float32, device=w.device)
+    _check(lib().bakron_unpack(w.ref, ctypes.c_void_p(V.data_ptr()), _stream(stream)), "bakron_unpack")
+    return V[0] if w.count == 1 else V
+
+
+def bakron_async_status(stream=None):
+    """Raises BakronError if an enqueued call left an error on the device."""
+    _check(lib().bakron_async_status(_stream(stream)), "bakron_async_status")
+
+
+def linear_workspace_size(w, T, dtype):
+    torch = _torch()
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[dtype]
+    key = (T, code)
+    size = w._ws.get(key)
+    if size is None:
+        b = ctypes.c_size_t(0)
+        _check(lib().bakron_linear_workspace_size(w.ref, T, code, ctypes.byref(b)), "bakron_linear_workspace_size")
+        size = b.value
+        if len(w._ws) > 64:
+            w._ws.clear()
+        w._ws[key] = size
+    return size
+
+
+def linear_workspace(w, T, dtype):
+    """A workspace for bakron_linear of up to T tokens,
+    None when none is needed."""
+    nb = linear_workspace_size(w, T, dtype)
+    return _torch().empty(nb, dtype=_torch().uint8, device=w.device) if nb else None
+
+
+def _linear(fn, where, x, w, out, workspace, stream):
+    name = "X"
+    T, _, code = _act(x, name, w.n)
+    w._check(x, name)
+    if w.count != 1:
+        raise ValueError("%s takes a single matrix, got %d" % (where, w.count))
+    y = _out(out, x, (T, w.m), "out")
+    nb = linear_workspace_size(w, T, x.dtype)
+    ws = _ws(nb, workspace) if nb else None
+    _check(fn(x.data_ptr(), T, code, w.ref, y.data_ptr(), None if ws is None else ws.data_ptr(), nb,
+              _stream(stream)), where)
+    return y
+
+
+def bakron_linear(x, w, out=None, workspace=None, stream=None):
+    """Y = X V^T: x (T, n) float32, bfloat16 or float16, w a PackedWeight of
+    one m x n matrix; returns (T, m) of x's type."""
+    return _linear(lib().bakron_linear, "bakron_linear", x, w, out, workspace, stream)
+
+
+def bakron_layernorm(x, gamma=None, beta=None, eps=1e-5, out=None, want_stats=True, stream=None):
+    """Layer norm of the rows of x (T, d); gamma, beta (d,) float32 or None.
+    Returns (y, mean, rstd); mean and rstd (T,) float32 feed the gradient
+    (None without want_stats)."""
+    torch = _torch()
+    T, d, code = _act(x, "X")
+    y = _out(out, x, (T, d), "out")
+    mean = rstd = None
+    if want_stats:
+        stats = torch.empty((2, T), dtype=torch.float32, device=x.device)
+        mean, rstd = stats[0], stats[1]
+    _check(lib().bakron_layernorm(x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"), _vec(beta, d, x, "beta"),
+                                  float(eps), y.data_ptr(), mean.data_ptr() if want_stats else None,
+                                  rstd.data_ptr() if want_stats else None, _stream(stream)),
+           "bakron_layernorm")
+    return y, mean, rstd
+
+
+def layernorm_grad_workspace_size(T, d):
+    b = ctypes.c_size_t(0)
+    _check(lib().bakron_layernorm_grad_workspace_size(T, d, ctypes.byref(b)),
+           "bakron_layernorm_grad_workspace_size")
+    return b.value
+
+
+def layernorm_grad_workspace(T, d):
+    """A workspace for bakron_layernorm_grad of up to T rows of d."""
+    return _torch().empty(layernorm_grad_workspace_size(T, d), dtype=_torch().uint8, device="cuda")
+
+
+def bakron_layernorm_grad(dy, x, gamma, mean, rstd, want_weight_grads=True, out=None, workspace=None,
+                          stream=None):
+    """Gradients of bakron_layernorm: returns (dx, dgamma, dbeta), dgamma and
+    dbeta (d,) float32 (None without want_weight_grads)."""
+    torch = _torch()
+    T, d, code = _act(x, "X")
+    if dy.dtype != x.dtype or dy.device != x.device or tuple(dy.shape) != (T, d) or not dy.is_contiguous():
+        raise ValueError("dY must be a contiguous %s tensor of shape %s on %s" % (x.dtype, (T, d), x.device))
+    dx = _out(out, x, (T, d), "out")
+    dg = db = ws = None
+    nb = 0
+    if want_weight_grads:
+        grads = torch.empty((2, d), dtype=torch.float32, device=x.device)
+        dg, db = grads[0], grads[1]
+        nb = layernorm_grad_workspace_size(T, d)
+        ws = _ws(nb, workspace)
+    _check(lib().bakron_layernorm_grad(dy.data_ptr(), x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"),
+                                       _vec(mean, T, x, "mean"), _vec(rstd, T, x, "rstd"), dx.data_ptr(),
+                                       None if dg is None else dg.data_ptr(),
+                                       None if db is None else db.data_ptr(),
+                                       None if ws is None else ws.data_ptr(), nb, _stream(stream)),
+           "bakron_layernorm_grad")
+    return dx, dg, db
 
 
 class Solver:

@@ -934,7 +934,7 @@ const char* bakron_status_string(int st) {
   }
 }
 
-int bakron_version(void) { return 20000; }
+int bakron_version(void) { return 20100; }
 
 int64_t bakron_kernel_launches(void) { return (int64_t)bakron::launches_so_far(); }
 

@@ -1,0 +1,24 @@
+// Shared between the entry points of the quantised linear layer and its
+// kernels.
+#pragma once
+
+#include "packed.cuh"
+
+namespace bakron {
+
+struct LinearArgs {
+  const void* x;        // T x n (gradient: T x m)
+  void* y;              // T x m (gradient: T x n)
+  int64_t T;
+  int dtype;
+  PackedView w;
+  void* ws;
+  size_t ws_bytes;
+};
+
+// Tokens up to which bakron_linear runs linear_few_kernel.
+constexpr int64_t kFewTokens = 16;
+
+cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
+
+}  // namespace bakron
