@@ -349,8 +349,8 @@ bakron_status bakron_quantize_noalloc(const float* W, int64_t m, int64_t n,
 /* ------------------------------------------------ quantised layers in use
  *
  * The calls below run the layers that the solver has quantised: products
- * with the packed codes, and the layer norm in front of them with its
- * gradients.
+ * with the packed codes in both directions, and the layer norm in front of
+ * them with its gradients.
  * They differ from the solver's calls in two points:
  *  - activations are fp32, bf16 or fp16 (bakron_dtype; one type per call),
  *    still dense, row-major and contiguous, at any address that is a multiple
@@ -425,6 +425,14 @@ bakron_status bakron_linear_workspace_size(const bakron_packed* w, int64_t T, in
                                            size_t* bytes);
 bakron_status bakron_linear(const void* X, int64_t T, int dtype, const bakron_packed* w, void* Y,
                             void* ws, size_t ws_bytes, void* stream);
+/* The gradient of bakron_linear for its activations (the weights are
+ * frozen): dX = dY V, dY T x m, dX T x n.  For 16-bit dY each value of V is
+ * rounded to dY's type before the product; for fp32 it is not. */
+bakron_status bakron_linear_grad_workspace_size(const bakron_packed* w, int64_t T, int dtype,
+                                                size_t* bytes);
+bakron_status bakron_linear_grad(const void* dY, int64_t T, int dtype, const bakron_packed* w,
+                                 void* dX, void* ws, size_t ws_bytes, void* stream);
+
 /* Layer norm over the rows of X (T x d; d <= 2^20): with mu and var the mean and
  * the biased variance of a row and r = 1 / sqrt(var + eps),
  *   Y = (X - mu) r gamma + beta.

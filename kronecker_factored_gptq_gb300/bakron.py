@@ -29,6 +29,7 @@ EXPORTS = ["bakron_default_opts", "bakron_status_string", "bakron_version", "bak
            "bakron_quantize_batch", "bakron_schedule_export", "bakron_fma_probe", "bakron_sm_count",
            "bakron_plan_size", "bakron_plan_init", "bakron_async_status", "bakron_pack_size",
            "bakron_pack", "bakron_unpack", "bakron_linear_workspace_size", "bakron_linear",
+           "bakron_linear_grad_workspace_size", "bakron_linear_grad",
            "bakron_layernorm", "bakron_layernorm_grad_workspace_size",
            "bakron_layernorm_grad"]
 FACTORS_KFAC = 0
@@ -123,6 +124,8 @@ def lib():
     L.bakron_unpack.argtypes = [pk, vp, vp]
     L.bakron_linear_workspace_size.argtypes = [pk, i64, ctypes.c_int, ctypes.POINTER(sz)]
     L.bakron_linear.argtypes = [vp, i64, ctypes.c_int, pk, vp, vp, sz, vp]
+    L.bakron_linear_grad_workspace_size.argtypes = [pk, i64, ctypes.c_int, ctypes.POINTER(sz)]
+    L.bakron_linear_grad.argtypes = [vp, i64, ctypes.c_int, pk, vp, vp, sz, vp]
     L.bakron_layernorm.argtypes = [vp, i64, i64, ctypes.c_int, vp, vp, f32, vp, vp, vp, vp]
     L.bakron_layernorm_grad_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
     L.bakron_layernorm_grad.argtypes = [vp, vp, i64, i64, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -133,6 +136,7 @@ def lib():
               "bakron_quantize_batch", "bakron_fma_probe", "bakron_plan_size",
               "bakron_plan_init", "bakron_async_status", "bakron_pack_size", "bakron_pack",
               "bakron_unpack", "bakron_linear_workspace_size", "bakron_linear",
+              "bakron_linear_grad_workspace_size", "bakron_linear_grad",
               "bakron_layernorm",
               "bakron_layernorm_grad_workspace_size", "bakron_layernorm_grad"):
         getattr(L, f).restype = ctypes.c_int
@@ -617,14 +621,15 @@ def bakron_async_status(stream=None):
     _check(lib().bakron_async_status(_stream(stream)), "bakron_async_status")
 
 
-def linear_workspace_size(w, T, dtype):
+def linear_workspace_size(w, T, dtype, grad=False):
     torch = _torch()
     code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[dtype]
-    key = (T, code)
+    key = (T, code, grad)
     size = w._ws.get(key)
     if size is None:
+        f = lib().bakron_linear_grad_workspace_size if grad else lib().bakron_linear_workspace_size
         b = ctypes.c_size_t(0)
-        _check(lib().bakron_linear_workspace_size(w.ref, T, code, ctypes.byref(b)), "bakron_linear_workspace_size")
+        _check(f(w.ref, T, code, ctypes.byref(b)), "bakron_linear_workspace_size")
         size = b.value
         if len(w._ws) > 64:
             w._ws.clear()
@@ -632,21 +637,21 @@ def linear_workspace_size(w, T, dtype):
     return size
 
 
-def linear_workspace(w, T, dtype):
-    """A workspace for bakron_linear of up to T tokens,
+def linear_workspace(w, T, dtype, grad=False):
+    """A workspace for bakron_linear (or its gradient) of up to T tokens,
     None when none is needed."""
-    nb = linear_workspace_size(w, T, dtype)
+    nb = linear_workspace_size(w, T, dtype, grad)
     return _torch().empty(nb, dtype=_torch().uint8, device=w.device) if nb else None
 
 
-def _linear(fn, where, x, w, out, workspace, stream):
-    name = "X"
-    T, _, code = _act(x, name, w.n)
+def _linear(fn, where, grad, x, w, out, workspace, stream):
+    name = "dY" if grad else "X"
+    T, _, code = _act(x, name, w.m if grad else w.n)
     w._check(x, name)
     if w.count != 1:
         raise ValueError("%s takes a single matrix, got %d" % (where, w.count))
-    y = _out(out, x, (T, w.m), "out")
-    nb = linear_workspace_size(w, T, x.dtype)
+    y = _out(out, x, (T, w.n if grad else w.m), "out")
+    nb = linear_workspace_size(w, T, x.dtype, grad)
     ws = _ws(nb, workspace) if nb else None
     _check(fn(x.data_ptr(), T, code, w.ref, y.data_ptr(), None if ws is None else ws.data_ptr(), nb,
               _stream(stream)), where)
@@ -656,7 +661,13 @@ def _linear(fn, where, x, w, out, workspace, stream):
 def bakron_linear(x, w, out=None, workspace=None, stream=None):
     """Y = X V^T: x (T, n) float32, bfloat16 or float16, w a PackedWeight of
     one m x n matrix; returns (T, m) of x's type."""
-    return _linear(lib().bakron_linear, "bakron_linear", x, w, out, workspace, stream)
+    return _linear(lib().bakron_linear, "bakron_linear", False, x, w, out, workspace, stream)
+
+
+def bakron_linear_grad(dy, w, out=None, workspace=None, stream=None):
+    """dX = dY V, the gradient of bakron_linear for its activations: dy
+    (T, m); returns (T, n) of dy's type."""
+    return _linear(lib().bakron_linear_grad, "bakron_linear_grad", True, dy, w, out, workspace, stream)
 
 
 def bakron_layernorm(x, gamma=None, beta=None, eps=1e-5, out=None, want_stats=True, stream=None):

@@ -13,12 +13,16 @@ struct LinearArgs {
   int dtype;
   PackedView w;
   void* ws;
-  size_t ws_bytes;
 };
 
 // Tokens up to which bakron_linear runs linear_few_kernel.
 constexpr int64_t kFewTokens = 16;
 
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
+
+// tcgen05 products of T tokens in either direction; K is the length of the
+// sums (n, gradient: m).
+size_t linear_tc_workspace(int64_t T, int64_t K, int dtype);
+cudaError_t launch_linear_tc(const LinearArgs& a, bool grad, cudaStream_t s);
 
 }  // namespace bakron

@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
     }
   }
   if (S > 1) {
+    __syncwarp();
     cluster.sync();
     if (rank == 0) {
       for (int i = threadIdx.x; i < NT * 8 * 16 * RB; i += kThreads) {
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
         static_cast<TX*>(a.y)[(t0 + c) * a.w.m + row0 + r] = from_float<TX>(v);
       }
     }
+    __syncwarp();
     cluster.sync();   // no block leaves while its sums are read
   }
 }

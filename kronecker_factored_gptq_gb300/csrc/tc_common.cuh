@@ -105,6 +105,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 // rows x cols fp32 row-major matrix with leading dimension ld (floats);
 // box = 32 columns (128 bytes) x 128 rows, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const float* ptr, int64_t rows, int64_t ld);
+// rows x cols matrix of 16-bit values (bf16 or fp16) without padding; box = 64
+// columns (128 bytes) x box_rows (at most 256) rows, 128-byte swizzle.  The
+// address and the row size must be multiples of 16 bytes.
+bool make_map16(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int box_rows, bool bf16);
 bool encode_available();
 
 }  // namespace tc

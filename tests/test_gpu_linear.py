@@ -1,11 +1,11 @@
 """The quantised linear layer on the GPU: bakron_pack, bakron_unpack,
-bakron_linear against the plain 64-bit forms."""
+bakron_linear and bakron_linear_grad against the plain 64-bit forms."""
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from _layer_helpers import bound, product_depth, random_weight, value
+from _layer_helpers import HALF_ULP, U, bound, product_depth, random_weight, value
 
 pytestmark = pytest.mark.gpu
 
@@ -29,6 +29,18 @@ def check_linear(y, x, V, dtype):
     b = bound(xd.abs() @ V.abs().T, product_depth(V.shape[1]), dtype, ref)
     assert torch.isfinite(y).all()
     worst = ((y.double() - ref).abs() / b).max().item()
+    assert worst <= 1.0, "error %.3g times the bound" % worst
+
+
+def check_grad(dx, dy, V, dtype):
+    yd = dy.double()
+    ref = yd @ V
+    mag = yd.abs() @ V.abs()
+    b = bound(mag, product_depth(V.shape[0], terms=6), dtype, ref)
+    if dtype != torch.float32:
+        b = b + HALF_ULP[dtype] * mag      # V rounded to dY's type
+    worst = ((dx.double() - ref).abs() / b).max().item()
+    assert torch.isfinite(dx).all()
     assert worst <= 1.0, "error %.3g times the bound" % worst
 
 
@@ -115,6 +127,7 @@ def test_linear_no_tokens():
     codes, scale, zero, qmin, qmax = random_weight((20, 40), 0, False, 8)
     w = kb.bakron_pack(codes, scale, qmin, qmax)
     assert kb.bakron_linear(torch.empty((0, 40), device="cuda"), w).shape == (0, 20)
+    assert kb.bakron_linear_grad(torch.empty((0, 20), device="cuda"), w).shape == (0, 40)
 
 
 @pytest.mark.parametrize("T", [4, 300])
@@ -190,6 +203,8 @@ def test_refusals():
     with pytest.raises(ValueError):
         kb.bakron_linear(x, w, out=torch.zeros((4, 32), dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError):
+        kb.bakron_linear_grad(x, w)
+    with pytest.raises(ValueError):
         kb.bakron_pack(codes, scale, qmin, qmax, group=48)
     bad = codes.clone()
     bad[31, 63] = 9
@@ -210,3 +225,57 @@ def test_refusals():
     two = kb.bakron_pack(torch.stack([codes, codes]), torch.stack([scale, scale]), qmin, qmax)
     with pytest.raises(ValueError):
         kb.bakron_linear(x, two)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,m,n,group,asym", [
+    (1, 64, 64, 0, False), (1, 1, 1, 0, True), (5, 130, 257, 32, True), (16, 17, 1111, 96, False),
+    (33, 4097, 100, 64, True), (64, 1000, 300, 128, False), (65, 256, 515, 0, True), (100, 128, 128, 32, False),
+    (200, 1111, 1000, 32, True), (257, 1024, 512, 128, False), (333, 520, 1300, 256, True), (1000, 200, 384, 96, False)])
+def test_linear_grad(T, m, n, group, asym, dtype):
+    kb = _kb()
+    codes, scale, zero, qmin, qmax = random_weight((m, n), group, asym, T + m + n)
+    w = kb.bakron_pack(codes, scale, qmin, qmax, zero=zero, group=group)
+    dy = _x(T, m, dtype, n)
+    dx = kb.bakron_linear_grad(dy, w)
+    assert dx.shape == (T, n) and dx.dtype == dtype
+    check_grad(dx, dy, value(codes, scale, zero, group), dtype)
+    assert torch.equal(dx, kb.bakron_linear_grad(dy, w)), "two runs differ"
+    kb.bakron_async_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_linear_grad_from_unaligned_rows(dtype):
+    kb = _kb()
+    T, m, n = 40, 256, 101
+    codes, scale, zero, qmin, qmax = random_weight((m, n), 64, True, 3)
+    w = kb.bakron_pack(codes, scale, qmin, qmax, zero=zero, group=64)
+    base = torch.zeros(T * m + 1, dtype=dtype, device="cuda")
+    base[1:] = _x(T, m, dtype, 4).reshape(-1)
+    dy = base[1:].view(T, m)
+    obase = torch.full((T * n + 2,), 7.0, dtype=dtype, device="cuda")
+    out = obase[1:-1].view(T, n)
+    kb.bakron_linear_grad(dy, w, out=out)
+    check_grad(out, dy, value(codes, scale, zero, 64), dtype)
+    assert obase[0] == 7.0 and obase[-1] == 7.0
+
+
+def test_linear_grad_against_differences():
+    """The loss sum(g * linear(x)) is linear in x, so a central difference of
+    the 64-bit form is exact up to its rounding (1e-10 here)."""
+    kb = _kb()
+    T, m, n = 3, 20, 45
+    codes, scale, zero, qmin, qmax = random_weight((m, n), 32, True, 21)
+    w = kb.bakron_pack(codes, scale, qmin, qmax, zero=zero, group=32)
+    V = value(codes, scale, zero, 32)
+    x, g = _x(T, n, torch.float32, 1).double(), _x(T, m, torch.float32, 2)
+    dx = kb.bakron_linear_grad(g, w)
+    mag = g.double().abs() @ V.abs()
+    for t in range(T):
+        for j in range(n):
+            a, b = x.clone(), x.clone()
+            a[t, j] += 1e-3
+            b[t, j] -= 1e-3
+            d = ((g.double() * (a @ V.T)).sum() - (g.double() * (b @ V.T)).sum()) / 2e-3
+            tol = bound(mag[t, j], product_depth(m, 6), torch.float32, d) + 1e-9
+            assert abs(dx[t, j].item() - d.item()) <= tol
