@@ -349,8 +349,8 @@ bakron_status bakron_quantize_noalloc(const float* W, int64_t m, int64_t n,
 /* ------------------------------------------------ quantised layers in use
  *
  * The calls below run the layers that the solver has quantised: products
- * with the packed codes in both directions, and the layer norm in front of
- * them with its gradients.
+ * with the packed codes in both directions, a mixture-of-experts layer over
+ * packed experts, and the layer norm in front of them with its gradients.
  * They differ from the solver's calls in two points:
  *  - activations are fp32, bf16 or fp16 (bakron_dtype; one type per call),
  *    still dense, row-major and contiguous, at any address that is a multiple
@@ -432,6 +432,24 @@ bakron_status bakron_linear_grad_workspace_size(const bakron_packed* w, int64_t 
                                                 size_t* bytes);
 bakron_status bakron_linear_grad(const void* dY, int64_t T, int dtype, const bakron_packed* w,
                                  void* dX, void* ws, size_t ws_bytes, void* stream);
+
+/* A mixture-of-experts layer for a few tokens.  X is T x d; router (E x d)
+ * has X's type; w_in holds E matrices of 2 f x d, rows 0..f-1 the gate and
+ * rows f..2f-1 the up projection; w_out holds E matrices of d x f.  Per token
+ *   l_e = sum_j X_j router_ej,   p = softmax(l) over all experts,
+ *   the top_k experts with the largest l_e (a tie goes to the lowest index),
+ *   q_e = p_e, or with renormalize p_e over the sum of the chosen ones,
+ *   h_e = silu(gate_e X) * (up_e X),   Y = sum over the chosen e of q_e (w_out_e h_e).
+ * 1 <= top_k <= E <= 1024, top_k <= 16.  A logit that is NaN makes the
+ * token's row of Y NaN.  Any T >= 0; a launch takes BAKRON_MOE_TOKENS tokens,
+ * so larger T run as several.  ws: device, 256-byte aligned,
+ * bakron_moe_workspace_size bytes. */
+enum { BAKRON_MOE_TOKENS = 32 };
+bakron_status bakron_moe_workspace_size(const bakron_packed* w_in, const bakron_packed* w_out,
+                                        int64_t T, int top_k, int dtype, size_t* bytes);
+bakron_status bakron_moe(const void* X, int64_t T, int dtype, const void* router,
+                         const bakron_packed* w_in, const bakron_packed* w_out, int top_k,
+                         int renormalize, void* Y, void* ws, size_t ws_bytes, void* stream);
 
 /* Layer norm over the rows of X (T x d; d <= 2^20): with mu and var the mean and
  * the biased variance of a row and r = 1 / sqrt(var + eps),

@@ -29,12 +29,13 @@ EXPORTS = ["bakron_default_opts", "bakron_status_string", "bakron_version", "bak
            "bakron_quantize_batch", "bakron_schedule_export", "bakron_fma_probe", "bakron_sm_count",
            "bakron_plan_size", "bakron_plan_init", "bakron_async_status", "bakron_pack_size",
            "bakron_pack", "bakron_unpack", "bakron_linear_workspace_size", "bakron_linear",
-           "bakron_linear_grad_workspace_size", "bakron_linear_grad",
-           "bakron_layernorm", "bakron_layernorm_grad_workspace_size",
+           "bakron_linear_grad_workspace_size", "bakron_linear_grad", "bakron_moe_workspace_size",
+           "bakron_moe", "bakron_layernorm", "bakron_layernorm_grad_workspace_size",
            "bakron_layernorm_grad"]
 FACTORS_KFAC = 0
 FACTORS_SHAMPOO = 1
 F32, BF16, F16 = 0, 1, 2      # bakron_dtype
+MOE_TOKENS = 32               # tokens of one bakron_moe launch
 
 
 class PhaseTimes(ctypes.Structure):
@@ -126,6 +127,8 @@ def lib():
     L.bakron_linear.argtypes = [vp, i64, ctypes.c_int, pk, vp, vp, sz, vp]
     L.bakron_linear_grad_workspace_size.argtypes = [pk, i64, ctypes.c_int, ctypes.POINTER(sz)]
     L.bakron_linear_grad.argtypes = [vp, i64, ctypes.c_int, pk, vp, vp, sz, vp]
+    L.bakron_moe_workspace_size.argtypes = [pk, pk, i64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(sz)]
+    L.bakron_moe.argtypes = [vp, i64, ctypes.c_int, vp, pk, pk, ctypes.c_int, ctypes.c_int, vp, vp, sz, vp]
     L.bakron_layernorm.argtypes = [vp, i64, i64, ctypes.c_int, vp, vp, f32, vp, vp, vp, vp]
     L.bakron_layernorm_grad_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
     L.bakron_layernorm_grad.argtypes = [vp, vp, i64, i64, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -137,7 +140,7 @@ def lib():
               "bakron_plan_init", "bakron_async_status", "bakron_pack_size", "bakron_pack",
               "bakron_unpack", "bakron_linear_workspace_size", "bakron_linear",
               "bakron_linear_grad_workspace_size", "bakron_linear_grad",
-              "bakron_layernorm",
+              "bakron_moe_workspace_size", "bakron_moe", "bakron_layernorm",
               "bakron_layernorm_grad_workspace_size", "bakron_layernorm_grad"):
         getattr(L, f).restype = ctypes.c_int
     _LIB = L
@@ -668,6 +671,49 @@ def bakron_linear_grad(dy, w, out=None, workspace=None, stream=None):
     """dX = dY V, the gradient of bakron_linear for its activations: dy
     (T, m); returns (T, n) of dy's type."""
     return _linear(lib().bakron_linear_grad, "bakron_linear_grad", True, dy, w, out, workspace, stream)
+
+
+def moe_workspace_size(w_in, w_out, T, top_k, dtype):
+    torch = _torch()
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[dtype]
+    key = (T, code, top_k, w_out.n)
+    size = w_in._ws.get(key)
+    if size is None:
+        b = ctypes.c_size_t(0)
+        _check(lib().bakron_moe_workspace_size(w_in.ref, w_out.ref, T, int(top_k), code, ctypes.byref(b)),
+               "bakron_moe_workspace_size")
+        size = b.value
+        if len(w_in._ws) > 64:
+            w_in._ws.clear()
+        w_in._ws[key] = size
+    return size
+
+
+def moe_workspace(w_in, w_out, T, top_k, dtype):
+    """A workspace for bakron_moe of up to T tokens."""
+    nb = moe_workspace_size(w_in, w_out, T, top_k, dtype)
+    return _torch().empty(nb, dtype=_torch().uint8, device=w_in.device)
+
+
+def bakron_moe(x, router, w_in, w_out, top_k, renormalize=True, out=None, workspace=None, stream=None):
+    """A mixture-of-experts layer: x (T, d), router (E, d) of x's type, w_in
+    (E matrices of 2f x d: gate rows, then up rows), w_out (E of d x f).
+    Returns (T, d) of x's type."""
+    T, d, code = _act(x, "X", w_in.n)
+    if (w_in.count, w_out.m) != (w_out.count, d) or w_in.m != 2 * w_out.n:
+        raise ValueError("w_in must hold E matrices of 2f x d and w_out E of d x f, got %d of %d x %d and "
+                         "%d of %d x %d" % (w_in.count, w_in.m, w_in.n, w_out.count, w_out.m, w_out.n))
+    w_in._check(x, "X")
+    w_out._check(x, "X")
+    w_in._check(router, "router")
+    rp = _dev(router, x.dtype, (w_in.count, d), "router")
+    y = _out(out, x, (T, d), "out")
+    nb = moe_workspace_size(w_in, w_out, T, top_k, x.dtype)
+    ws = _ws(nb, workspace)
+    _check(lib().bakron_moe(x.data_ptr(), T, code, rp, w_in.ref, w_out.ref, int(top_k),
+                            1 if renormalize else 0, y.data_ptr(), ws.data_ptr(), nb, _stream(stream)),
+           "bakron_moe")
+    return y
 
 
 def bakron_layernorm(x, gamma=None, beta=None, eps=1e-5, out=None, want_stats=True, stream=None):

@@ -52,12 +52,8 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
   const int64_t c_lo = a.w.nc * rank / S, c_hi = a.w.nc * (rank + 1) / S;
 
   qm::TileRef tile[RB];
-  bool live[RB];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    live[b] = row0 + 16 * b < a.w.mp;
-    tile[b] = qm::tile_ref(a.w, 0, live[b] ? row0 + 16 * b : 0);
-  }
+  for (int b = 0; b < RB; ++b) tile[b] = qm::tile_ref(a.w, 0, row0 + 16 * b, lane);
   int col[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) col[j] = min(8 * j + (lane >> 2), cols - 1);
@@ -78,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
     // the first codes are on their way while the activations are staged
     if (c < s1) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b) qm::load_chunk<NS>(f[b], a.w, tile[b], c, lane);
+      for (int b = 0; b < RB; ++b) qm::load_chunk<NS>(f[b], a.w, tile[b], c);
     }
     if (s0 != c_lo) __syncthreads();
     qm::stage_x<TX, TERMS>(xs, plane, pitch, x, a.w.n, cols, [](int r) { return (int64_t)r; },
@@ -90,12 +86,13 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         g[b] = f[b];
-        if (more) qm::load_chunk<NS>(f[b], a.w, tile[b], c + kWarps, lane);
+        if (more) qm::load_chunk<NS>(f[b], a.w, tile[b], c + kWarps);
       }
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-        qm::chunk_product<H, TERMS, NT, NS>(tot[b], g[b], a.w.zero != nullptr, a.w.zu,
-                                            xs + (c - s0) * 256, plane, pitch, col, lane);
+      const uint8_t* xc = xs + (c - s0) * 256 + (lane & 3) * 16;
+      qm::chunk_product<H, TERMS, RB, NT, NS>(
+          tot, g, a.w.zero != nullptr, a.w.zu, NT, [&](int j, int q, int s) {
+            return *reinterpret_cast<const uint4*>(xc + q * plane + (uint32_t)col[j] * pitch + s * 64);
+          });
     }
   }
 

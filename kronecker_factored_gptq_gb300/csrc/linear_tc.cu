@@ -629,11 +629,7 @@ cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
   t.plane = a.T;
   if (TX != 1 || !aligned_to(a.x, 16) || K % 8 != 0) {
     const int64_t kp = k_padded(K);
-    const int64_t total = a.T * kp / 8;
-    const unsigned g = (unsigned)std::max<int64_t>(1, std::min<int64_t>((total + 255) / 256, (int64_t)sm_count() * 16));
-    count_launch();
-    planes_kernel<TO, TX><<<g, 256, 0, s>>>(static_cast<const TO*>(a.x), a.T, K, kp, static_cast<uint16_t*>(a.ws));
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_planes(a.x, a.dtype, a.T, K, kp, a.ws, s);
     if (e != cudaSuccess) return e;
     x = a.ws;
     ldx = kp;
@@ -678,6 +674,17 @@ cudaError_t run16(const LinearArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_t kp, void* out,
+                          cudaStream_t s) {
+  const int64_t total = T * kp / 8;
+  const unsigned g = (unsigned)std::max<int64_t>(1, std::min<int64_t>((total + 255) / 256, (int64_t)sm_count() * 16));
+  uint16_t* o = static_cast<uint16_t*>(out);
+  count_launch();
+  if (dtype == BAKRON_F32) planes_kernel<float, 3><<<g, 256, 0, s>>>(static_cast<const float*>(x), T, K, kp, o);
+  else planes_kernel<uint16_t, 1><<<g, 256, 0, s>>>(static_cast<const uint16_t*>(x), T, K, kp, o);
+  return cudaGetLastError();
+}
 
 size_t linear_tc_workspace(int64_t T, int64_t K, int dtype) {
   return (size_t)(dtype == BAKRON_F32 ? 3 : 1) * (size_t)T * (size_t)k_padded(K) * 2;

@@ -59,28 +59,42 @@ struct Chunk16 {
   uint32_t z[2][NS];
 };
 
-// Address of a 16-row tile: codes of its first 8-row block, scales, zeros.
+// A thread's two rows of a 16-row tile: codes (at the thread's 16 bytes of
+// the first chunk) and grid.
 struct TileRef {
-  const uint8_t* codes;   // block row of rows 0..7; rows 8..15 are nc blocks further
-  const float* scale;     // + k mp
-  const uint8_t* zero;
+  const uint8_t* codes[2];
+  const float* scale[2];    // + k mp
+  const uint8_t* zero[2];   // likewise; NULL when every zero point is the same
 };
 
-__device__ __forceinline__ TileRef tile_ref(const PackedView& w, int64_t e, int64_t row0) {
+// Rows row0 + lane / 4 and + 8 of matrix e; rows past the padding repeat its
+// last row (their products are dropped by the caller).
+__device__ __forceinline__ TileRef tile_ref(const PackedView& w, int64_t e, int64_t row0, int lane) {
   TileRef t;
-  t.codes = w.codes + (e * (w.mp / 8) + row0 / 8) * w.nc * kBlockBytes;
-  t.scale = w.scale + e * w.ng * w.mp + row0;
-  t.zero = w.zero ? w.zero + e * w.ng * w.mp + row0 : nullptr;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = min(row0 + (lane >> 2) + 8 * i, w.mp - 1);
+    t.codes[i] = w.codes + (e * (w.mp / 8) + r / 8) * w.nc * kBlockBytes + (r & 7) * 64 + (lane & 3) * 16;
+    t.scale[i] = w.scale + e * w.ng * w.mp + r;
+    t.zero[i] = w.zero ? w.zero + e * w.ng * w.mp + r : nullptr;
+  }
   return t;
+}
+
+// The codes are read once: past L1.
+__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
 template <int NS>
 __device__ __forceinline__ void load_chunk(Chunk16<NS>& f, const PackedView& w, const TileRef& t,
-                                           int64_t c, int lane) {
-  const uint8_t* p = t.codes + c * kBlockBytes + lane * 16;
-  f.w[0] = __ldg(reinterpret_cast<const uint4*>(p));
-  f.w[1] = __ldg(reinterpret_cast<const uint4*>(p + w.nc * kBlockBytes));
-  const int r = lane >> 2;
+                                           int64_t c) {
+  f.w[0] = ld_codes(t.codes[0] + c * kBlockBytes);
+  f.w[1] = ld_codes(t.codes[1] + c * kBlockBytes);
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     int64_t k = 0;
@@ -89,62 +103,70 @@ __device__ __forceinline__ void load_chunk(Chunk16<NS>& f, const PackedView& w, 
       if (k > w.ng - 1) k = w.ng - 1;
     }
     k *= w.mp;
-    f.s[0][s] = __ldg(t.scale + k + r);
-    f.s[1][s] = __ldg(t.scale + k + r + 8);
-    if (t.zero) {
-      f.z[0][s] = __ldg(t.zero + k + r);
-      f.z[1][s] = __ldg(t.zero + k + r + 8);
+    f.s[0][s] = __ldg(t.scale[0] + k);
+    f.s[1][s] = __ldg(t.scale[1] + k);
+    if (w.zero) {
+      f.z[0][s] = __ldg(t.zero[0] + k);
+      f.z[1][s] = __ldg(t.zero[1] + k);
     }
   }
 }
 
-// tot += the chunk's products with the activations of NT x 8 columns.
-// xs: shared memory, TERMS planes of xplane bytes, a column's row of xpitch
-// bytes, the chunk's first column at xs; col[j]: this thread's column of
-// column tile j.
-template <typename H, int TERMS, int NT, int NS>
-__device__ __forceinline__ void chunk_product(float (&tot)[NT][4], const Chunk16<NS>& f, bool has_zero,
-                                              int zu, const uint8_t* xs, uint32_t xplane,
-                                              uint32_t xpitch, const int (&col)[NT], int lane) {
-  const int t = lane & 3;
-  float acc[NT][4];
+// tot[r][j] += products of the chunk of row tile r with column tile j, for j <
+// live (uniform).  fetch(j, q, s): this thread's 8 columns 32 s + 8 t .. of
+// term q of its activation row in column tile j.
+template <typename H, int TERMS, int RT, int NT, int NS, typename Fetch>
+__device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chunk16<NS> (&f)[RT],
+                                              bool has_zero, int zu, int live, Fetch fetch) {
+  float acc[RT][NT][4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-  uint32_t off0 = 0, off1 = 0;
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[r][j][i] = 0.f;
+  uint32_t off[RT][2];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    if (s < NS) {
-      const int z0 = has_zero ? (int)f.z[0][s] : zu, z1 = has_zero ? (int)f.z[1][s] : zu;
-      off0 = Half2<H>::pair(Half2<H>::kBase + (float)z0);
-      off1 = Half2<H>::pair(Half2<H>::kBase + (float)z1);
+    uint32_t a[RT][4], b[RT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if (s < NS) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          off[r][i] = Half2<H>::pair(Half2<H>::kBase + (float)(has_zero ? (int)f[r].z[i][s] : zu));
+      }
+      const uint4 w0 = f[r].w[0], w1 = f[r].w[1];
+      unpack_word<H>(s == 0 ? w0.x : s == 1 ? w0.y : s == 2 ? w0.z : w0.w, off[r][0], a[r]);
+      unpack_word<H>(s == 0 ? w1.x : s == 1 ? w1.y : s == 2 ? w1.z : w1.w, off[r][1], b[r]);
     }
-    const uint32_t wa = s == 0 ? f.w[0].x : s == 1 ? f.w[0].y : s == 2 ? f.w[0].z : f.w[0].w;
-    const uint32_t wb = s == 0 ? f.w[1].x : s == 1 ? f.w[1].y : s == 2 ? f.w[1].z : f.w[1].w;
-    uint32_t a[4], b[4];
-    unpack_word<H>(wa, off0, a);
-    unpack_word<H>(wb, off1, b);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
+      if (j < live) {
 #pragma unroll
-      for (int q = 0; q < TERMS; ++q) {
-        const uint4 x = *reinterpret_cast<const uint4*>(xs + q * xplane + (uint32_t)col[j] * xpitch +
-                                                        s * 64 + t * 16);
-        mma16816<H>(acc[j], a[0], b[0], a[1], b[1], x.x, x.y);
-        mma16816<H>(acc[j], a[2], b[2], a[3], b[3], x.z, x.w);
+        for (int q = 0; q < TERMS; ++q) {
+          const uint4 x = fetch(j, q, s);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            mma16816<H>(acc[r][j], a[r][0], b[r][0], a[r][1], b[r][1], x.x, x.y);
+            mma16816<H>(acc[r][j], a[r][2], b[r][2], a[r][3], b[r][3], x.z, x.w);
+          }
+        }
       }
     }
     if (NS == 4 || s == 3) {
-      const float s0 = f.s[0][NS == 4 ? s : 0], s1 = f.s[1][NS == 4 ? s : 0];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        tot[j][0] = fmaf(s0, acc[j][0], tot[j][0]);
-        tot[j][1] = fmaf(s0, acc[j][1], tot[j][1]);
-        tot[j][2] = fmaf(s1, acc[j][2], tot[j][2]);
-        tot[j][3] = fmaf(s1, acc[j][3], tot[j][3]);
+      for (int r = 0; r < RT; ++r) {
+        const float s0 = f[r].s[0][NS == 4 ? s : 0], s1 = f[r].s[1][NS == 4 ? s : 0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+        for (int j = 0; j < NT; ++j) {
+          tot[r][j][0] = fmaf(s0, acc[r][j][0], tot[r][j][0]);
+          tot[r][j][1] = fmaf(s0, acc[r][j][1], tot[r][j][1]);
+          tot[r][j][2] = fmaf(s1, acc[r][j][2], tot[r][j][2]);
+          tot[r][j][3] = fmaf(s1, acc[r][j][3], tot[r][j][3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][j][i] = 0.f;
+        }
       }
     }
   }
