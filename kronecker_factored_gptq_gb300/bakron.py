@@ -204,11 +204,17 @@ def _check(st, where):
         raise BakronError(st, where)
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    if not torch.cuda.is_available():
-        raise RuntimeError("no CUDA device: the BaKron library runs on the GPU only")
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        if not torch.cuda.is_available():
+            raise RuntimeError("no CUDA device: the BaKron library runs on the GPU only")
+        _TORCH = torch
+    return _TORCH
 
 
 def _dev(t, dtype, shape, name):
@@ -522,6 +528,11 @@ def bakron_factors(X=None, G=None, mode=FACTORS_KFAC, want_A=True, want_B=True, 
 
 # ------------------------------------------------ quantised layers in use
 #
+# A call for one token takes a few microseconds on the GPU, less than careless
+# marshalling takes on the host: what these functions look up more than once
+# is kept, addresses go to ctypes as plain integers, and the current stream is
+# asked for its handle only.
+#
 # These calls only enqueue (bakron_pack and bakron_unpack excepted) on
 # ``stream``, or on the current stream.  Tensors allocated here belong to the
 # current stream as far as PyTorch's allocator knows; a caller who passes
@@ -529,30 +540,56 @@ def bakron_factors(X=None, G=None, mode=FACTORS_KFAC, want_A=True, want_B=True, 
 # streams ordered.
 
 
+_DTYPES = {}
+
+
+def _dtypes():
+    """torch dtype -> bakron_dtype of the activations."""
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    return _DTYPES
+
+
+def _handle(stream):
+    """cudaStream_t of ``stream``, or of the current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+
+
 def _act(t, name, cols=None):
     """Checks an activation matrix; returns (rows, columns, bakron_dtype)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    dt = t.dtype
-    code = BF16 if dt == torch.bfloat16 else F16 if dt == torch.float16 else F32 if dt == torch.float32 else -1
-    if code < 0:
-        raise ValueError("%s must be float32, bfloat16 or float16, got %s" % (name, dt))
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+    code = (_DTYPES or _dtypes()).get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols):
         raise ValueError("%s must have shape (tokens, %s), got %s"
-                         % (name, "columns" if cols is None else cols, tuple(t.shape)))
+                         % (name, "columns" if cols is None else cols, tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return t.shape[0], t.shape[1], code
+    return shape[0], shape[1], code
+
+
+def _same(t, like, shape, name):
+    """Checks a tensor that must have the type and device of ``like``; returns its address."""
+    if not isinstance(t, _torch().Tensor) or t.dtype != like.dtype or t.get_device() != like.get_device():
+        raise ValueError("%s must be a %s tensor on %s" % (name, like.dtype, like.device))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def _out(out, like, shape, name):
-    torch = _torch()
     if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    _dev(out, like.dtype, shape, name)
-    if out.device != like.device:
-        raise ValueError("%s must be on %s" % (name, like.device))
+        return _torch().empty(shape, dtype=like.dtype, device=like.device)
+    _same(out, like, shape, name)
     return out
 
 
@@ -560,9 +597,11 @@ def _vec(t, n, like, name):
     """Device address of a float32 vector of n elements, or None."""
     if t is None:
         return None
-    if t.device != like.device:
-        raise ValueError("%s must be on %s" % (name, like.device))
-    return _dev(t, _torch().float32, (n,), name)
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.get_device() != like.get_device() or \
+            t.shape != (n,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of shape (%d,) on %s" % (name, n, like.device))
+    return t.data_ptr()
 
 
 class PackedWeight:
@@ -575,10 +614,11 @@ class PackedWeight:
         self.desc = Packed(count, m, n, group, qmin, 1 if has_zero else 0, data.data_ptr(), data.numel())
         self.ref = ctypes.byref(self.desc)
         self.device = data.device
+        self._index = data.get_device()
         self._ws = {}
 
     def _check(self, like, name):
-        if like.device != self.device:
+        if like.get_device() != self._index:
             raise ValueError("%s must be on %s, the weight's device" % (name, self.device))
 
     def unpack(self, stream=None):
@@ -625,11 +665,10 @@ def bakron_async_status(stream=None):
 
 
 def linear_workspace_size(w, T, dtype, grad=False):
-    torch = _torch()
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[dtype]
-    key = (T, code, grad)
+    key = (T, dtype, grad)
     size = w._ws.get(key)
     if size is None:
+        code = _dtypes()[dtype]
         f = lib().bakron_linear_grad_workspace_size if grad else lib().bakron_linear_workspace_size
         b = ctypes.c_size_t(0)
         _check(f(w.ref, T, code, ctypes.byref(b)), "bakron_linear_workspace_size")
@@ -655,9 +694,10 @@ def _linear(fn, where, grad, x, w, out, workspace, stream):
         raise ValueError("%s takes a single matrix, got %d" % (where, w.count))
     y = _out(out, x, (T, w.n if grad else w.m), "out")
     nb = linear_workspace_size(w, T, x.dtype, grad)
-    ws = _ws(nb, workspace) if nb else None
-    _check(fn(x.data_ptr(), T, code, w.ref, y.data_ptr(), None if ws is None else ws.data_ptr(), nb,
-              _stream(stream)), where)
+    ws = _ws(nb, workspace) if nb else None     # alive until the call is enqueued
+    st = fn(x.data_ptr(), T, code, w.ref, y.data_ptr(), None if ws is None else ws.data_ptr(), nb, _handle(stream))
+    if st != OK:
+        raise BakronError(st, where)
     return y
 
 
@@ -674,11 +714,10 @@ def bakron_linear_grad(dy, w, out=None, workspace=None, stream=None):
 
 
 def moe_workspace_size(w_in, w_out, T, top_k, dtype):
-    torch = _torch()
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[dtype]
-    key = (T, code, top_k, w_out.n)
+    key = (T, dtype, top_k, w_out.n)
     size = w_in._ws.get(key)
     if size is None:
+        code = _dtypes()[dtype]
         b = ctypes.c_size_t(0)
         _check(lib().bakron_moe_workspace_size(w_in.ref, w_out.ref, T, int(top_k), code, ctypes.byref(b)),
                "bakron_moe_workspace_size")
@@ -705,13 +744,12 @@ def bakron_moe(x, router, w_in, w_out, top_k, renormalize=True, out=None, worksp
                          "%d of %d x %d" % (w_in.count, w_in.m, w_in.n, w_out.count, w_out.m, w_out.n))
     w_in._check(x, "X")
     w_out._check(x, "X")
-    w_in._check(router, "router")
-    rp = _dev(router, x.dtype, (w_in.count, d), "router")
+    rp = _same(router, x, (w_in.count, d), "router")
     y = _out(out, x, (T, d), "out")
     nb = moe_workspace_size(w_in, w_out, T, top_k, x.dtype)
     ws = _ws(nb, workspace)
     _check(lib().bakron_moe(x.data_ptr(), T, code, rp, w_in.ref, w_out.ref, int(top_k),
-                            1 if renormalize else 0, y.data_ptr(), ws.data_ptr(), nb, _stream(stream)),
+                            1 if renormalize else 0, y.data_ptr(), ws.data_ptr(), nb, _handle(stream)),
            "bakron_moe")
     return y
 
@@ -720,25 +758,33 @@ def bakron_layernorm(x, gamma=None, beta=None, eps=1e-5, out=None, want_stats=Tr
     """Layer norm of the rows of x (T, d); gamma, beta (d,) float32 or None.
     Returns (y, mean, rstd); mean and rstd (T,) float32 feed the gradient
     (None without want_stats)."""
-    torch = _torch()
     T, d, code = _act(x, "X")
     y = _out(out, x, (T, d), "out")
-    mean = rstd = None
+    mean = rstd = mp = rp = None
     if want_stats:
-        stats = torch.empty((2, T), dtype=torch.float32, device=x.device)
-        mean, rstd = stats[0], stats[1]
+        torch = _torch()
+        mean = torch.empty(T, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
     _check(lib().bakron_layernorm(x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"), _vec(beta, d, x, "beta"),
-                                  float(eps), y.data_ptr(), mean.data_ptr() if want_stats else None,
-                                  rstd.data_ptr() if want_stats else None, _stream(stream)),
-           "bakron_layernorm")
+                                  eps, y.data_ptr(), mp, rp, _handle(stream)), "bakron_layernorm")
     return y, mean, rstd
 
 
+_NORM_WS = {}
+
+
 def layernorm_grad_workspace_size(T, d):
-    b = ctypes.c_size_t(0)
-    _check(lib().bakron_layernorm_grad_workspace_size(T, d, ctypes.byref(b)),
-           "bakron_layernorm_grad_workspace_size")
-    return b.value
+    size = _NORM_WS.get((T, d))
+    if size is None:
+        b = ctypes.c_size_t(0)
+        _check(lib().bakron_layernorm_grad_workspace_size(T, d, ctypes.byref(b)),
+               "bakron_layernorm_grad_workspace_size")
+        size = b.value
+        if len(_NORM_WS) > 256:
+            _NORM_WS.clear()
+        _NORM_WS[(T, d)] = size
+    return size
 
 
 def layernorm_grad_workspace(T, d):
@@ -750,24 +796,23 @@ def bakron_layernorm_grad(dy, x, gamma, mean, rstd, want_weight_grads=True, out=
                           stream=None):
     """Gradients of bakron_layernorm: returns (dx, dgamma, dbeta), dgamma and
     dbeta (d,) float32 (None without want_weight_grads)."""
-    torch = _torch()
     T, d, code = _act(x, "X")
-    if dy.dtype != x.dtype or dy.device != x.device or tuple(dy.shape) != (T, d) or not dy.is_contiguous():
-        raise ValueError("dY must be a contiguous %s tensor of shape %s on %s" % (x.dtype, (T, d), x.device))
+    yp = _same(dy, x, (T, d), "dY")
     dx = _out(out, x, (T, d), "out")
-    dg = db = ws = None
+    dg = db = gp = bp = ws = None
     nb = 0
     if want_weight_grads:
-        grads = torch.empty((2, d), dtype=torch.float32, device=x.device)
-        dg, db = grads[0], grads[1]
+        torch = _torch()
+        dg = torch.empty(d, dtype=torch.float32, device=x.device)
+        db = torch.empty(d, dtype=torch.float32, device=x.device)
+        gp, bp = dg.data_ptr(), db.data_ptr()
         nb = layernorm_grad_workspace_size(T, d)
-        ws = _ws(nb, workspace)
-    _check(lib().bakron_layernorm_grad(dy.data_ptr(), x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"),
+        # kept until the call is enqueued, then the allocator may reuse it in stream order
+        keep = _ws(nb, workspace)
+        ws = keep.data_ptr()
+    _check(lib().bakron_layernorm_grad(yp, x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"),
                                        _vec(mean, T, x, "mean"), _vec(rstd, T, x, "rstd"), dx.data_ptr(),
-                                       None if dg is None else dg.data_ptr(),
-                                       None if db is None else db.data_ptr(),
-                                       None if ws is None else ws.data_ptr(), nb, _stream(stream)),
-           "bakron_layernorm_grad")
+                                       gp, bp, ws, nb, _handle(stream)), "bakron_layernorm_grad")
     return dx, dg, db
 
 
