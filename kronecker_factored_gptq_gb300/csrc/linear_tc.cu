@@ -153,6 +153,7 @@ struct Ctx {
   Bars* bars;
   uint32_t ring;       // first stage
   uint32_t stage_bytes;
+  uint32_t full_a, full_b, empty;   // barriers of the stages, 8 bytes each
   uint32_t tmem;
   int steps;           // K steps of 64
   int64_t c0;          // first K chunk
@@ -160,18 +161,39 @@ struct Ctx {
   int64_t t0;
 };
 
-__device__ __forceinline__ bool wait_or_abort(const TcArgs& a, const Ctx& x, const unsigned long long* bar,
-                                              uint32_t parity) {
+// Bounded wait; the clock is read only once the first try has failed.
+__device__ __forceinline__ bool wait_or_abort(const TcArgs& a, const Ctx& x, uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
   volatile int* ab = &x.bars->abort;
-  if (mbar_wait(smem_u32(bar), parity, ab)) return true;
+  if (mbar_wait(bar, parity, ab)) return true;
   atomicCAS(a.status, 0, (int)BAKRON_ERR_TIMEOUT);
   *ab = 1;
   return false;
 }
-// Wait until stage i may be written.
-__device__ __forceinline__ bool wait_free(const TcArgs& a, const Ctx& x, int i) {
-  if (i < a.stages) return true;
-  return wait_or_abort(a, x, &x.bars->empty[i % a.stages], (uint32_t)((i / a.stages) & 1) ^ 1u);
+// Position in the ring of stages, advanced without divisions: stage s and the
+// parity of its current use.
+struct Ring {
+  int s = 0;
+  uint32_t parity = 0;
+  bool first = true;      // first time round: the stage is free
+  __device__ __forceinline__ void advance(int by, int stages) {
+    s += by;
+    if (s >= stages) {
+      s -= stages;
+      parity ^= 1;
+      first = false;
+    }
+  }
+};
+// Wait until the stage may be written.
+__device__ __forceinline__ bool wait_free(const TcArgs& a, const Ctx& x, const Ring& r) {
+  return r.first || wait_or_abort(a, x, x.empty + 8u * (uint32_t)r.s, r.parity ^ 1u);
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 // Weights of the forward product: warp dw of DW takes 16 / DW blocks of 8
@@ -199,18 +221,18 @@ __device__ __forceinline__ void weights_forward(const TcArgs& a, const Ctx& x, i
       qq[b] = make_uint4(0, 0, 0, 0);
       zz[b] = 0;
       if (live) {
-        qq[b] = __ldg(reinterpret_cast<const uint4*>(src + b * stride + (int64_t)c * kBlockBytes));
+        qq[b] = ld_codes(src + b * stride + (int64_t)c * kBlockBytes);
         if (w.zero) {
           const uint8_t* zp = w.zero + (block0 + b) * 8 + r;
           const uint32_t k0 = (uint32_t)((x.c0 + c) * 128);
           if (!narrow) {
-            const uint32_t v = __ldg(zp + (w.ng > 1 ? (int64_t)min(k0 / (uint32_t)w.g, (uint32_t)w.ng - 1) * w.mp : 0));
+            const uint32_t v = ld_ahead(zp + (w.ng > 1 ? (int64_t)min(k0 / (uint32_t)w.g, (uint32_t)w.ng - 1) * w.mp : 0));
             zz[b] = v * 0x01010101u;
           } else {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
               const int64_t g = min((k0 + 32 * s) / (uint32_t)w.g, (uint32_t)w.ng - 1);
-              zz[b] |= (uint32_t)__ldg(zp + g * w.mp) << (8 * s);
+              zz[b] |= ld_ahead(zp + g * w.mp) << (8 * s);
             }
           }
         }
@@ -220,15 +242,15 @@ __device__ __forceinline__ void weights_forward(const TcArgs& a, const Ctx& x, i
   const uint32_t off_const = Half2<H>::pair(Half2<H>::kBase + (float)w.zu);
 #pragma unroll
   for (int p = 0; p < PF; ++p) load(q[p], z[p], p);
+  Ring rg;
   for (int c = 0; c < chunks; c += PF) {
 #pragma unroll
     for (int p = 0; p < PF; ++p) {
       if (c + p < chunks) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int i = 2 * (c + p) + h;
-          if (!wait_free(a, x, i)) return;
-          const uint32_t sa = x.ring + (uint32_t)(i % a.stages) * x.stage_bytes;
+          if (!wait_free(a, x, rg)) return;
+          const uint32_t sa = x.ring + (uint32_t)rg.s * x.stage_bytes;
 #pragma unroll
           for (int b = 0; b < RB; ++b) {
             const int row = (dw * RB + b) * 8 + r;
@@ -245,7 +267,8 @@ __device__ __forceinline__ void weights_forward(const TcArgs& a, const Ctx& x, i
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&x.bars->full_a[i % a.stages]));
+          if (lane == 0) mbar_arrive(x.full_a + 8u * (uint32_t)rg.s);
+          rg.advance(1, a.stages);
         }
         load(q[p], z[p], c + p + PF);
       }
@@ -273,18 +296,20 @@ __device__ __forceinline__ void weights_gradient(const TcArgs& a, const Ctx& x, 
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       q[k] = make_uint4(0, 0, 0, 0);
-      if (live) q[k] = __ldg(reinterpret_cast<const uint4*>(src + b * w.nc * kBlockBytes + k * 64));
+      if (live) q[k] = ld_codes(src + b * w.nc * kBlockBytes + k * 64);
     }
   };
   const int turn = min(DW, a.stages);
   if (dw >= turn) return;
   load(dw);
+  Ring rg;
+  rg.advance(dw, a.stages);
   for (int i = dw; i < x.steps; i += turn) {
     const int64_t b = first + (int64_t)i * 8;
     const bool live = b < nb;
     float sc[8];
     uint32_t off[4];
-    const uint32_t sa = x.ring + (uint32_t)(i % a.stages) * x.stage_bytes;
+    const uint32_t sa = x.ring + (uint32_t)rg.s * x.stage_bytes;
     bool waited = false;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -312,7 +337,7 @@ __device__ __forceinline__ void weights_gradient(const TcArgs& a, const Ctx& x, 
 #pragma unroll
       for (int k = 0; k < 8; ++k) word[k] = s == 0 ? q[k].x : s == 1 ? q[k].y : s == 2 ? q[k].z : q[k].w;
       if (!waited) {
-        if (!wait_free(a, x, i)) return;
+        if (!wait_free(a, x, rg)) return;
         waited = true;
       }
 #pragma unroll
@@ -349,7 +374,8 @@ __device__ __forceinline__ void weights_gradient(const TcArgs& a, const Ctx& x, 
     load(i + turn);
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&x.bars->full_a[i % a.stages]));
+    if (lane == 0) mbar_arrive(x.full_a + 8u * (uint32_t)rg.s);
+    rg.advance(turn, a.stages);
   }
 }
 
@@ -368,6 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t tile = blockIdx.x / S;
   Ctx x;
   x.bars = &bars;
+  x.full_a = smem_u32(bars.full_a);
+  x.full_b = smem_u32(bars.full_b);
+  x.empty = smem_u32(bars.empty);
   const uint32_t base_raw = smem_u32(dsm);
   x.ring = (base_raw + 1023u) & ~1023u;
   const uint32_t plane_b = (uint32_t)a.N * 128u;
@@ -414,66 +443,86 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     if constexpr (NC == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------- activations
       int issued = 0;
+      Ring rg;
       for (int i = 0; i < x.steps; ++i) {
-        if (!wait_free(a, x, i)) break;
-        const uint32_t fb = smem_u32(&bars.full_b[i % a.stages]);
-        mbar_expect_tx(fb, TX * plane_b);
-        const uint32_t sb = x.ring + (uint32_t)(i % a.stages) * x.stage_bytes + TW * kABytes;
+        if (!__all_sync(0xffffffffu, wait_free(a, x, rg))) break;
+        if (elect_one()) {
+          const uint32_t fb = x.full_b + 8u * (uint32_t)rg.s;
+          mbar_expect_tx(fb, TX * plane_b);
+          const uint32_t sb = x.ring + (uint32_t)rg.s * x.stage_bytes + TW * kABytes;
 #pragma unroll
-        for (int q = 0; q < TX; ++q)
-          tma_load_2d(sb + q * plane_b, &map, fb, (int)(x.c0 * 128) + i * 64, (int)(q * a.plane + x.t0));
+          for (int q = 0; q < TX; ++q)
+            tma_load_2d(sb + q * plane_b, &map, fb, (int)(x.c0 * 128) + i * 64, (int)(q * a.plane + x.t0));
+        }
+        rg.advance(1, a.stages);
         ++issued;
       }
+      __syncwarp();
       // every issued copy must have landed before the block may exit
       for (int i = max(0, issued - a.stages); i < issued; ++i) {
         const long long t0 = clock64();
-        while (!mbar_try_wait(smem_u32(&bars.full_b[i % a.stages]), (uint32_t)((i / a.stages) & 1))) {
+        while (!mbar_try_wait(x.full_b + 8u * (uint32_t)(i % a.stages), (uint32_t)((i / a.stages) & 1))) {
           if (clock64() - t0 > kBudget) {
             atomicCAS(a.status, 0, (int)BAKRON_ERR_TIMEOUT);
             break;
           }
         }
       }
-    } else if (warp == 1 && lane == 0) {
-      // ---------------- MMA issuer
+    } else if (warp == 1) {
+      // ---------------- MMA issuer: the warp waits together, one lane issues
       const uint32_t idesc = idesc_f16<H>(a.N);
+      const uint64_t desc_a0 = desc_sw128(x.ring), desc_b0 = desc_sw128(x.ring + TW * kABytes);
+      const uint32_t af = smem_u32(&bars.acc_full[0]), ae = smem_u32(&bars.acc_empty[0]);
       int u = 0, pos = 0;
+      uint32_t u_par = 1;                     // parity of the buffer's previous reading
       bool go = true;
+      Ring rg;
       for (int i = 0; i < x.steps && go; ++i) {
-        const int s = i % a.stages;
-        const uint32_t par = (uint32_t)((i / a.stages) & 1);
-        if (!wait_or_abort(a, x, &bars.full_b[s], par) || !wait_or_abort(a, x, &bars.full_a[s], par)) break;
-        const uint32_t sd = x.ring + (uint32_t)s * x.stage_bytes;
+        go = wait_or_abort(a, x, x.full_b + 8u * (uint32_t)rg.s, rg.parity) &&
+             wait_or_abort(a, x, x.full_a + 8u * (uint32_t)rg.s, rg.parity);
+        go = __all_sync(0xffffffffu, go);
+        if (!go) break;
+        fence_after_sync();
+        const uint64_t off = (uint64_t)(((uint32_t)rg.s * x.stage_bytes) >> 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (pos == 0 && u >= 2 && !wait_or_abort(a, x, &bars.acc_empty[u & 1], (uint32_t)((u / 2 - 1) & 1))) {
-            go = false;
-            break;
+          if (pos == 0 && u >= 2) {
+            go = __all_sync(0xffffffffu, wait_or_abort(a, x, ae + 8u * (uint32_t)(u & 1), u_par));
+            if (!go) break;
+            fence_after_sync();
           }
-          fence_after_sync();
-          const uint32_t d = x.tmem + (uint32_t)((u & 1) * a.N);
-          bool first = pos == 0;
+          const bool last = pos + 1 == a.ku16 || i * 4 + j == n16 - 1;
+          if (elect_one()) {
+            const uint32_t d = x.tmem + (uint32_t)((u & 1) * a.N);
+            bool first = pos == 0;
 #pragma unroll
-          for (int qw = 0; qw < TW; ++qw)
+            for (int qw = 0; qw < TW; ++qw)
 #pragma unroll
-            for (int qx = 0; qx < TX; ++qx) {
-              if (qw + qx > 2) continue;   // below 2^-24 of the product
-              mma_f16(d, desc_sw128(sd + qw * kABytes) + (uint64_t)(j * 2),
-                      desc_sw128(sd + TW * kABytes + qx * plane_b) + (uint64_t)(j * 2), idesc, first ? 0u : 1u);
-              first = false;
-            }
-          if (++pos == a.ku16 || i * 4 + j == n16 - 1) {
-            mma_commit(smem_u32(&bars.acc_full[u & 1]));
+              for (int qx = 0; qx < TX; ++qx) {
+                if (qw + qx > 2) continue;   // below 2^-24 of the product
+                mma_f16(d, desc_a0 + off + (uint64_t)(qw * (kABytes >> 4) + j * 2),
+                        desc_b0 + off + (uint64_t)(qx * (plane_b >> 4) + j * 2), idesc, first ? 0u : 1u);
+                first = false;
+              }
+            if (last) mma_commit(af + 8u * (uint32_t)(u & 1));
+          }
+          __syncwarp();
+          ++pos;
+          if (last) {
             pos = 0;
+            if (u & 1) u_par ^= 1;
             ++u;
           }
         }
-        mma_commit(smem_u32(&bars.empty[s]));
+        if (elect_one()) mma_commit(x.empty + 8u * (uint32_t)rg.s);
+        __syncwarp();
+        rg.advance(1, a.stages);
       }
-      mma_commit(smem_u32(&bars.done));
+      if (elect_one()) mma_commit(smem_u32(&bars.done));
+      __syncwarp();
     }
     if constexpr (NC == 128) role_end(false, warp);
   } else if (warp < 4 + DW) {
@@ -495,13 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!live || u >= units) return 0.f;
       const uint32_t k = (uint32_t)(x.c0 * 128) + (uint32_t)u * (uint32_t)(a.ku16 * 16);
       const int64_t g = a.w.ng > 1 ? (int64_t)min(k / (uint32_t)a.w.g, (uint32_t)a.w.ng - 1) : 0;
-      return __ldg(a.w.scale + g * a.w.mp + row);
+      return ld_ahead(a.w.scale + g * a.w.mp + row);
     };
     float s_next = scale_of(0);
     for (int u = 0; u < units; ++u) {
       const float s = GRAD ? 1.f : s_next;
       if constexpr (!GRAD) s_next = scale_of(u + 1);
-      ok = wait_or_abort(a, x, &bars.acc_full[u & 1], (uint32_t)((u >> 1) & 1));
+      ok = wait_or_abort(a, x, smem_u32(&bars.acc_full[u & 1]), (uint32_t)((u >> 1) & 1));
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       fence_after_sync();

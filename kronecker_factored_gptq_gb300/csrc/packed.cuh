@@ -100,6 +100,27 @@ int* async_status_word();
 
 // ------------------------------------------------------------ device code
 
+// Loads ahead of their use.  The compiler may move an ordinary read-only load
+// down to its use, past the barriers in between, which would expose its latency;
+// these stay where they are written.  The codes are read once: past L1.
+__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_ahead(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_ahead(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // The 16-bit operand type of the products: exact for integers up to 256
 // (bf16) or 2048 (fp16), so u - z never rounds.
 template <typename H>

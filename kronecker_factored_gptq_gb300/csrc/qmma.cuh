@@ -81,15 +81,6 @@ __device__ __forceinline__ TileRef tile_ref(const PackedView& w, int64_t e, int6
   return t;
 }
 
-// The codes are read once: past L1.
-__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 template <int NS>
 __device__ __forceinline__ void load_chunk(Chunk16<NS>& f, const PackedView& w, const TileRef& t,
                                            int64_t c) {
@@ -103,11 +94,11 @@ __device__ __forceinline__ void load_chunk(Chunk16<NS>& f, const PackedView& w, 
       if (k > w.ng - 1) k = w.ng - 1;
     }
     k *= w.mp;
-    f.s[0][s] = __ldg(t.scale[0] + k);
-    f.s[1][s] = __ldg(t.scale[1] + k);
+    f.s[0][s] = ld_ahead(t.scale[0] + k);
+    f.s[1][s] = ld_ahead(t.scale[1] + k);
     if (w.zero) {
-      f.z[0][s] = __ldg(t.zero[0] + k);
-      f.z[1][s] = __ldg(t.zero[1] + k);
+      f.z[0][s] = ld_ahead(t.zero[0] + k);
+      f.z[1][s] = ld_ahead(t.zero[1] + k);
     }
   }
 }
