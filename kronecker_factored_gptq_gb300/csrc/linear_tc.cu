@@ -67,7 +67,6 @@ struct TcArgs {
   int tiles_m;
   int chunks;         // 128-wide K chunks
   int N;              // tokens per tile, a multiple of 32 per epilogue column part
-  int ku16;           // accumulation unit in steps of 16
   int stages;
   int* status;
 };
@@ -142,7 +141,7 @@ __device__ __forceinline__ void role_end(bool epilogue, int warp) {
 }
 
 struct Bars {
-  unsigned long long full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages];
+  unsigned long long full[kMaxStages], empty[kMaxStages];
   unsigned long long acc_full[2], acc_empty[2], done;
   uint32_t tmem;
   int abort;
@@ -153,7 +152,7 @@ struct Ctx {
   Bars* bars;
   uint32_t ring;       // first stage
   uint32_t stage_bytes;
-  uint32_t full_a, full_b, empty;   // barriers of the stages, 8 bytes each
+  uint32_t full, empty;   // barriers of the stages, 8 bytes each
   uint32_t tmem;
   int steps;           // K steps of 64
   int64_t c0;          // first K chunk
@@ -267,7 +266,7 @@ __device__ __forceinline__ void weights_forward(const TcArgs& a, const Ctx& x, i
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(x.full_a + 8u * (uint32_t)rg.s);
+          if (lane == 0) mbar_arrive(x.full + 8u * (uint32_t)rg.s);
           rg.advance(1, a.stages);
         }
         load(q[p], z[p], c + p + PF);
@@ -374,14 +373,15 @@ __device__ __forceinline__ void weights_gradient(const TcArgs& a, const Ctx& x, 
     load(i + turn);
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.full_a + 8u * (uint32_t)rg.s);
+    if (lane == 0) mbar_arrive(x.full + 8u * (uint32_t)rg.s);
     rg.advance(turn, a.stages);
   }
 }
 
 // GRAD: direction; TX, TW: 16-bit terms of the activations and of the
-// weights; NC: columns per epilogue warp; DW: weight warps (EW = 12 - DW).
-template <typename TO, typename H, bool GRAD, int TX, int TW, int NC, int DW>
+// weights; NC: columns per epilogue warp; DW: weight warps (EW = 12 - DW);
+// KU: accumulation unit in MMA steps of 16 (2, 4 or 8).
+template <typename TO, typename H, bool GRAD, int TX, int TW, int NC, int DW, int KU>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TcArgs a) {
   constexpr int EW = 12 - DW;
@@ -394,8 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t tile = blockIdx.x / S;
   Ctx x;
   x.bars = &bars;
-  x.full_a = smem_u32(bars.full_a);
-  x.full_b = smem_u32(bars.full_b);
+  x.full = smem_u32(bars.full);
   x.empty = smem_u32(bars.empty);
   const uint32_t base_raw = smem_u32(dsm);
   x.ring = (base_raw + 1023u) & ~1023u;
@@ -405,8 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   x.t0 = tile / a.tiles_m * a.N;
   x.c0 = (int64_t)a.chunks * rank / S;
   x.steps = 2 * (int)((int64_t)a.chunks * (rank + 1) / S - x.c0);
-  const int n16 = x.steps * 4;                          // MMA steps of 16
-  const int units = (n16 + a.ku16 - 1) / a.ku16;
+  const int units = x.steps * 4 / KU;
   uint32_t cols = 32;
   while (cols < 2u * (uint32_t)a.N) cols *= 2;
 
@@ -414,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     bars.abort = 0;
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(smem_u32(&bars.full_a[s]), GRAD ? 1 : DW);
-      mbar_init(smem_u32(&bars.full_b[s]), 1);
+      mbar_init(smem_u32(&bars.full[s]), 1 + (GRAD ? 1 : DW));   // the copies and the weights
       mbar_init(smem_u32(&bars.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -450,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < x.steps; ++i) {
         if (!__all_sync(0xffffffffu, wait_free(a, x, rg))) break;
         if (elect_one()) {
-          const uint32_t fb = x.full_b + 8u * (uint32_t)rg.s;
+          const uint32_t fb = x.full + 8u * (uint32_t)rg.s;
           mbar_expect_tx(fb, TX * plane_b);
           const uint32_t sb = x.ring + (uint32_t)rg.s * x.stage_bytes + TW * kABytes;
 #pragma unroll
@@ -464,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every issued copy must have landed before the block may exit
       for (int i = max(0, issued - a.stages); i < issued; ++i) {
         const long long t0 = clock64();
-        while (!mbar_try_wait(x.full_b + 8u * (uint32_t)(i % a.stages), (uint32_t)((i / a.stages) & 1))) {
+        while (!mbar_try_wait(x.full + 8u * (uint32_t)(i % a.stages), (uint32_t)((i / a.stages) & 1))) {
           if (clock64() - t0 > kBudget) {
             atomicCAS(a.status, 0, (int)BAKRON_ERR_TIMEOUT);
             break;
@@ -472,54 +469,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 1) {
-      // ---------------- MMA issuer: the warp waits together, one lane issues
+      // ---------------- MMA issuer: the warp waits together, one lane issues.
+      // A single warp's dependent instructions, not the tensor core, bound
+      // this loop when it is long, so everything is fixed per K chunk of two
+      // stages: where units begin and end, and the descriptors' offsets.
       const uint32_t idesc = idesc_f16<H>(a.N);
       const uint64_t desc_a0 = desc_sw128(x.ring), desc_b0 = desc_sw128(x.ring + TW * kABytes);
+      const uint32_t stage16 = x.stage_bytes >> 4, plane16 = plane_b >> 4;
       const uint32_t af = smem_u32(&bars.acc_full[0]), ae = smem_u32(&bars.acc_empty[0]);
-      int u = 0, pos = 0;
-      uint32_t u_par = 1;                     // parity of the buffer's previous reading
+      constexpr int UPS = KU >= 4 ? 1 : 2;    // units that a stage takes part in
+      uint32_t u = 0;                         // units begun
       bool go = true;
       Ring rg;
-      for (int i = 0; i < x.steps && go; ++i) {
-        go = wait_or_abort(a, x, x.full_b + 8u * (uint32_t)rg.s, rg.parity) &&
-             wait_or_abort(a, x, x.full_a + 8u * (uint32_t)rg.s, rg.parity);
-        go = __all_sync(0xffffffffu, go);
-        if (!go) break;
-        fence_after_sync();
-        const uint64_t off = (uint64_t)(((uint32_t)rg.s * x.stage_bytes) >> 4);
+      for (int c = 0; c < x.steps / 2 && go; ++c) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (pos == 0 && u >= 2) {
-            go = __all_sync(0xffffffffu, wait_or_abort(a, x, ae + 8u * (uint32_t)(u & 1), u_par));
-            if (!go) break;
-            fence_after_sync();
+        for (int h = 0; h < 2; ++h) {
+          if (KU < 8 || h == 0) {
+#pragma unroll
+            for (int k = 0; k < UPS; ++k) {
+              // the buffer's previous unit, u - 2, has been read
+              if (u >= 2) go = go && wait_or_abort(a, x, ae + 8u * (u & 1), ((u >> 1) & 1) ^ 1u);
+              ++u;
+            }
           }
-          const bool last = pos + 1 == a.ku16 || i * 4 + j == n16 - 1;
+          go = go && wait_or_abort(a, x, x.full + 8u * (uint32_t)rg.s, rg.parity);
+          go = __all_sync(0xffffffffu, go);
+          if (!go) break;
+          fence_after_sync();
           if (elect_one()) {
-            const uint32_t d = x.tmem + (uint32_t)((u & 1) * a.N);
-            bool first = pos == 0;
+            const uint64_t da = desc_a0 + (uint32_t)rg.s * stage16, db = desc_b0 + (uint32_t)rg.s * stage16;
+            const uint32_t first_u = u - UPS;
 #pragma unroll
-            for (int qw = 0; qw < TW; ++qw)
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t buf = (first_u + (KU == 2 ? j / 2 : 0)) & 1;
+              const uint32_t d = x.tmem + buf * (uint32_t)a.N;
+              const bool begin = KU == 8 ? h == 0 && j == 0 : j % KU == 0;
+              const bool end = KU == 8 ? h == 1 && j == 3 : j % KU == KU - 1;
+              bool fresh = begin;
 #pragma unroll
-              for (int qx = 0; qx < TX; ++qx) {
-                if (qw + qx > 2) continue;   // below 2^-24 of the product
-                mma_f16(d, desc_a0 + off + (uint64_t)(qw * (kABytes >> 4) + j * 2),
-                        desc_b0 + off + (uint64_t)(qx * (plane_b >> 4) + j * 2), idesc, first ? 0u : 1u);
-                first = false;
-              }
-            if (last) mma_commit(af + 8u * (uint32_t)(u & 1));
+              for (int qw = 0; qw < TW; ++qw)
+#pragma unroll
+                for (int qx = 0; qx < TX; ++qx) {
+                  if (qw + qx > 2) continue;   // below 2^-24 of the product
+                  mma_f16(d, da + (uint32_t)(qw * (kABytes >> 4) + j * 2), db + (qx * plane16 + j * 2), idesc,
+                          fresh ? 0u : 1u);
+                  fresh = false;
+                }
+              if (end) mma_commit(af + 8u * buf);
+            }
+            mma_commit(x.empty + 8u * (uint32_t)rg.s);
           }
           __syncwarp();
-          ++pos;
-          if (last) {
-            pos = 0;
-            if (u & 1) u_par ^= 1;
-            ++u;
-          }
+          rg.advance(1, a.stages);
         }
-        if (elect_one()) mma_commit(x.empty + 8u * (uint32_t)rg.s);
-        __syncwarp();
-        rg.advance(1, a.stages);
       }
       if (elect_one()) mma_commit(smem_u32(&bars.done));
       __syncwarp();
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = !GRAD && row < a.w.mp;
     auto scale_of = [&](int u) {
       if (!live || u >= units) return 0.f;
-      const uint32_t k = (uint32_t)(x.c0 * 128) + (uint32_t)u * (uint32_t)(a.ku16 * 16);
+      const uint32_t k = (uint32_t)(x.c0 * 128) + (uint32_t)u * (KU * 16);
       const int64_t g = a.w.ng > 1 ? (int64_t)min(k / (uint32_t)a.w.g, (uint32_t)a.w.ng - 1) : 0;
       return ld_ahead(a.w.scale + g * a.w.mp + row);
     };
@@ -654,9 +656,9 @@ __global__ void __launch_bounds__(256) planes_kernel(const TX* __restrict__ x, i
 
 int64_t k_padded(int64_t K) { return (K + 127) / 128 * 128; }
 
-template <typename TO, typename H, bool GRAD, int TX, int TW, int NC, int DW>
-cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
-  auto k = linear_tc_kernel<TO, H, GRAD, TX, TW, NC, DW>;
+template <typename TO, typename H, bool GRAD, int TX, int TW, int NC, int DW, int KU>
+cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
+  auto k = linear_tc_kernel<TO, H, GRAD, TX, TW, NC, DW, KU>;
   const int64_t K = GRAD ? a.w.m : a.w.n, M = GRAD ? a.w.n : a.w.m;
   TcArgs t = {};
   t.w = a.w;
@@ -666,8 +668,6 @@ cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
   t.tiles_m = (int)((M + 127) / 128);
   t.chunks = (int)((K + 127) / 128);
   t.N = N;
-  t.ku16 = 8;
-  if (!GRAD && a.w.ng > 1 && a.w.g % 128 != 0) t.ku16 = a.w.g % 64 == 0 ? 4 : 2;
   const uint32_t stage = TW * kABytes + TX * (uint32_t)N * 128u;
   t.stages = (int)std::min<uint32_t>(kMaxStages, kRing / stage);
   t.status = async_status_word();
@@ -709,6 +709,17 @@ cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
   cfg.numAttrs = 1;
   count_launch();
   return cudaLaunchKernelEx(&cfg, k, map, t);
+}
+
+// A unit ends where a group does: 128, 64 or 32 columns.
+template <typename TO, typename H, bool GRAD, int TX, int TW, int NC, int DW>
+cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
+  if constexpr (!GRAD) {
+    if (a.w.ng > 1 && a.w.g % 128 != 0)
+      return a.w.g % 64 == 0 ? run_unit<TO, H, GRAD, TX, TW, NC, DW, 4>(a, N, s)
+                             : run_unit<TO, H, GRAD, TX, TW, NC, DW, 2>(a, N, s);
+  }
+  return run_unit<TO, H, GRAD, TX, TW, NC, DW, 8>(a, N, s);
 }
 
 int tokens_per_tile(int64_t T, int most) {
