@@ -402,7 +402,8 @@ typedef struct {
  *     word 4 t + s (32 bits; s, t = 0..3) of a row holds columns 32 s + 8 t
  *     .. + 7, the even ones (0, 2, 4, 6) in bits 0..15 and the odd ones in
  *     bits 16..31; a nibble is c - qmin;
- *   scales, count groups mp floats, group by group (0 on the padding rows);
+ *   scales, count mp groups floats: per 16 rows, group by group, 16 floats each
+ *     (0 on the padding rows);
  *   with zero points: count groups mp bytes z - qmin, likewise; the region
  *     ends on a multiple of 16 bytes. */
 bakron_status bakron_pack_size(int64_t count, int64_t m, int64_t n, int64_t group, int has_zero,

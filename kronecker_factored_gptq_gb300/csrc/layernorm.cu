@@ -418,7 +418,7 @@ extern "C" bakron_status bakron_layernorm(const void* X, int64_t T, int64_t d, i
   const cudaError_t e = dtype == BAKRON_F32    ? run_fwd<float, 4>(q, a, s)
                         : dtype == BAKRON_BF16 ? run_fwd<__nv_bfloat16, 8>(q, a, s)
                                                : run_fwd<__half, 8>(q, a, s);
-  return e == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
+  return launch_status(e);
 }
 
 extern "C" bakron_status bakron_layernorm_grad_workspace_size(int64_t T, int64_t d, size_t* bytes) {
@@ -462,7 +462,7 @@ extern "C" bakron_status bakron_layernorm_grad(const void* dY, const void* X, in
   const cudaError_t e = dtype == BAKRON_F32    ? run_grad<float, 4>(q, a, s)
                         : dtype == BAKRON_BF16 ? run_grad<__nv_bfloat16, 8>(q, a, s)
                                                : run_grad<__half, 8>(q, a, s);
-  if (e != cudaSuccess) return BAKRON_ERR_CUDA;
+  if (e != cudaSuccess) return launch_status(e);
   if (dgamma) {
     count_launch();
     norm_join_kernel<<<(unsigned)((2 * d + 31) / 32), 512, 0, s>>>(a.part, grad_rows(q, T), d, dgamma,

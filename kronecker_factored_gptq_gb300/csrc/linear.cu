@@ -33,9 +33,9 @@ bakron_status run_linear(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, vo
   a.ws = ws;
   cudaStream_t s = (cudaStream_t)stream;
   if (!grad && a.T <= kFewTokens)
-    return launch_linear_few(a, s) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
+    return launch_status(launch_linear_few(a, s));
   if (!prop_tc_supported()) return BAKRON_ERR_UNSUPPORTED;
-  return launch_linear_tc(a, grad, s) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
+  return launch_status(launch_linear_tc(a, grad, s));
 }
 
 }  // namespace

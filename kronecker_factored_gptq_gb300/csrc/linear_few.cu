@@ -5,9 +5,11 @@
 // (m n / 2; at 8192 x 8192 33.6 MB, 5.0 us at 6.68 TB/s); the products run on
 // warp-level matrix instructions (qmma.cuh), which cost a fraction of that.
 //
-// A block takes 16 RB rows; its 8 warps take the 128-column chunks of the
-// rows in turn, so that one block's loads in flight cover a long run of each
-// row, and add their partial sums in shared memory in a fixed order.  Few
+// A block takes 16 rows; its 8 warps take the 128-column chunks of the rows in
+// turn, each with several chunks on their way, and add their partial sums in
+// shared memory in a fixed order.  An activation meets one warp of a block only,
+// so 16-bit activations are read where they are; fp32 ones (which become three
+// terms) and rows that are not 16-byte aligned are staged in shared memory.  Few
 // rows leave SMs without a block: then the columns are also split over the
 // blocks of a cluster, which are joined through distributed shared memory by
 // the first of them, again in a fixed order.
@@ -26,109 +28,128 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr uint32_t kMaxXBytes = 96 * 1024;   // activations staged at a time
+constexpr uint32_t kMaxXBytes = 64 * 1024;   // activations staged at a time
 
 struct FewArgs {
   PackedView w;
   const void* x;
   void* y;
   int64_t T;
-  int slab;      // chunks of activations staged at a time
+  int slab;      // chunks of activations staged at a time; 0: read in place
   int vec_ok;    // rows of x are 16-byte aligned
 };
 
-template <typename TX, typename H, int TERMS, int NT, int RB, int NS>
+// Chunks in flight per warp.
+template <int NS>
+constexpr int kDepth = 6;
+
+template <typename TX, typename H, int TERMS, int NT, int NS>
 __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_constant__ FewArgs a) {
-  extern __shared__ __align__(16) uint8_t xs[];
-  __shared__ float red[kWarps][NT * 8][16 * RB];
-  __shared__ float part[NT * 8 * 16 * RB];
+  using P = qm::Pipe<1, NS, kDepth<NS>>;
+  extern __shared__ __align__(16) uint8_t dsm[];      // the warps' chunks, then staged activations
+  __shared__ float red[kWarps][NT * 8][16];
+  __shared__ float part[NT * 8 * 16];
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0 = (int64_t)(blockIdx.x / S) * (16 * RB);
+  const int64_t row0[1] = {(int64_t)(blockIdx.x / S) * 16};
   const int64_t t0 = (int64_t)blockIdx.y * (8 * NT);
   const int cols = (int)min((int64_t)(8 * NT), a.T - t0);
   const TX* x = static_cast<const TX*>(a.x) + t0 * a.w.n;
   const int64_t c_lo = a.w.nc * rank / S, c_hi = a.w.nc * (rank + 1) / S;
 
-  qm::TileRef tile[RB];
+  qm::TileRef<1> tile;
+  qm::tile_ref<1>(tile, a.w, 0, row0, lane);
+  P pipe;
+  pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
+  int64_t ahead = c_lo + warp;
 #pragma unroll
-  for (int b = 0; b < RB; ++b) tile[b] = qm::tile_ref(a.w, 0, row0 + 16 * b, lane);
+  for (int p = 0; p < kDepth<NS> - 1; ++p, ahead += kWarps) pipe.issue(a.w, tile, ahead, ahead < c_hi, lane);
+
   int col[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) col[j] = min(8 * j + (lane >> 2), cols - 1);
-  float tot[RB][NT][4];
+  float tot[1][NT][4];
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tot[b][j][i] = 0.f;
+    for (int i = 0; i < 4; ++i) tot[0][j][i] = 0.f;
 
-  const uint32_t pitch = qm::x_pitch(a.slab);
-  const uint32_t plane = pitch * (uint32_t)cols;
-  qm::Chunk16<NS> f[RB];
-  for (int64_t s0 = c_lo; s0 < c_hi; s0 += a.slab) {
-    const int64_t s1 = min(s0 + a.slab, c_hi);
-    int64_t c = s0 + warp;
-    // the first codes are on their way while the activations are staged
-    if (c < s1) {
+  uint32_t z[1][2][NS];
+  if (c_lo + warp < c_hi) qm::load_zeros<1, NS>(z, a.w, tile, c_lo + warp);
+  qm::Chunk16<NS> f[1];
+  // the chunk c of this warp: next copies on their way, then its products
+  auto step = [&](int64_t c, auto fetch) {
+    pipe.issue(a.w, tile, ahead, ahead < c_hi, lane);
+    ahead += kWarps;
+    pipe.take(f, lane);
+    qm::set_zeros<1, NS>(f, z);
+    if (c + kWarps < c_hi) qm::load_zeros<1, NS>(z, a.w, tile, c + kWarps);
+    qm::chunk_product<H, TERMS, 1, NT, NS>(tot, f, a.w.zero != nullptr, a.w.zu, NT, fetch);
+  };
+  if (TERMS == 1 && a.slab == 0) {
+    const TX* xr[NT];
 #pragma unroll
-      for (int b = 0; b < RB; ++b) qm::load_chunk<NS>(f[b], a.w, tile[b], c);
+    for (int j = 0; j < NT; ++j) xr[j] = x + (int64_t)col[j] * a.w.n;
+    for (int64_t c = c_lo + warp; c < c_hi; c += kWarps) {
+      const int64_t k0 = c * 128 + 8 * (lane & 3);
+      step(c, [&](int j, int, int s) {
+        const int64_t k = k0 + 32 * s;
+        return k < a.w.n ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k)) : make_uint4(0, 0, 0, 0);
+      });
     }
-    if (s0 != c_lo) __syncthreads();
-    qm::stage_x<TX, TERMS>(xs, plane, pitch, x, a.w.n, cols, [](int r) { return (int64_t)r; },
-                           s0 * 128, (int)(s1 - s0), a.w.n, a.vec_ok != 0);
-    __syncthreads();
-    for (; c < s1; c += kWarps) {
-      qm::Chunk16<NS> g[RB];
-      const bool more = c + kWarps < s1;
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        g[b] = f[b];
-        if (more) qm::load_chunk<NS>(f[b], a.w, tile[b], c + kWarps);
+  } else {
+    uint8_t* xs = dsm + kWarps * P::kBytes;
+    const uint32_t pitch = qm::x_pitch(a.slab);
+    const uint32_t plane = pitch * (uint32_t)cols;
+    int64_t c = c_lo + warp;
+    for (int64_t s0 = c_lo; s0 < c_hi; s0 += a.slab) {
+      const int64_t s1 = min(s0 + a.slab, c_hi);
+      if (s0 != c_lo) __syncthreads();
+      qm::stage_x<TX, TERMS>(xs, plane, pitch, x, a.w.n, cols, [](int r) { return (int64_t)r; }, s0 * 128,
+                             (int)(s1 - s0), a.w.n, a.vec_ok != 0);
+      __syncthreads();
+      for (; c < s1; c += kWarps) {
+        const uint8_t* xc = xs + (c - s0) * 256 + (lane & 3) * 16;
+        step(c, [&](int j, int q, int s) {
+          return *reinterpret_cast<const uint4*>(xc + q * plane + (uint32_t)col[j] * pitch + s * 64);
+        });
       }
-      const uint8_t* xc = xs + (c - s0) * 256 + (lane & 3) * 16;
-      qm::chunk_product<H, TERMS, RB, NT, NS>(
-          tot, g, a.w.zero != nullptr, a.w.zu, NT, [&](int j, int q, int s) {
-            return *reinterpret_cast<const uint4*>(xc + q * plane + (uint32_t)col[j] * pitch + s * 64);
-          });
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 
   // partial sums of the warps: [column][row], rows fastest
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int r = 16 * b + (lane >> 2), c = 8 * j + 2 * (lane & 3);
-      red[warp][c][r] = tot[b][j][0];
-      red[warp][c + 1][r] = tot[b][j][1];
-      red[warp][c][r + 8] = tot[b][j][2];
-      red[warp][c + 1][r + 8] = tot[b][j][3];
-    }
+  for (int j = 0; j < NT; ++j) {
+    const int r = lane >> 2, c = 8 * j + 2 * (lane & 3);
+    red[warp][c][r] = tot[0][j][0];
+    red[warp][c + 1][r] = tot[0][j][1];
+    red[warp][c][r + 8] = tot[0][j][2];
+    red[warp][c + 1][r + 8] = tot[0][j][3];
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < NT * 8 * 16 * RB; i += kThreads) {
-    const int c = i / (16 * RB), r = i - c * (16 * RB);
+  for (int i = threadIdx.x; i < NT * 8 * 16; i += kThreads) {
+    const int c = i >> 4, r = i & 15;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += red[w][c][r];
     if (S > 1) {
       part[i] = v;
-    } else if (c < cols && row0 + r < a.w.m) {
-      static_cast<TX*>(a.y)[(t0 + c) * a.w.m + row0 + r] = from_float<TX>(v);
+    } else if (c < cols && row0[0] + r < a.w.m) {
+      static_cast<TX*>(a.y)[(t0 + c) * a.w.m + row0[0] + r] = from_float<TX>(v);
     }
   }
   if (S > 1) {
     __syncwarp();
     cluster.sync();
     if (rank == 0) {
-      for (int i = threadIdx.x; i < NT * 8 * 16 * RB; i += kThreads) {
-        const int c = i / (16 * RB), r = i - c * (16 * RB);
-        if (c >= cols || row0 + r >= a.w.m) continue;
+      for (int i = threadIdx.x; i < NT * 8 * 16; i += kThreads) {
+        const int c = i >> 4, r = i & 15;
+        if (c >= cols || row0[0] + r >= a.w.m) continue;
         float v = 0.f;
         for (int k = 0; k < S; ++k) v += cluster.map_shared_rank(part, k)[i];
-        static_cast<TX*>(a.y)[(t0 + c) * a.w.m + row0 + r] = from_float<TX>(v);
+        static_cast<TX*>(a.y)[(t0 + c) * a.w.m + row0[0] + r] = from_float<TX>(v);
       }
     }
     __syncwarp();
@@ -136,57 +157,52 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
   }
 }
 
-template <typename TX, typename H, int TERMS, int NT, int RB, int NS>
+template <typename TX, typename H, int TERMS, int NT, int NS>
 cudaError_t run(const LinearArgs& a, cudaStream_t s) {
-  auto k = linear_few_kernel<TX, H, TERMS, NT, RB, NS>;
+  auto k = linear_few_kernel<TX, H, TERMS, NT, NS>;
+  constexpr size_t ring = kWarps * qm::Pipe<1, NS, kDepth<NS>>::kBytes;
   FewArgs f;
   f.w = a.w;
   f.x = a.x;
   f.y = a.y;
   f.T = a.T;
   f.vec_ok = aligned_to(a.x, 16) && (a.w.n * sizeof(TX)) % 16 == 0;
-  const int64_t tiles = (a.w.mp + 16 * RB - 1) / (16 * RB);
-  const int64_t tt = (a.T + 8 * NT - 1) / (8 * NT);
-  // blocks per row tile: enough that every SM has a few, at least one chunk a warp
+  const int64_t tiles = a.w.mp / 16;
+  const int64_t tt = (a.T + 8 * NT - 1) / (8 * NT);   // T <= kFewTokens: a handful
+  // blocks per row tile: enough that every SM has a few, at least two chunks a warp
   int S = 1;
   while (S < 8 && tiles * tt * S < 2 * sm_count() && a.w.nc >= (int64_t)2 * S * kWarps) S *= 2;
-  const int cols = (int)std::min<int64_t>(8 * NT, a.T);
-  const int64_t most = (a.w.nc + S - 1) / S;
-  int64_t slab = (kMaxXBytes / (uint32_t)(TERMS * cols) - 64) / 256;
-  f.slab = (int)std::max<int64_t>(1, std::min<int64_t>(slab, most));
-  const size_t smem = (size_t)qm::x_pitch(f.slab) * TERMS * cols;
-  static std::atomic<unsigned long long> done;
-  cudaError_t e = ensure_smem_limit((const void*)k, kMaxXBytes, done);
-  if (e != cudaSuccess) return e;
-  for (int64_t y0 = 0; y0 < tt; y0 += 65535) {   // grid.y limit
-    FewArgs g = f;
-    g.x = static_cast<const TX*>(a.x) + y0 * 8 * NT * a.w.n;
-    g.y = static_cast<TX*>(a.y) + y0 * 8 * NT * a.w.m;
-    g.T = a.T - y0 * 8 * NT;
-    g.vec_ok = aligned_to(g.x, 16) && (a.w.n * sizeof(TX)) % 16 == 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * S), (unsigned)std::min<int64_t>(65535, tt - y0), 1);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)S;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    count_launch();
-    e = cudaLaunchKernelEx(&cfg, k, g);
-    if (e != cudaSuccess) return e;
+  size_t smem = ring;
+  f.slab = 0;
+  if (TERMS != 1 || !f.vec_ok) {
+    const int cols = (int)std::min<int64_t>(8 * NT, a.T);
+    const int64_t slab = (kMaxXBytes / (uint32_t)(TERMS * cols) - 64) / 256;
+    f.slab = (int)std::max<int64_t>(1, std::min<int64_t>(slab, (a.w.nc + S - 1) / S));
+    smem += (size_t)qm::x_pitch(f.slab) * TERMS * cols;
   }
-  return cudaSuccess;
+  static std::atomic<unsigned long long> done;
+  cudaError_t e = ensure_smem_limit((const void*)k, ring + kMaxXBytes, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * S), (unsigned)tt, 1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, k, f);
 }
 
 template <typename TX, typename H, int TERMS>
 cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
   const bool wide = a.w.ng == 1 || a.w.g % 128 == 0;
-  if (a.T <= 8) return wide ? run<TX, H, TERMS, 1, 1, 1>(a, s) : run<TX, H, TERMS, 1, 1, 4>(a, s);
-  return wide ? run<TX, H, TERMS, 2, 1, 1>(a, s) : run<TX, H, TERMS, 2, 1, 4>(a, s);
+  if (a.T <= 8) return wide ? run<TX, H, TERMS, 1, 1>(a, s) : run<TX, H, TERMS, 1, 4>(a, s);
+  return wide ? run<TX, H, TERMS, 2, 1>(a, s) : run<TX, H, TERMS, 2, 4>(a, s);
 }
 
 }  // namespace

@@ -222,16 +222,15 @@ __device__ __forceinline__ void weights_forward(const TcArgs& a, const Ctx& x, i
       if (live) {
         qq[b] = ld_codes(src + b * stride + (int64_t)c * kBlockBytes);
         if (w.zero) {
-          const uint8_t* zp = w.zero + (block0 + b) * 8 + r;
+          const uint8_t* zp = w.zero + grid_row(w, 0, (block0 + b) * 8 + r);
           const uint32_t k0 = (uint32_t)((x.c0 + c) * 128);
           if (!narrow) {
-            const uint32_t v = ld_ahead(zp + (w.ng > 1 ? (int64_t)min(k0 / (uint32_t)w.g, (uint32_t)w.ng - 1) * w.mp : 0));
+            const uint32_t v = ld_ahead(zp + grid_group(w, k0) * 16);
             zz[b] = v * 0x01010101u;
           } else {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-              const int64_t g = min((k0 + 32 * s) / (uint32_t)w.g, (uint32_t)w.ng - 1);
-              zz[b] |= ld_ahead(zp + g * w.mp) << (8 * s);
+              zz[b] |= ld_ahead(zp + grid_group(w, k0 + 32 * s) * 16) << (8 * s);
             }
           }
         }
@@ -313,8 +312,7 @@ __device__ __forceinline__ void weights_gradient(const TcArgs& a, const Ctx& x, 
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s == 0 || narrow) {
-        const int64_t g = w.ng > 1 ? (int64_t)min((j0 + 32 * s) / (uint32_t)w.g, (uint32_t)w.ng - 1) : 0;
-        const int64_t at = g * w.mp + b * 8;
+        const int64_t at = live ? grid_row(w, 0, b * 8) + grid_group(w, j0 + 32 * s) * 16 : 0;
         float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
         if (live) {
           s0 = __ldg(reinterpret_cast<const float4*>(w.scale + at));
@@ -542,11 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < NC; ++t) acc[t] = 0.f;
     const int64_t row = (int64_t)x.tile_m * 128 + quarter * 32 + lane;
     const bool live = !GRAD && row < a.w.mp;
+    const float* scale_row = a.w.scale + (live ? grid_row(a.w, 0, row) : 0);
     auto scale_of = [&](int u) {
       if (!live || u >= units) return 0.f;
       const uint32_t k = (uint32_t)(x.c0 * 128) + (uint32_t)u * (KU * 16);
-      const int64_t g = a.w.ng > 1 ? (int64_t)min(k / (uint32_t)a.w.g, (uint32_t)a.w.ng - 1) : 0;
-      return ld_ahead(a.w.scale + g * a.w.mp + row);
+      return ld_ahead(scale_row + grid_group(a.w, k) * 16);
     };
     float s_next = scale_of(0);
     for (int u = 0; u < units; ++u) {

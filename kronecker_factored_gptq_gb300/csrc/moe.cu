@@ -41,6 +41,8 @@ constexpr int kCluster = 8;
 constexpr int kMaxTokens = BAKRON_MOE_TOKENS;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 1024;
+constexpr int kDepthIn = 4;      // chunks in flight per warp
+constexpr int kDepthOut = 6;
 
 struct MoeArgs {
   const void* x;        // T x d
@@ -183,12 +185,19 @@ __device__ void select_experts(const float* l, int E, int k, bool renormalize, i
   if (lane < k) weight[lane] = bad ? NAN : expf(mine - top) / sum;
 }
 
-// Shared memory of the routing, after the logits.
+// Index of the c-th set bit (from 0).
+__device__ __forceinline__ int nth_bit(uint32_t m, int c) {
+  for (int i = 0; i < c; ++i) m &= m - 1;
+  return __ffs((int)m) - 1;
+}
+
+// Shared memory of the routing.
 struct Routing {
   int choice[kMaxTokens][kMaxTopK];
   float weight[kMaxTokens][kMaxTopK];
   int na;
   int active[kMaxTokens * kMaxTopK];
+  uint32_t who[kMaxTokens * kMaxTopK];                    // bit t: token t chose the expert
   float parts[kWarps * kMaxTokens];
 };
 
@@ -196,8 +205,10 @@ template <typename TX, typename H, int TERMS, int HT, int NT, int NS>
 __global__ void __launch_bounds__(kThreads, 2) moe_in_kernel(const __grid_constant__ MoeArgs a) {
   extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ Routing R;
-  __shared__ float red[kWarps][NT * 8][33];
-  float* logits = reinterpret_cast<float*>(dsm);          // [T][E]
+  using P = qm::Pipe<2, NS, kDepthIn>;
+  // the routing's arrays end before the chunks' slots and the joins begin
+  float* red = reinterpret_cast<float*>(dsm + kWarps * P::kBytes);
+  float* logits = reinterpret_cast<float*>(dsm);               // [T][E]
   int* slot_of = reinterpret_cast<int*>(logits + a.T * a.E);   // [E]: index among the chosen, or -1
   cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -217,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_in_kernel(const __grid_consta
       if (in) {
         const int at = n + __popc(m & ((1u << lane) - 1));
         R.active[at] = e0 + lane;
+        slot_of[e0 + lane] = at;
       }
       n += __popc(m);
     }
@@ -224,6 +236,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_in_kernel(const __grid_consta
   }
   __syncthreads();
   const int na = R.na;
+  for (int i = threadIdx.x; i < na; i += kThreads) R.who[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.T * a.k; i += kThreads)
+    atomicOr(&R.who[slot_of[R.choice[i / a.k][i % a.k]]], 1u << (i / a.k));
+  __syncthreads();
   if (blockIdx.x == 0) {
     // for the second launch: the chosen experts, and who chose them
     if (threadIdx.x == 0) a.active[0] = na;
@@ -247,30 +264,58 @@ __global__ void __launch_bounds__(kThreads, 2) moe_in_kernel(const __grid_consta
     }
   }
 
+  // Items: (chosen expert, row tile), a gate tile and its up tile each, for
+  // groups of G warps that split the columns: as many groups as the items can
+  // feed.  A warp runs through its (item, chunk) pairs as one sequence, so the
+  // copies of the next item start while this one ends.
   const int tiles = (int)((a.f + 15) / 16);
   const int64_t items = (int64_t)na * tiles;
   const int nc = (int)a.wi.nc;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+  int G = 1;
+  while (G < kWarps && items * 2 * G <= (int64_t)gridDim.x * kWarps && nc >= 2 * G) G *= 2;
+  const int group = warp / G, part = warp % G;
+  const int64_t groups = (int64_t)gridDim.x * (kWarps / G);
+  const int64_t first = (int64_t)blockIdx.x + (int64_t)gridDim.x * group;
+  const int c_lo = nc * part / G, c_hi = nc * (part + 1) / G;
+
+  P pipe;
+  pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
+  auto open_item = [&](qm::TileRef<2>& t, int64_t it) {
+    const int ai = (int)(it / tiles);
+    const int64_t r0 = (it - (int64_t)ai * tiles) * 16;
+    const int64_t rows[2] = {r0, a.f + r0};
+    qm::tile_ref<2>(t, a.wi, R.active[ai], rows, lane);
+  };
+  qm::TileRef<2> t_ahead, t_now;
+  int64_t it_ahead = first;
+  int c_ahead = c_lo;
+  if (it_ahead < items) open_item(t_ahead, it_ahead);
+  auto issue = [&]() {
+    pipe.issue(a.wi, t_ahead, c_ahead, it_ahead < items, lane);
+    if (it_ahead < items && ++c_ahead == c_hi) {
+      c_ahead = c_lo;
+      it_ahead += groups;
+      if (it_ahead < items) open_item(t_ahead, it_ahead);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < kDepthIn - 1; ++p) issue();
+
+  for (int64_t it = first; it < items; it += groups) {
     const int ai = (int)(it / tiles);
     const int64_t row0 = (it - (int64_t)ai * tiles) * 16;
     const int e = R.active[ai];
-    // the expert's tokens, by ballot: thread's column 8 j + lane / 4
-    uint32_t who = 0;
-    int my_slot = -1;
-    if (lane < a.T)
-      for (int s = 0; s < a.k; ++s)
-        if (R.choice[lane][s] == e) my_slot = s;
-    who = __ballot_sync(0xffffffffu, my_slot >= 0);
+    if (a.wi.zero) open_item(t_now, it);
+    // the expert's tokens: thread's column 8 j + lane / 4
+    const uint32_t who = R.who[ai];
     const int cnt = __popc(who);
     const int live = (cnt + 7) / 8;
     const uint8_t* xr[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int c = 8 * j + (lane >> 2);
-      xr[j] = nullptr;
-      if (c < cnt) xr[j] = a.xp + (int64_t)__fns(who, 0, c + 1) * a.xp_pitch + (lane & 3) * 16;
+      xr[j] = c < cnt ? a.xp + (int64_t)nth_bit(who, c) * a.xp_pitch + (lane & 3) * 16 : nullptr;
     }
-    const qm::TileRef tile[2] = {qm::tile_ref(a.wi, e, row0, lane), qm::tile_ref(a.wi, e, a.f + row0, lane)};
     float tot[2][NT][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -278,73 +323,74 @@ __global__ void __launch_bounds__(kThreads, 2) moe_in_kernel(const __grid_consta
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tot[r][j][i] = 0.f;
-    qm::Chunk16<NS> f[2];
-    if (warp < nc) {
-      qm::load_chunk<NS>(f[0], a.wi, tile[0], warp);
-      qm::load_chunk<NS>(f[1], a.wi, tile[1], warp);
-    }
-    for (int c = warp; c < nc; c += kWarps) {
-      const qm::Chunk16<NS> g[2] = {f[0], f[1]};
-      if (c + kWarps < nc) {
-        qm::load_chunk<NS>(f[0], a.wi, tile[0], c + kWarps);
-        qm::load_chunk<NS>(f[1], a.wi, tile[1], c + kWarps);
-      }
+    uint32_t z[2][2][NS];
+    qm::load_zeros<2, NS>(z, a.wi, t_now, c_lo);
+    for (int c = c_lo; c < c_hi; ++c) {
+      qm::Chunk16<NS> f[2];
+      issue();
+      pipe.take(f, lane);
+      qm::set_zeros<2, NS>(f, z);
+      if (c + 1 < c_hi) qm::load_zeros<2, NS>(z, a.wi, t_now, c + 1);
       const int64_t k0 = (int64_t)c * 128 + 8 * (lane & 3);
       qm::chunk_product<H, TERMS, 2, NT, NS>(
-          tot, g, a.wi.zero != nullptr, a.wi.zu, live, [&](int j, int q, int s) {
+          tot, f, a.wi.zero != nullptr, a.wi.zu, live, [&](int j, int q, int s) {
             if (xr[j] == nullptr || k0 + 32 * s >= a.xp_cols) return make_uint4(0, 0, 0, 0);
             return __ldg(reinterpret_cast<const uint4*>(xr[j] + q * a.xp_plane + (int64_t)c * 256 + s * 64));
           });
     }
-    // gate and up in turn through the same array
-    float gate[NT], up[NT];       // of outputs threadIdx.x + 256 j: row i & 15, column i / 16
+    // the group's sums of gate and up (thread: rows lane / 4 and + 8, columns
+    // 2 (lane & 3) and + 1 of each column tile)
+    if (G > 1) {
+      float* mine = red + (size_t)warp * (2 * NT * 4 * 32) + lane;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      __syncthreads();
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int rr = lane >> 2, cc = 8 * j + 2 * (lane & 3);
-        red[warp][cc][rr] = tot[r][j][0];
-        red[warp][cc + 1][rr] = tot[r][j][1];
-        red[warp][cc][rr + 8] = tot[r][j][2];
-        red[warp][cc + 1][rr + 8] = tot[r][j][3];
-      }
-      __syncthreads();
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < (NT + 1) / 2; ++j) {
-        const int i = threadIdx.x + kThreads * j;
-        if (i < NT * 8 * 16) {
-          float v = 0.f;
+          for (int i = 0; i < 4; ++i) mine[((r * NT + j) * 4 + i) * 32] = tot[r][j][i];
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * G) : "memory");
+      if (part == 0) {
+        for (int w = 1; w < G; ++w) {
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) v += red[w][i >> 4][i & 15];
-          (r == 0 ? gate : up)[j] = v;
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tot[r][j][i] += mine[(size_t)w * (2 * NT * 4 * 32) + ((r * NT + j) * 4 + i) * 32];
         }
       }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * G) : "memory");
     }
+    if (part == 0) {
 #pragma unroll
-    for (int j = 0; j < (NT + 1) / 2; ++j) {
-      const int i = threadIdx.x + kThreads * j;
-      const int c = i >> 4;
-      const int64_t row = row0 + (i & 15);
-      if (i < NT * 8 * 16 && c < cnt && row < a.f) {
-        const int t = (int)__fns(who, 0, c + 1);
-        int s = 0;
-        for (int q = 0; q < a.k; ++q)
-          if (R.choice[t][q] == e) s = q;
-        const float g = gate[j];
-        const float v = g / (1.f + expf(-g)) * up[j] * R.weight[t][s];
-        float p[3];
-        split3(v, p[0], p[1], p[2]);
-        uint8_t* o = a.h + ((int64_t)(t * a.k + s) * a.fp + row) * 2;
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int q = 0; q < HT; ++q) *reinterpret_cast<uint16_t*>(o + q * a.h_plane) = bf16_bits(p[q]);
-      }
+        for (int i = 0; i < 4; ++i) {
+          const int c = 8 * j + 2 * (lane & 3) + (i & 1);
+          const int64_t row = row0 + (lane >> 2) + 8 * (i >> 1);
+          if (c < cnt && row < a.f) {
+            const int t = nth_bit(who, c);
+            int s = 0;
+            for (int q = 0; q < a.k; ++q)
+              if (R.choice[t][q] == e) s = q;
+            const float g = tot[0][j][i];
+            const float v = g / (1.f + expf(-g)) * tot[1][j][i] * R.weight[t][s];
+            float p[3];
+            split3(v, p[0], p[1], p[2]);
+            uint8_t* o = a.h + ((int64_t)(t * a.k + s) * a.fp + row) * 2;
+#pragma unroll
+            for (int q = 0; q < HT; ++q) *reinterpret_cast<uint16_t*>(o + q * a.h_plane) = bf16_bits(p[q]);
+          }
+        }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <typename TX, int HT, int NT, int NS>
 __global__ void __launch_bounds__(kThreads, 2) moe_out_kernel(const __grid_constant__ MoeArgs a) {
+  using P = qm::Pipe<1, NS, kDepthOut>;
+  extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ float red[kWarps][NT * 8][17];
   __shared__ float part[NT * 8 * 16];
   cg::cluster_group cluster = cg::this_cluster();
@@ -362,26 +408,35 @@ __global__ void __launch_bounds__(kThreads, 2) moe_out_kernel(const __grid_const
     for (int i = 0; i < 4; ++i) tot[0][j][i] = 0.f;
   const int live = (a.T + 7) / 8;
 
-  int cur = -1;
-  qm::TileRef tile;
-  qm::Chunk16<NS> f[1];
-  auto load = [&](int64_t u) {
-    const int ai = (int)(u / nc);
-    if (ai != cur) {
-      cur = ai;
-      tile = qm::tile_ref(a.wo, a.active[1 + ai], row0, lane);
+  // this warp's run of the list
+  const int64_t v0 = u0 + (u1 - u0) * warp / kWarps, v1 = u0 + (u1 - u0) * (warp + 1) / kWarps;
+  P pipe;
+  pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
+  qm::TileRef<1> t_ahead, t_now;
+  int ai_ahead = (int)(v0 / nc), c_ahead = (int)(v0 - (int64_t)ai_ahead * nc);
+  int64_t v_ahead = v0;
+  const int64_t rows[1] = {row0};
+  if (v0 < v1) qm::tile_ref<1>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
+  auto issue = [&]() {
+    pipe.issue(a.wo, t_ahead, c_ahead, v_ahead < v1, lane);
+    if (v_ahead < v1) {
+      ++v_ahead;
+      if (++c_ahead == nc && v_ahead < v1) {
+        c_ahead = 0;
+        ++ai_ahead;
+        qm::tile_ref<1>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
+      }
     }
-    qm::load_chunk<NS>(f[0], a.wo, tile, u - (int64_t)ai * nc);
   };
+#pragma unroll
+  for (int p = 0; p < kDepthOut - 1; ++p) issue();
+  int ai = (int)(v0 / nc), c = (int)(v0 - (int64_t)ai * nc);
   int have = -1;
   const uint8_t* hr[NT];
-  if (u0 + warp < u1) load(u0 + warp);
-  for (int64_t u = u0 + warp; u < u1; u += kWarps) {
-    const qm::Chunk16<NS> g[1] = {f[0]};
-    if (u + kWarps < u1) load(u + kWarps);
-    const int ai = (int)(u / nc), c = (int)(u - (int64_t)ai * nc);
+  for (int64_t v = v0; v < v1; ++v) {
     if (ai != have) {
       have = ai;
+      if (a.wo.zero) qm::tile_ref<1>(t_now, a.wo, a.active[1 + ai], rows, lane);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int t = 8 * j + (lane >> 2);
@@ -389,12 +444,23 @@ __global__ void __launch_bounds__(kThreads, 2) moe_out_kernel(const __grid_const
         hr[j] = p < 0 ? nullptr : a.h + (int64_t)p * a.fp * 2 + (lane & 3) * 16;
       }
     }
+    uint32_t z[1][2][NS];
+    qm::load_zeros<1, NS>(z, a.wo, t_now, c);
+    issue();
+    qm::Chunk16<NS> f[1];
+    pipe.take(f, lane);
+    qm::set_zeros<1, NS>(f, z);
     qm::chunk_product<__nv_bfloat16, HT, 1, NT, NS>(
-        tot, g, a.wo.zero != nullptr, a.wo.zu, live, [&](int j, int q, int s) {
+        tot, f, a.wo.zero != nullptr, a.wo.zu, live, [&](int j, int q, int s) {
           if (hr[j] == nullptr) return make_uint4(0, 0, 0, 0);
-          return *reinterpret_cast<const uint4*>(hr[j] + q * a.h_plane + (int64_t)c * 256 + s * 64);
+          return __ldg(reinterpret_cast<const uint4*>(hr[j] + q * a.h_plane + (int64_t)c * 256 + s * 64));
         });
+    if (++c == nc) {
+      c = 0;
+      ++ai;
+    }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int rr = lane >> 2, cc = 8 * j + 2 * (lane & 3);
@@ -447,16 +513,18 @@ cudaError_t launch_cluster(const void* k, unsigned grid, unsigned cluster, size_
   return cudaLaunchKernelExC(&cfg, k, args);
 }
 
-constexpr size_t kMaxDynamic = (size_t)kMaxTokens * kMaxExperts * 4 + kMaxExperts * 4;
-
 template <typename TX, typename H, int TERMS, int HT, int NT, int NS, int NSO>
 cudaError_t run(MoeArgs& a, cudaStream_t s) {
   const void* k1 = (const void*)moe_in_kernel<TX, H, TERMS, HT, NT, NS>;
   const void* k2 = (const void*)moe_out_kernel<TX, HT, NT, NSO>;
-  static std::atomic<unsigned long long> done;
-  cudaError_t e = ensure_smem_limit(k1, kMaxDynamic, done);
+  constexpr size_t in_fixed = kWarps * (size_t)qm::Pipe<2, NS, kDepthIn>::kBytes + kWarps * 2 * NT * 4 * 32 * 4;
+  constexpr size_t in_most = std::max(in_fixed, (size_t)(8 * NT + 1) * kMaxExperts * 4);
+  constexpr size_t out_bytes = kWarps * (size_t)qm::Pipe<1, NSO, kDepthOut>::kBytes;
+  static std::atomic<unsigned long long> done, done2;
+  cudaError_t e = ensure_smem_limit(k1, in_most, done);
+  if (e == cudaSuccess) e = ensure_smem_limit(k2, out_bytes, done2);
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)a.T * a.E * 4 + (size_t)a.E * 4;
+  const size_t smem = std::max(in_fixed, (size_t)(a.T + 1) * a.E * 4);
   const int64_t most = (int64_t)std::min(a.E, a.T * a.k) * ((a.f + 15) / 16);
   // two blocks per SM, not more than there can be items
   int64_t clusters = std::min<int64_t>(2 * sm_count() / kCluster, (most + kCluster - 1) / kCluster);
@@ -466,7 +534,7 @@ cudaError_t run(MoeArgs& a, cudaStream_t s) {
   const int64_t units = (int64_t)std::min(a.E, a.T * a.k) * a.wo.nc;
   int S = 1;
   while (S < 8 && tiles * S < 2 * sm_count() && units >= (int64_t)2 * S * kWarps) S *= 2;
-  return launch_cluster(k2, (unsigned)(tiles * S), (unsigned)S, 0, a, s);
+  return launch_cluster(k2, (unsigned)(tiles * S), (unsigned)S, out_bytes, a, s);
 }
 
 template <typename TX, typename H, int TERMS, int HT, int NT>
@@ -579,7 +647,7 @@ extern "C" bakron_status bakron_moe(const void* X, int64_t T, int dtype, const v
         default: e = by_tokens<__half, __half, 1, 2>(a, s); break;
       }
     }
-    if (e != cudaSuccess) return BAKRON_ERR_CUDA;
+    if (e != cudaSuccess) return launch_status(e);
   }
   return BAKRON_OK;
 }

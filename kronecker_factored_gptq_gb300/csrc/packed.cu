@@ -45,7 +45,7 @@ __global__ void pack_codes_kernel(const int8_t* __restrict__ codes, int64_t coun
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) set_status(st, BAKRON_ERR_CODE_RANGE);
 }
 
-// scale[e][i][k] -> [e][k][i], 0 on the padding rows; zero points likewise
+// scale[e][i][k] -> [e][i / 16][k][i % 16], 0 on the padding rows; zero points likewise
 // as bytes z - qmin.
 __global__ void pack_grid_kernel(const float* __restrict__ scale, const float* __restrict__ zero,
                                  int64_t count, int64_t m, int64_t mp, int64_t ng, float qmin,
@@ -55,7 +55,7 @@ __global__ void pack_grid_kernel(const float* __restrict__ scale, const float* _
   bool bad = false, badz = false;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t r = i % mp, k = (i / mp) % ng, e = i / (mp * ng);
+    const int64_t b = i / 16, k = b % ng, r = (b / ng) % (mp / 16) * 16 + i % 16, e = i / (mp * ng);
     float s = 0.f;
     uint8_t z = 0;
     if (r < m) {
@@ -89,7 +89,7 @@ __global__ void unpack_kernel(const PackedView w, float* __restrict__ V) {
     const int t = word >> 2, s = word & 3;
     const int64_t j0 = c * 128 + 32 * s + 8 * t;
     if (r >= w.m || j0 >= w.n) continue;
-    const int64_t at = (e * w.ng + j0 / w.g) * w.mp + r;
+    const int64_t at = grid_row(w, e, r) + j0 / w.g * 16;
     const float sc = w.scale[at];
     const int z = w.zero ? w.zero[at] : w.zu;
     const uint32_t v = words[i];

@@ -59,7 +59,7 @@ inline bool pack_layout(int64_t count, int64_t m, int64_t n, int64_t group, int 
 // A packed matrix as the kernels see it.
 struct PackedView {
   const uint8_t* codes;   // [count][mp / 8][nc][512]
-  const float* scale;     // [count][ng][mp]
+  const float* scale;     // [count][mp / 16][ng][16]
   const uint8_t* zero;    // likewise, or NULL: every zero point is `zu`
   int zu;                 // -qmin
   int64_t count, m, n, mp, nc, ng, g;
@@ -86,12 +86,28 @@ inline bool packed_view(const bakron_packed* w, PackedView* v) {
   return true;
 }
 
+// Offset of row r's grid entry of its first group; a group is 16 entries further.
+__host__ __device__ __forceinline__ int64_t grid_row(const PackedView& w, int64_t e, int64_t r) {
+  return ((e * (w.mp / 16) + r / 16) * w.ng) * 16 + r % 16;
+}
+// Group of column k; a padded column belongs to the last one.
+__device__ __forceinline__ uint32_t grid_group(const PackedView& w, uint32_t k) {
+  return w.ng > 1 ? min(k / (uint32_t)w.g, (uint32_t)w.ng - 1) : 0u;
+}
+
 inline bool dtype_ok(int dtype) {
   return dtype == BAKRON_F32 || dtype == BAKRON_BF16 || dtype == BAKRON_F16;
 }
 inline size_t dtype_size(int dtype) { return dtype == BAKRON_F32 ? 4 : 2; }
 inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// The status of a launch; a failed one leaves no error behind for the next call.
+inline bakron_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return BAKRON_OK;
+  (void)cudaGetLastError();
+  return BAKRON_ERR_CUDA;
 }
 
 // Device word of the current device that keeps the first error of the

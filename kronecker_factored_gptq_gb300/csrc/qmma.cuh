@@ -3,11 +3,11 @@
 // few-token linear layer and the mixture-of-experts layer.
 //
 // These products are bound by the weights' bytes: a 16 x 128 block of codes
-// is 1 KB and meets at most a few dozen tokens.  What matters is that the
-// codes go from memory to the operand registers with few instructions and
-// nothing in between: a warp's 16-byte loads are two whole blocks (8 rows x
-// 128 columns) and already hold the A fragments of 8 matrix instructions
-// (packed.cuh), so the codes never pass through shared memory.  The k slots
+// is 1 KB and meets at most a few dozen tokens.  What matters is that enough
+// of them are in flight and that few instructions stand between memory and the
+// matrix instructions: asynchronous copies bring whole blocks (8 rows x 128
+// columns) to shared memory several chunks ahead, and a thread's 16 bytes of
+// them are already the A fragments of 8 matrix instructions (packed.cuh).  The k slots
 // of an instruction are any 16 columns as long as both operands agree: slots
 // (2 t, 2 t + 1) and (2 t + 8, 2 t + 9) of thread t are four consecutive
 // columns, and the thread's eight columns of a step are one 16-byte read of
@@ -32,7 +32,7 @@ template <>
 __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1,
                                                         uint32_t a2, uint32_t a3, uint32_t b0,
                                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -42,16 +42,16 @@ template <>
 __device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uint32_t a1,
                                                  uint32_t a2, uint32_t a3, uint32_t b0,
                                                  uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// What one 128-column chunk of a 16-row tile needs from memory, per thread:
-// rows lane / 4 and lane / 4 + 8.  NS scales per row: 1 when the group is a
-// multiple of 128 columns, else one per 32 columns.
+// What one 128-column chunk of a 16-row tile needs, per thread: rows lane / 4
+// and lane / 4 + 8.  NS scales per row: 1 when the group is a multiple of 128
+// columns, else one per 32 columns.
 template <int NS>
 struct Chunk16 {
   uint4 w[2];
@@ -59,48 +59,118 @@ struct Chunk16 {
   uint32_t z[2][NS];
 };
 
-// A thread's two rows of a 16-row tile: codes (at the thread's 16 bytes of
-// the first chunk) and grid.
+// A thread's part of RT 16-row tiles: the codes of its rows (at its 16 bytes of
+// the first chunk), their zero points, and the scale of the one row it fetches
+// for the warp (row lane of the 16 RT rows).
+template <int RT>
 struct TileRef {
-  const uint8_t* codes[2];
-  const float* scale[2];    // + k mp
-  const uint8_t* zero[2];   // likewise; NULL when every zero point is the same
+  const uint8_t* codes[RT][2];
+  const uint8_t* zero[RT][2];
+  const float* scale;
 };
 
-// Rows row0 + lane / 4 and + 8 of matrix e; rows past the padding repeat its
-// last row (their products are dropped by the caller).
-__device__ __forceinline__ TileRef tile_ref(const PackedView& w, int64_t e, int64_t row0, int lane) {
-  TileRef t;
+// Tile r holds rows row0[r] .. + 15 of matrix e; rows past the padding repeat
+// its last row (their products are dropped by the caller).
+template <int RT>
+__device__ __forceinline__ void tile_ref(TileRef<RT>& t, const PackedView& w, int64_t e,
+                                         const int64_t (&row0)[RT], int lane) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r = min(row0 + (lane >> 2) + 8 * i, w.mp - 1);
-    t.codes[i] = w.codes + (e * (w.mp / 8) + r / 8) * w.nc * kBlockBytes + (r & 7) * 64 + (lane & 3) * 16;
-    t.scale[i] = w.scale + e * w.ng * w.mp + r;
-    t.zero[i] = w.zero ? w.zero + e * w.ng * w.mp + r : nullptr;
+  for (int r = 0; r < RT; ++r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = min(row0[r] + (lane >> 2) + 8 * i, w.mp - 1);
+      t.codes[r][i] = w.codes + (e * (w.mp / 8) + row / 8) * w.nc * kBlockBytes + (row & 7) * 64 + (lane & 3) * 16;
+      t.zero[r][i] = w.zero ? w.zero + grid_row(w, e, row) : nullptr;
+    }
   }
-  return t;
+  const int mine = RT == 1 ? 0 : lane >> 4;
+  t.scale = w.scale + grid_row(w, e, min(row0[mine] + (lane & 15), w.mp - 1));
 }
 
-template <int NS>
-__device__ __forceinline__ void load_chunk(Chunk16<NS>& f, const PackedView& w, const TileRef& t,
+// A warp's chunks in flight: D slots in shared memory, filled by asynchronous
+// copies D - 1 chunks ahead.  A thread copies the 16 bytes of codes that it
+// reads itself, so they need no synchronisation; only the scales, one row per
+// thread, pass between the lanes of the warp.
+template <int RT, int NS, int D>
+struct Pipe {
+  static constexpr uint32_t kSlot = RT * 2 * 512 + NS * 128;
+  static constexpr uint32_t kBytes = D * kSlot;     // per warp
+  uint32_t base;                                    // of the warp
+  int fill = 0, read = 0;
+
+  static __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  }
+  static __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+  }
+  // Start chunk c of the tiles; a call without one (live false) keeps the count.
+  __device__ __forceinline__ void issue(const PackedView& w, const TileRef<RT>& t, int64_t c, bool live, int lane) {
+    if (live) {
+      const uint32_t slot = base + (uint32_t)fill * kSlot;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          copy16(slot + (uint32_t)((r * 2 + i) * 512 + lane * 16), t.codes[r][i] + c * kBlockBytes);
+      if (lane < 16 * RT) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          copy4(slot + RT * 1024 + (uint32_t)(s * 128 + lane * 4),
+                t.scale + grid_group(w, (uint32_t)(c * 128 + 32 * s)) * 16);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++fill == D) fill = 0;
+  }
+  // The oldest chunk, once its copies have landed.
+  __device__ __forceinline__ void take(Chunk16<NS> (&f)[RT], int lane) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    __syncwarp();
+    const uint32_t slot = base + (uint32_t)read * kSlot;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint4& v = f[r].w[i];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(slot + (uint32_t)((r * 2 + i) * 512 + lane * 16))
+                     : "memory");
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          asm volatile("ld.shared.f32 %0, [%1];"
+                       : "=f"(f[r].s[i][s])
+                       : "r"(slot + RT * 1024 + (uint32_t)(s * 128 + (r * 16 + i * 8 + (lane >> 2)) * 4))
+                       : "memory");
+      }
+    if (++read == D) read = 0;
+    __syncwarp();     // the slot's scales have been read by every lane
+  }
+};
+
+// Zero points of chunk c, where the grid has them.
+template <int RT, int NS>
+__device__ __forceinline__ void load_zeros(uint32_t (&z)[RT][2][NS], const PackedView& w, const TileRef<RT>& t,
                                            int64_t c) {
-  f.w[0] = ld_codes(t.codes[0] + c * kBlockBytes);
-  f.w[1] = ld_codes(t.codes[1] + c * kBlockBytes);
+  if (w.zero == nullptr) return;
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
-    int64_t k = 0;
-    if (w.ng > 1) {
-      k = (int64_t)((uint32_t)(c * 128 + 32 * s) / (uint32_t)w.g);
-      if (k > w.ng - 1) k = w.ng - 1;
-    }
-    k *= w.mp;
-    f.s[0][s] = ld_ahead(t.scale[0] + k);
-    f.s[1][s] = ld_ahead(t.scale[1] + k);
-    if (w.zero) {
-      f.z[0][s] = ld_ahead(t.zero[0] + k);
-      f.z[1][s] = ld_ahead(t.zero[1] + k);
-    }
+    const uint32_t g = grid_group(w, (uint32_t)(c * 128 + 32 * s)) * 16;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) z[r][i][s] = ld_ahead(t.zero[r][i] + g);
   }
+}
+template <int RT, int NS>
+__device__ __forceinline__ void set_zeros(Chunk16<NS> (&f)[RT], const uint32_t (&z)[RT][2][NS]) {
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) f[r].z[i][s] = z[r][i][s];
 }
 
 // tot[r][j] += products of the chunk of row tile r with column tile j, for j <
