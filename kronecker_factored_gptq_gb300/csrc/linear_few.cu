@@ -5,7 +5,7 @@
 // (m n / 2; at 8192 x 8192 33.6 MB, 5.0 us at 6.68 TB/s); the products run on
 // warp-level matrix instructions (qmma.cuh), which cost a fraction of that.
 //
-// A block takes 16 rows; its 8 warps take the 128-column chunks of the rows in
+// A block takes 16 or 32 rows; its 8 warps take the 128-column chunks of the rows in
 // turn, each with several chunks on their way, and add their partial sums in
 // shared memory in a fixed order.  An activation meets one warp of a block only,
 // so 16-bit activations are read where they are; fp32 ones (which become three
@@ -35,79 +35,88 @@ struct FewArgs {
   const void* x;
   void* y;
   int64_t T;
+  int S;         // blocks per row tile (a cluster)
   int slab;      // chunks of activations staged at a time; 0: read in place
   int vec_ok;    // rows of x are 16-byte aligned
 };
 
-// Chunks in flight per warp.
-template <int NS>
-constexpr int kDepth = 6;
+constexpr int kDepth = 4;   // chunks in flight per warp
 
-template <typename TX, typename H, int TERMS, int NT, int NS>
-__global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_constant__ FewArgs a) {
-  using P = qm::Pipe<1, NS, kDepth<NS>>;
+template <typename TX, typename H, int TERMS, int NT, int RT, int NS>
+__global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_constant__ FewArgs a) {
+  using P = qm::Pipe<RT, NS, kDepth>;
+  constexpr int ROWS = 16 * RT, OUT = NT * 8 * ROWS;
   extern __shared__ __align__(16) uint8_t dsm[];      // the warps' chunks, then staged activations
-  __shared__ float red[kWarps][NT * 8][16];
-  __shared__ float part[NT * 8 * 16];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  __shared__ float red[kWarps][NT * 8][ROWS];
+  __shared__ float part[OUT];
+  const int S = a.S, rank = S > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0[1] = {(int64_t)(blockIdx.x / S) * 16};
-  const int64_t t0 = (int64_t)blockIdx.y * (8 * NT);
-  const int cols = (int)min((int64_t)(8 * NT), a.T - t0);
+  const int64_t row0 = (int64_t)(blockIdx.x / S) * ROWS;
+  int64_t rows[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) rows[r] = row0 + 16 * r;
+  const int t0 = blockIdx.y * (8 * NT);
+  const int cols = min(8 * NT, (int)a.T - t0);
   const TX* x = static_cast<const TX*>(a.x) + t0 * a.w.n;
-  const int64_t c_lo = a.w.nc * rank / S, c_hi = a.w.nc * (rank + 1) / S;
+  const int nc = (int)a.w.nc;
+  const int c_lo = nc * rank / S, c_hi = nc * (rank + 1) / S;
 
-  qm::TileRef<1> tile;
-  qm::tile_ref<1>(tile, a.w, 0, row0, lane);
+  qm::TileRef<RT> tile;
+  qm::tile_ref<RT>(tile, a.w, 0, rows, lane);
   P pipe;
   pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
-  int64_t ahead = c_lo + warp;
+  int ahead = c_lo + warp;
 #pragma unroll
-  for (int p = 0; p < kDepth<NS> - 1; ++p, ahead += kWarps) pipe.issue(a.w, tile, ahead, ahead < c_hi, lane);
+  for (int p = 0; p < kDepth - 1; ++p, ahead += kWarps) pipe.issue(a.w, tile, ahead, ahead < c_hi, lane);
 
   int col[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) col[j] = min(8 * j + (lane >> 2), cols - 1);
-  float tot[1][NT][4];
+  float tot[RT][NT][4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tot[0][j][i] = 0.f;
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tot[r][j][i] = 0.f;
 
-  uint32_t z[1][2][NS];
-  if (c_lo + warp < c_hi) qm::load_zeros<1, NS>(z, a.w, tile, c_lo + warp);
-  qm::Chunk16<NS> f[1];
+  uint32_t z[RT][2][NS];
+  if (c_lo + warp < c_hi) qm::load_zeros<RT, NS>(z, a.w, tile, c_lo + warp);
+  qm::Chunk16<NS> f[RT];
   // the chunk c of this warp: next copies on their way, then its products
-  auto step = [&](int64_t c, auto fetch) {
+  auto step = [&](int c, auto fetch) {
     pipe.issue(a.w, tile, ahead, ahead < c_hi, lane);
     ahead += kWarps;
     pipe.take(f, lane);
-    qm::set_zeros<1, NS>(f, z);
-    if (c + kWarps < c_hi) qm::load_zeros<1, NS>(z, a.w, tile, c + kWarps);
-    qm::chunk_product<H, TERMS, 1, NT, NS>(tot, f, a.w.zero != nullptr, a.w.zu, NT, fetch);
+    qm::set_zeros<RT, NS>(f, z);
+    if (c + kWarps < c_hi) qm::load_zeros<RT, NS>(z, a.w, tile, c + kWarps);
+    qm::chunk_product<H, TERMS, RT, NT, NS>(tot, f, a.w.zero != nullptr, a.w.zu, NT, fetch);
   };
   if (TERMS == 1 && a.slab == 0) {
     const TX* xr[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) xr[j] = x + (int64_t)col[j] * a.w.n;
-    for (int64_t c = c_lo + warp; c < c_hi; c += kWarps) {
-      const int64_t k0 = c * 128 + 8 * (lane & 3);
-      step(c, [&](int j, int, int s) {
-        const int64_t k = k0 + 32 * s;
-        return k < a.w.n ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k)) : make_uint4(0, 0, 0, 0);
-      });
+    for (int j = 0; j < NT; ++j) xr[j] = x + (int64_t)col[j] * a.w.n + 8 * (lane & 3);
+    const int whole = (int)(a.w.n / 128);       // chunks without padding
+    for (int c = c_lo + warp; c < c_hi; c += kWarps) {
+      if (c < whole) {
+        step(c, [&](int j, int, int s) { return __ldg(reinterpret_cast<const uint4*>(xr[j] + c * 128 + 32 * s)); });
+      } else {
+        step(c, [&](int j, int, int s) {
+          const int k = c * 128 + 32 * s;
+          return k + 8 * (lane & 3) < a.w.n ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k)) : make_uint4(0, 0, 0, 0);
+        });
+      }
     }
   } else {
     uint8_t* xs = dsm + kWarps * P::kBytes;
     const uint32_t pitch = qm::x_pitch(a.slab);
     const uint32_t plane = pitch * (uint32_t)cols;
-    int64_t c = c_lo + warp;
-    for (int64_t s0 = c_lo; s0 < c_hi; s0 += a.slab) {
-      const int64_t s1 = min(s0 + a.slab, c_hi);
+    int c = c_lo + warp;
+    for (int s0 = c_lo; s0 < c_hi; s0 += a.slab) {
+      const int s1 = min(s0 + a.slab, c_hi);
       if (s0 != c_lo) __syncthreads();
       qm::stage_x<TX, TERMS>(xs, plane, pitch, x, a.w.n, cols, [](int r) { return (int64_t)r; }, s0 * 128,
-                             (int)(s1 - s0), a.w.n, a.vec_ok != 0);
+                             s1 - s0, a.w.n, a.vec_ok != 0);
       __syncthreads();
       for (; c < s1; c += kWarps) {
         const uint8_t* xc = xs + (c - s0) * 256 + (lane & 3) * 16;
@@ -121,35 +130,36 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
 
   // partial sums of the warps: [column][row], rows fastest
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int r = lane >> 2, c = 8 * j + 2 * (lane & 3);
-    red[warp][c][r] = tot[0][j][0];
-    red[warp][c + 1][r] = tot[0][j][1];
-    red[warp][c][r + 8] = tot[0][j][2];
-    red[warp][c + 1][r + 8] = tot[0][j][3];
-  }
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int o = 16 * r + (lane >> 2), c = 8 * j + 2 * (lane & 3);
+      red[warp][c][o] = tot[r][j][0];
+      red[warp][c + 1][o] = tot[r][j][1];
+      red[warp][c][o + 8] = tot[r][j][2];
+      red[warp][c + 1][o + 8] = tot[r][j][3];
+    }
   __syncthreads();
-  for (int i = threadIdx.x; i < NT * 8 * 16; i += kThreads) {
-    const int c = i >> 4, r = i & 15;
+  TX* y = static_cast<TX*>(a.y) + t0 * a.w.m + row0;
+  for (int i = threadIdx.x; i < OUT; i += kThreads) {
+    const int c = i / ROWS, r = i % ROWS;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += red[w][c][r];
-    if (S > 1) {
-      part[i] = v;
-    } else if (c < cols && row0[0] + r < a.w.m) {
-      static_cast<TX*>(a.y)[(t0 + c) * a.w.m + row0[0] + r] = from_float<TX>(v);
-    }
+    if (S > 1) part[i] = v;
+    else if (c < cols && row0 + r < a.w.m) y[c * a.w.m + r] = from_float<TX>(v);
   }
   if (S > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
     __syncwarp();
     cluster.sync();
     if (rank == 0) {
-      for (int i = threadIdx.x; i < NT * 8 * 16; i += kThreads) {
-        const int c = i >> 4, r = i & 15;
-        if (c >= cols || row0[0] + r >= a.w.m) continue;
+      for (int i = threadIdx.x; i < OUT; i += kThreads) {
+        const int c = i / ROWS, r = i % ROWS;
+        if (c >= cols || row0 + r >= a.w.m) continue;
         float v = 0.f;
         for (int k = 0; k < S; ++k) v += cluster.map_shared_rank(part, k)[i];
-        static_cast<TX*>(a.y)[(t0 + c) * a.w.m + row0[0] + r] = from_float<TX>(v);
+        y[c * a.w.m + r] = from_float<TX>(v);
       }
     }
     __syncwarp();
@@ -157,52 +167,59 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
   }
 }
 
-template <typename TX, typename H, int TERMS, int NT, int NS>
+template <typename TX, typename H, int TERMS, int NT, int RT, int NS>
 cudaError_t run(const LinearArgs& a, cudaStream_t s) {
-  auto k = linear_few_kernel<TX, H, TERMS, NT, NS>;
-  constexpr size_t ring = kWarps * qm::Pipe<1, NS, kDepth<NS>>::kBytes;
+  auto k = linear_few_kernel<TX, H, TERMS, NT, RT, NS>;
+  constexpr size_t ring = kWarps * qm::Pipe<RT, NS, kDepth>::kBytes;
   FewArgs f;
   f.w = a.w;
   f.x = a.x;
   f.y = a.y;
   f.T = a.T;
   f.vec_ok = aligned_to(a.x, 16) && (a.w.n * sizeof(TX)) % 16 == 0;
-  const int64_t tiles = a.w.mp / 16;
+  const int64_t tiles = (a.w.mp + 16 * RT - 1) / (16 * RT);
   const int64_t tt = (a.T + 8 * NT - 1) / (8 * NT);   // T <= kFewTokens: a handful
-  // blocks per row tile: enough that every SM has a few, at least two chunks a warp
-  int S = 1;
-  while (S < 8 && tiles * tt * S < 2 * sm_count() && a.w.nc >= (int64_t)2 * S * kWarps) S *= 2;
+  // blocks per row tile: enough that every SM has one or two, at least two
+  // chunks a warp
+  f.S = 1;
+  while (f.S < 8 && tiles * tt * f.S < sm_count() && a.w.nc >= (int64_t)2 * f.S * kWarps) f.S *= 2;
   size_t smem = ring;
   f.slab = 0;
   if (TERMS != 1 || !f.vec_ok) {
     const int cols = (int)std::min<int64_t>(8 * NT, a.T);
     const int64_t slab = (kMaxXBytes / (uint32_t)(TERMS * cols) - 64) / 256;
-    f.slab = (int)std::max<int64_t>(1, std::min<int64_t>(slab, (a.w.nc + S - 1) / S));
+    f.slab = (int)std::max<int64_t>(1, std::min<int64_t>(slab, (a.w.nc + f.S - 1) / f.S));
     smem += (size_t)qm::x_pitch(f.slab) * TERMS * cols;
   }
   static std::atomic<unsigned long long> done;
   cudaError_t e = ensure_smem_limit((const void*)k, ring + kMaxXBytes, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * S), (unsigned)tt, 1);
+  cfg.gridDim = dim3((unsigned)(tiles * f.S), (unsigned)tt, 1);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)S;
+  at[0].val.clusterDim.x = (unsigned)f.S;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = f.S > 1 ? 1 : 0;
   count_launch();
   return cudaLaunchKernelEx(&cfg, k, f);
+}
+
+template <typename TX, typename H, int TERMS, int NT, int NS>
+cudaError_t by_rows(const LinearArgs& a, cudaStream_t s) {
+  // two row tiles a warp once that leaves a block for every SM
+  return a.w.mp >= (int64_t)32 * sm_count() ? run<TX, H, TERMS, NT, 2, NS>(a, s) : run<TX, H, TERMS, NT, 1, NS>(a, s);
 }
 
 template <typename TX, typename H, int TERMS>
 cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
   const bool wide = a.w.ng == 1 || a.w.g % 128 == 0;
-  if (a.T <= 8) return wide ? run<TX, H, TERMS, 1, 1>(a, s) : run<TX, H, TERMS, 1, 4>(a, s);
-  return wide ? run<TX, H, TERMS, 2, 1>(a, s) : run<TX, H, TERMS, 2, 4>(a, s);
+  if (a.T <= 8) return wide ? by_rows<TX, H, TERMS, 1, 1>(a, s) : by_rows<TX, H, TERMS, 1, 4>(a, s);
+  return wide ? by_rows<TX, H, TERMS, 2, 1>(a, s) : by_rows<TX, H, TERMS, 2, 4>(a, s);
 }
 
 }  // namespace

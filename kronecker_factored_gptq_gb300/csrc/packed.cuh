@@ -63,6 +63,7 @@ struct PackedView {
   const uint8_t* zero;    // likewise, or NULL: every zero point is `zu`
   int zu;                 // -qmin
   int64_t count, m, n, mp, nc, ng, g;
+  uint64_t g_mul;         // floor(2^40 / g) + 1: k / g = (k g_mul) >> 40 for k, g <= 2^20
 };
 
 // The view of a caller's descriptor, checked; false when it is not usable.
@@ -83,6 +84,7 @@ inline bool packed_view(const bakron_packed* w, PackedView* v) {
   v->nc = L.nc;
   v->ng = L.ng;
   v->g = L.g;
+  v->g_mul = (uint64_t(1) << 40) / (uint64_t)L.g + 1;
   return true;
 }
 
@@ -92,7 +94,7 @@ __host__ __device__ __forceinline__ int64_t grid_row(const PackedView& w, int64_
 }
 // Group of column k; a padded column belongs to the last one.
 __device__ __forceinline__ uint32_t grid_group(const PackedView& w, uint32_t k) {
-  return w.ng > 1 ? min(k / (uint32_t)w.g, (uint32_t)w.ng - 1) : 0u;
+  return min((uint32_t)(((uint64_t)k * w.g_mul) >> 40), (uint32_t)w.ng - 1);
 }
 
 inline bool dtype_ok(int dtype) {

@@ -175,7 +175,8 @@ __device__ __forceinline__ void set_zeros(Chunk16<NS> (&f)[RT], const uint32_t (
 
 // tot[r][j] += products of the chunk of row tile r with column tile j, for j <
 // live (uniform).  fetch(j, q, s): this thread's 8 columns 32 s + 8 t .. of
-// term q of its activation row in column tile j.
+// term q of its activation row in column tile j.  A warp's instructions, not the
+// matrix pipe, are what a chunk costs, so two row tiles share a fetch where they can.
 template <typename H, int TERMS, int RT, int NT, int NS, typename Fetch>
 __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chunk16<NS> (&f)[RT],
                                               bool has_zero, int zu, int live, Fetch fetch) {
