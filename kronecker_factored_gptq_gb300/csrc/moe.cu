@@ -7,21 +7,23 @@
 // expert's matrices are read once for all its tokens.  Two launches:
 //
 // moe_in_kernel.  Which experts to read is known only after routing, so the
-// routing must not take a launch of its own: each cluster of 8 blocks computes
-// all logits, an eighth of the experts per block, and exchanges them through
-// distributed shared memory; every block then selects the experts itself
-// (the router is small and comes from L2).  The work that follows is a list of
-// (chosen expert, 16 rows of gate and the same 16 of up) dealt to the blocks in
-// turn.  A block's warps split the columns; the tokens of the expert are the
-// columns of the matrix instructions (qmma.cuh), gathered from x by index.
-// h leaves multiplied by q, in two bf16 terms (three for fp32), so that the
-// second product sees it to 2^-16 (2^-24).
+// routing must not take a launch of its own: every block computes it.  A router
+// too large for that is shared by the blocks of a cluster, which exchange their
+// parts of the logits through distributed shared memory.  The work that follows
+// is a list of (chosen expert, 16 rows of gate and the same 16 of up), cut into
+// equal runs, one per block, so that a block meets one expert or two and holds
+// that expert's tokens in shared memory; they are the columns of the matrix
+// instructions (qmma.cuh).  A warp takes whole items, or a part of the columns
+// of one when there are fewer items than warps.  h leaves multiplied by q, in two
+// bf16 terms (three for fp32), so that the second product sees it to 2^-16
+// (2^-24).
 //
-// moe_out_kernel.  A block owns 16 rows of y for all tokens and runs over the
-// chosen experts one after the other: a token that did not choose the expert has
-// a zero column.  So the sum over experts stays in the accumulators, in expert
-// order, and nothing is joined by atomics.  When there are few row tiles the
-// list of (expert, chunk) is also split over the blocks of a cluster.
+// moe_out_kernel.  A block owns 256 rows of y (32 per warp) and a run of the list
+// of (chosen expert, chunk of f); the expert's tokens are again the columns, and
+// their sums are added to per-token sums in shared memory when the expert changes.
+// The blocks that share rows leave their sums in the workspace; the last of
+// them to arrive (a counter that the first launch cleared) adds them in order, so
+// nothing depends on who was last.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -35,31 +37,36 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCluster = 8;
+constexpr int kInWarps = 16, kInThreads = 32 * kInWarps;
+constexpr int kOutWarps = 8, kOutThreads = 32 * kOutWarps;
+constexpr int kOutRows = 32 * kOutWarps;
+constexpr int kMaxCluster = 8;
 constexpr int kMaxTokens = BAKRON_MOE_TOKENS;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 1024;
-constexpr int kDepthIn = 4;      // chunks in flight per warp
-constexpr int kDepthOut = 6;
+template <int NS>
+constexpr int kDepthIn = NS == 1 ? 4 : 3;    // chunk slots per warp
+constexpr int kDepthOut = 3;
+constexpr uint32_t kInX = 64 * 1024;     // shared memory for an expert's tokens
+constexpr uint32_t kOutX = 32 * 1024;    // and for their h (one chunk of 32 tokens fits)
 
 struct MoeArgs {
   const void* x;        // T x d
   const void* router;   // E x d
-  const uint8_t* xp;    // activations as 16-bit terms: x itself or planes in the workspace
-  int64_t xp_pitch;     // bytes between its rows
-  int64_t xp_plane;     // bytes between its terms
-  int64_t xp_cols;      // columns that exist in a row (a multiple of 8)
   int T, E, k;
   int renormalize;
-  int vec_ok;           // x and router rows are 16-byte aligned
+  int x_vec, vec_ok;    // rows of x (of x and the router) are 16-byte aligned
+  int cluster;          // blocks that share the router
   int64_t d, f, fp;     // fp: f rounded up to 128
   PackedView wi, wo;
   uint8_t* h;           // terms x (T k) x fp 16-bit values
   int64_t h_plane;
   int* active;          // [0] chosen experts na, then their indices
-  int16_t* pair;        // [na][T]: t k + slot where token t chose the expert, else -1
+  uint32_t* who;        // [na]: bit t set where token t chose the expert
+  uint8_t* slot;        // [na][T]: which of its choices
+  int* arrived;         // [row groups of y]
+  float* part;          // [row groups][S][T][256]
+  int row_groups, S;    // blocks per row group
   void* y;
 };
 
@@ -83,65 +90,76 @@ __device__ __forceinline__ void load8(float (&v)[8], const TX* p, bool vec, int6
   }
 }
 
-// Logits of this block's experts (rank, rank + 8, ...) for every token, into
-// every block of the cluster.  The warps split an expert's columns when there
+// Logits of this block's experts (its rank in the cluster, then every C-th) for
+// every token, into every block of the cluster.  The warps split an expert's columns when there
 // are fewer experts than warps; the parts are added in a fixed order.
 template <typename TX>
-__device__ void router_logits(const MoeArgs& a, cg::cluster_group& cluster, float* logits, float* parts) {
+__device__ void router_logits(const MoeArgs& a, float* logits, float* parts) {
+  constexpr int kWarps = kInWarps;
+  const int C = a.cluster;
   constexpr int TT = 4;                      // tokens at a time
-  const int rank = (int)cluster.block_rank();
+  const int rank = C > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mine = (a.E - rank + kCluster - 1) / kCluster;     // experts of this block
+  const int mine = (a.E - rank + C - 1) / C;                   // experts of this block
   if (mine > 0) {
-    int split = 1;                           // warps per expert
-    while (split < kWarps && mine * split * 2 <= kWarps) split *= 2;
+    // tasks: (expert, TT tokens); warps share a task's columns when there are
+    // fewer tasks than warps
+    const int tts = (a.T + TT - 1) / TT, tasks = mine * tts;
+    int split = 1;
+    while (split < kWarps && tasks * split * 2 <= kWarps) split *= 2;
     const int at_once = kWarps / split;
     const int part = warp % split;
     const TX* x = static_cast<const TX*>(a.x);
-    for (int i0 = 0; i0 < mine; i0 += at_once) {
+    for (int i0 = 0; i0 < tasks; i0 += at_once) {
       const int i = i0 + warp / split;
-      if (i < mine) {
-        const TX* r = static_cast<const TX*>(a.router) + (int64_t)(rank + i * kCluster) * a.d;
-        for (int t0 = 0; t0 < a.T; t0 += TT) {
-          float acc[TT];
+      if (i < tasks) {
+        const TX* r = static_cast<const TX*>(a.router) + (int64_t)(rank + i / tts * C) * a.d;
+        const int t0 = i % tts * TT;
+        float acc[TT];
 #pragma unroll
-          for (int t = 0; t < TT; ++t) acc[t] = 0.f;
-          for (int64_t c = 8 * (lane + 32 * part); c < a.d; c += 8 * 32 * split) {
-            float w[8];
-            load8(w, r + c, a.vec_ok != 0, a.d - c);
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-              if (t0 + t < a.T) {
-                float v[8];
-                load8(v, x + (int64_t)(t0 + t) * a.d + c, a.vec_ok != 0, a.d - c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[t] = fmaf(v[e], w[e], acc[t]);
-              }
-            }
-          }
+        for (int t = 0; t < TT; ++t) acc[t] = 0.f;
+        for (int64_t c = 8 * (lane + 32 * part); c < a.d; c += 8 * 32 * split) {
+          float w[8];
+          load8(w, r + c, a.vec_ok != 0, a.d - c);
 #pragma unroll
           for (int t = 0; t < TT; ++t) {
+            if (t0 + t < a.T) {
+              float v[8];
+              load8(v, x + (int64_t)(t0 + t) * a.d + c, a.vec_ok != 0, a.d - c);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-            if (lane == 0 && t0 + t < a.T) parts[warp * kMaxTokens + t0 + t] = acc[t];
+              for (int e = 0; e < 8; ++e) acc[t] = fmaf(v[e], w[e], acc[t]);
+            }
           }
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+          if (lane == 0) parts[warp * TT + t] = acc[t];
         }
       }
       __syncthreads();
-      for (int q = threadIdx.x; q < at_once * a.T; q += kThreads) {
-        const int il = q / a.T, t = q - il * a.T;
-        if (i0 + il < mine) {
+      if (threadIdx.x < at_once * TT) {
+        const int il = threadIdx.x / TT, t = (i0 + il) % tts * TT + threadIdx.x % TT;
+        if (i0 + il < tasks && t < a.T) {
           float v = 0.f;
-          for (int p = 0; p < split; ++p) v += parts[(il * split + p) * kMaxTokens + t];
-          const int at = t * a.E + rank + (i0 + il) * kCluster;
-          for (int b = 0; b < kCluster; ++b) cluster.map_shared_rank(logits, b)[at] = v;
+          for (int p = 0; p < split; ++p) v += parts[(il * split + p) * TT + threadIdx.x % TT];
+          const int at = t * a.E + rank + (i0 + il) / tts * C;
+          if (C == 1) {
+            logits[at] = v;
+          } else {
+            cg::cluster_group cluster = cg::this_cluster();
+            for (int b = 0; b < C; ++b) cluster.map_shared_rank(logits, b)[at] = v;
+          }
         }
       }
       __syncthreads();
     }
   }
-  __syncwarp();
-  cluster.sync();
+  if (C > 1) {
+    __syncwarp();
+    cg::this_cluster().sync();
+  }
 }
 
 // The experts of one token (one warp): choice[i], weight[i] for i < k, the
@@ -198,21 +216,21 @@ struct Routing {
   int na;
   int active[kMaxTokens * kMaxTopK];
   uint32_t who[kMaxTokens * kMaxTopK];                    // bit t: token t chose the expert
-  float parts[kWarps * kMaxTokens];
+  float parts[kInWarps * kMaxTokens];
 };
 
 template <typename TX, typename H, int TERMS, int HT, int NT, int NS>
-__global__ void __launch_bounds__(kThreads, 2) moe_in_kernel(const __grid_constant__ MoeArgs a) {
+__global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_constant__ MoeArgs a) {
+  constexpr int kWarps = kInWarps, kThreads = kInThreads;
   extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ Routing R;
-  using P = qm::Pipe<2, NS, kDepthIn>;
-  // the routing's arrays end before the chunks' slots and the joins begin
-  float* red = reinterpret_cast<float*>(dsm + kWarps * P::kBytes);
+  using P = qm::Pipe<2, NS, kDepthIn<NS>>;
+  // the routing's arrays end before the chunks' slots and the tokens begin
+  uint8_t* xs = dsm + kWarps * P::kBytes;
   float* logits = reinterpret_cast<float*>(dsm);               // [T][E]
   int* slot_of = reinterpret_cast<int*>(logits + a.T * a.E);   // [E]: index among the chosen, or -1
-  cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  router_logits<TX>(a, cluster, logits, R.parts);
+  router_logits<TX>(a, logits, R.parts);
   for (int t = warp; t < a.T; t += kWarps)
     select_experts(logits + t * a.E, a.E, a.k, a.renormalize != 0, R.choice[t], R.weight[t], lane);
   for (int e = threadIdx.x; e < a.E; e += kThreads) slot_of[e] = -1;
@@ -240,17 +258,18 @@ __global__ void __launch_bounds__(kThreads, 2) moe_in_kernel(const __grid_consta
   __syncthreads();
   for (int i = threadIdx.x; i < a.T * a.k; i += kThreads)
     atomicOr(&R.who[slot_of[R.choice[i / a.k][i % a.k]]], 1u << (i / a.k));
-  __syncthreads();
   if (blockIdx.x == 0) {
     // for the second launch: the chosen experts, and who chose them
+    for (int i = threadIdx.x; i < a.T * a.k; i += kThreads)
+      a.slot[slot_of[R.choice[i / a.k][i % a.k]] * a.T + i / a.k] = (uint8_t)(i % a.k);
+    for (int i = threadIdx.x; i < a.row_groups; i += kThreads) a.arrived[i] = 0;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
     if (threadIdx.x == 0) a.active[0] = na;
-    for (int i = threadIdx.x; i < na; i += kThreads) a.active[1 + i] = R.active[i];
-    for (int i = threadIdx.x; i < na * a.T; i += kThreads) {
-      const int e = R.active[i / a.T], t = i % a.T;
-      int p = -1;
-      for (int s = 0; s < a.k; ++s)
-        if (R.choice[t][s] == e) p = t * a.k + s;
-      a.pair[i] = (int16_t)p;
+    for (int i = threadIdx.x; i < na; i += kThreads) {
+      a.active[1 + i] = R.active[i];
+      a.who[i] = R.who[i];
     }
   }
   // zeros past f, for the padded columns of w_out
@@ -264,277 +283,363 @@ __global__ void __launch_bounds__(kThreads, 2) moe_in_kernel(const __grid_consta
     }
   }
 
-  // Items: (chosen expert, row tile), a gate tile and its up tile each, for
-  // groups of G warps that split the columns: as many groups as the items can
-  // feed.  A warp runs through its (item, chunk) pairs as one sequence, so the
-  // copies of the next item start while this one ends.
+  // This block's run of items (expert, row tile); G warps per item.
   const int tiles = (int)((a.f + 15) / 16);
   const int64_t items = (int64_t)na * tiles;
+  const int i_lo = (int)(items * blockIdx.x / gridDim.x), i_hi = (int)(items * (blockIdx.x + 1) / gridDim.x);
   const int nc = (int)a.wi.nc;
   int G = 1;
-  while (G < kWarps && items * 2 * G <= (int64_t)gridDim.x * kWarps && nc >= 2 * G) G *= 2;
-  const int group = warp / G, part = warp % G;
-  const int64_t groups = (int64_t)gridDim.x * (kWarps / G);
-  const int64_t first = (int64_t)blockIdx.x + (int64_t)gridDim.x * group;
+  while (G < kWarps && (i_hi - i_lo) * 2 * G <= kWarps && nc >= 2 * G) G *= 2;
+  const int group = warp / G, part = warp % G, groups = kWarps / G;
   const int c_lo = nc * part / G, c_hi = nc * (part + 1) / G;
 
   P pipe;
   pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
-  auto open_item = [&](qm::TileRef<2>& t, int64_t it) {
-    const int ai = (int)(it / tiles);
-    const int64_t r0 = (it - (int64_t)ai * tiles) * 16;
+  auto open_item = [&](qm::TileRef<2>& t, int it) {
+    const int ai = it / tiles;
+    const int64_t r0 = (int64_t)(it - ai * tiles) * 16;
     const int64_t rows[2] = {r0, a.f + r0};
     qm::tile_ref<2>(t, a.wi, R.active[ai], rows, lane);
   };
+  // a warp's items: group, group + groups, ... of each expert's part of the run
+  auto segment_end = [&](int it) { return min(i_hi, (it / tiles + 1) * tiles); };
+  auto next_item = [&](int it, int seg_end) { return it + groups < seg_end ? it + groups : -1; };
   qm::TileRef<2> t_ahead, t_now;
-  int64_t it_ahead = first;
-  int c_ahead = c_lo;
-  if (it_ahead < items) open_item(t_ahead, it_ahead);
+  int seg_a = i_lo, seg_a_end = i_lo < i_hi ? segment_end(i_lo) : i_lo;   // where the copies are
+  int it_ahead = -1, c_ahead = c_lo;
+  auto settle = [&]() {      // first item of this warp at or after segment seg_a
+    while (it_ahead < 0 && seg_a < i_hi) {
+      if (seg_a + group < seg_a_end) {
+        it_ahead = seg_a + group;
+      } else {
+        seg_a = seg_a_end;
+        if (seg_a < i_hi) seg_a_end = segment_end(seg_a);
+      }
+    }
+    if (it_ahead >= 0) open_item(t_ahead, it_ahead);
+  };
+  settle();
   auto issue = [&]() {
-    pipe.issue(a.wi, t_ahead, c_ahead, it_ahead < items, lane);
-    if (it_ahead < items && ++c_ahead == c_hi) {
+    pipe.issue(a.wi, t_ahead, c_ahead, it_ahead >= 0, lane);
+    if (it_ahead >= 0 && ++c_ahead == c_hi) {
       c_ahead = c_lo;
-      it_ahead += groups;
-      if (it_ahead < items) open_item(t_ahead, it_ahead);
+      it_ahead = next_item(it_ahead, seg_a_end);
+      if (it_ahead < 0) {
+        seg_a = seg_a_end;
+        if (seg_a < i_hi) seg_a_end = segment_end(seg_a);
+        settle();
+      } else {
+        open_item(t_ahead, it_ahead);
+      }
     }
   };
+  __syncthreads();             // the routing's arrays are done with
 #pragma unroll
-  for (int p = 0; p < kDepthIn - 1; ++p) issue();
+  for (int p = 0; p < kDepthIn<NS> - 1; ++p) issue();
 
-  for (int64_t it = first; it < items; it += groups) {
-    const int ai = (int)(it / tiles);
-    const int64_t row0 = (it - (int64_t)ai * tiles) * 16;
-    const int e = R.active[ai];
-    if (a.wi.zero) open_item(t_now, it);
-    // the expert's tokens: thread's column 8 j + lane / 4
+  const uint32_t xs_addr = (uint32_t)__cvta_generic_to_shared(xs);
+  for (int seg = i_lo; seg < i_hi;) {
+    const int end = segment_end(seg);
+    const int ai = seg / tiles, e = R.active[ai];
     const uint32_t who = R.who[ai];
-    const int cnt = __popc(who);
-    const int live = (cnt + 7) / 8;
-    const uint8_t* xr[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int c = 8 * j + (lane >> 2);
-      xr[j] = c < cnt ? a.xp + (int64_t)nth_bit(who, c) * a.xp_pitch + (lane & 3) * 16 : nullptr;
+    const int cnt = __popc(who), live = (cnt + 7) / 8;
+    // the expert's tokens: all columns at once, or slab by slab
+    const int slab = min(nc, (int)((kInX / (uint32_t)(TERMS * cnt) - 64) / 256));
+    const uint32_t pitch = qm::x_pitch(slab), plane = pitch * (uint32_t)cnt;
+    auto stage = [&](int s0) {
+      qm::stage_x<TX, TERMS>(xs, plane, pitch, static_cast<const TX*>(a.x), a.d, cnt,
+                             [&](int r) { return (int64_t)nth_bit(who, r); }, (int64_t)s0 * 128, min(slab, nc - s0),
+                             a.d, a.x_vec != 0);
+    };
+    __syncthreads();
+    if (slab == nc) {
+      stage(0);
+      __syncthreads();
     }
-    float tot[2][NT][4];
+    uint32_t col[NT];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int j = 0; j < NT; ++j)
+      col[j] = xs_addr + (uint32_t)min(8 * j + (lane >> 2), cnt - 1) * pitch + (uint32_t)(lane & 3) * 16;
+    const int rounds = (end - seg + groups - 1) / groups;    // the same for every warp
+    for (int r = 0; r < rounds; ++r) {
+      const int it = seg + r * groups + group;
+      const bool on = it < end;
+      const int64_t row0 = (int64_t)(it - ai * tiles) * 16;
+      if (on && a.wi.zero) open_item(t_now, it);
+      float tot[2][NT][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[r][j][i] = 0.f;
-    uint32_t z[2][2][NS];
-    qm::load_zeros<2, NS>(z, a.wi, t_now, c_lo);
-    for (int c = c_lo; c < c_hi; ++c) {
-      qm::Chunk16<NS> f[2];
-      issue();
-      pipe.take(f, lane);
-      qm::set_zeros<2, NS>(f, z);
-      if (c + 1 < c_hi) qm::load_zeros<2, NS>(z, a.wi, t_now, c + 1);
-      const int64_t k0 = (int64_t)c * 128 + 8 * (lane & 3);
-      qm::chunk_product<H, TERMS, 2, NT, NS>(
-          tot, f, a.wi.zero != nullptr, a.wi.zu, live, [&](int j, int q, int s) {
-            if (xr[j] == nullptr || k0 + 32 * s >= a.xp_cols) return make_uint4(0, 0, 0, 0);
-            return __ldg(reinterpret_cast<const uint4*>(xr[j] + q * a.xp_plane + (int64_t)c * 256 + s * 64));
-          });
-    }
-    // the group's sums of gate and up (thread: rows lane / 4 and + 8, columns
-    // 2 (lane & 3) and + 1 of each column tile)
-    if (G > 1) {
-      float* mine = red + (size_t)warp * (2 * NT * 4 * 32) + lane;
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mine[((r * NT + j) * 4 + i) * 32] = tot[r][j][i];
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * G) : "memory");
-      if (part == 0) {
-        for (int w = 1; w < G; ++w) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) tot[r][j][i] += mine[(size_t)w * (2 * NT * 4 * 32) + ((r * NT + j) * 4 + i) * 32];
+          for (int i = 0; i < 4; ++i) tot[q][j][i] = 0.f;
+      uint32_t z[2][2][NS];
+      if (on) qm::load_zeros<2, NS>(z, a.wi, t_now, c_lo);
+      for (int s0 = 0; s0 < nc; s0 += slab) {
+        if (slab < nc) {
+          __syncthreads();
+          stage(s0);
+          __syncthreads();
         }
-      }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * G) : "memory");
-    }
-    if (part == 0) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 8 * j + 2 * (lane & 3) + (i & 1);
-          const int64_t row = row0 + (lane >> 2) + 8 * (i >> 1);
-          if (c < cnt && row < a.f) {
-            const int t = nth_bit(who, c);
-            int s = 0;
-            for (int q = 0; q < a.k; ++q)
-              if (R.choice[t][q] == e) s = q;
-            const float g = tot[0][j][i];
-            const float v = g / (1.f + expf(-g)) * tot[1][j][i] * R.weight[t][s];
-            float p[3];
-            split3(v, p[0], p[1], p[2]);
-            uint8_t* o = a.h + ((int64_t)(t * a.k + s) * a.fp + row) * 2;
-#pragma unroll
-            for (int q = 0; q < HT; ++q) *reinterpret_cast<uint16_t*>(o + q * a.h_plane) = bf16_bits(p[q]);
+        if (on) {
+          const int s1 = min(s0 + slab, c_hi);
+          for (int c = max(s0, c_lo); c < s1; ++c) {
+            qm::Chunk16<NS> f[2];
+            issue();
+            pipe.take(f, lane);
+            qm::set_zeros<2, NS>(f, z);
+            if (c + 1 < c_hi) qm::load_zeros<2, NS>(z, a.wi, t_now, c + 1);
+            const uint32_t xc = (uint32_t)(c - s0) * 256;
+            qm::chunk_product<H, TERMS, 2, NT, NS>(
+                tot, f, a.wi.zero != nullptr, a.wi.zu, live,
+                [&](int j, int q, int s) { return qm::lds128(col[j] + q * plane + xc + s * 64); });
           }
         }
+      }
+      // the group's sums of gate and up (thread: rows lane / 4 and + 8, columns
+      // 2 (lane & 3) and + 1 of each column tile); the joins use the tokens' area
+      if (G > 1) {
+        __syncthreads();
+        float* mine = reinterpret_cast<float*>(xs) + (size_t)warp * (2 * NT * 4 * 32) + lane;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mine[((q * NT + j) * 4 + i) * 32] = tot[q][j][i];
+        __syncthreads();
+        if (part == 0) {
+          for (int w = 1; w < G; ++w) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  tot[q][j][i] += mine[(size_t)w * (2 * NT * 4 * 32) + ((q * NT + j) * 4 + i) * 32];
+          }
+        }
+        if (rounds > 1) {      // the tokens are needed again
+          __syncthreads();
+          if (slab == nc) {
+            stage(0);
+            __syncthreads();
+          }
+        }
+      }
+      if (on && part == 0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 8 * j + 2 * (lane & 3) + (i & 1);
+            const int64_t row = row0 + (lane >> 2) + 8 * (i >> 1);
+            if (c < cnt && row < a.f) {
+              const int t = nth_bit(who, c);
+              int s = 0;
+              for (int q = 0; q < a.k; ++q)
+                if (R.choice[t][q] == e) s = q;
+              const float g = tot[0][j][i];
+              const float v = g / (1.f + expf(-g)) * tot[1][j][i] * R.weight[t][s];
+              float p[3];
+              split3(v, p[0], p[1], p[2]);
+              uint8_t* o = a.h + ((int64_t)(t * a.k + s) * a.fp + row) * 2;
+#pragma unroll
+              for (int q = 0; q < HT; ++q) *reinterpret_cast<uint16_t*>(o + q * a.h_plane) = bf16_bits(p[q]);
+            }
+          }
+      }
     }
+    seg = end;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <typename TX, int HT, int NT, int NS>
-__global__ void __launch_bounds__(kThreads, 2) moe_out_kernel(const __grid_constant__ MoeArgs a) {
-  using P = qm::Pipe<1, NS, kDepthOut>;
+__global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_constant__ MoeArgs a) {
+  constexpr int kWarps = kOutWarps, kThreads = kOutThreads;
+  using P = qm::Pipe<2, NS, kDepthOut>;
   extern __shared__ __align__(16) uint8_t dsm[];
-  __shared__ float red[kWarps][NT * 8][17];
-  __shared__ float part[NT * 8 * 16];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  uint8_t* hs = dsm + kWarps * P::kBytes;
+  float* sums = reinterpret_cast<float*>(hs + kOutX);       // [T][256]: the block's rows of y
+  __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0 = (int64_t)(blockIdx.x / S) * 16;
+  const int S = a.S, rank = blockIdx.x % S, rg = blockIdx.x / S;
+  const int64_t row0 = (int64_t)rg * kOutRows;
   const int na = a.active[0];
   const int nc = (int)a.wo.nc;
-  const int64_t units = (int64_t)na * nc;          // (expert, chunk)
-  const int64_t u0 = units * rank / S, u1 = units * (rank + 1) / S;
-  float tot[1][NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tot[0][j][i] = 0.f;
-  const int live = (a.T + 7) / 8;
+  const int units = na * nc;                                // (expert, chunk)
+  const int u0 = (int)((int64_t)units * rank / S), u1 = (int)((int64_t)units * (rank + 1) / S);
+  for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) sums[i] = 0.f;
 
-  // this warp's run of the list
-  const int64_t v0 = u0 + (u1 - u0) * warp / kWarps, v1 = u0 + (u1 - u0) * (warp + 1) / kWarps;
+  const int64_t rows[2] = {row0 + 32 * warp, row0 + 32 * warp + 16};
   P pipe;
   pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
-  qm::TileRef<1> t_ahead, t_now;
-  int ai_ahead = (int)(v0 / nc), c_ahead = (int)(v0 - (int64_t)ai_ahead * nc);
-  int64_t v_ahead = v0;
-  const int64_t rows[1] = {row0};
-  if (v0 < v1) qm::tile_ref<1>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
+  qm::TileRef<2> t_ahead, t_now;
+  int u_ahead = u0, ai_ahead = u0 / nc, c_ahead = u0 - ai_ahead * nc;
+  if (u0 < u1) qm::tile_ref<2>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
   auto issue = [&]() {
-    pipe.issue(a.wo, t_ahead, c_ahead, v_ahead < v1, lane);
-    if (v_ahead < v1) {
-      ++v_ahead;
-      if (++c_ahead == nc && v_ahead < v1) {
+    pipe.issue(a.wo, t_ahead, c_ahead, u_ahead < u1, lane);
+    if (u_ahead < u1) {
+      ++u_ahead;
+      if (++c_ahead == nc && u_ahead < u1) {
         c_ahead = 0;
         ++ai_ahead;
-        qm::tile_ref<1>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
+        qm::tile_ref<2>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
       }
     }
   };
 #pragma unroll
   for (int p = 0; p < kDepthOut - 1; ++p) issue();
-  int ai = (int)(v0 / nc), c = (int)(v0 - (int64_t)ai * nc);
-  int have = -1;
-  const uint8_t* hr[NT];
-  for (int64_t v = v0; v < v1; ++v) {
-    if (ai != have) {
-      have = ai;
-      if (a.wo.zero) qm::tile_ref<1>(t_now, a.wo, a.active[1 + ai], rows, lane);
+
+  const uint32_t hs_addr = (uint32_t)__cvta_generic_to_shared(hs);
+  for (int u = u0; u < u1;) {
+    const int ai = u / nc, c0 = u - ai * nc;
+    const int c1 = min(nc, c0 + (u1 - u));                  // this block's chunks of the expert
+    const uint32_t who = a.who[ai];
+    const int cnt = __popc(who), live = (cnt + 7) / 8;
+    if (a.wo.zero) qm::tile_ref<2>(t_now, a.wo, a.active[1 + ai], rows, lane);
+    const int slab = min(c1 - c0, (int)((kOutX / (uint32_t)(HT * cnt) - 64) / 256));
+    const uint32_t pitch = qm::x_pitch(slab), plane = pitch * (uint32_t)cnt;
+    uint32_t col[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int t = 8 * j + (lane >> 2);
-        const int p = t < a.T ? a.pair[ai * a.T + t] : -1;
-        hr[j] = p < 0 ? nullptr : a.h + (int64_t)p * a.fp * 2 + (lane & 3) * 16;
+    for (int j = 0; j < NT; ++j)
+      col[j] = hs_addr + (uint32_t)min(8 * j + (lane >> 2), cnt - 1) * pitch + (uint32_t)(lane & 3) * 16;
+    float tot[2][NT][4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tot[q][j][i] = 0.f;
+    uint32_t z[2][2][NS];
+    qm::load_zeros<2, NS>(z, a.wo, t_now, c0);
+    for (int s0 = c0; s0 < c1; s0 += slab) {
+      const int s1 = min(s0 + slab, c1);
+      __syncthreads();
+      const int per = (s1 - s0) * 16;
+      for (int i = threadIdx.x; i < HT * cnt * per; i += kThreads) {
+        const int row = i / per, p = i - row * per;
+        const int q = row / cnt, t = nth_bit(who, row - q * cnt);
+        const uint8_t* src = a.h + q * a.h_plane + (int64_t)(t * a.k + a.slot[ai * a.T + t]) * a.fp * 2;
+        *reinterpret_cast<uint4*>(hs + q * plane + (row - q * cnt) * pitch + p * 16) =
+            *reinterpret_cast<const uint4*>(src + (int64_t)s0 * 256 + p * 16);
+      }
+      __syncthreads();
+      for (int c = s0; c < s1; ++c) {
+        qm::Chunk16<NS> f[2];
+        issue();
+        pipe.take(f, lane);
+        qm::set_zeros<2, NS>(f, z);
+        if (c + 1 < c1) qm::load_zeros<2, NS>(z, a.wo, t_now, c + 1);
+        const uint32_t hc = (uint32_t)(c - s0) * 256;
+        qm::chunk_product<__nv_bfloat16, HT, 2, NT, NS>(
+            tot, f, a.wo.zero != nullptr, a.wo.zu, live,
+            [&](int j, int q, int s) { return qm::lds128(col[j] + q * plane + hc + s * 64); });
       }
     }
-    uint32_t z[1][2][NS];
-    qm::load_zeros<1, NS>(z, a.wo, t_now, c);
-    issue();
-    qm::Chunk16<NS> f[1];
-    pipe.take(f, lane);
-    qm::set_zeros<1, NS>(f, z);
-    qm::chunk_product<__nv_bfloat16, HT, 1, NT, NS>(
-        tot, f, a.wo.zero != nullptr, a.wo.zu, live, [&](int j, int q, int s) {
-          if (hr[j] == nullptr) return make_uint4(0, 0, 0, 0);
-          return __ldg(reinterpret_cast<const uint4*>(hr[j] + q * a.h_plane + (int64_t)c * 256 + s * 64));
-        });
-    if (++c == nc) {
-      c = 0;
-      ++ai;
-    }
+    // to the tokens' sums; a warp's rows are its own
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 8 * j + 2 * (lane & 3) + (i & 1);
+        if (c < cnt) {
+          const int t = nth_bit(who, c);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            sums[t * kOutRows + 32 * warp + 16 * q + (lane >> 2) + 8 * (i >> 1)] += tot[q][j][i];
+        }
+      }
+    __syncwarp();
+    u += c1 - c0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int rr = lane >> 2, cc = 8 * j + 2 * (lane & 3);
-    red[warp][cc][rr] = tot[0][j][0];
-    red[warp][cc + 1][rr] = tot[0][j][1];
-    red[warp][cc][rr + 8] = tot[0][j][2];
-    red[warp][cc + 1][rr + 8] = tot[0][j][3];
-  }
   __syncthreads();
+
   TX* y = static_cast<TX*>(a.y);
-  for (int i = threadIdx.x; i < NT * 8 * 16; i += kThreads) {
-    const int t = i >> 4, r = i & 15;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][t][r];
-    if (S > 1) part[i] = v;
-    else if (t < a.T && row0 + r < a.d) y[(int64_t)t * a.d + row0 + r] = from_float<TX>(v);
-  }
-  if (S > 1) {
-    __syncwarp();
-    cluster.sync();
-    if (rank == 0) {
-      for (int i = threadIdx.x; i < NT * 8 * 16; i += kThreads) {
-        const int t = i >> 4, r = i & 15;
-        if (t >= a.T || row0 + r >= a.d) continue;
-        float v = 0.f;
-        for (int k = 0; k < S; ++k) v += cluster.map_shared_rank(part, k)[i];
-        y[(int64_t)t * a.d + row0 + r] = from_float<TX>(v);
-      }
+  if (S == 1) {
+    for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) {
+      const int64_t row = row0 + i % kOutRows;
+      if (row < a.d) y[(int64_t)(i / kOutRows) * a.d + row] = from_float<TX>(sums[i]);
     }
-    __syncwarp();
-    cluster.sync();
+    return;
+  }
+  float* mine = a.part + ((int64_t)rg * S + rank) * a.T * kOutRows;
+  for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) mine[i] = sums[i];
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(&a.arrived[rg], 1) == S - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const float* all = a.part + (int64_t)rg * S * a.T * kOutRows;
+  for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) {
+    const int64_t row = row0 + i % kOutRows;
+    float v = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < S; ++k) v += __ldcg(all + (int64_t)k * a.T * kOutRows + i);
+    if (row < a.d) y[(int64_t)(i / kOutRows) * a.d + row] = from_float<TX>(v);
   }
 }
 
-cudaError_t launch_cluster(const void* k, unsigned grid, unsigned cluster, size_t smem, MoeArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  void* args[] = {&a};
-  count_launch();
-  return cudaLaunchKernelExC(&cfg, k, args);
+// Blocks that share a row group of y, at most: two blocks per SM in all.
+int out_split(int64_t d, int64_t T, int64_t E, int k, int64_t nc) {
+  const int64_t groups = (d + kOutRows - 1) / kOutRows;
+  const int64_t units = std::min<int64_t>(E, T * k) * nc;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(2 * sm_count() / groups, units));
 }
 
 template <typename TX, typename H, int TERMS, int HT, int NT, int NS, int NSO>
 cudaError_t run(MoeArgs& a, cudaStream_t s) {
-  const void* k1 = (const void*)moe_in_kernel<TX, H, TERMS, HT, NT, NS>;
-  const void* k2 = (const void*)moe_out_kernel<TX, HT, NT, NSO>;
-  constexpr size_t in_fixed = kWarps * (size_t)qm::Pipe<2, NS, kDepthIn>::kBytes + kWarps * 2 * NT * 4 * 32 * 4;
-  constexpr size_t in_most = std::max(in_fixed, (size_t)(8 * NT + 1) * kMaxExperts * 4);
-  constexpr size_t out_bytes = kWarps * (size_t)qm::Pipe<1, NSO, kDepthOut>::kBytes;
+  auto k1 = moe_in_kernel<TX, H, TERMS, HT, NT, NS>;
+  auto k2 = moe_out_kernel<TX, HT, NT, NSO>;
+  constexpr size_t pipes = kInWarps * (size_t)qm::Pipe<2, NS, kDepthIn<NS>>::kBytes;
+  static_assert(kInWarps * 2 * NT * 4 * 32 * 4 <= kInX, "the joins fit the tokens' area");
+  constexpr size_t in_bytes = std::max(pipes + kInX, (size_t)(8 * NT + 1) * kMaxExperts * 4);
+  const size_t out_bytes = kOutWarps * (size_t)qm::Pipe<2, NSO, kDepthOut>::kBytes + kOutX + (size_t)a.T * kOutRows * 4;
   static std::atomic<unsigned long long> done, done2;
-  cudaError_t e = ensure_smem_limit(k1, in_most, done);
-  if (e == cudaSuccess) e = ensure_smem_limit(k2, out_bytes, done2);
+  cudaError_t e = ensure_smem_limit((const void*)k1, in_bytes, done);
+  if (e == cudaSuccess)
+    e = ensure_smem_limit((const void*)k2, out_bytes - (size_t)a.T * kOutRows * 4 + (size_t)kMaxTokens * kOutRows * 4, done2);
   if (e != cudaSuccess) return e;
-  const size_t smem = std::max(in_fixed, (size_t)(a.T + 1) * a.E * 4);
-  const int64_t most = (int64_t)std::min(a.E, a.T * a.k) * ((a.f + 15) / 16);
-  // two blocks per SM, not more than there can be items
-  int64_t clusters = std::min<int64_t>(2 * sm_count() / kCluster, (most + kCluster - 1) / kCluster);
-  e = launch_cluster(k1, (unsigned)(clusters * kCluster), kCluster, smem, a, s);
+  // a block reads up to about 128 KB of router (from L2); a larger one is shared
+  const size_t router = (size_t)a.E * a.d * sizeof(TX);
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && router / a.cluster > 128 * 1024) a.cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kInThreads);
+  cfg.dynamicSmemBytes = in_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)a.cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  // one block per SM, all at once: as many clusters as fit
+  int blocks = sm_count();
+  if (a.cluster > 1) {
+    static std::atomic<int> fit[4];          // per cluster size 2, 4, 8 (0: not asked yet)
+    std::atomic<int>& f = fit[a.cluster == 2 ? 1 : a.cluster == 4 ? 2 : 3];
+    int n = f.load(std::memory_order_relaxed);
+    if (n == 0) {
+      cfg.gridDim = dim3((unsigned)a.cluster);
+      e = cudaOccupancyMaxActiveClusters(&n, k1, &cfg);
+      if (e != cudaSuccess) return e;
+      n = std::max(1, std::min(n, sm_count() / a.cluster));
+      f.store(n, std::memory_order_relaxed);
+    }
+    blocks = n * a.cluster;
+  }
+  cfg.gridDim = dim3((unsigned)blocks);
+  count_launch();
+  e = cudaLaunchKernelEx(&cfg, k1, a);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (a.d + 15) / 16;
-  const int64_t units = (int64_t)std::min(a.E, a.T * a.k) * a.wo.nc;
-  int S = 1;
-  while (S < 8 && tiles * S < 2 * sm_count() && units >= (int64_t)2 * S * kWarps) S *= 2;
-  return launch_cluster(k2, (unsigned)(tiles * S), (unsigned)S, out_bytes, a, s);
+  count_launch();
+  k2<<<(unsigned)(a.row_groups * a.S), kOutThreads, out_bytes, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename TX, typename H, int TERMS, int HT, int NT>
@@ -554,21 +659,24 @@ cudaError_t by_tokens(MoeArgs& a, cudaStream_t s) {
 }
 
 struct MoeLayout {
-  size_t xp, h, active, pair, total;
-  int64_t dp, fp;
+  size_t h, active, who, slot, arrived, part, total;
+  int64_t fp;
 };
 
 MoeLayout moe_layout(int64_t T, int64_t d, int64_t f, int64_t E, int k, int dtype) {
   MoeLayout L;
   const int64_t t = std::min<int64_t>(T, kMaxTokens);
-  L.dp = (d + 127) / 128 * 128;
+  const int64_t na = std::min<int64_t>(E, t * k), groups = (d + kOutRows - 1) / kOutRows;
   L.fp = (f + 127) / 128 * 128;
   size_t off = 0;
   auto take = [&](size_t b) { const size_t o = off; off += (b + 255) / 256 * 256; return o; };
-  L.xp = take((size_t)(dtype == BAKRON_F32 ? 3 : 1) * t * L.dp * 2);
   L.h = take((size_t)(dtype == BAKRON_F32 ? 3 : 2) * t * k * L.fp * 2);
-  L.active = take((size_t)(1 + std::min<int64_t>(E, t * k)) * 4);
-  L.pair = take((size_t)std::min<int64_t>(E, t * k) * t * 2);
+  L.active = take((size_t)(1 + na) * 4);
+  L.who = take((size_t)na * 4);
+  L.slot = take((size_t)(na * t));
+  L.arrived = take((size_t)groups * 4);
+  // a smaller call (the last tokens of many) may split further: bound every split
+  L.part = take((size_t)std::max<int64_t>(groups, 2 * sm_count()) * t * kOutRows * 4);
   L.total = off;
   return L;
 }
@@ -619,33 +727,24 @@ extern "C" bakron_status bakron_moe(const void* X, int64_t T, int dtype, const v
   a.fp = L.fp;
   a.h = base + L.h;
   a.active = reinterpret_cast<int*>(base + L.active);
-  a.pair = reinterpret_cast<int16_t*>(base + L.pair);
+  a.who = reinterpret_cast<uint32_t*>(base + L.who);
+  a.slot = base + L.slot;
+  a.arrived = reinterpret_cast<int*>(base + L.arrived);
+  a.part = reinterpret_cast<float*>(base + L.part);
+  a.row_groups = (int)((a.d + kOutRows - 1) / kOutRows);
   for (int64_t t0 = 0; t0 < T; t0 += kMaxTokens) {
     a.T = (int)std::min<int64_t>(kMaxTokens, T - t0);
     a.x = static_cast<const uint8_t*>(X) + (size_t)(t0 * a.d) * es;
     a.y = static_cast<uint8_t*>(Y) + (size_t)(t0 * a.d) * es;
     a.h_plane = (int64_t)a.T * a.k * a.fp * 2;
-    const bool rows16 = (a.d * es) % 16 == 0;
-    a.vec_ok = rows16 && aligned_to(a.x, 16) && aligned_to(router, 16);
-    cudaError_t e = cudaSuccess;
-    if (dtype != BAKRON_F32 && rows16 && aligned_to(a.x, 16)) {
-      a.xp = static_cast<const uint8_t*>(a.x);
-      a.xp_pitch = a.d * 2;
-      a.xp_plane = 0;
-      a.xp_cols = a.d;
-    } else {
-      a.xp = base + L.xp;
-      a.xp_pitch = L.dp * 2;
-      a.xp_plane = (int64_t)a.T * L.dp * 2;
-      a.xp_cols = L.dp;
-      e = launch_planes(a.x, dtype, a.T, a.d, L.dp, base + L.xp, s);
-    }
-    if (e == cudaSuccess) {
-      switch (dtype) {
-        case BAKRON_F32: e = by_tokens<float, __nv_bfloat16, 3, 3>(a, s); break;
-        case BAKRON_BF16: e = by_tokens<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, s); break;
-        default: e = by_tokens<__half, __half, 1, 2>(a, s); break;
-      }
+    a.S = out_split(a.d, a.T, a.E, a.k, a.wo.nc);
+    a.x_vec = (a.d * es) % 16 == 0 && aligned_to(a.x, 16);
+    a.vec_ok = a.x_vec && aligned_to(router, 16);
+    cudaError_t e;
+    switch (dtype) {
+      case BAKRON_F32: e = by_tokens<float, __nv_bfloat16, 3, 3>(a, s); break;
+      case BAKRON_BF16: e = by_tokens<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, s); break;
+      default: e = by_tokens<__half, __half, 1, 2>(a, s); break;
     }
     if (e != cudaSuccess) return launch_status(e);
   }

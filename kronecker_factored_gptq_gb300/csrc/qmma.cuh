@@ -49,6 +49,14 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
 // What one 128-column chunk of a 16-row tile needs, per thread: rows lane / 4
 // and lane / 4 + 8.  NS scales per row: 1 when the group is a multiple of 128
 // columns, else one per 32 columns.
