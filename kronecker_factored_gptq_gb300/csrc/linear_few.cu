@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
     pipe.take(f, lane);
     qm::set_zeros<RT, NS>(f, z);
     if (c + kWarps < c_hi) qm::load_zeros<RT, NS>(z, a.w, tile, c + kWarps);
-    qm::chunk_product<H, TERMS, RT, NT, NS>(tot, f, a.w.zero != nullptr, a.w.zu, NT, fetch);
+    qm::chunk_product<H, TERMS, RT, NT, NS>(tot, f, a.w.zero != nullptr, a.w.zu, fetch);
   };
   if (TERMS == 1 && a.slab == 0) {
     const TX* xr[NT];

@@ -27,6 +27,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "linear.cuh"
 #include "qmma.cuh"
@@ -209,6 +210,16 @@ __device__ __forceinline__ int nth_bit(uint32_t m, int c) {
   return __ffs((int)m) - 1;
 }
 
+// Calls f with the number of column tiles as a constant: a kernel holds the loop
+// for 1, 2 and 4 tiles of 8 tokens, and an expert with few tokens does not pay
+// for registers and instructions of many.
+template <typename F>
+__device__ __forceinline__ void by_columns(int live, F f) {
+  if (live <= 1) f(std::integral_constant<int, 1>());
+  else if (live == 2) f(std::integral_constant<int, 2>());
+  else f(std::integral_constant<int, 4>());
+}
+
 // Shared memory of the routing.
 struct Routing {
   int choice[kMaxTokens][kMaxTopK];
@@ -219,7 +230,7 @@ struct Routing {
   float parts[kInWarps * kMaxTokens];
 };
 
-template <typename TX, typename H, int TERMS, int HT, int NT, int NS>
+template <typename TX, typename H, int TERMS, int HT, int NS>
 __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_constant__ MoeArgs a) {
   constexpr int kWarps = kInWarps, kThreads = kInThreads;
   extern __shared__ __align__(16) uint8_t dsm[];
@@ -356,11 +367,14 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
       stage(0);
       __syncthreads();
     }
+    const int rounds = (end - seg + groups - 1) / groups;    // the same for every warp
+    // NT column tiles of tokens
+    auto rounds_of = [&](auto nt_) {
+    constexpr int NT = decltype(nt_)::value;
     uint32_t col[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       col[j] = xs_addr + (uint32_t)min(8 * j + (lane >> 2), cnt - 1) * pitch + (uint32_t)(lane & 3) * 16;
-    const int rounds = (end - seg + groups - 1) / groups;    // the same for every warp
     for (int r = 0; r < rounds; ++r) {
       const int it = seg + r * groups + group;
       const bool on = it < end;
@@ -391,7 +405,7 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
             if (c + 1 < c_hi) qm::load_zeros<2, NS>(z, a.wi, t_now, c + 1);
             const uint32_t xc = (uint32_t)(c - s0) * 256;
             qm::chunk_product<H, TERMS, 2, NT, NS>(
-                tot, f, a.wi.zero != nullptr, a.wi.zu, live,
+                tot, f, a.wi.zero != nullptr, a.wi.zu,
                 [&](int j, int q, int s) { return qm::lds128(col[j] + q * plane + xc + s * 64); });
           }
         }
@@ -450,12 +464,14 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
           }
       }
     }
+    };
+    by_columns(live, rounds_of);
     seg = end;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <typename TX, int HT, int NT, int NS>
+template <typename TX, int HT, int NS>
 __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_constant__ MoeArgs a) {
   constexpr int kWarps = kOutWarps, kThreads = kOutThreads;
   using P = qm::Pipe<2, NS, kDepthOut>;
@@ -501,6 +517,8 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
     if (a.wo.zero) qm::tile_ref<2>(t_now, a.wo, a.active[1 + ai], rows, lane);
     const int slab = min(c1 - c0, (int)((kOutX / (uint32_t)(HT * cnt) - 64) / 256));
     const uint32_t pitch = qm::x_pitch(slab), plane = pitch * (uint32_t)cnt;
+    auto chunks_of = [&](auto nt_) {
+    constexpr int NT = decltype(nt_)::value;
     uint32_t col[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -534,7 +552,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
         if (c + 1 < c1) qm::load_zeros<2, NS>(z, a.wo, t_now, c + 1);
         const uint32_t hc = (uint32_t)(c - s0) * 256;
         qm::chunk_product<__nv_bfloat16, HT, 2, NT, NS>(
-            tot, f, a.wo.zero != nullptr, a.wo.zu, live,
+            tot, f, a.wo.zero != nullptr, a.wo.zu,
             [&](int j, int q, int s) { return qm::lds128(col[j] + q * plane + hc + s * 64); });
       }
     }
@@ -553,6 +571,8 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
         }
       }
     __syncwarp();
+    };
+    by_columns(live, chunks_of);
     u += c1 - c0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -591,13 +611,13 @@ int out_split(int64_t d, int64_t T, int64_t E, int k, int64_t nc) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(2 * sm_count() / groups, units));
 }
 
-template <typename TX, typename H, int TERMS, int HT, int NT, int NS, int NSO>
+template <typename TX, typename H, int TERMS, int HT, int NS, int NSO>
 cudaError_t run(MoeArgs& a, cudaStream_t s) {
-  auto k1 = moe_in_kernel<TX, H, TERMS, HT, NT, NS>;
-  auto k2 = moe_out_kernel<TX, HT, NT, NSO>;
+  auto k1 = moe_in_kernel<TX, H, TERMS, HT, NS>;
+  auto k2 = moe_out_kernel<TX, HT, NSO>;
   constexpr size_t pipes = kInWarps * (size_t)qm::Pipe<2, NS, kDepthIn<NS>>::kBytes;
-  static_assert(kInWarps * 2 * NT * 4 * 32 * 4 <= kInX, "the joins fit the tokens' area");
-  constexpr size_t in_bytes = std::max(pipes + kInX, (size_t)(8 * NT + 1) * kMaxExperts * 4);
+  static_assert(kInWarps * 2 * (kMaxTokens / 8) * 4 * 32 * 4 <= kInX, "the joins fit the tokens' area");
+  constexpr size_t in_bytes = std::max(pipes + kInX, (size_t)(kMaxTokens + 1) * kMaxExperts * 4);
   const size_t out_bytes = kOutWarps * (size_t)qm::Pipe<2, NSO, kDepthOut>::kBytes + kOutX + (size_t)a.T * kOutRows * 4;
   static std::atomic<unsigned long long> done, done2;
   cudaError_t e = ensure_smem_limit((const void*)k1, in_bytes, done);
@@ -642,20 +662,13 @@ cudaError_t run(MoeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename TX, typename H, int TERMS, int HT, int NT>
+template <typename TX, typename H, int TERMS, int HT>
 cudaError_t by_groups(MoeArgs& a, cudaStream_t s) {
   const bool wi = a.wi.ng == 1 || a.wi.g % 128 == 0, wo = a.wo.ng == 1 || a.wo.g % 128 == 0;
-  if (wi && wo) return run<TX, H, TERMS, HT, NT, 1, 1>(a, s);
-  if (wi) return run<TX, H, TERMS, HT, NT, 1, 4>(a, s);
-  if (wo) return run<TX, H, TERMS, HT, NT, 4, 1>(a, s);
-  return run<TX, H, TERMS, HT, NT, 4, 4>(a, s);
-}
-
-template <typename TX, typename H, int TERMS, int HT>
-cudaError_t by_tokens(MoeArgs& a, cudaStream_t s) {
-  if (a.T <= 8) return by_groups<TX, H, TERMS, HT, 1>(a, s);
-  if (a.T <= 16) return by_groups<TX, H, TERMS, HT, 2>(a, s);
-  return by_groups<TX, H, TERMS, HT, 4>(a, s);
+  if (wi && wo) return run<TX, H, TERMS, HT, 1, 1>(a, s);
+  if (wi) return run<TX, H, TERMS, HT, 1, 4>(a, s);
+  if (wo) return run<TX, H, TERMS, HT, 4, 1>(a, s);
+  return run<TX, H, TERMS, HT, 4, 4>(a, s);
 }
 
 struct MoeLayout {
@@ -742,9 +755,9 @@ extern "C" bakron_status bakron_moe(const void* X, int64_t T, int dtype, const v
     a.vec_ok = a.x_vec && aligned_to(router, 16);
     cudaError_t e;
     switch (dtype) {
-      case BAKRON_F32: e = by_tokens<float, __nv_bfloat16, 3, 3>(a, s); break;
-      case BAKRON_BF16: e = by_tokens<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, s); break;
-      default: e = by_tokens<__half, __half, 1, 2>(a, s); break;
+      case BAKRON_F32: e = by_groups<float, __nv_bfloat16, 3, 3>(a, s); break;
+      case BAKRON_BF16: e = by_groups<__nv_bfloat16, __nv_bfloat16, 1, 2>(a, s); break;
+      default: e = by_groups<__half, __half, 1, 2>(a, s); break;
     }
     if (e != cudaSuccess) return launch_status(e);
   }

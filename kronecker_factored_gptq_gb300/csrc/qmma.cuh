@@ -181,13 +181,12 @@ __device__ __forceinline__ void set_zeros(Chunk16<NS> (&f)[RT], const uint32_t (
       for (int s = 0; s < NS; ++s) f[r].z[i][s] = z[r][i][s];
 }
 
-// tot[r][j] += products of the chunk of row tile r with column tile j, for j <
-// live (uniform).  fetch(j, q, s): this thread's 8 columns 32 s + 8 t .. of
+// tot[r][j] += products of the chunk of row tile r with column tile j.  fetch(j, q, s): this thread's 8 columns 32 s + 8 t .. of
 // term q of its activation row in column tile j.  A warp's instructions, not the
 // matrix pipe, are what a chunk costs, so two row tiles share a fetch where they can.
 template <typename H, int TERMS, int RT, int NT, int NS, typename Fetch>
 __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chunk16<NS> (&f)[RT],
-                                              bool has_zero, int zu, int live, Fetch fetch) {
+                                              bool has_zero, int zu, Fetch fetch) {
   float acc[RT][NT][4];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -212,15 +211,13 @@ __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chu
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      if (j < live) {
 #pragma unroll
-        for (int q = 0; q < TERMS; ++q) {
-          const uint4 x = fetch(j, q, s);
+      for (int q = 0; q < TERMS; ++q) {
+        const uint4 x = fetch(j, q, s);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            mma16816<H>(acc[r][j], a[r][0], b[r][0], a[r][1], b[r][1], x.x, x.y);
-            mma16816<H>(acc[r][j], a[r][2], b[r][2], a[r][3], b[r][3], x.z, x.w);
-          }
+        for (int r = 0; r < RT; ++r) {
+          mma16816<H>(acc[r][j], a[r][0], b[r][0], a[r][1], b[r][1], x.x, x.y);
+          mma16816<H>(acc[r][j], a[r][2], b[r][2], a[r][3], b[r][3], x.z, x.w);
         }
       }
     }
