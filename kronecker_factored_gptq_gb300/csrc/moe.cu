@@ -6,11 +6,13 @@
 // The layer is bound by the bytes of the experts that any token chose: every
 // expert's matrices are read once for all its tokens.  Two launches:
 //
-// moe_in_kernel.  Which experts to read is known only after routing, so the
-// routing must not take a launch of its own: every block computes it.  A router
-// too large for that is shared by the blocks of a cluster, which exchange their
-// parts of the logits through distributed shared memory.  The work that follows
-// is a list of (chosen expert, 16 rows of gate and the same 16 of up), cut into
+// moe_route_kernel forms the logits, one block per expert and 8 tokens.  (Formed
+// by every block of the next launch instead, the same rows went to all SMs and
+// took 58 us at 16 tokens x 8 experts x 4096 and 5.6 us at 1 x 32 x 1024; this
+// launch, chained to the next without a gap, takes about 3.)
+//
+// moe_in_kernel.  Every block selects the experts from the logits.  The work
+// that follows is a list of (chosen expert, 16 rows of gate and the same 16 of up), cut into
 // equal runs, one per block, so that a block meets one expert or two and holds
 // that expert's tokens in shared memory; they are the columns of the matrix
 // instructions (qmma.cuh).  A warp takes whole items, or a part of the columns
@@ -22,10 +24,10 @@
 // of (chosen expert, chunk of f); the expert's tokens are again the columns, and
 // their sums are added to per-token sums in shared memory when the expert changes.
 // The blocks that share rows leave their sums in the workspace; the last of
-// them to arrive (a counter that the first launch cleared) adds them in order, so
-// nothing depends on who was last.
-#include <cooperative_groups.h>
-
+// them to arrive (a counter that the launch before cleared) adds them in rank order,
+// so nothing depends on who was last.  (As clusters of 16 with the sums in
+// distributed shared memory not all blocks fitted at once: 184 us against 122 at 16
+// tokens x 8 experts of 4096 x 14336.)
 #include <algorithm>
 #include <type_traits>
 
@@ -34,14 +36,12 @@
 
 namespace bakron {
 
-namespace cg = cooperative_groups;
-
 namespace {
 
 constexpr int kInWarps = 16, kInThreads = 32 * kInWarps;
 constexpr int kOutWarps = 8, kOutThreads = 32 * kOutWarps;
 constexpr int kOutRows = 32 * kOutWarps;
-constexpr int kMaxCluster = 8;
+constexpr int kRouteWarps = 8, kRouteTokens = 8;
 constexpr int kMaxTokens = BAKRON_MOE_TOKENS;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 1024;
@@ -57,7 +57,6 @@ struct MoeArgs {
   int T, E, k;
   int renormalize;
   int x_vec, vec_ok;    // rows of x (of x and the router) are 16-byte aligned
-  int cluster;          // blocks that share the router
   int64_t d, f, fp;     // fp: f rounded up to 128
   PackedView wi, wo;
   uint8_t* h;           // terms x (T k) x fp 16-bit values
@@ -65,9 +64,10 @@ struct MoeArgs {
   int* active;          // [0] chosen experts na, then their indices
   uint32_t* who;        // [na]: bit t set where token t chose the expert
   uint8_t* slot;        // [na][T]: which of its choices
+  float* logits;        // [T][E]
   int* arrived;         // [row groups of y]
   float* part;          // [row groups][S][T][256]
-  int row_groups, S;    // blocks per row group
+  int row_groups, S;    // blocks per row group of y
   void* y;
 };
 
@@ -91,76 +91,53 @@ __device__ __forceinline__ void load8(float (&v)[8], const TX* p, bool vec, int6
   }
 }
 
-// Logits of this block's experts (its rank in the cluster, then every C-th) for
-// every token, into every block of the cluster.  The warps split an expert's columns when there
-// are fewer experts than warps; the parts are added in a fixed order.
+// logits[t][e] of one expert and kRouteTokens tokens; the warps split the columns
+// and their parts are added in a fixed order.
 template <typename TX>
-__device__ void router_logits(const MoeArgs& a, float* logits, float* parts) {
-  constexpr int kWarps = kInWarps;
-  const int C = a.cluster;
-  constexpr int TT = 4;                      // tokens at a time
-  const int rank = C > 1 ? (int)cg::this_cluster().block_rank() : 0;
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const __grid_constant__ MoeArgs a) {
+  __shared__ float parts[kRouteWarps][kRouteTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mine = (a.E - rank + C - 1) / C;                   // experts of this block
-  if (mine > 0) {
-    // tasks: (expert, TT tokens); warps share a task's columns when there are
-    // fewer tasks than warps
-    const int tts = (a.T + TT - 1) / TT, tasks = mine * tts;
-    int split = 1;
-    while (split < kWarps && tasks * split * 2 <= kWarps) split *= 2;
-    const int at_once = kWarps / split;
-    const int part = warp % split;
-    const TX* x = static_cast<const TX*>(a.x);
-    for (int i0 = 0; i0 < tasks; i0 += at_once) {
-      const int i = i0 + warp / split;
-      if (i < tasks) {
-        const TX* r = static_cast<const TX*>(a.router) + (int64_t)(rank + i / tts * C) * a.d;
-        const int t0 = i % tts * TT;
-        float acc[TT];
+  const int e = blockIdx.x, t0 = blockIdx.y * kRouteTokens;
+  const TX* r = static_cast<const TX*>(a.router) + (int64_t)e * a.d;
+  const TX* x = static_cast<const TX*>(a.x) + (int64_t)t0 * a.d;
+  grid_dep_wait();
+  grid_dep_launch();
+  float acc[kRouteTokens];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) acc[t] = 0.f;
-        for (int64_t c = 8 * (lane + 32 * part); c < a.d; c += 8 * 32 * split) {
-          float w[8];
-          load8(w, r + c, a.vec_ok != 0, a.d - c);
+  for (int t = 0; t < kRouteTokens; ++t) acc[t] = 0.f;
+  for (int64_t c = 8 * threadIdx.x; c < a.d; c += 8 * 32 * kRouteWarps) {
+    float w[8];
+    load8(w, r + c, a.vec_ok != 0, a.d - c);
 #pragma unroll
-          for (int t = 0; t < TT; ++t) {
-            if (t0 + t < a.T) {
-              float v[8];
-              load8(v, x + (int64_t)(t0 + t) * a.d + c, a.vec_ok != 0, a.d - c);
+    for (int t = 0; t < kRouteTokens; ++t) {
+      if (t0 + t < a.T) {
+        float v[8];
+        load8(v, x + (int64_t)t * a.d + c, a.vec_ok != 0, a.d - c);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) acc[t] = fmaf(v[e], w[e], acc[t]);
-            }
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-          if (lane == 0) parts[warp * TT + t] = acc[t];
-        }
+        for (int i = 0; i < 8; ++i) acc[t] = fmaf(v[i], w[i], acc[t]);
       }
-      __syncthreads();
-      if (threadIdx.x < at_once * TT) {
-        const int il = threadIdx.x / TT, t = (i0 + il) % tts * TT + threadIdx.x % TT;
-        if (i0 + il < tasks && t < a.T) {
-          float v = 0.f;
-          for (int p = 0; p < split; ++p) v += parts[(il * split + p) * TT + threadIdx.x % TT];
-          const int at = t * a.E + rank + (i0 + il) / tts * C;
-          if (C == 1) {
-            logits[at] = v;
-          } else {
-            cg::cluster_group cluster = cg::this_cluster();
-            for (int b = 0; b < C; ++b) cluster.map_shared_rank(logits, b)[at] = v;
-          }
-        }
-      }
-      __syncthreads();
     }
   }
-  if (C > 1) {
-    __syncwarp();
-    cg::this_cluster().sync();
+#pragma unroll
+  for (int t = 0; t < kRouteTokens; ++t) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+    if (lane == 0) parts[warp][t] = acc[t];
   }
+  __syncthreads();
+  if (threadIdx.x < kRouteTokens && t0 + (int)threadIdx.x < a.T) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRouteWarps; ++w) v += parts[w][threadIdx.x];
+    a.logits[(t0 + threadIdx.x) * a.E + e] = v;
+  }
+}
+
+// A key that orders floats as unsigned integers; NaN lowest.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0u;
+  const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);   // -0 ties with 0
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
 // The experts of one token (one warp): choice[i], weight[i] for i < k, the
@@ -168,27 +145,27 @@ __device__ void router_logits(const MoeArgs& a, float* logits, float* parts) {
 // make the weights NaN.
 __device__ void select_experts(const float* l, int E, int k, bool renormalize, int* choice, float* weight,
                                int lane) {
-  uint32_t taken = 0;                        // bit i: expert lane + 32 i (E <= 1024)
+  uint32_t taken = 0;                        // bit j: expert lane + 32 j (E <= 1024)
   float top = 0.f, mine = 0.f;
+  bool bad = false;
+  for (int e = lane; e < E; e += 32) bad |= l[e] != l[e];
   for (int i = 0; i < k; ++i) {
-    float best = 0.f;
-    int at = -1;
+    uint32_t best = 0;
+    int at = 0x7fffffff;                     // this lane's best that is not taken
     for (int j = 0; 32 * j + lane < E; ++j) {
       if (taken >> j & 1) continue;
-      float v = l[32 * j + lane];
-      if (v != v) v = -INFINITY;
-      if (at < 0 || v > best) { best = v; at = 32 * j + lane; }
+      const uint32_t v = order_key(l[32 * j + lane]);
+      if (at == 0x7fffffff || v > best) { best = v; at = 32 * j + lane; }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, best, o);
-      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-      if (oa >= 0 && (at < 0 || ov > best || (ov == best && oa < at))) { best = ov; at = oa; }
-    }
+    const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+    at = (int)__reduce_min_sync(0xffffffffu, best == most ? (unsigned)at : 0x7fffffffu);
     if ((at & 31) == lane) taken |= 1u << (at >> 5);
-    if (i == 0) top = best;
-    if (lane == 0) choice[i] = at;
-    if (lane == i) mine = l[at];
+    const float v = l[at];
+    if (i == 0) top = v;
+    if (lane == i) {
+      mine = v;
+      choice[i] = at;
+    }
   }
   float sum = 0.f;
   if (renormalize) {
@@ -196,8 +173,6 @@ __device__ void select_experts(const float* l, int E, int k, bool renormalize, i
   } else {
     for (int e = lane; e < E; e += 32) sum += expf(l[e] - top);
   }
-  bool bad = false;
-  for (int e = lane; e < E; e += 32) bad |= l[e] != l[e];
   bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -227,7 +202,6 @@ struct Routing {
   int na;
   int active[kMaxTokens * kMaxTopK];
   uint32_t who[kMaxTokens * kMaxTopK];                    // bit t: token t chose the expert
-  float parts[kInWarps * kMaxTokens];
 };
 
 template <typename TX, typename H, int TERMS, int HT, int NS>
@@ -241,10 +215,13 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
   float* logits = reinterpret_cast<float*>(dsm);               // [T][E]
   int* slot_of = reinterpret_cast<int*>(logits + a.T * a.E);   // [E]: index among the chosen, or -1
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  router_logits<TX>(a, logits, R.parts);
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = threadIdx.x; i < a.T * a.E; i += kThreads) logits[i] = __ldcg(a.logits + i);
+  for (int e = threadIdx.x; e < a.E; e += kThreads) slot_of[e] = -1;
+  __syncthreads();
   for (int t = warp; t < a.T; t += kWarps)
     select_experts(logits + t * a.E, a.E, a.k, a.renormalize != 0, R.choice[t], R.weight[t], lane);
-  for (int e = threadIdx.x; e < a.E; e += kThreads) slot_of[e] = -1;
   __syncthreads();
   // the chosen experts in ascending order
   for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) slot_of[R.choice[i / a.k][i % a.k]] = 0;
@@ -273,10 +250,10 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
     // for the second launch: the chosen experts, and who chose them
     for (int i = threadIdx.x; i < a.T * a.k; i += kThreads)
       a.slot[slot_of[R.choice[i / a.k][i % a.k]] * a.T + i / a.k] = (uint8_t)(i % a.k);
-    for (int i = threadIdx.x; i < a.row_groups; i += kThreads) a.arrived[i] = 0;
   }
   __syncthreads();
   if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < a.row_groups; i += kThreads) a.arrived[i] = 0;
     if (threadIdx.x == 0) a.active[0] = na;
     for (int i = threadIdx.x; i < na; i += kThreads) {
       a.active[1 + i] = R.active[i];
@@ -478,10 +455,12 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
   extern __shared__ __align__(16) uint8_t dsm[];
   uint8_t* hs = dsm + kWarps * P::kBytes;
   float* sums = reinterpret_cast<float*>(hs + kOutX);       // [T][256]: the block's rows of y
-  __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.S, rank = blockIdx.x % S, rg = blockIdx.x / S;
+  __shared__ int last;
   const int64_t row0 = (int64_t)rg * kOutRows;
+  grid_dep_wait();
+  grid_dep_launch();
   const int na = a.active[0];
   const int nc = (int)a.wo.nc;
   const int units = na * nc;                                // (expert, chunk)
@@ -586,25 +565,42 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
     }
     return;
   }
-  float* mine = a.part + ((int64_t)rg * S + rank) * a.T * kOutRows;
-  for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) mine[i] = sums[i];
+  const int n4 = a.T * kOutRows / 4;
+  float4* mine = reinterpret_cast<float4*>(a.part) + ((int64_t)rg * S + rank) * n4;
+  for (int i = threadIdx.x; i < n4; i += kThreads) mine[i] = reinterpret_cast<const float4*>(sums)[i];
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = atomicAdd(&a.arrived[rg], 1) == S - 1;
   __syncthreads();
   if (!last) return;
   __threadfence();
-  const float* all = a.part + (int64_t)rg * S * a.T * kOutRows;
-  for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) {
-    const int64_t row = row0 + i % kOutRows;
-    float v = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < S; ++k) v += __ldcg(all + (int64_t)k * a.T * kOutRows + i);
-    if (row < a.d) y[(int64_t)(i / kOutRows) * a.d + row] = from_float<TX>(v);
+  const float4* all = reinterpret_cast<const float4*>(a.part) + (int64_t)rg * S * n4;
+  for (int i = threadIdx.x; i < n4; i += kThreads) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < S; k0 += 8) {       // eight blocks' sums on their way at a time
+      float4 p[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        p[k] = k0 + k < S ? __ldcg(all + (int64_t)(k0 + k) * n4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v.x += p[k].x;
+        v.y += p[k].y;
+        v.z += p[k].z;
+        v.w += p[k].w;
+      }
+    }
+    const int64_t row = row0 + 4 * i % kOutRows;
+    TX* o = y + (int64_t)(4 * i / kOutRows) * a.d + row;
+    if (row < a.d) o[0] = from_float<TX>(v.x);
+    if (row + 1 < a.d) o[1] = from_float<TX>(v.y);
+    if (row + 2 < a.d) o[2] = from_float<TX>(v.z);
+    if (row + 3 < a.d) o[3] = from_float<TX>(v.w);
   }
 }
 
-// Blocks that share a row group of y, at most: two blocks per SM in all.
+// Blocks that share a row group of y: two blocks per SM in all, each with a
+// unit at least.
 int out_split(int64_t d, int64_t T, int64_t E, int k, int64_t nc) {
   const int64_t groups = (d + kOutRows - 1) / kOutRows;
   const int64_t units = std::min<int64_t>(E, T * k) * nc;
@@ -624,42 +620,27 @@ cudaError_t run(MoeArgs& a, cudaStream_t s) {
   if (e == cudaSuccess)
     e = ensure_smem_limit((const void*)k2, out_bytes - (size_t)a.T * kOutRows * 4 + (size_t)kMaxTokens * kOutRows * 4, done2);
   if (e != cudaSuccess) return e;
-  // a block reads up to about 128 KB of router (from L2); a larger one is shared
-  const size_t router = (size_t)a.E * a.d * sizeof(TX);
-  a.cluster = 1;
-  while (a.cluster < kMaxCluster && router / a.cluster > 128 * 1024) a.cluster *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kInThreads);
-  cfg.dynamicSmemBytes = in_bytes;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)a.cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-  // one block per SM, all at once: as many clusters as fit
-  int blocks = sm_count();
-  if (a.cluster > 1) {
-    static std::atomic<int> fit[4];          // per cluster size 2, 4, 8 (0: not asked yet)
-    std::atomic<int>& f = fit[a.cluster == 2 ? 1 : a.cluster == 4 ? 2 : 3];
-    int n = f.load(std::memory_order_relaxed);
-    if (n == 0) {
-      cfg.gridDim = dim3((unsigned)a.cluster);
-      e = cudaOccupancyMaxActiveClusters(&n, k1, &cfg);
-      if (e != cudaSuccess) return e;
-      n = std::max(1, std::min(n, sm_count() / a.cluster));
-      f.store(n, std::memory_order_relaxed);
-    }
-    blocks = n * a.cluster;
-  }
-  cfg.gridDim = dim3((unsigned)blocks);
-  count_launch();
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)a.E, (unsigned)((a.T + kRouteTokens - 1) / kRouteTokens));
+  cfg.blockDim = dim3(32 * kRouteWarps);
+  count_launch(3);
+  e = cudaLaunchKernelEx(&cfg, moe_route_kernel<TX>, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)sm_count());    // one block per SM
+  cfg.blockDim = dim3(kInThreads);
+  cfg.dynamicSmemBytes = in_bytes;
   e = cudaLaunchKernelEx(&cfg, k1, a);
   if (e != cudaSuccess) return e;
-  count_launch();
-  k2<<<(unsigned)(a.row_groups * a.S), kOutThreads, out_bytes, s>>>(a);
-  return cudaGetLastError();
+  cfg.gridDim = dim3((unsigned)(a.row_groups * a.S));
+  cfg.blockDim = dim3(kOutThreads);
+  cfg.dynamicSmemBytes = out_bytes;
+  return cudaLaunchKernelEx(&cfg, k2, a);
 }
 
 template <typename TX, typename H, int TERMS, int HT>
@@ -672,7 +653,7 @@ cudaError_t by_groups(MoeArgs& a, cudaStream_t s) {
 }
 
 struct MoeLayout {
-  size_t h, active, who, slot, arrived, part, total;
+  size_t h, active, who, slot, logits, arrived, part, total;
   int64_t fp;
 };
 
@@ -687,8 +668,9 @@ MoeLayout moe_layout(int64_t T, int64_t d, int64_t f, int64_t E, int k, int dtyp
   L.active = take((size_t)(1 + na) * 4);
   L.who = take((size_t)na * 4);
   L.slot = take((size_t)(na * t));
+  L.logits = take((size_t)(t * E) * 4);
   L.arrived = take((size_t)groups * 4);
-  // a smaller call (the last tokens of many) may split further: bound every split
+  // at most two blocks per SM in all (a smaller last launch may split more finely)
   L.part = take((size_t)std::max<int64_t>(groups, 2 * sm_count()) * t * kOutRows * 4);
   L.total = off;
   return L;
@@ -742,6 +724,7 @@ extern "C" bakron_status bakron_moe(const void* X, int64_t T, int dtype, const v
   a.active = reinterpret_cast<int*>(base + L.active);
   a.who = reinterpret_cast<uint32_t*>(base + L.who);
   a.slot = base + L.slot;
+  a.logits = reinterpret_cast<float*>(base + L.logits);
   a.arrived = reinterpret_cast<int*>(base + L.arrived);
   a.part = reinterpret_cast<float*>(base + L.part);
   a.row_groups = (int)((a.d + kOutRows - 1) / kOutRows);

@@ -25,28 +25,27 @@
 namespace bakron {
 namespace qm {
 
+// c = A B + c, or c = A B when fresh (a constant at each use).
 template <typename H>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+__device__ __forceinline__ void mma16816(float (&c)[4], bool fresh, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1);
 template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1,
-                                                        uint32_t a2, uint32_t a3, uint32_t b0,
-                                                        uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], bool fresh, uint32_t a0, uint32_t a1,
+                                                        uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(fresh ? 0.f : c[0]), "f"(fresh ? 0.f : c[1]),
+        "f"(fresh ? 0.f : c[2]), "f"(fresh ? 0.f : c[3]));
 }
 template <>
-__device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uint32_t a1,
-                                                 uint32_t a2, uint32_t a3, uint32_t b0,
-                                                 uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], bool fresh, uint32_t a0, uint32_t a1,
+                                                        uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(fresh ? 0.f : c[0]), "f"(fresh ? 0.f : c[1]),
+        "f"(fresh ? 0.f : c[2]), "f"(fresh ? 0.f : c[3]));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -188,12 +187,6 @@ template <typename H, int TERMS, int RT, int NT, int NS, typename Fetch>
 __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chunk16<NS> (&f)[RT],
                                               bool has_zero, int zu, Fetch fetch) {
   float acc[RT][NT][4];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][j][i] = 0.f;
   uint32_t off[RT][2];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -216,8 +209,8 @@ __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chu
         const uint4 x = fetch(j, q, s);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          mma16816<H>(acc[r][j], a[r][0], b[r][0], a[r][1], b[r][1], x.x, x.y);
-          mma16816<H>(acc[r][j], a[r][2], b[r][2], a[r][3], b[r][3], x.z, x.w);
+          mma16816<H>(acc[r][j], q == 0 && (s == 0 || NS == 4), a[r][0], b[r][0], a[r][1], b[r][1], x.x, x.y);
+          mma16816<H>(acc[r][j], false, a[r][2], b[r][2], a[r][3], b[r][3], x.z, x.w);
         }
       }
     }
@@ -231,8 +224,6 @@ __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chu
           tot[r][j][1] = fmaf(s0, acc[r][j][1], tot[r][j][1]);
           tot[r][j][2] = fmaf(s1, acc[r][j][2], tot[r][j][2]);
           tot[r][j][3] = fmaf(s1, acc[r][j][3], tot[r][j][3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][j][i] = 0.f;
         }
       }
     }
