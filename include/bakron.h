@@ -442,8 +442,8 @@ bakron_status bakron_linear_grad(const void* dY, int64_t T, int dtype, const bak
  *   q_e = p_e, or with renormalize p_e over the sum of the chosen ones,
  *   h_e = silu(gate_e X) * (up_e X),   Y = sum over the chosen e of q_e (w_out_e h_e).
  * 1 <= top_k <= E <= 1024, top_k <= 16.  A logit that is NaN makes the
- * token's row of Y NaN.  Any T >= 0; a launch takes BAKRON_MOE_TOKENS tokens,
- * so larger T run as several.  ws: device, 256-byte aligned,
+ * token's row of Y NaN.  Any T >= 0; BAKRON_MOE_TOKENS tokens go together (half
+ * as many in fp32), larger T run as several such groups.  ws: device, 256-byte aligned,
  * bakron_moe_workspace_size bytes. */
 enum { BAKRON_MOE_TOKENS = 32 };
 bakron_status bakron_moe_workspace_size(const bakron_packed* w_in, const bakron_packed* w_out,

@@ -35,7 +35,7 @@ EXPORTS = ["bakron_default_opts", "bakron_status_string", "bakron_version", "bak
 FACTORS_KFAC = 0
 FACTORS_SHAMPOO = 1
 F32, BF16, F16 = 0, 1, 2      # bakron_dtype
-MOE_TOKENS = 32               # tokens of one bakron_moe launch
+MOE_TOKENS = 32               # tokens that bakron_moe takes together
 
 
 class PhaseTimes(ctypes.Structure):

@@ -40,11 +40,13 @@ struct FewArgs {
   int vec_ok;    // rows of x are 16-byte aligned
 };
 
-constexpr int kDepth = 4;   // chunks in flight per warp
+// Slots of two chunks per warp.
+template <int RT>
+constexpr int kDepth = RT == 1 ? 3 : 2;
 
 template <typename TX, typename H, int TERMS, int NT, int RT, int NS>
 __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_constant__ FewArgs a) {
-  using P = qm::Pipe<RT, NS, kDepth>;
+  using P = qm::Pipe<RT, NS, kDepth<RT>>;
   constexpr int ROWS = 16 * RT, OUT = NT * 8 * ROWS;
   extern __shared__ __align__(16) uint8_t dsm[];      // the warps' chunks, then staged activations
   __shared__ float red[kWarps][NT * 8][ROWS];
@@ -65,9 +67,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
   qm::tile_ref<RT>(tile, a.w, 0, rows, lane);
   P pipe;
   pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
-  int ahead = c_lo + warp;
+  // the warps take the chunks two by two, in turn
+  int ahead = c_lo + 2 * warp;
+  auto issue = [&]() {
+    pipe.issue(a.w, tile, ahead, max(0, min(2, c_hi - ahead)), lane);
+    ahead += 2 * kWarps;
+  };
 #pragma unroll
-  for (int p = 0; p < kDepth - 1; ++p, ahead += kWarps) pipe.issue(a.w, tile, ahead, ahead < c_hi, lane);
+  for (int p = 0; p < kDepth<RT> - 1; ++p) issue();
 
   int col[NT];
 #pragma unroll
@@ -81,15 +88,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
       for (int i = 0; i < 4; ++i) tot[r][j][i] = 0.f;
 
   uint32_t z[RT][2][NS];
-  if (c_lo + warp < c_hi) qm::load_zeros<RT, NS>(z, a.w, tile, c_lo + warp);
+  if (c_lo + 2 * warp < c_hi) qm::load_zeros<RT, NS>(z, a.w, tile, c_lo + 2 * warp);
   qm::Chunk16<NS> f[RT];
-  // the chunk c of this warp: next copies on their way, then its products
-  auto step = [&](int c, auto fetch) {
-    pipe.issue(a.w, tile, ahead, ahead < c_hi, lane);
-    ahead += kWarps;
-    pipe.take(f, lane);
+  // chunk c, half h of the slot at hand; its successor's zero points are on their way
+  auto half = [&](int c, int h, auto fetch) {
+    pipe.take(f, h, lane);
     qm::set_zeros<RT, NS>(f, z);
-    if (c + kWarps < c_hi) qm::load_zeros<RT, NS>(z, a.w, tile, c + kWarps);
+    const int next = h == 0 && c + 1 < c_hi ? c + 1 : c - h + 2 * kWarps;
+    if (next < c_hi) qm::load_zeros<RT, NS>(z, a.w, tile, next);
     qm::chunk_product<H, TERMS, RT, NT, NS>(tot, f, a.w.zero != nullptr, a.w.zu, fetch);
   };
   if (TERMS == 1 && a.slab == 0) {
@@ -97,32 +103,49 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
 #pragma unroll
     for (int j = 0; j < NT; ++j) xr[j] = x + (int64_t)col[j] * a.w.n + 8 * (lane & 3);
     const int whole = (int)(a.w.n / 128);       // chunks without padding
-    for (int c = c_lo + warp; c < c_hi; c += kWarps) {
-      if (c < whole) {
-        step(c, [&](int j, int, int s) { return __ldg(reinterpret_cast<const uint4*>(xr[j] + c * 128 + 32 * s)); });
-      } else {
-        step(c, [&](int j, int, int s) {
-          const int k = c * 128 + 32 * s;
-          return k + 8 * (lane & 3) < a.w.n ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k)) : make_uint4(0, 0, 0, 0);
-        });
+    for (int c = c_lo + 2 * warp; c < c_hi; c += 2 * kWarps) {
+      issue();
+      pipe.wait();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (c + h < min(whole, c_hi)) {
+          half(c + h, h, [&](int j, int, int s) {
+            return __ldg(reinterpret_cast<const uint4*>(xr[j] + (c + h) * 128 + 32 * s));
+          });
+        } else if (c + h < c_hi) {
+          half(c + h, h, [&](int j, int, int s) {
+            const int k = (c + h) * 128 + 32 * s;
+            return k + 8 * (lane & 3) < a.w.n ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k))
+                                              : make_uint4(0, 0, 0, 0);
+          });
+        }
       }
+      pipe.release();
     }
   } else {
     uint8_t* xs = dsm + kWarps * P::kBytes;
-    const uint32_t pitch = qm::x_pitch(a.slab);
+    const uint32_t pitch = qm::x_pitch(a.slab);      // slab is even
     const uint32_t plane = pitch * (uint32_t)cols;
-    int c = c_lo + warp;
+    int c = c_lo + 2 * warp;
     for (int s0 = c_lo; s0 < c_hi; s0 += a.slab) {
       const int s1 = min(s0 + a.slab, c_hi);
       if (s0 != c_lo) __syncthreads();
       qm::stage_x<TX, TERMS>(xs, plane, pitch, x, a.w.n, cols, [](int r) { return (int64_t)r; }, s0 * 128,
                              s1 - s0, a.w.n, a.vec_ok != 0);
       __syncthreads();
-      for (; c < s1; c += kWarps) {
-        const uint8_t* xc = xs + (c - s0) * 256 + (lane & 3) * 16;
-        step(c, [&](int j, int q, int s) {
-          return *reinterpret_cast<const uint4*>(xc + q * plane + (uint32_t)col[j] * pitch + s * 64);
-        });
+      for (; c < s1; c += 2 * kWarps) {
+        issue();
+        pipe.wait();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (c + h < s1) {
+            const uint8_t* xc = xs + (c + h - s0) * 256 + (lane & 3) * 16;
+            half(c + h, h, [&](int j, int q, int s) {
+              return *reinterpret_cast<const uint4*>(xc + q * plane + (uint32_t)col[j] * pitch + s * 64);
+            });
+          }
+        }
+        pipe.release();
       }
     }
   }
@@ -170,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
 template <typename TX, typename H, int TERMS, int NT, int RT, int NS>
 cudaError_t run(const LinearArgs& a, cudaStream_t s) {
   auto k = linear_few_kernel<TX, H, TERMS, NT, RT, NS>;
-  constexpr size_t ring = kWarps * qm::Pipe<RT, NS, kDepth>::kBytes;
+  constexpr size_t ring = kWarps * qm::Pipe<RT, NS, kDepth<RT>>::kBytes;
   FewArgs f;
   f.w = a.w;
   f.x = a.x;
@@ -179,8 +202,8 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
   f.vec_ok = aligned_to(a.x, 16) && (a.w.n * sizeof(TX)) % 16 == 0;
   const int64_t tiles = (a.w.mp + 16 * RT - 1) / (16 * RT);
   const int64_t tt = (a.T + 8 * NT - 1) / (8 * NT);   // T <= kFewTokens: a handful
-  // blocks per row tile: enough that every SM has one or two, at least two
-  // chunks a warp
+  // blocks per row tile: enough that every SM has one or two, at least one slot
+  // a warp
   f.S = 1;
   while (f.S < 8 && tiles * tt * f.S < sm_count() && a.w.nc >= (int64_t)2 * f.S * kWarps) f.S *= 2;
   size_t smem = ring;
@@ -188,7 +211,7 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
   if (TERMS != 1 || !f.vec_ok) {
     const int cols = (int)std::min<int64_t>(8 * NT, a.T);
     const int64_t slab = (kMaxXBytes / (uint32_t)(TERMS * cols) - 64) / 256;
-    f.slab = (int)std::max<int64_t>(1, std::min<int64_t>(slab, (a.w.nc + f.S - 1) / f.S));
+    f.slab = (int)std::max<int64_t>(2, std::min<int64_t>(slab, (a.w.nc + f.S - 1) / f.S + 1) / 2 * 2);
     smem += (size_t)qm::x_pitch(f.slab) * TERMS * cols;
   }
   static std::atomic<unsigned long long> done;

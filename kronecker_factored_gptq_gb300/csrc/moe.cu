@@ -45,11 +45,12 @@ constexpr int kRouteWarps = 8, kRouteTokens = 8;
 constexpr int kMaxTokens = BAKRON_MOE_TOKENS;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 1024;
+constexpr int kDepthIn = 2, kDepthOut = 2;      // slots of two chunks per warp
 template <int NS>
-constexpr int kDepthIn = NS == 1 ? 4 : 3;    // chunk slots per warp
-constexpr int kDepthOut = 3;
-constexpr uint32_t kInX = 64 * 1024;     // shared memory for an expert's tokens
-constexpr uint32_t kOutX = 32 * 1024;    // and for their h (one chunk of 32 tokens fits)
+constexpr uint32_t kInX = NS == 1 ? 64 * 1024 : 48 * 1024;     // shared memory for an expert's tokens
+constexpr uint32_t kOutX = 24 * 1024;    // and for their h
+// Tokens of one launch: fp32 ones take three times the room.
+constexpr int launch_tokens(int terms) { return terms == 1 ? kMaxTokens : kMaxTokens / 2; }
 
 struct MoeArgs {
   const void* x;        // T x d
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
   constexpr int kWarps = kInWarps, kThreads = kInThreads;
   extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ Routing R;
-  using P = qm::Pipe<2, NS, kDepthIn<NS>>;
+  using P = qm::Pipe<2, NS, kDepthIn>;
   // the routing's arrays end before the chunks' slots and the tokens begin
   uint8_t* xs = dsm + kWarps * P::kBytes;
   float* logits = reinterpret_cast<float*>(dsm);               // [T][E]
@@ -276,10 +277,11 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
   const int64_t items = (int64_t)na * tiles;
   const int i_lo = (int)(items * blockIdx.x / gridDim.x), i_hi = (int)(items * (blockIdx.x + 1) / gridDim.x);
   const int nc = (int)a.wi.nc;
+  const int np = (nc + 1) / 2;             // pairs of chunks
   int G = 1;
-  while (G < kWarps && (i_hi - i_lo) * 2 * G <= kWarps && nc >= 2 * G) G *= 2;
+  while (G < kWarps && (i_hi - i_lo) * 2 * G <= kWarps && np >= 2 * G) G *= 2;
   const int group = warp / G, part = warp % G, groups = kWarps / G;
-  const int c_lo = nc * part / G, c_hi = nc * (part + 1) / G;
+  const int c_lo = np * part / G * 2, c_hi = min(nc, np * (part + 1) / G * 2);
 
   P pipe;
   pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
@@ -308,8 +310,10 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
   };
   settle();
   auto issue = [&]() {
-    pipe.issue(a.wi, t_ahead, c_ahead, it_ahead >= 0, lane);
-    if (it_ahead >= 0 && ++c_ahead == c_hi) {
+    const int n = it_ahead >= 0 ? min(2, c_hi - c_ahead) : 0;
+    pipe.issue(a.wi, t_ahead, c_ahead, n, lane);
+    c_ahead += n;
+    if (it_ahead >= 0 && c_ahead == c_hi) {
       c_ahead = c_lo;
       it_ahead = next_item(it_ahead, seg_a_end);
       if (it_ahead < 0) {
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
   };
   __syncthreads();             // the routing's arrays are done with
 #pragma unroll
-  for (int p = 0; p < kDepthIn<NS> - 1; ++p) issue();
+  for (int p = 0; p < kDepthIn - 1; ++p) issue();
 
   const uint32_t xs_addr = (uint32_t)__cvta_generic_to_shared(xs);
   for (int seg = i_lo; seg < i_hi;) {
@@ -332,7 +336,8 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
     const uint32_t who = R.who[ai];
     const int cnt = __popc(who), live = (cnt + 7) / 8;
     // the expert's tokens: all columns at once, or slab by slab
-    const int slab = min(nc, (int)((kInX / (uint32_t)(TERMS * cnt) - 64) / 256));
+    const int room = (int)((kInX<NS> / (uint32_t)(TERMS * cnt) - 64) / 256);
+    const int slab = room >= nc ? nc : room & ~1;
     const uint32_t pitch = qm::x_pitch(slab), plane = pitch * (uint32_t)cnt;
     auto stage = [&](int s0) {
       qm::stage_x<TX, TERMS>(xs, plane, pitch, static_cast<const TX*>(a.x), a.d, cnt,
@@ -373,41 +378,47 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
           __syncthreads();
         }
         if (on) {
+          // slabs are even and so is each warp's first chunk: a slot never straddles two
           const int s1 = min(s0 + slab, c_hi);
-          for (int c = max(s0, c_lo); c < s1; ++c) {
-            qm::Chunk16<NS> f[2];
+          for (int c = max(s0, c_lo); c < s1; c += 2) {
             issue();
-            pipe.take(f, lane);
-            qm::set_zeros<2, NS>(f, z);
-            if (c + 1 < c_hi) qm::load_zeros<2, NS>(z, a.wi, t_now, c + 1);
-            const uint32_t xc = (uint32_t)(c - s0) * 256;
-            qm::chunk_product<H, TERMS, 2, NT, NS>(
-                tot, f, a.wi.zero != nullptr, a.wi.zu,
-                [&](int j, int q, int s) { return qm::lds128(col[j] + q * plane + xc + s * 64); });
+            pipe.wait();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (c + h < s1) {
+                qm::Chunk16<NS> f[2];
+                pipe.take(f, h, lane);
+                qm::set_zeros<2, NS>(f, z);
+                if (c + h + 1 < c_hi) qm::load_zeros<2, NS>(z, a.wi, t_now, c + h + 1);
+                const uint32_t xc = (uint32_t)(c + h - s0) * 256;
+                qm::chunk_product<H, TERMS, 2, NT, NS>(
+                    tot, f, a.wi.zero != nullptr, a.wi.zu,
+                    [&](int j, int q, int s) { return qm::lds128(col[j] + q * plane + xc + s * 64); });
+              }
+            }
+            pipe.release();
           }
         }
       }
       // the group's sums of gate and up (thread: rows lane / 4 and + 8, columns
       // 2 (lane & 3) and + 1 of each column tile); the joins use the tokens' area
       if (G > 1) {
-        __syncthreads();
-        float* mine = reinterpret_cast<float*>(xs) + (size_t)warp * (2 * NT * 4 * 32) + lane;
+        float* mine = reinterpret_cast<float*>(xs) + (size_t)warp * (NT * 4 * 32) + lane;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 2; ++q) {
+          __syncthreads();
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mine[((q * NT + j) * 4 + i) * 32] = tot[q][j][i];
-        __syncthreads();
-        if (part == 0) {
-          for (int w = 1; w < G; ++w) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int i = 0; i < 4; ++i) mine[(j * 4 + i) * 32] = tot[q][j][i];
+          __syncthreads();
+          if (part == 0) {
+            for (int w = 1; w < G; ++w) {
 #pragma unroll
               for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  tot[q][j][i] += mine[(size_t)w * (2 * NT * 4 * 32) + ((q * NT + j) * 4 + i) * 32];
+                for (int i = 0; i < 4; ++i) tot[q][j][i] += mine[(size_t)w * (NT * 4 * 32) + (j * 4 + i) * 32];
+            }
           }
         }
         if (rounds > 1) {      // the tokens are needed again
@@ -467,21 +478,34 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
   const int u0 = (int)((int64_t)units * rank / S), u1 = (int)((int64_t)units * (rank + 1) / S);
   for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) sums[i] = 0.f;
 
+  // chunks of an expert's h that are staged at a time, of `part` chunks in all:
+  // an even number, unless it is all of them or there is room for one only
+  auto slab_of = [&](int ai, int part) {
+    const int room = (int)((kOutX / (uint32_t)(HT * __popc(a.who[ai])) - 64) / 256);
+    return room >= part ? part : max(1, room & ~1);
+  };
   const int64_t rows[2] = {row0 + 32 * warp, row0 + 32 * warp + 16};
   P pipe;
   pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
   qm::TileRef<2> t_ahead, t_now;
   int u_ahead = u0, ai_ahead = u0 / nc, c_ahead = u0 - ai_ahead * nc;
   if (u0 < u1) qm::tile_ref<2>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
+  // two chunks at a time, fewer at the end of an expert's part of the run or of
+  // what is staged of its h
+  int slab_ahead = u0 < u1 ? slab_of(ai_ahead, min(nc, c_ahead + (u1 - u0)) - c_ahead) : 0;
+  int left = slab_ahead;                                    // of the slab
   auto issue = [&]() {
-    pipe.issue(a.wo, t_ahead, c_ahead, u_ahead < u1, lane);
-    if (u_ahead < u1) {
-      ++u_ahead;
-      if (++c_ahead == nc && u_ahead < u1) {
-        c_ahead = 0;
-        ++ai_ahead;
-        qm::tile_ref<2>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
-      }
+    const int n = u_ahead < u1 ? min(min(2, left), min(u1 - u_ahead, nc - c_ahead)) : 0;
+    pipe.issue(a.wo, t_ahead, c_ahead, n, lane);
+    u_ahead += n;
+    c_ahead += n;
+    left -= n;
+    if (left == 0) left = slab_ahead;
+    if (n > 0 && c_ahead == nc && u_ahead < u1) {
+      c_ahead = 0;
+      ++ai_ahead;
+      left = slab_ahead = slab_of(ai_ahead, min(nc, u1 - u_ahead));
+      qm::tile_ref<2>(t_ahead, a.wo, a.active[1 + ai_ahead], rows, lane);
     }
   };
 #pragma unroll
@@ -494,7 +518,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
     const uint32_t who = a.who[ai];
     const int cnt = __popc(who), live = (cnt + 7) / 8;
     if (a.wo.zero) qm::tile_ref<2>(t_now, a.wo, a.active[1 + ai], rows, lane);
-    const int slab = min(c1 - c0, (int)((kOutX / (uint32_t)(HT * cnt) - 64) / 256));
+    const int slab = slab_of(ai, c1 - c0);
     const uint32_t pitch = qm::x_pitch(slab), plane = pitch * (uint32_t)cnt;
     auto chunks_of = [&](auto nt_) {
     constexpr int NT = decltype(nt_)::value;
@@ -523,16 +547,23 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
             *reinterpret_cast<const uint4*>(src + (int64_t)s0 * 256 + p * 16);
       }
       __syncthreads();
-      for (int c = s0; c < s1; ++c) {
-        qm::Chunk16<NS> f[2];
+      for (int c = s0; c < s1; c += 2) {
         issue();
-        pipe.take(f, lane);
-        qm::set_zeros<2, NS>(f, z);
-        if (c + 1 < c1) qm::load_zeros<2, NS>(z, a.wo, t_now, c + 1);
-        const uint32_t hc = (uint32_t)(c - s0) * 256;
-        qm::chunk_product<__nv_bfloat16, HT, 2, NT, NS>(
-            tot, f, a.wo.zero != nullptr, a.wo.zu,
-            [&](int j, int q, int s) { return qm::lds128(col[j] + q * plane + hc + s * 64); });
+        pipe.wait();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (c + h < s1) {
+            qm::Chunk16<NS> f[2];
+            pipe.take(f, h, lane);
+            qm::set_zeros<2, NS>(f, z);
+            if (c + h + 1 < c1) qm::load_zeros<2, NS>(z, a.wo, t_now, c + h + 1);
+            const uint32_t hc = (uint32_t)(c + h - s0) * 256;
+            qm::chunk_product<__nv_bfloat16, HT, 2, NT, NS>(
+                tot, f, a.wo.zero != nullptr, a.wo.zu,
+                [&](int j, int q, int s) { return qm::lds128(col[j] + q * plane + hc + s * 64); });
+          }
+        }
+        pipe.release();
       }
     }
     // to the tokens' sums; a warp's rows are its own
@@ -611,9 +642,11 @@ template <typename TX, typename H, int TERMS, int HT, int NS, int NSO>
 cudaError_t run(MoeArgs& a, cudaStream_t s) {
   auto k1 = moe_in_kernel<TX, H, TERMS, HT, NS>;
   auto k2 = moe_out_kernel<TX, HT, NSO>;
-  constexpr size_t pipes = kInWarps * (size_t)qm::Pipe<2, NS, kDepthIn<NS>>::kBytes;
-  static_assert(kInWarps * 2 * (kMaxTokens / 8) * 4 * 32 * 4 <= kInX, "the joins fit the tokens' area");
-  constexpr size_t in_bytes = std::max(pipes + kInX, (size_t)(kMaxTokens + 1) * kMaxExperts * 4);
+  static_assert(kInX<NS> / (TERMS * launch_tokens(TERMS)) >= 2 * 256 + 64, "two chunks of every token fit");
+  static_assert(kOutX / (HT * launch_tokens(TERMS)) >= 256 + 64, "one chunk of every token's h fits");
+  constexpr size_t pipes = kInWarps * (size_t)qm::Pipe<2, NS, kDepthIn>::kBytes;
+  static_assert(kInWarps * (kMaxTokens / 8) * 4 * 32 * 4 <= kInX<NS>, "the joins fit the tokens' area");
+  constexpr size_t in_bytes = std::max(pipes + kInX<NS>, (size_t)(kMaxTokens + 1) * kMaxExperts * 4);
   const size_t out_bytes = kOutWarps * (size_t)qm::Pipe<2, NSO, kDepthOut>::kBytes + kOutX + (size_t)a.T * kOutRows * 4;
   static std::atomic<unsigned long long> done, done2;
   cudaError_t e = ensure_smem_limit((const void*)k1, in_bytes, done);
@@ -728,8 +761,9 @@ extern "C" bakron_status bakron_moe(const void* X, int64_t T, int dtype, const v
   a.arrived = reinterpret_cast<int*>(base + L.arrived);
   a.part = reinterpret_cast<float*>(base + L.part);
   a.row_groups = (int)((a.d + kOutRows - 1) / kOutRows);
-  for (int64_t t0 = 0; t0 < T; t0 += kMaxTokens) {
-    a.T = (int)std::min<int64_t>(kMaxTokens, T - t0);
+  const int64_t most = launch_tokens(dtype == BAKRON_F32 ? 3 : 1);
+  for (int64_t t0 = 0; t0 < T; t0 += most) {
+    a.T = (int)std::min<int64_t>(most, T - t0);
     a.x = static_cast<const uint8_t*>(X) + (size_t)(t0 * a.d) * es;
     a.y = static_cast<uint8_t*>(Y) + (size_t)(t0 * a.d) * es;
     a.h_plane = (int64_t)a.T * a.k * a.fp * 2;

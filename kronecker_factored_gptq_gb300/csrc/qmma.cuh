@@ -94,16 +94,18 @@ __device__ __forceinline__ void tile_ref(TileRef<RT>& t, const PackedView& w, in
   t.scale = w.scale + grid_row(w, e, min(row0[mine] + (lane & 15), w.mp - 1));
 }
 
-// A warp's chunks in flight: D slots in shared memory, filled by asynchronous
-// copies D - 1 chunks ahead.  A thread copies the 16 bytes of codes that it
-// reads itself, so they need no synchronisation; only the scales, one row per
-// thread, pass between the lanes of the warp.
+// A warp's codes in flight: D slots in shared memory of two chunks each (two, so
+// that the addresses and counters of a step are paid once per 256 columns),
+// filled by asynchronous copies D - 1 slots ahead.  A thread copies the 16 bytes
+// of codes that it reads itself, so they need no synchronisation; only the
+// scales, one row per thread, pass between the lanes of the warp.
 template <int RT, int NS, int D>
 struct Pipe {
-  static constexpr uint32_t kSlot = RT * 2 * 512 + NS * 128;
-  static constexpr uint32_t kBytes = D * kSlot;     // per warp
-  uint32_t base;                                    // of the warp
-  int fill = 0, read = 0;
+  static constexpr uint32_t kHalf = RT * 2 * 512 + NS * 128;   // one chunk
+  static constexpr uint32_t kSlot = 2 * kHalf;
+  static constexpr uint32_t kBytes = D * kSlot;                // per warp
+  uint32_t base;                                               // of the warp
+  uint32_t fill = 0, read = 0;                                 // byte offsets of slots
 
   static __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -111,48 +113,53 @@ struct Pipe {
   static __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
   }
-  // Start chunk c of the tiles; a call without one (live false) keeps the count.
-  __device__ __forceinline__ void issue(const PackedView& w, const TileRef<RT>& t, int64_t c, bool live, int lane) {
-    if (live) {
-      const uint32_t slot = base + (uint32_t)fill * kSlot;
+  // Start chunks c .. c + n - 1 (n 0, 1 or 2) of the tiles; n 0 keeps the count.
+  __device__ __forceinline__ void issue(const PackedView& w, const TileRef<RT>& t, int c, int n, int lane) {
+    const uint32_t slot = base + fill;
+    const int64_t at = (int64_t)c * kBlockBytes;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+    for (int h = 0; h < 2; ++h) {
+      if (h < n) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          copy16(slot + (uint32_t)((r * 2 + i) * 512 + lane * 16), t.codes[r][i] + c * kBlockBytes);
-      if (lane < 16 * RT) {
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-          copy4(slot + RT * 1024 + (uint32_t)(s * 128 + lane * 4),
-                t.scale + grid_group(w, (uint32_t)(c * 128 + 32 * s)) * 16);
+          for (int i = 0; i < 2; ++i)
+            copy16(slot + h * kHalf + (uint32_t)((r * 2 + i) * 512 + lane * 16), t.codes[r][i] + at + h * kBlockBytes);
+        if (lane < 16 * RT) {
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+            copy4(slot + h * kHalf + RT * 1024 + (uint32_t)(s * 128 + lane * 4),
+                  t.scale + grid_group(w, (uint32_t)((c + h) * 128 + 32 * s)) * 16);
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (++fill == D) fill = 0;
+    fill = fill + kSlot == kBytes ? 0 : fill + kSlot;
   }
-  // The oldest chunk, once its copies have landed.
-  __device__ __forceinline__ void take(Chunk16<NS> (&f)[RT], int lane) {
+  // Wait for the oldest slot.
+  __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
     __syncwarp();
-    const uint32_t slot = base + (uint32_t)read * kSlot;
+  }
+  // Its chunk h (0 or 1).
+  __device__ __forceinline__ void take(Chunk16<NS> (&f)[RT], int h, int lane) const {
+    const uint32_t slot = base + read + h * kHalf;
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        uint4& v = f[r].w[i];
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(slot + (uint32_t)((r * 2 + i) * 512 + lane * 16))
-                     : "memory");
+        f[r].w[i] = lds128(slot + (uint32_t)((r * 2 + i) * 512 + lane * 16));
 #pragma unroll
         for (int s = 0; s < NS; ++s)
           asm volatile("ld.shared.f32 %0, [%1];"
                        : "=f"(f[r].s[i][s])
-                       : "r"(slot + RT * 1024 + (uint32_t)(s * 128 + (r * 16 + i * 8 + (lane >> 2)) * 4))
-                       : "memory");
+                       : "r"(slot + RT * 1024 + (uint32_t)(s * 128 + (r * 16 + i * 8 + (lane >> 2)) * 4)));
       }
-    if (++read == D) read = 0;
-    __syncwarp();     // the slot's scales have been read by every lane
+  }
+  // The slot may be filled again.
+  __device__ __forceinline__ void release() {
+    read = read + kSlot == kBytes ? 0 : read + kSlot;
+    __syncwarp();     // its scales have been read by every lane
   }
 };
 
