@@ -7,11 +7,14 @@
 // reads two and writes one.  A row stays in registers between its reductions
 // (the variance from the deviations, not from a difference of two large
 // sums), so nothing is read twice: one warp per row while a warp's registers
-// hold it, else one block per row.  A thread owns the same columns of
-// every row that its block takes, so the sums over rows of dgamma and dbeta
-// grow in registers and leave the block once, into a row of the workspace; a
-// second launch adds the blocks' rows in a fixed order (no atomics, so the
-// bits do not depend on the run).
+// hold it, else one block per row.  A block's barriers leave the memory idle unless
+// the rows after the one at hand are on their way, so the block-per-row kernels
+// copy them asynchronously into shared memory, a few rows ahead; a thread
+// copies what it reads itself, so the copies need no barrier.  A thread owns the
+// same columns of every row that its block takes, so the sums over rows of
+// dgamma and dbeta grow in registers and leave the block once, into a row of the
+// workspace; a second launch adds the blocks' rows in a fixed order (no atomics,
+// so the bits do not depend on the run).
 #include <algorithm>
 
 #include "packed.cuh"
@@ -32,30 +35,39 @@ struct NormArgs {
   const float* mean_in;
   const float* rstd_in;
   float* part;           // [blocks][2][d], NULL without weight gradients
+  int depth;             // slots of rows in shared memory
 };
 
 constexpr int kMaxWarps = 32;
 
-// Sum of (a, b) over the threads that share a row: the warp, or the block.
+// Sums of N values over the threads that share a row: the warp, or the block.
 // `slot` alternates between calls, so one barrier per call is enough: a
 // slot is written again only after the barrier of the call in between.
-template <bool kBlock>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float2 (*red)[kMaxWarps], int& slot) {
+template <bool kBlock, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[2][kMaxWarps], int& slot) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   if constexpr (kBlock) {
-    if ((threadIdx.x & 31) == 0) red[slot][threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const int nw = blockDim.x >> 5;
-    a = b = 0.f;
-    for (int w = 0; w < nw; ++w) {
-      const float2 v = red[slot][w];
-      a += v.x;
-      b += v.y;
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) red[slot][k][threadIdx.x >> 5] = v[k];
     }
+    __syncthreads();
+    // every warp adds the warps' sums in the same way
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = lane < warps ? red[slot][k][lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o < warps) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
     slot ^= 1;
   }
 }
@@ -66,9 +78,95 @@ struct alignas(sizeof(TX) * V) Vec {
   TX v[V];
 };
 
-template <typename TX, int V, int NV, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? 1024 : 256) norm_kernel(const __grid_constant__ NormArgs p) {
-  __shared__ float2 red[2][kMaxWarps];
+// The rows of a block (or warp) from memory, V elements at a time: loaded when
+// asked for (kAhead false), or copied to shared memory `depth` - 1 rows ahead.
+template <typename TX, int V, int NV, int ARRAYS, bool kAhead>
+struct Rows {
+  const TX* src[ARRAYS];
+  int64_t d, step, T;
+  int64_t next;             // next row to copy
+  uint32_t slot, bytes;     // this thread's place in a slot; bytes of all slots
+  uint32_t fill = 0, read = 0;
+  int tid, tpr, depth;
+
+  __device__ __forceinline__ uint32_t slot_bytes() const { return (uint32_t)(ARRAYS * NV * tpr) * 16u; }
+  __device__ __forceinline__ void copy() {
+    if (next < T) {
+#pragma unroll
+      for (int k = 0; k < ARRAYS; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (tid + i * tpr) * V;
+          if (c < (int)d)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             slot + fill + (uint32_t)((k * NV + i) * tpr) * 16u),
+                         "l"(src[k] + next * d + c)
+                         : "memory");
+        }
+      next += step;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    fill = fill + slot_bytes() == bytes ? 0 : fill + slot_bytes();
+  }
+  __device__ __forceinline__ void start(int64_t first, void* smem) {
+    if constexpr (kAhead) {
+      next = first;
+      slot = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)tid * 16u;
+      bytes = slot_bytes() * (uint32_t)depth;
+      for (int p = 0; p < depth - 1; ++p) copy();
+    }
+  }
+  // Row `row`, the successor of the one asked for before.
+  __device__ __forceinline__ void get(int64_t row, Vec<TX, V> (&v)[ARRAYS][NV]) {
+    if constexpr (kAhead) {
+      copy();
+      // `depth` is 1 to 4
+      if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+      else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+#pragma unroll
+    for (int k = 0; k < ARRAYS; ++k)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * V;
+        if (c < (int)d) {
+          if constexpr (kAhead) {
+            uint4 u;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                         : "r"(slot + read + (uint32_t)((k * NV + i) * tpr) * 16u)
+                         : "memory");
+            v[k][i] = *reinterpret_cast<const Vec<TX, V>*>(&u);
+          } else {
+            v[k][i] = *reinterpret_cast<const Vec<TX, V>*>(src[k] + row * d + c);
+          }
+        }
+      }
+    if constexpr (kAhead) read = read + slot_bytes() == bytes ? 0 : read + slot_bytes();
+  }
+};
+
+// gamma and beta of V columns (1 and 0 where there are none).
+template <int V>
+__device__ __forceinline__ void params(Vec<float, V>& g, Vec<float, V>& b, const NormArgs& p, int c) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    g.v[e] = 1.f;
+    b.v[e] = 0.f;
+  }
+  if (c < (int)p.d) {
+    if (p.gamma) g = *reinterpret_cast<const Vec<float, V>*>(p.gamma + c);
+    if (p.beta) b = *reinterpret_cast<const Vec<float, V>*>(p.beta + c);
+  }
+}
+
+template <typename TX, int V, int NV, bool kBlock, int MAXB>
+__global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ NormArgs p) {
+  constexpr bool kAhead = kBlock && V > 1;
+  extern __shared__ __align__(16) uint8_t dsm[];
+  __shared__ float red[2][2][kMaxWarps];
   int slot = 0;
   const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
   const int tpr = kBlock ? blockDim.x : 32;
@@ -76,63 +174,77 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) norm_kernel(const __grid_
   const int64_t row0 = (int64_t)blockIdx.x * rows_at_once + (kBlock ? 0 : threadIdx.x >> 5);
   const int64_t step = (int64_t)gridDim.x * rows_at_once;
   const float inv_d = 1.f / (float)p.d;
+  const int d = (int)p.d;
+  Rows<TX, V, NV, 1, kAhead> rows;
+  rows.src[0] = static_cast<const TX*>(p.x);
+  rows.d = p.d;
+  rows.step = step;
+  rows.T = p.T;
+  rows.tid = tid;
+  rows.tpr = tpr;
+  rows.depth = p.depth;
+  rows.start(row0, dsm);
+  // gamma and beta stay in registers when there is room
+  constexpr bool kKeep = NV * V <= 16;
+  Vec<float, V> gk[kKeep ? NV : 1], bk[kKeep ? NV : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) params(gk[i], bk[i], p, (tid + i * tpr) * V);
+  }
   for (int64_t row = row0; row < p.T; row += step) {
-    const TX* x = static_cast<const TX*>(p.x) + row * p.d;
     TX* y = static_cast<TX*>(p.y) + row * p.d;
+    Vec<TX, V> v[1][NV];
+    rows.get(row, v);
     float f[NV][V];
-    float sum = 0.f, sq = 0.f, unused = 0.f;
+    float sum[1] = {0.f}, sq[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(tid + i * tpr) * V;
-      if (c < p.d) {
-        const Vec<TX, V> v = *reinterpret_cast<const Vec<TX, V>*>(x + c);
+      if ((tid + i * tpr) * V < d) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          f[i][e] = to_float(v.v[e]);
-          sum += f[i][e];
+          f[i][e] = to_float(v[0][i].v[e]);
+          sum[0] += f[i][e];
         }
       }
     }
-    row_sum2<kBlock>(sum, unused, red, slot);
-    const float mu = sum * inv_d;
+    row_sums<kBlock, 1>(sum, red, slot);
+    const float mu = sum[0] * inv_d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(tid + i * tpr) * V;
-      if (c < p.d) {
+      if ((tid + i * tpr) * V < d) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           f[i][e] -= mu;
-          sq = fmaf(f[i][e], f[i][e], sq);
+          sq[0] = fmaf(f[i][e], f[i][e], sq[0]);
         }
       }
     }
-    row_sum2<kBlock>(sq, unused, red, slot);
-    const float r = 1.f / sqrtf(sq * inv_d + p.eps);
+    row_sums<kBlock, 1>(sq, red, slot);
+    const float r = rsqrtf(sq[0] * inv_d + p.eps);
     if (tid == 0) {
       if (p.mean) p.mean[row] = mu;
       if (p.rstd) p.rstd[row] = r;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(tid + i * tpr) * V;
-      if (c < p.d) {
+      const int c = (tid + i * tpr) * V;
+      if (c < d) {
+        if constexpr (!kKeep) params(gk[0], bk[0], p, c);
+        const Vec<float, V>&g = gk[kKeep ? i : 0], &b = bk[kKeep ? i : 0];
         Vec<TX, V> o;
-        Vec<float, V> g, b;
-        if (p.gamma) g = *reinterpret_cast<const Vec<float, V>*>(p.gamma + c);
-        if (p.beta) b = *reinterpret_cast<const Vec<float, V>*>(p.beta + c);
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          o.v[e] = from_float<TX>(fmaf(f[i][e] * r, p.gamma ? g.v[e] : 1.f, p.beta ? b.v[e] : 0.f));
+        for (int e = 0; e < V; ++e) o.v[e] = from_float<TX>(fmaf(f[i][e] * r, g.v[e], b.v[e]));
         *reinterpret_cast<Vec<TX, V>*>(y + c) = o;
       }
     }
   }
 }
 
-template <typename TX, int V, int NV, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? 1024 : 256)
-    norm_grad_kernel(const __grid_constant__ NormArgs p) {
-  __shared__ float2 red[2][kMaxWarps];
+template <typename TX, int V, int NV, bool kBlock, int MAXB>
+__global__ void __launch_bounds__(MAXB) norm_grad_kernel(const __grid_constant__ NormArgs p) {
+  constexpr bool kAhead = kBlock && V > 1;
+  extern __shared__ __align__(16) uint8_t dsm[];
+  __shared__ float red[2][2][kMaxWarps];
   int slot = 0;
   const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
   const int tpr = kBlock ? blockDim.x : 32;
@@ -140,77 +252,117 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256)
   const int64_t lead = (int64_t)blockIdx.x * rows_at_once + (kBlock ? 0 : threadIdx.x >> 5);
   const int64_t step = (int64_t)gridDim.x * rows_at_once;
   const float inv_d = 1.f / (float)p.d;
+  const int d = (int)p.d;
+  constexpr bool kKeep = NV * V <= 16;
+  Vec<float, V> gk[kKeep ? NV : 1], unused;
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) params(gk[i], unused, p, (tid + i * tpr) * V);
+  }
   float dg[NV][V], db[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) dg[i][e] = db[i][e] = 0.f;
+  Rows<TX, V, NV, 2, kAhead> rows;
+  rows.src[0] = static_cast<const TX*>(p.x);
+  rows.src[1] = static_cast<const TX*>(p.dy);
+  rows.d = p.d;
+  rows.step = step;
+  rows.T = p.T;
+  rows.tid = tid;
+  rows.tpr = tpr;
+  rows.depth = p.depth;
+  rows.start(lead, dsm);
+  float mu_next = 0.f, r_next = 0.f;
+  if (lead < p.T) {
+    mu_next = p.mean_in[lead];
+    r_next = p.rstd_in[lead];
+  }
   for (int64_t row = lead; row < p.T; row += step) {
-    const TX* x = static_cast<const TX*>(p.x) + row * p.d;
-    const TX* dy = static_cast<const TX*>(p.dy) + row * p.d;
     TX* dx = static_cast<TX*>(p.y) + row * p.d;
-    const float mu = p.mean_in[row], r = p.rstd_in[row];
-    Vec<TX, V> vx[NV], vy[NV];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(tid + i * tpr) * V;
-      if (c < p.d) {
-        vx[i] = *reinterpret_cast<const Vec<TX, V>*>(x + c);
-        vy[i] = *reinterpret_cast<const Vec<TX, V>*>(dy + c);
-      }
+    const float mu = mu_next, r = r_next;
+    if (row + step < p.T) {
+      mu_next = ld_ahead(p.mean_in + row + step);
+      r_next = ld_ahead(p.rstd_in + row + step);
     }
+    Vec<TX, V> v[2][NV];
+    rows.get(row, v);
+    float sums[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(tid + i * tpr) * V;
-      if (c < p.d) {
-        Vec<float, V> g;
-        if (p.gamma) g = *reinterpret_cast<const Vec<float, V>*>(p.gamma + c);
+      const int c = (tid + i * tpr) * V;
+      if (c < d) {
+        if constexpr (!kKeep) params(gk[0], unused, p, c);
+        const Vec<float, V>& g = gk[kKeep ? i : 0];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float h = (to_float(vx[i].v[e]) - mu) * r, d = to_float(vy[i].v[e]);
-          const float a = d * (p.gamma ? g.v[e] : 1.f);
-          s1 += a;
-          s2 = fmaf(a, h, s2);
-          dg[i][e] = fmaf(d, h, dg[i][e]);
-          db[i][e] += d;
+          const float h = (to_float(v[0][i].v[e]) - mu) * r, w = to_float(v[1][i].v[e]);
+          const float a = w * g.v[e];
+          sums[0] += a;
+          sums[1] = fmaf(a, h, sums[1]);
+          dg[i][e] = fmaf(w, h, dg[i][e]);
+          db[i][e] += w;
         }
       }
     }
-    row_sum2<kBlock>(s1, s2, red, slot);
-    s1 *= inv_d;
-    s2 *= inv_d;
+    row_sums<kBlock, 2>(sums, red, slot);
+    // dX = r a - (r m1) - h (r m2): three constants of the row
+    const float m1 = r * (sums[0] * inv_d), m2 = r * (sums[1] * inv_d);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(tid + i * tpr) * V;
-      if (c < p.d) {
+      const int c = (tid + i * tpr) * V;
+      if (c < d) {
+        if constexpr (!kKeep) params(gk[0], unused, p, c);
+        const Vec<float, V>& g = gk[kKeep ? i : 0];
         Vec<TX, V> o;
-        Vec<float, V> g;
-        if (p.gamma) g = *reinterpret_cast<const Vec<float, V>*>(p.gamma + c);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float h = (to_float(vx[i].v[e]) - mu) * r;
-          const float a = to_float(vy[i].v[e]) * (p.gamma ? g.v[e] : 1.f);
-          o.v[e] = from_float<TX>(r * (a - s1 - h * s2));
+          const float h = (to_float(v[0][i].v[e]) - mu) * r;
+          const float a = to_float(v[1][i].v[e]) * g.v[e];
+          o.v[e] = from_float<TX>(fmaf(-h, m2, fmaf(r, a, -m1)));
         }
         *reinterpret_cast<Vec<TX, V>*>(dx + c) = o;
       }
     }
   }
-  if (p.part) {
-    // one row of partial sums per block, or per warp
-    float* o = p.part + lead * 2 * p.d;
+  if (!p.part) return;
+  float* o = p.part + (int64_t)blockIdx.x * 2 * p.d;
+  if constexpr (kBlock) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = (int64_t)(tid + i * tpr) * V;
       if (c < p.d) {
+        Vec<float, V> a, b;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          o[c + e] = dg[i][e];
-          o[p.d + c + e] = db[i][e];
+          a.v[e] = dg[i][e];
+          b.v[e] = db[i][e];
         }
+        *reinterpret_cast<Vec<float, V>*>(o + c) = a;
+        if constexpr (V == 1) o[p.d + c] = b.v[0];
+        else *reinterpret_cast<Vec<float, V>*>(o + p.d + c) = b;
       }
     }
+  } else {
+    // the warps of the block add theirs one after the other
+    float* sum = reinterpret_cast<float*>(dsm);     // [2][d]
+    for (int w = 0; w < rows_at_once; ++w) {
+      if ((int)(threadIdx.x >> 5) == w) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const int64_t c = (int64_t)(tid + i * tpr) * V + e;
+            if (c < p.d) {
+              sum[c] = (w ? sum[c] : 0.f) + dg[i][e];
+              sum[p.d + c] = (w ? sum[p.d + c] : 0.f) + db[i][e];
+            }
+          }
+      }
+      __syncthreads();
+    }
+    for (int64_t c = threadIdx.x; c < 2 * p.d; c += blockDim.x) o[c] = sum[c];
   }
 }
 
@@ -220,22 +372,22 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256)
 // column.
 template <typename TX>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormArgs p) {
-  __shared__ float2 red[2][kMaxWarps];
+  __shared__ float red[2][2][kMaxWarps];
   int slot = 0;
   const float inv_d = 1.f / (float)p.d;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
     const TX* x = static_cast<const TX*>(p.x) + row * p.d;
     TX* y = static_cast<TX*>(p.y) + row * p.d;
-    float sum = 0.f, sq = 0.f, unused = 0.f;
-    for (int64_t c = threadIdx.x; c < p.d; c += blockDim.x) sum += to_float(x[c]);
-    row_sum2<true>(sum, unused, red, slot);
-    const float mu = sum * inv_d;
+    float sum[1] = {0.f}, sq[1] = {0.f};
+    for (int64_t c = threadIdx.x; c < p.d; c += blockDim.x) sum[0] += to_float(x[c]);
+    row_sums<true, 1>(sum, red, slot);
+    const float mu = sum[0] * inv_d;
     for (int64_t c = threadIdx.x; c < p.d; c += blockDim.x) {
       const float v = to_float(x[c]) - mu;
-      sq = fmaf(v, v, sq);
+      sq[0] = fmaf(v, v, sq[0]);
     }
-    row_sum2<true>(sq, unused, red, slot);
-    const float r = 1.f / sqrtf(sq * inv_d + p.eps);
+    row_sums<true, 1>(sq, red, slot);
+    const float r = 1.f / sqrtf(sq[0] * inv_d + p.eps);
     if (threadIdx.x == 0) {
       if (p.mean) p.mean[row] = mu;
       if (p.rstd) p.rstd[row] = r;
@@ -248,7 +400,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
 
 template <typename TX>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const __grid_constant__ NormArgs p) {
-  __shared__ float2 red[2][kMaxWarps];
+  __shared__ float red[2][2][kMaxWarps];
   int slot = 0;
   const float inv_d = 1.f / (float)p.d;
   float* o = p.part ? p.part + (int64_t)blockIdx.x * 2 * p.d : nullptr;
@@ -259,20 +411,19 @@ __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const __grid_const
     const TX* dy = static_cast<const TX*>(p.dy) + row * p.d;
     TX* dx = static_cast<TX*>(p.y) + row * p.d;
     const float mu = p.mean_in[row], r = p.rstd_in[row];
-    float s1 = 0.f, s2 = 0.f;
+    float sums[2] = {0.f, 0.f};
     for (int64_t c = threadIdx.x; c < p.d; c += blockDim.x) {
       const float h = (to_float(x[c]) - mu) * r, d = to_float(dy[c]);
       const float a = d * (p.gamma ? p.gamma[c] : 1.f);
-      s1 += a;
-      s2 = fmaf(a, h, s2);
+      sums[0] += a;
+      sums[1] = fmaf(a, h, sums[1]);
       if (o) {
         o[c] = fmaf(d, h, o[c]);
         o[p.d + c] += d;
       }
     }
-    row_sum2<true>(s1, s2, red, slot);
-    s1 *= inv_d;
-    s2 *= inv_d;
+    row_sums<true, 2>(sums, red, slot);
+    const float s1 = sums[0] * inv_d, s2 = sums[1] * inv_d;
     for (int64_t c = threadIdx.x; c < p.d; c += blockDim.x) {
       const float h = (to_float(x[c]) - mu) * r;
       const float a = to_float(dy[c]) * (p.gamma ? p.gamma[c] : 1.f);
@@ -291,8 +442,8 @@ __global__ void __launch_bounds__(512) norm_join_kernel(const float* __restrict_
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;      // over 2 d columns
   float v = 0.f;
   if (c < 2 * d) {
-#pragma unroll 4
-    for (int64_t r = warp; r < rows; r += 16) v += part[r * 2 * d + c];
+#pragma unroll 8
+    for (int64_t r = warp; r < rows; r += 16) v += __ldcg(part + r * 2 * d + c);
   }
   red[warp][lane] = v;
   __syncthreads();
@@ -305,88 +456,100 @@ __global__ void __launch_bounds__(512) norm_join_kernel(const float* __restrict_
   }
 }
 
-// How a shape runs: vector width, vectors per thread, threads per row.
+// How a shape runs: vector width, vectors per thread, threads per row, and for
+// the block-per-row kernels the rows in flight.
 struct NormPlan {
   int v, nv;        // nv 0: the long-row kernels
   bool block;       // one block per row, else one warp
   int threads;      // of a block
+  int depth, per_sm;
+  size_t smem;
 };
 
-NormPlan norm_plan(int64_t d, int dtype, bool aligned) {
-  NormPlan q;
+// Shared memory per SM that the rows in flight may take (of 228 KB).
+constexpr size_t kRowBytes = 200 * 1024;
+
+NormPlan norm_plan(int64_t d, int dtype, bool aligned, int arrays) {
+  NormPlan q = {};
   const int wide = dtype == BAKRON_F32 ? 4 : 8;
   q.v = (aligned && d % wide == 0) ? wide : 1;
   const int64_t vecs = d / q.v;
   const int most = q.v == 1 ? 16 : 4;
+  q.per_sm = arrays == 1 ? 8 : 4;
   if (vecs <= 32 * most) {
-    q.block = false;
     q.threads = 256;
     q.nv = most;
+    q.smem = arrays == 2 ? (size_t)(2 * d) * 4 : 0;    // the warps' sums
     return q;
   }
   q.block = true;
   if (vecs > (int64_t)1024 * most) {
-    q.nv = 0;
     q.threads = 1024;
+    q.per_sm = 2;
     return q;
   }
-  q.nv = q.v == 1 ? most : vecs <= 256 ? 1 : vecs <= 512 ? 2 : 4;
+  q.nv = most;
   q.threads = (int)(((vecs + q.nv - 1) / q.nv + 31) / 32 * 32);
+  if (q.v == 1) {
+    q.per_sm = arrays == 1 ? 4 : 2;
+    return q;
+  }
+  // blocks per SM: what the registers allow (64, and 128 backward, a thread), fewer
+  // for long rows; as many rows ahead as fit beside that
+  const size_t row = (size_t)arrays * q.nv * q.threads * 16;
+  q.per_sm = std::max(1, std::min(8, (arrays == 1 ? 1024 : 512) / q.threads));
+  while (q.per_sm > 1 && row * 2 * q.per_sm > kRowBytes) --q.per_sm;
+  q.depth = (int)std::max<size_t>(1, std::min<size_t>(4, kRowBytes / (row * q.per_sm)));
+  q.smem = row * q.depth;
   return q;
 }
 
-int64_t fwd_blocks(const NormPlan& q, int64_t T) {
+int64_t norm_blocks(const NormPlan& q, int64_t T) {
   const int rows = q.block ? 1 : q.threads / 32;
-  return std::min<int64_t>((T + rows - 1) / rows, (int64_t)sm_count() * 32);
+  return std::min<int64_t>((T + rows - 1) / rows, (int64_t)sm_count() * q.per_sm);
 }
 
-// Blocks of the backward launch.  Upper bound in the workspace size: the
-// alignment of the pointers is not known there.
-constexpr int kGradBlocksPerSm = 2;
-int64_t grad_blocks(const NormPlan& q, int64_t T) {
-  const int rows = q.block ? 1 : q.threads / 32;
-  return std::min<int64_t>((T + rows - 1) / rows, (int64_t)sm_count() * kGradBlocksPerSm);
+template <typename K>
+cudaError_t launch_norm(K k, const NormPlan& q, const NormArgs& a, std::atomic<unsigned long long>& done,
+                        cudaStream_t s) {
+  if (q.smem > 46 * 1024) {      // beyond the default of 48 KB with the static part
+    const cudaError_t e = ensure_smem_limit((const void*)k, 226 * 1024, done);
+    if (e != cudaSuccess) return e;
+  }
+  count_launch();
+  k<<<(unsigned)norm_blocks(q, a.T), q.threads, q.smem, s>>>(a);
+  return cudaGetLastError();
 }
-int64_t grad_rows(const NormPlan& q, int64_t T) {
-  return grad_blocks(q, T) * (q.block ? 1 : q.threads / 32);
-}
+
+// Every variant of one direction: f(kernel) for the plan's.
+#define NORM_VARIANTS(KERNEL, LONG)                                                                    \
+  static std::atomic<unsigned long long> d[8];                                                         \
+  if (q.nv == 0) return launch_norm(LONG<TX>, q, a, d[0], s);                                          \
+  if (q.v == 1 && !q.block) return launch_norm(KERNEL<TX, 1, 16, false, 256>, q, a, d[1], s);          \
+  if (q.v == 1 && q.threads <= 512) return launch_norm(KERNEL<TX, 1, 16, true, 512>, q, a, d[2], s);   \
+  if (q.v == 1) return launch_norm(KERNEL<TX, 1, 16, true, 1024>, q, a, d[3], s);                      \
+  if (!q.block) return launch_norm(KERNEL<TX, W, 4, false, 256>, q, a, d[4], s);                       \
+  if (q.threads <= 448) return launch_norm(KERNEL<TX, W, 4, true, 448>, q, a, d[5], s);                \
+  return launch_norm(KERNEL<TX, W, 4, true, 1024>, q, a, d[6], s)
 
 template <typename TX, int W>
 cudaError_t run_fwd(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
-  const unsigned g = (unsigned)fwd_blocks(q, a.T);
-  count_launch();
-  if (q.nv == 0) norm_long_kernel<TX><<<g, q.threads, 0, s>>>(a);
-  else if (q.v == 1 && !q.block) norm_kernel<TX, 1, 16, false><<<g, q.threads, 0, s>>>(a);
-  else if (q.v == 1) norm_kernel<TX, 1, 16, true><<<g, q.threads, 0, s>>>(a);
-  else if (!q.block) norm_kernel<TX, W, 4, false><<<g, q.threads, 0, s>>>(a);
-  else if (q.nv == 1) norm_kernel<TX, W, 1, true><<<g, q.threads, 0, s>>>(a);
-  else if (q.nv == 2) norm_kernel<TX, W, 2, true><<<g, q.threads, 0, s>>>(a);
-  else norm_kernel<TX, W, 4, true><<<g, q.threads, 0, s>>>(a);
-  return cudaGetLastError();
+  NORM_VARIANTS(norm_kernel, norm_long_kernel);
 }
-
 template <typename TX, int W>
 cudaError_t run_grad(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
-  const unsigned g = (unsigned)grad_blocks(q, a.T);
-  count_launch();
-  if (q.nv == 0) norm_grad_long_kernel<TX><<<g, q.threads, 0, s>>>(a);
-  else if (q.v == 1 && !q.block) norm_grad_kernel<TX, 1, 16, false><<<g, q.threads, 0, s>>>(a);
-  else if (q.v == 1) norm_grad_kernel<TX, 1, 16, true><<<g, q.threads, 0, s>>>(a);
-  else if (!q.block) norm_grad_kernel<TX, W, 4, false><<<g, q.threads, 0, s>>>(a);
-  else if (q.nv == 1) norm_grad_kernel<TX, W, 1, true><<<g, q.threads, 0, s>>>(a);
-  else if (q.nv == 2) norm_grad_kernel<TX, W, 2, true><<<g, q.threads, 0, s>>>(a);
-  else norm_grad_kernel<TX, W, 4, true><<<g, q.threads, 0, s>>>(a);
-  return cudaGetLastError();
+  NORM_VARIANTS(norm_grad_kernel, norm_grad_long_kernel);
 }
 
 bool norm_args_ok(int64_t T, int64_t d, int dtype) {
   return dtype_ok(dtype) && T >= 0 && T <= (int64_t(1) << 31) && d >= 1 && d <= (int64_t(1) << 20);
 }
 
+// The alignment of the pointers and the type are not known to the size call.
 size_t grad_bytes(int64_t T, int64_t d) {
   int64_t rows = 0;
   for (int dt : {BAKRON_F32, BAKRON_BF16})
-    for (bool al : {false, true}) rows = std::max(rows, grad_rows(norm_plan(d, dt, al), T));
+    for (bool al : {false, true}) rows = std::max(rows, norm_blocks(norm_plan(d, dt, al, 2), T));
   return (size_t)(rows * 2 * d) * sizeof(float);
 }
 
@@ -413,7 +576,8 @@ extern "C" bakron_status bakron_layernorm(const void* X, int64_t T, int64_t d, i
   a.mean = mean;
   a.rstd = rstd;
   const bool al = aligned_to(X, 16) && aligned_to(Y, 16) && aligned_to(gamma, 32) && aligned_to(beta, 32);
-  const NormPlan q = norm_plan(d, dtype, al);
+  const NormPlan q = norm_plan(d, dtype, al, 1);
+  a.depth = q.depth;
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = dtype == BAKRON_F32    ? run_fwd<float, 4>(q, a, s)
                         : dtype == BAKRON_BF16 ? run_fwd<__nv_bfloat16, 8>(q, a, s)
@@ -458,14 +622,15 @@ extern "C" bakron_status bakron_layernorm_grad(const void* dY, const void* X, in
   a.rstd_in = rstd;
   a.part = dgamma ? static_cast<float*>(ws) : nullptr;
   const bool al = aligned_to(X, 16) && aligned_to(dY, 16) && aligned_to(dX, 16) && aligned_to(gamma, 32);
-  const NormPlan q = norm_plan(d, dtype, al);
+  const NormPlan q = norm_plan(d, dtype, al, 2);
+  a.depth = q.depth;
   const cudaError_t e = dtype == BAKRON_F32    ? run_grad<float, 4>(q, a, s)
                         : dtype == BAKRON_BF16 ? run_grad<__nv_bfloat16, 8>(q, a, s)
                                                : run_grad<__half, 8>(q, a, s);
   if (e != cudaSuccess) return launch_status(e);
   if (dgamma) {
     count_launch();
-    norm_join_kernel<<<(unsigned)((2 * d + 31) / 32), 512, 0, s>>>(a.part, grad_rows(q, T), d, dgamma,
+    norm_join_kernel<<<(unsigned)((2 * d + 31) / 32), 512, 0, s>>>(a.part, norm_blocks(q, T), d, dgamma,
                                                                      dbeta);
     if (cudaGetLastError() != cudaSuccess) return BAKRON_ERR_CUDA;
   }
