@@ -16,6 +16,7 @@
 // workspace; a second launch adds the blocks' rows in a fixed order (no atomics,
 // so the bits do not depend on the run).
 #include <algorithm>
+#include <type_traits>
 
 #include "packed.cuh"
 
@@ -148,6 +149,47 @@ struct Rows {
   }
 };
 
+// V elements to and from fp32, two at a time for the 16-bit types.
+template <typename TX, int V>
+__device__ __forceinline__ void widen(float (&f)[V], const Vec<TX, V>& v) {
+  if constexpr (V > 1 && sizeof(TX) == 2) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      if constexpr (std::is_same<TX, __half>::value) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
+        f[2 * e] = p.x;
+        f[2 * e + 1] = p.y;
+      } else {
+        f[2 * e] = __uint_as_float(u[e] << 16);
+        f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = to_float(v.v[e]);
+  }
+}
+template <typename TX, int V>
+__device__ __forceinline__ void narrow(Vec<TX, V>& v, const float (&f)[V]) {
+  if constexpr (V > 1 && sizeof(TX) == 2) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      if constexpr (std::is_same<TX, __half>::value) {
+        const __half2 h = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+        u[e] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+        u[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v.v[e] = from_float<TX>(f[e]);
+  }
+}
+
 // gamma and beta of V columns (1 and 0 where there are none).
 template <int V>
 __device__ __forceinline__ void params(Vec<float, V>& g, Vec<float, V>& b, const NormArgs& p, int c) {
@@ -200,11 +242,9 @@ __global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ Norm
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if ((tid + i * tpr) * V < d) {
+        widen(f[i], v[0][i]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          f[i][e] = to_float(v[0][i].v[e]);
-          sum[0] += f[i][e];
-        }
+        for (int e = 0; e < V; ++e) sum[0] += f[i][e];
       }
     }
     row_sums<kBlock, 1>(sum, red, slot);
@@ -233,15 +273,18 @@ __global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ Norm
         const Vec<float, V>&g = gk[kKeep ? i : 0], &b = bk[kKeep ? i : 0];
         Vec<TX, V> o;
 #pragma unroll
-        for (int e = 0; e < V; ++e) o.v[e] = from_float<TX>(fmaf(f[i][e] * r, g.v[e], b.v[e]));
+        for (int e = 0; e < V; ++e) f[i][e] = fmaf(f[i][e] * r, g.v[e], b.v[e]);
+        narrow(o, f[i]);
         *reinterpret_cast<Vec<TX, V>*>(y + c) = o;
       }
     }
   }
 }
 
+__device__ __forceinline__ float norm_h(float x, float mu, float r) { return (x - mu) * r; }
+
 template <typename TX, int V, int NV, bool kBlock, int MAXB>
-__global__ void __launch_bounds__(MAXB) norm_grad_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad_kernel(const __grid_constant__ NormArgs p) {
   constexpr bool kAhead = kBlock && V > 1;
   extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ float red[2][2][kMaxWarps];
@@ -253,7 +296,8 @@ __global__ void __launch_bounds__(MAXB) norm_grad_kernel(const __grid_constant__
   const int64_t step = (int64_t)gridDim.x * rows_at_once;
   const float inv_d = 1.f / (float)p.d;
   const int d = (int)p.d;
-  constexpr bool kKeep = NV * V <= 16;
+  // gamma, and a row's h and a, stay in registers when there is room
+  constexpr bool kKeep = NV * V <= 16 && MAXB <= 512;
   Vec<float, V> gk[kKeep ? NV : 1], unused;
   if constexpr (kKeep) {
 #pragma unroll
@@ -289,20 +333,28 @@ __global__ void __launch_bounds__(MAXB) norm_grad_kernel(const __grid_constant__
     Vec<TX, V> v[2][NV];
     rows.get(row, v);
     float sums[2] = {0.f, 0.f};
+    float hk[kKeep ? NV : 1][V], ak[kKeep ? NV : 1][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (tid + i * tpr) * V;
       if (c < d) {
         if constexpr (!kKeep) params(gk[0], unused, p, c);
         const Vec<float, V>& g = gk[kKeep ? i : 0];
+        float fx[V], fw[V];
+        widen(fx, v[0][i]);
+        widen(fw, v[1][i]);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float h = (to_float(v[0][i].v[e]) - mu) * r, w = to_float(v[1][i].v[e]);
+          const float h = norm_h(fx[e], mu, r), w = fw[e];
           const float a = w * g.v[e];
           sums[0] += a;
           sums[1] = fmaf(a, h, sums[1]);
           dg[i][e] = fmaf(w, h, dg[i][e]);
           db[i][e] += w;
+          if constexpr (kKeep) {
+            hk[i][e] = h;
+            ak[i][e] = a;
+          }
         }
       }
     }
@@ -316,12 +368,18 @@ __global__ void __launch_bounds__(MAXB) norm_grad_kernel(const __grid_constant__
         if constexpr (!kKeep) params(gk[0], unused, p, c);
         const Vec<float, V>& g = gk[kKeep ? i : 0];
         Vec<TX, V> o;
+        float fx[V], fw[V], fo[V];
+        if constexpr (!kKeep) {
+          widen(fx, v[0][i]);
+          widen(fw, v[1][i]);
+        }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float h = (to_float(v[0][i].v[e]) - mu) * r;
-          const float a = to_float(v[1][i].v[e]) * g.v[e];
-          o.v[e] = from_float<TX>(fmaf(-h, m2, fmaf(r, a, -m1)));
+          const float h = kKeep ? hk[kKeep ? i : 0][e] : norm_h(fx[e], mu, r);
+          const float a = kKeep ? ak[kKeep ? i : 0][e] : fw[e] * g.v[e];
+          fo[e] = fmaf(-h, m2, fmaf(r, a, -m1));
         }
+        narrow(o, fo);
         *reinterpret_cast<Vec<TX, V>*>(dx + c) = o;
       }
     }
@@ -474,11 +532,13 @@ NormPlan norm_plan(int64_t d, int dtype, bool aligned, int arrays) {
   const int wide = dtype == BAKRON_F32 ? 4 : 8;
   q.v = (aligned && d % wide == 0) ? wide : 1;
   const int64_t vecs = d / q.v;
-  const int most = q.v == 1 ? 16 : 4;
+  // columns per thread: 32 forward, 16 backward (two sums per column live in
+  // registers there), 32 once a block of 896 threads is too small for that
+  const int most = q.v == 1 ? 16 : arrays == 1 || vecs > 16 / q.v * 896 ? 32 / q.v : 16 / q.v;
   q.per_sm = arrays == 1 ? 8 : 4;
-  if (vecs <= 32 * most) {
+  if (vecs <= 128 / q.v * (q.v == 1 ? 4 : 8)) {        // 512 odd columns, 1024 others
     q.threads = 256;
-    q.nv = most;
+    q.nv = q.v == 1 ? 16 : 32 / q.v;
     q.smem = arrays == 2 ? (size_t)(2 * d) * 4 : 0;    // the warps' sums
     return q;
   }
@@ -494,10 +554,10 @@ NormPlan norm_plan(int64_t d, int dtype, bool aligned, int arrays) {
     q.per_sm = arrays == 1 ? 4 : 2;
     return q;
   }
-  // blocks per SM: what the registers allow (64, and 128 backward, a thread), fewer
-  // for long rows; as many rows ahead as fit beside that
+  // blocks per SM: what the registers allow, fewer for long rows; as many rows
+  // ahead as fit beside that
   const size_t row = (size_t)arrays * q.nv * q.threads * 16;
-  q.per_sm = std::max(1, std::min(8, (arrays == 1 ? 1024 : 512) / q.threads));
+  q.per_sm = std::max(1, std::min(arrays == 1 ? 8 : 2, (arrays == 1 ? 1024 : 512) / q.threads));
   while (q.per_sm > 1 && row * 2 * q.per_sm > kRowBytes) --q.per_sm;
   q.depth = (int)std::max<size_t>(1, std::min<size_t>(4, kRowBytes / (row * q.per_sm)));
   q.smem = row * q.depth;
@@ -521,24 +581,31 @@ cudaError_t launch_norm(K k, const NormPlan& q, const NormArgs& a, std::atomic<u
   return cudaGetLastError();
 }
 
-// Every variant of one direction: f(kernel) for the plan's.
-#define NORM_VARIANTS(KERNEL, LONG)                                                                    \
-  static std::atomic<unsigned long long> d[8];                                                         \
-  if (q.nv == 0) return launch_norm(LONG<TX>, q, a, d[0], s);                                          \
-  if (q.v == 1 && !q.block) return launch_norm(KERNEL<TX, 1, 16, false, 256>, q, a, d[1], s);          \
-  if (q.v == 1 && q.threads <= 512) return launch_norm(KERNEL<TX, 1, 16, true, 512>, q, a, d[2], s);   \
-  if (q.v == 1) return launch_norm(KERNEL<TX, 1, 16, true, 1024>, q, a, d[3], s);                      \
-  if (!q.block) return launch_norm(KERNEL<TX, W, 4, false, 256>, q, a, d[4], s);                       \
-  if (q.threads <= 448) return launch_norm(KERNEL<TX, W, 4, true, 448>, q, a, d[5], s);                \
-  return launch_norm(KERNEL<TX, W, 4, true, 1024>, q, a, d[6], s)
-
 template <typename TX, int W>
 cudaError_t run_fwd(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
-  NORM_VARIANTS(norm_kernel, norm_long_kernel);
+  constexpr int N = 32 / W;
+  static std::atomic<unsigned long long> d[7];
+  if (q.nv == 0) return launch_norm(norm_long_kernel<TX>, q, a, d[0], s);
+  if (q.v == 1 && !q.block) return launch_norm(norm_kernel<TX, 1, 16, false, 256>, q, a, d[1], s);
+  if (q.v == 1 && q.threads <= 512) return launch_norm(norm_kernel<TX, 1, 16, true, 512>, q, a, d[2], s);
+  if (q.v == 1) return launch_norm(norm_kernel<TX, 1, 16, true, 1024>, q, a, d[3], s);
+  if (!q.block) return launch_norm(norm_kernel<TX, W, N, false, 256>, q, a, d[4], s);
+  if (q.threads <= 512) return launch_norm(norm_kernel<TX, W, N, true, 512>, q, a, d[5], s);
+  return launch_norm(norm_kernel<TX, W, N, true, 1024>, q, a, d[6], s);
 }
 template <typename TX, int W>
 cudaError_t run_grad(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
-  NORM_VARIANTS(norm_grad_kernel, norm_grad_long_kernel);
+  constexpr int N = 16 / W;
+  static std::atomic<unsigned long long> d[9];
+  if (q.nv == 0) return launch_norm(norm_grad_long_kernel<TX>, q, a, d[0], s);
+  if (q.v == 1 && !q.block) return launch_norm(norm_grad_kernel<TX, 1, 16, false, 256>, q, a, d[1], s);
+  if (q.v == 1 && q.threads <= 512) return launch_norm(norm_grad_kernel<TX, 1, 16, true, 512>, q, a, d[2], s);
+  if (q.v == 1) return launch_norm(norm_grad_kernel<TX, 1, 16, true, 1024>, q, a, d[3], s);
+  if (!q.block) return launch_norm(norm_grad_kernel<TX, W, 2 * N, false, 256>, q, a, d[4], s);
+  if (q.nv == 2 * N) return launch_norm(norm_grad_kernel<TX, W, 2 * N, true, 1024>, q, a, d[5], s);
+  if (q.threads <= 256) return launch_norm(norm_grad_kernel<TX, W, N, true, 256>, q, a, d[6], s);
+  if (q.threads <= 512) return launch_norm(norm_grad_kernel<TX, W, N, true, 512>, q, a, d[7], s);
+  return launch_norm(norm_grad_kernel<TX, W, N, true, 896>, q, a, d[8], s);
 }
 
 bool norm_args_ok(int64_t T, int64_t d, int dtype) {
