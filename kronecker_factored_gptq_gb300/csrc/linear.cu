@@ -34,6 +34,7 @@ bakron_status run_linear(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, vo
   cudaStream_t s = (cudaStream_t)stream;
   if (!grad && a.T <= kFewTokens)
     return launch_status(launch_linear_few(a, s));
+  if (!grad && a.T <= kMidTokens && a.dtype != BAKRON_F32) return launch_status(launch_linear_mid(a, s));
   if (!prop_tc_supported()) return BAKRON_ERR_UNSUPPORTED;
   return launch_status(launch_linear_tc(a, grad, s));
 }

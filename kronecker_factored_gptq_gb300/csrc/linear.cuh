@@ -15,10 +15,13 @@ struct LinearArgs {
   void* ws;
 };
 
-// Tokens up to which bakron_linear runs linear_few_kernel.
+// Tokens up to which bakron_linear runs linear_few_kernel, and, of 16-bit
+// types, linear_mid_kernel.
 constexpr int64_t kFewTokens = 16;
+constexpr int64_t kMidTokens = 64;
 
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_mid(const LinearArgs& a, cudaStream_t s);
 
 // tcgen05 products of T tokens in either direction; K is the length of the
 // sums (n, gradient: m).
