@@ -69,6 +69,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const __grid_co
   pipe.base = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * P::kBytes;
   // the warps take the chunks two by two, in turn
   int ahead = c_lo + 2 * warp;
+  if (ahead + 1 < c_hi) qm::prefetch_codes<RT>(tile, ahead, lane);
+  grid_dep_wait();
+  grid_dep_launch();
   auto issue = [&]() {
     pipe.issue(a.w, tile, ahead, max(0, min(2, c_hi - ahead)), lane);
     ahead += 2 * kWarps;
@@ -222,12 +225,14 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)f.S;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)f.S;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = f.S > 1 ? 1 : 0;
+  cfg.numAttrs = f.S > 1 ? 2 : 1;
   count_launch();
   return cudaLaunchKernelEx(&cfg, k, f);
 }

@@ -80,6 +80,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) linear_mid_kernel(const __g
     ++ahead;
     fill = fill + slot_bytes == kDepth * slot_bytes ? 0 : fill + slot_bytes;
   };
+  if (2 * ahead + 1 < c_hi) qm::prefetch_codes<1>(tile, 2 * ahead, lane);
+  grid_dep_wait();
+  grid_dep_launch();
 #pragma unroll
   for (int p = 0; p < kDepth - 1; ++p) issue();
 
@@ -157,10 +160,11 @@ constexpr size_t kSmem = 226 * 1024;
 
 struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   Launch() = default;
   Launch(const Launch& o) : cfg(o.cfg) {
     at[0] = o.at[0];
+    at[1] = o.at[1];
     cfg.attrs = at;
   }
 };
@@ -171,11 +175,13 @@ Launch cluster_config(int threads, size_t smem, int cluster, unsigned blocks, cu
   q.cfg.blockDim = dim3((unsigned)threads);
   q.cfg.dynamicSmemBytes = smem;
   q.cfg.stream = s;
-  q.at[0].id = cudaLaunchAttributeClusterDimension;
-  q.at[0].val.clusterDim.x = (unsigned)cluster;
-  q.at[0].val.clusterDim.y = q.at[0].val.clusterDim.z = 1;
+  q.at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  q.at[0].val.programmaticStreamSerializationAllowed = 1;
+  q.at[1].id = cudaLaunchAttributeClusterDimension;
+  q.at[1].val.clusterDim.x = (unsigned)cluster;
+  q.at[1].val.clusterDim.y = q.at[1].val.clusterDim.z = 1;
   q.cfg.attrs = q.at;
-  q.cfg.numAttrs = cluster > 1 ? 1 : 0;
+  q.cfg.numAttrs = cluster > 1 ? 2 : 1;
   return q;
 }
 

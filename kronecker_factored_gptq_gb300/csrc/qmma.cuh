@@ -94,6 +94,23 @@ __device__ __forceinline__ void tile_ref(TileRef<RT>& t, const PackedView& w, in
   t.scale = w.scale + grid_row(w, e, min(row0[mine] + (lane & 15), w.mp - 1));
 }
 
+// Chunks c and c + 1 into L2, ahead of the wait for the kernel before: only a
+// hint, so it may run while that kernel still writes.
+template <int RT>
+__device__ __forceinline__ void prefetch_codes(const TileRef<RT>& t, int c, int lane) {
+  // a lane in eight per row block and 128 bytes of its two chunks (codes[r][i]
+  // is at row lane / 4, 16 (lane % 4) bytes: 512 bytes per row block and chunk)
+  if (lane % 8 == 0) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(t.codes[r][i] + (int64_t)(c + h) * kBlockBytes));
+  }
+}
+
 // A warp's codes in flight: D slots in shared memory of two chunks each (two, so
 // that the addresses and counters of a step are paid once per 256 columns),
 // filled by asynchronous copies D - 1 slots ahead.  A thread copies the 16 bytes
