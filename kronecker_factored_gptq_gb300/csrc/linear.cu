@@ -36,7 +36,7 @@ bakron_status run_linear(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, vo
     return launch_status(launch_linear_few(a, s));
   if (!grad && a.T <= kMidTokens && a.dtype != BAKRON_F32) return launch_status(launch_linear_mid(a, s));
   if (!prop_tc_supported()) return BAKRON_ERR_UNSUPPORTED;
-  return launch_status(launch_linear_tc(a, grad, s));
+  return launch_status(grad ? launch_linear_tc(a, grad, s) : launch_linear_fwd(a, s));
 }
 
 }  // namespace

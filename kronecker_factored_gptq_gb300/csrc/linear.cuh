@@ -31,5 +31,6 @@ size_t linear_tc_workspace(int64_t T, int64_t K, int dtype);
 cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_t kp, void* out,
                           cudaStream_t s);
 cudaError_t launch_linear_tc(const LinearArgs& a, bool grad, cudaStream_t s);
+cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace bakron
