@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   __shared__ Bars bars;
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the shuffle tells the compiler that the warp's number, and so its role, is uniform
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base_raw = smem_u32(dsm);
   const uint32_t ring = (base_raw + 1023u) & ~1023u;
   const uint32_t plane_b = (uint32_t)a.N * 128u, half_bytes = TX * plane_b, stage_bytes = 2 * half_bytes;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = bars.tmem, tmem_a = tmem + 2u * (uint32_t)a.N;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), tmem_a = tmem + 2u * (uint32_t)a.N;
   grid_dep_wait();
   grid_dep_launch();
 

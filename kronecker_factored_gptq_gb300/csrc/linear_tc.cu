@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the shuffle tells the compiler that the warp's number, and so its role, is uniform
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int64_t tile = blockIdx.x / S;
   Ctx x;
   x.bars = &bars;
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  x.tmem = bars.tmem;
+  x.tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
   grid_dep_wait();
   grid_dep_launch();
 
