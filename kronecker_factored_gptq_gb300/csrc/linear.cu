@@ -7,6 +7,39 @@
 namespace bakron {
 namespace {
 
+// x (T x K, any alignment) -> planes [TERMS][T][kp] of 16-bit terms, zeros
+// past K: the activations as the tensor map wants them.
+template <typename TX, int TERMS>
+__global__ void __launch_bounds__(256) planes_kernel(const TX* __restrict__ x, int64_t T, int64_t K,
+                                                     int64_t kp, uint16_t* __restrict__ out) {
+  const int64_t per = kp / 8, total = T * per;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t t = i / per, k = (i - t * per) * 8;
+    uint32_t h[TERMS][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t v[3] = {0, 0, 0};
+      if (k + e < K) {
+        const TX* p = x + t * K + k + e;
+        if constexpr (TERMS == 1) {
+          v[0] = *reinterpret_cast<const uint16_t*>(p);
+        } else {
+          float f[3];
+          split3(to_float(*p), f[0], f[1], f[2]);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) v[q] = bf16_bits(f[q]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < TERMS; ++q) h[q][e >> 1] = (e & 1) ? (h[q][e >> 1] | v[q] << 16) : v[q];
+    }
+#pragma unroll
+    for (int q = 0; q < TERMS; ++q)
+      *reinterpret_cast<uint4*>(out + (q * T + t) * kp + k) = make_uint4(h[q][0], h[q][1], h[q][2], h[q][3]);
+  }
+}
+
 // Arguments both directions share; T = 0 is a valid call that does nothing.
 bool linear_args(const void* x, int64_t T, int dtype, const bakron_packed* w, const void* y,
                  LinearArgs* a) {
@@ -23,7 +56,8 @@ bool linear_args(const void* x, int64_t T, int dtype, const bakron_packed* w, co
 
 size_t workspace_bytes(const LinearArgs& a, bool grad) {
   if (!grad && a.T <= kFewTokens) return 0;
-  return linear_tc_workspace(a.T, grad ? a.w.m : a.w.n, a.dtype);
+  const int64_t K = grad ? a.w.m : a.w.n;
+  return (size_t)(a.dtype == BAKRON_F32 ? 3 : 1) * (size_t)a.T * (size_t)((K + 127) / 128 * 128) * 2;
 }
 
 bakron_status run_linear(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, void* stream) {
@@ -36,10 +70,22 @@ bakron_status run_linear(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, vo
     return launch_status(launch_linear_few(a, s));
   if (!grad && a.T <= kMidTokens && a.dtype != BAKRON_F32) return launch_status(launch_linear_mid(a, s));
   if (!prop_tc_supported()) return BAKRON_ERR_UNSUPPORTED;
-  return launch_status(grad ? launch_linear_tc(a, grad, s) : launch_linear_fwd(a, s));
+  return launch_status(grad ? launch_linear_grad(a, s) : launch_linear_fwd(a, s));
 }
 
 }  // namespace
+
+cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_t kp, void* out,
+                          cudaStream_t s) {
+  const int64_t total = T * kp / 8;
+  const unsigned g = (unsigned)std::max<int64_t>(1, std::min<int64_t>((total + 255) / 256, (int64_t)sm_count() * 16));
+  uint16_t* o = static_cast<uint16_t*>(out);
+  count_launch();
+  if (dtype == BAKRON_F32) planes_kernel<float, 3><<<g, 256, 0, s>>>(static_cast<const float*>(x), T, K, kp, o);
+  else planes_kernel<uint16_t, 1><<<g, 256, 0, s>>>(static_cast<const uint16_t*>(x), T, K, kp, o);
+  return cudaGetLastError();
+}
+
 }  // namespace bakron
 
 using namespace bakron;

@@ -23,14 +23,13 @@ constexpr int64_t kMidTokens = 64;
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_mid(const LinearArgs& a, cudaStream_t s);
 
-// tcgen05 products of T tokens in either direction; K is the length of the
-// sums (n, gradient: m).
-size_t linear_tc_workspace(int64_t T, int64_t K, int dtype);
 // x (T x K of dtype, any alignment) -> planes [terms][T][kp] of 16-bit terms (1,
 // or 3 for fp32), zeros past K; out is 16-byte aligned, kp a multiple of 8.
 cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_t kp, void* out,
                           cudaStream_t s);
-cudaError_t launch_linear_tc(const LinearArgs& a, bool grad, cudaStream_t s);
+
+// tcgen05 products for many tokens, and the gradient for any number.
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_grad(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace bakron
