@@ -149,6 +149,38 @@ struct Rows {
   }
 };
 
+// Two fp32 values at a time: one instruction for two additions, products or
+// fused ones.  What bounds the block-per-row kernels after HBM is the number of
+// instructions per element.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 f2(float v) { return F2{v, v}; }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("{\n .reg .b64 a, b, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 r, a, b;\n"
+      " mov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("{\n .reg .b64 a, b, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 r, a, b;\n"
+      " mov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("{\n .reg .b64 a, b, c, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 r, a, b, c;\n mov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
 // V elements to and from fp32, two at a time for the 16-bit types.
 template <typename TX, int V>
 __device__ __forceinline__ void widen(float (&f)[V], const Vec<TX, V>& v) {
@@ -193,14 +225,17 @@ __device__ __forceinline__ void narrow(Vec<TX, V>& v, const float (&f)[V]) {
 // gamma and beta of V columns (1 and 0 where there are none).
 template <int V>
 __device__ __forceinline__ void params(Vec<float, V>& g, Vec<float, V>& b, const NormArgs& p, int c) {
+  if (p.gamma && c < (int)p.d) {
+    g = *reinterpret_cast<const Vec<float, V>*>(p.gamma + c);
+  } else {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    g.v[e] = 1.f;
-    b.v[e] = 0.f;
+    for (int e = 0; e < V; ++e) g.v[e] = 1.f;
   }
-  if (c < (int)p.d) {
-    if (p.gamma) g = *reinterpret_cast<const Vec<float, V>*>(p.gamma + c);
-    if (p.beta) b = *reinterpret_cast<const Vec<float, V>*>(p.beta + c);
+  if (p.beta && c < (int)p.d) {
+    b = *reinterpret_cast<const Vec<float, V>*>(p.beta + c);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) b.v[e] = 0.f;
   }
 }
 
@@ -239,26 +274,41 @@ __global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ Norm
     rows.get(row, v);
     float f[NV][V];
     float sum[1] = {0.f}, sq[1] = {0.f};
+    F2 p2 = f2(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if ((tid + i * tpr) * V < d) {
         widen(f[i], v[0][i]);
+        if constexpr (V == 1) {
+          sum[0] += f[i][0];
+        } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum[0] += f[i][e];
-      }
-    }
-    row_sums<kBlock, 1>(sum, red, slot);
-    const float mu = sum[0] * inv_d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if ((tid + i * tpr) * V < d) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          f[i][e] -= mu;
-          sq[0] = fmaf(f[i][e], f[i][e], sq[0]);
+          for (int e = 0; e < V; e += 2) p2 = add2(p2, F2{f[i][e], f[i][e + 1]});
         }
       }
     }
+    if constexpr (V > 1) sum[0] = p2.x + p2.y;
+    row_sums<kBlock, 1>(sum, red, slot);
+    const float mu = sum[0] * inv_d;
+    p2 = f2(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if ((tid + i * tpr) * V < d) {
+        if constexpr (V == 1) {
+          f[i][0] -= mu;
+          sq[0] = fmaf(f[i][0], f[i][0], sq[0]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const F2 t = add2(F2{f[i][e], f[i][e + 1]}, f2(-mu));
+            p2 = fma2(t, t, p2);
+            f[i][e] = t.x;
+            f[i][e + 1] = t.y;
+          }
+        }
+      }
+    }
+    if constexpr (V > 1) sq[0] = p2.x + p2.y;
     row_sums<kBlock, 1>(sq, red, slot);
     const float r = rsqrtf(sq[0] * inv_d + p.eps);
     if (tid == 0) {
@@ -272,8 +322,16 @@ __global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ Norm
         if constexpr (!kKeep) params(gk[0], bk[0], p, c);
         const Vec<float, V>&g = gk[kKeep ? i : 0], &b = bk[kKeep ? i : 0];
         Vec<TX, V> o;
+        if constexpr (V == 1) {
+          f[i][0] = fmaf(f[i][0] * r, g.v[0], b.v[0]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[i][e] = fmaf(f[i][e] * r, g.v[e], b.v[e]);
+          for (int e = 0; e < V; e += 2) {
+            const F2 t = fma2(mul2(F2{f[i][e], f[i][e + 1]}, f2(r)), F2{g.v[e], g.v[e + 1]}, F2{b.v[e], b.v[e + 1]});
+            f[i][e] = t.x;
+            f[i][e + 1] = t.y;
+          }
+        }
         narrow(o, f[i]);
         *reinterpret_cast<Vec<TX, V>*>(y + c) = o;
       }
@@ -334,6 +392,7 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad
     rows.get(row, v);
     float sums[2] = {0.f, 0.f};
     float hk[kKeep ? NV : 1][V], ak[kKeep ? NV : 1][V];
+    F2 t1 = f2(0.f), t2 = f2(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (tid + i * tpr) * V;
@@ -343,20 +402,41 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad
         float fx[V], fw[V];
         widen(fx, v[0][i]);
         widen(fw, v[1][i]);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float h = norm_h(fx[e], mu, r), w = fw[e];
-          const float a = w * g.v[e];
+        if constexpr (V == 1) {
+          const float h = norm_h(fx[0], mu, r), w = fw[0], a = w * g.v[0];
           sums[0] += a;
           sums[1] = fmaf(a, h, sums[1]);
-          dg[i][e] = fmaf(w, h, dg[i][e]);
-          db[i][e] += w;
+          dg[i][0] = fmaf(w, h, dg[i][0]);
+          db[i][0] += w;
           if constexpr (kKeep) {
-            hk[i][e] = h;
-            ak[i][e] = a;
+            hk[i][0] = h;
+            ak[i][0] = a;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const F2 h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu)), f2(r)), w = F2{fw[e], fw[e + 1]};
+            const F2 a = mul2(w, F2{g.v[e], g.v[e + 1]});
+            t1 = add2(t1, a);
+            t2 = fma2(a, h, t2);
+            const F2 q = fma2(w, h, F2{dg[i][e], dg[i][e + 1]}), s = add2(F2{db[i][e], db[i][e + 1]}, w);
+            dg[i][e] = q.x;
+            dg[i][e + 1] = q.y;
+            db[i][e] = s.x;
+            db[i][e + 1] = s.y;
+            if constexpr (kKeep) {
+              hk[i][e] = h.x;
+              hk[i][e + 1] = h.y;
+              ak[i][e] = a.x;
+              ak[i][e + 1] = a.y;
+            }
           }
         }
       }
+    }
+    if constexpr (V > 1) {
+      sums[0] = t1.x + t1.y;
+      sums[1] = t2.x + t2.y;
     }
     row_sums<kBlock, 2>(sums, red, slot);
     // dX = r a - (r m1) - h (r m2): three constants of the row
@@ -373,11 +453,25 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad
           widen(fx, v[0][i]);
           widen(fw, v[1][i]);
         }
+        if constexpr (V == 1) {
+          const float h = kKeep ? hk[kKeep ? i : 0][0] : norm_h(fx[0], mu, r);
+          const float a = kKeep ? ak[kKeep ? i : 0][0] : fw[0] * g.v[0];
+          fo[0] = fmaf(-h, m2, fmaf(r, a, -m1));
+        } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float h = kKeep ? hk[kKeep ? i : 0][e] : norm_h(fx[e], mu, r);
-          const float a = kKeep ? ak[kKeep ? i : 0][e] : fw[e] * g.v[e];
-          fo[e] = fmaf(-h, m2, fmaf(r, a, -m1));
+          for (int e = 0; e < V; e += 2) {
+            F2 h, a;
+            if constexpr (kKeep) {
+              h = F2{hk[i][e], hk[i][e + 1]};
+              a = F2{ak[i][e], ak[i][e + 1]};
+            } else {
+              h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu)), f2(r));
+              a = mul2(F2{fw[e], fw[e + 1]}, F2{g.v[e], g.v[e + 1]});
+            }
+            const F2 q = fma2(h, f2(-m2), fma2(a, f2(r), f2(-m1)));
+            fo[e] = q.x;
+            fo[e + 1] = q.y;
+          }
         }
         narrow(o, fo);
         *reinterpret_cast<Vec<TX, V>*>(dx + c) = o;

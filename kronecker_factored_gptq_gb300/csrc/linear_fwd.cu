@@ -14,7 +14,8 @@
 // accumulator, which the epilogue warps read, scale in fp32 and add to their
 // registers while the tensor core fills the other one: no rounding of the weights,
 // and no long chain of the tensor core's additions, which cut off instead of
-// rounding.  fp32 activations are three exact bf16 terms (three products).
+// rounding.  fp32 activations are three exact bf16 terms; the products of the two
+// small ones have an accumulator of their own.
 //
 // One block per SM, which takes output tiles in turn (or, when there are few, a
 // part of the columns of one, joined over a cluster through distributed shared memory):
@@ -284,7 +285,8 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), tmem_a = tmem + 2u * (uint32_t)a.N;
+  const uint32_t acc_cols = (TX == 1 ? 1u : 2u) * (uint32_t)a.N;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), tmem_a = tmem + 2u * acc_cols;
   grid_dep_wait();
   grid_dep_launch();
 
@@ -371,11 +373,11 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
 #pragma unroll
               for (int j = q4 * KU; j < (UPC > 1 ? (q4 + 2) * KU : 8); ++j) {
                 const uint32_t buf = (u + j / KU) & 1;
-                const uint32_t d = tmem + buf * (uint32_t)a.N;
+                const uint32_t d = tmem + buf * acc_cols;
 #pragma unroll
                 for (int q = 0; q < TX; ++q)
-                  mma_f16_ts(d, ta + j * 8, db + ((j / 4) * half16 + q * plane16 + (j % 4) * 2), idesc,
-                             j % KU == 0 && q == 0 ? 0u : 1u);
+                  mma_f16_ts(q == 0 ? d : d + (uint32_t)a.N, ta + j * 8,
+                             db + ((j / 4) * half16 + q * plane16 + (j % 4) * 2), idesc, j % KU == 0 && q <= 1 ? 0u : 1u);
                 if (j % KU == KU - 1) mma_commit(af + 8u * buf);
               }
               if (q4 + 2 >= UPC) {
@@ -430,13 +432,21 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         fence_after_sync();
-        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (u_all & 1) * (uint32_t)a.N + (uint32_t)col0;
+        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (u_all & 1) * acc_cols + (uint32_t)col0;
 #pragma unroll
         for (int g = 0; g < NC / 16; ++g) {
           if (g * 16 < ncols) {
             uint32_t v[16];
             tmem_ld16(ta + g * 16, v);
-            tmem_ld_wait();
+            if constexpr (TX > 1) {
+              uint32_t c[16];
+              tmem_ld16(ta + (uint32_t)a.N + g * 16, c);
+              tmem_ld_wait();
+#pragma unroll
+              for (int t = 0; t < 16; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) + __uint_as_float(c[t]));
+            } else {
+              tmem_ld_wait();
+            }
 #pragma unroll
             for (int t = 0; t < 16; ++t) acc[g * 16 + t] = fmaf(s, __uint_as_float(v[t]), acc[g * 16 + t]);
           }
