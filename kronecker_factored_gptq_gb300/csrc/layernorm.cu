@@ -45,7 +45,7 @@ constexpr int kMaxWarps = 32;
 // `slot` alternates between calls, so one barrier per call is enough: a
 // slot is written again only after the barrier of the call in between.
 template <bool kBlock, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[2][kMaxWarps], int& slot) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[4][kMaxWarps], int& slot) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -243,7 +243,7 @@ template <typename TX, int V, int NV, bool kBlock, int MAXB>
 __global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ NormArgs p) {
   constexpr bool kAhead = kBlock && V > 1;
   extern __shared__ __align__(16) uint8_t dsm[];
-  __shared__ float red[2][2][kMaxWarps];
+  __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
   const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
   const int tpr = kBlock ? blockDim.x : 32;
@@ -268,72 +268,89 @@ __global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ Norm
 #pragma unroll
     for (int i = 0; i < NV; ++i) params(gk[i], bk[i], p, (tid + i * tpr) * V);
   }
-  for (int64_t row = row0; row < p.T; row += step) {
-    TX* y = static_cast<TX*>(p.y) + row * p.d;
-    Vec<TX, V> v[1][NV];
-    rows.get(row, v);
-    float f[NV][V];
-    float sum[1] = {0.f}, sq[1] = {0.f};
-    F2 p2 = f2(0.f);
+  // R rows at a time: their sums share the barriers and the shuffles' latency
+  constexpr int R = kAhead ? 2 : 1;
+  for (int64_t row = row0; row < p.T; row += R * step) {
+    float f[R][NV][V];
+    float sum[R], sq[R];
+    F2 p2[R];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if ((tid + i * tpr) * V < d) {
-        widen(f[i], v[0][i]);
-        if constexpr (V == 1) {
-          sum[0] += f[i][0];
-        } else {
+    for (int q = 0; q < R; ++q) {
+      Vec<TX, V> v[1][NV];
+      rows.get(row + q * step, v);
+      sum[q] = sq[q] = 0.f;
+      p2[q] = f2(0.f);
 #pragma unroll
-          for (int e = 0; e < V; e += 2) p2 = add2(p2, F2{f[i][e], f[i][e + 1]});
-        }
-      }
-    }
-    if constexpr (V > 1) sum[0] = p2.x + p2.y;
-    row_sums<kBlock, 1>(sum, red, slot);
-    const float mu = sum[0] * inv_d;
-    p2 = f2(0.f);
+      for (int i = 0; i < NV; ++i) {
+        if ((tid + i * tpr) * V < d) {
+          widen(f[q][i], v[0][i]);
+          if constexpr (V == 1) {
+            sum[q] += f[q][i][0];
+          } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if ((tid + i * tpr) * V < d) {
-        if constexpr (V == 1) {
-          f[i][0] -= mu;
-          sq[0] = fmaf(f[i][0], f[i][0], sq[0]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            const F2 t = add2(F2{f[i][e], f[i][e + 1]}, f2(-mu));
-            p2 = fma2(t, t, p2);
-            f[i][e] = t.x;
-            f[i][e + 1] = t.y;
+            for (int e = 0; e < V; e += 2) p2[q] = add2(p2[q], F2{f[q][i][e], f[q][i][e + 1]});
           }
         }
       }
+      if constexpr (V > 1) sum[q] = p2[q].x + p2[q].y;
     }
-    if constexpr (V > 1) sq[0] = p2.x + p2.y;
-    row_sums<kBlock, 1>(sq, red, slot);
-    const float r = rsqrtf(sq[0] * inv_d + p.eps);
-    if (tid == 0) {
-      if (p.mean) p.mean[row] = mu;
-      if (p.rstd) p.rstd[row] = r;
-    }
+    row_sums<kBlock, R>(sum, red, slot);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (tid + i * tpr) * V;
-      if (c < d) {
-        if constexpr (!kKeep) params(gk[0], bk[0], p, c);
-        const Vec<float, V>&g = gk[kKeep ? i : 0], &b = bk[kKeep ? i : 0];
-        Vec<TX, V> o;
-        if constexpr (V == 1) {
-          f[i][0] = fmaf(f[i][0] * r, g.v[0], b.v[0]);
-        } else {
+    for (int q = 0; q < R; ++q) {
+      const float mu = sum[q] * inv_d;
+      sum[q] = mu;
+      p2[q] = f2(0.f);
 #pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            const F2 t = fma2(mul2(F2{f[i][e], f[i][e + 1]}, f2(r)), F2{g.v[e], g.v[e + 1]}, F2{b.v[e], b.v[e + 1]});
-            f[i][e] = t.x;
-            f[i][e + 1] = t.y;
+      for (int i = 0; i < NV; ++i) {
+        if ((tid + i * tpr) * V < d) {
+          if constexpr (V == 1) {
+            f[q][i][0] -= mu;
+            sq[q] = fmaf(f[q][i][0], f[q][i][0], sq[q]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const F2 t = add2(F2{f[q][i][e], f[q][i][e + 1]}, f2(-mu));
+              p2[q] = fma2(t, t, p2[q]);
+              f[q][i][e] = t.x;
+              f[q][i][e + 1] = t.y;
+            }
           }
         }
-        narrow(o, f[i]);
-        *reinterpret_cast<Vec<TX, V>*>(y + c) = o;
+      }
+      if constexpr (V > 1) sq[q] = p2[q].x + p2[q].y;
+    }
+    row_sums<kBlock, R>(sq, red, slot);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int64_t at = row + q * step;
+      if (at >= p.T) break;
+      const float r = rsqrtf(sq[q] * inv_d + p.eps);
+      if (tid == 0) {
+        if (p.mean) p.mean[at] = sum[q];
+        if (p.rstd) p.rstd[at] = r;
+      }
+      TX* y = static_cast<TX*>(p.y) + at * p.d;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * V;
+        if (c < d) {
+          if constexpr (!kKeep) params(gk[0], bk[0], p, c);
+          const Vec<float, V>&g = gk[kKeep ? i : 0], &b = bk[kKeep ? i : 0];
+          Vec<TX, V> o;
+          if constexpr (V == 1) {
+            f[q][i][0] = fmaf(f[q][i][0] * r, g.v[0], b.v[0]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const F2 t = fma2(mul2(F2{f[q][i][e], f[q][i][e + 1]}, f2(r)), F2{g.v[e], g.v[e + 1]},
+                                F2{b.v[e], b.v[e + 1]});
+              f[q][i][e] = t.x;
+              f[q][i][e + 1] = t.y;
+            }
+          }
+          narrow(o, f[q][i]);
+          *reinterpret_cast<Vec<TX, V>*>(y + c) = o;
+        }
       }
     }
   }
@@ -345,7 +362,7 @@ template <typename TX, int V, int NV, bool kBlock, int MAXB>
 __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad_kernel(const __grid_constant__ NormArgs p) {
   constexpr bool kAhead = kBlock && V > 1;
   extern __shared__ __align__(16) uint8_t dsm[];
-  __shared__ float red[2][2][kMaxWarps];
+  __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
   const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
   const int tpr = kBlock ? blockDim.x : 32;
@@ -354,7 +371,7 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad
   const int64_t step = (int64_t)gridDim.x * rows_at_once;
   const float inv_d = 1.f / (float)p.d;
   const int d = (int)p.d;
-  // gamma, and a row's h and a, stay in registers when there is room
+  // gamma stays in registers when there is room
   constexpr bool kKeep = NV * V <= 16 && MAXB <= 512;
   Vec<float, V> gk[kKeep ? NV : 1], unused;
   if constexpr (kKeep) {
@@ -376,105 +393,103 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad
   rows.tpr = tpr;
   rows.depth = p.depth;
   rows.start(lead, dsm);
-  float mu_next = 0.f, r_next = 0.f;
-  if (lead < p.T) {
-    mu_next = p.mean_in[lead];
-    r_next = p.rstd_in[lead];
-  }
-  for (int64_t row = lead; row < p.T; row += step) {
-    TX* dx = static_cast<TX*>(p.y) + row * p.d;
-    const float mu = mu_next, r = r_next;
-    if (row + step < p.T) {
-      mu_next = ld_ahead(p.mean_in + row + step);
-      r_next = ld_ahead(p.rstd_in + row + step);
+  // R rows at a time: their sums share the barrier and the shuffles' latency
+  constexpr int R = kAhead && MAXB <= 512 ? 2 : 1;
+  float mu_next[R], r_next[R];
+  auto stats = [&](int64_t row) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      mu_next[q] = r_next[q] = 0.f;
+      if (row + q * step < p.T) {
+        mu_next[q] = ld_ahead(p.mean_in + row + q * step);
+        r_next[q] = ld_ahead(p.rstd_in + row + q * step);
+      }
     }
-    Vec<TX, V> v[2][NV];
-    rows.get(row, v);
-    float sums[2] = {0.f, 0.f};
-    float hk[kKeep ? NV : 1][V], ak[kKeep ? NV : 1][V];
-    F2 t1 = f2(0.f), t2 = f2(0.f);
+  };
+  stats(lead);
+  for (int64_t row = lead; row < p.T; row += R * step) {
+    float mu[R], r[R];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (tid + i * tpr) * V;
-      if (c < d) {
-        if constexpr (!kKeep) params(gk[0], unused, p, c);
-        const Vec<float, V>& g = gk[kKeep ? i : 0];
-        float fx[V], fw[V];
-        widen(fx, v[0][i]);
-        widen(fw, v[1][i]);
-        if constexpr (V == 1) {
-          const float h = norm_h(fx[0], mu, r), w = fw[0], a = w * g.v[0];
-          sums[0] += a;
-          sums[1] = fmaf(a, h, sums[1]);
-          dg[i][0] = fmaf(w, h, dg[i][0]);
-          db[i][0] += w;
-          if constexpr (kKeep) {
-            hk[i][0] = h;
-            ak[i][0] = a;
-          }
-        } else {
+    for (int q = 0; q < R; ++q) {
+      mu[q] = mu_next[q];
+      r[q] = r_next[q];
+    }
+    stats(row + R * step);
+    Vec<TX, V> v[R][2][NV];
+    float sums[2 * R];
 #pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            const F2 h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu)), f2(r)), w = F2{fw[e], fw[e + 1]};
-            const F2 a = mul2(w, F2{g.v[e], g.v[e + 1]});
-            t1 = add2(t1, a);
-            t2 = fma2(a, h, t2);
-            const F2 q = fma2(w, h, F2{dg[i][e], dg[i][e + 1]}), s = add2(F2{db[i][e], db[i][e + 1]}, w);
-            dg[i][e] = q.x;
-            dg[i][e + 1] = q.y;
-            db[i][e] = s.x;
-            db[i][e + 1] = s.y;
-            if constexpr (kKeep) {
-              hk[i][e] = h.x;
-              hk[i][e + 1] = h.y;
-              ak[i][e] = a.x;
-              ak[i][e + 1] = a.y;
+    for (int q = 0; q < R; ++q) {
+      rows.get(row + q * step, v[q]);
+      const bool there = row + q * step < p.T;
+      float s1 = 0.f, s2 = 0.f;
+      F2 t1 = f2(0.f), t2 = f2(0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * V;
+        if (c < d && there) {
+          if constexpr (!kKeep) params(gk[0], unused, p, c);
+          const Vec<float, V>& g = gk[kKeep ? i : 0];
+          float fx[V], fw[V];
+          widen(fx, v[q][0][i]);
+          widen(fw, v[q][1][i]);
+          if constexpr (V == 1) {
+            const float h = norm_h(fx[0], mu[q], r[q]), w = fw[0], a = w * g.v[0];
+            s1 += a;
+            s2 = fmaf(a, h, s2);
+            dg[i][0] = fmaf(w, h, dg[i][0]);
+            db[i][0] += w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const F2 h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu[q])), f2(r[q])), w = F2{fw[e], fw[e + 1]};
+              const F2 a = mul2(w, F2{g.v[e], g.v[e + 1]});
+              t1 = add2(t1, a);
+              t2 = fma2(a, h, t2);
+              const F2 x = fma2(w, h, F2{dg[i][e], dg[i][e + 1]}), z = add2(F2{db[i][e], db[i][e + 1]}, w);
+              dg[i][e] = x.x;
+              dg[i][e + 1] = x.y;
+              db[i][e] = z.x;
+              db[i][e + 1] = z.y;
             }
           }
         }
       }
+      sums[2 * q] = V > 1 ? t1.x + t1.y : s1;
+      sums[2 * q + 1] = V > 1 ? t2.x + t2.y : s2;
     }
-    if constexpr (V > 1) {
-      sums[0] = t1.x + t1.y;
-      sums[1] = t2.x + t2.y;
-    }
-    row_sums<kBlock, 2>(sums, red, slot);
-    // dX = r a - (r m1) - h (r m2): three constants of the row
-    const float m1 = r * (sums[0] * inv_d), m2 = r * (sums[1] * inv_d);
+    row_sums<kBlock, 2 * R>(sums, red, slot);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (tid + i * tpr) * V;
-      if (c < d) {
-        if constexpr (!kKeep) params(gk[0], unused, p, c);
-        const Vec<float, V>& g = gk[kKeep ? i : 0];
-        Vec<TX, V> o;
-        float fx[V], fw[V], fo[V];
-        if constexpr (!kKeep) {
-          widen(fx, v[0][i]);
-          widen(fw, v[1][i]);
-        }
-        if constexpr (V == 1) {
-          const float h = kKeep ? hk[kKeep ? i : 0][0] : norm_h(fx[0], mu, r);
-          const float a = kKeep ? ak[kKeep ? i : 0][0] : fw[0] * g.v[0];
-          fo[0] = fmaf(-h, m2, fmaf(r, a, -m1));
-        } else {
+    for (int q = 0; q < R; ++q) {
+      const int64_t at = row + q * step;
+      if (at >= p.T) break;
+      TX* dx = static_cast<TX*>(p.y) + at * p.d;
+      // dX = r a - (r m1) - h (r m2): three constants of the row
+      const float m1 = r[q] * (sums[2 * q] * inv_d), m2 = r[q] * (sums[2 * q + 1] * inv_d);
 #pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            F2 h, a;
-            if constexpr (kKeep) {
-              h = F2{hk[i][e], hk[i][e + 1]};
-              a = F2{ak[i][e], ak[i][e + 1]};
-            } else {
-              h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu)), f2(r));
-              a = mul2(F2{fw[e], fw[e + 1]}, F2{g.v[e], g.v[e + 1]});
+      for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * V;
+        if (c < d) {
+          if constexpr (!kKeep) params(gk[0], unused, p, c);
+          const Vec<float, V>& g = gk[kKeep ? i : 0];
+          Vec<TX, V> o;
+          float fx[V], fw[V], fo[V];
+          widen(fx, v[q][0][i]);
+          widen(fw, v[q][1][i]);
+          if constexpr (V == 1) {
+            fo[0] = fmaf(-norm_h(fx[0], mu[q], r[q]), m2, fmaf(r[q], fw[0] * g.v[0], -m1));
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const F2 h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu[q])), f2(r[q]));
+              const F2 a = mul2(F2{fw[e], fw[e + 1]}, F2{g.v[e], g.v[e + 1]});
+              const F2 x = fma2(h, f2(-m2), fma2(a, f2(r[q]), f2(-m1)));
+              fo[e] = x.x;
+              fo[e + 1] = x.y;
             }
-            const F2 q = fma2(h, f2(-m2), fma2(a, f2(r), f2(-m1)));
-            fo[e] = q.x;
-            fo[e + 1] = q.y;
           }
+          narrow(o, fo);
+          *reinterpret_cast<Vec<TX, V>*>(dx + c) = o;
         }
-        narrow(o, fo);
-        *reinterpret_cast<Vec<TX, V>*>(dx + c) = o;
       }
     }
   }
@@ -524,7 +539,7 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad
 // column.
 template <typename TX>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormArgs p) {
-  __shared__ float red[2][2][kMaxWarps];
+  __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
   const float inv_d = 1.f / (float)p.d;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
@@ -552,7 +567,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
 
 template <typename TX>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const __grid_constant__ NormArgs p) {
-  __shared__ float red[2][2][kMaxWarps];
+  __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
   const float inv_d = 1.f / (float)p.d;
   float* o = p.part ? p.part + (int64_t)blockIdx.x * 2 * p.d : nullptr;
@@ -648,10 +663,10 @@ NormPlan norm_plan(int64_t d, int dtype, bool aligned, int arrays) {
     q.per_sm = arrays == 1 ? 4 : 2;
     return q;
   }
-  // blocks per SM: what the registers allow, fewer for long rows; as many rows
+  // blocks per SM: what the registers allow (128 a thread), fewer for long rows; as many rows
   // ahead as fit beside that
   const size_t row = (size_t)arrays * q.nv * q.threads * 16;
-  q.per_sm = std::max(1, std::min(arrays == 1 ? 8 : 2, (arrays == 1 ? 1024 : 512) / q.threads));
+  q.per_sm = std::max(1, std::min(arrays == 1 ? 8 : 2, 512 / q.threads));
   while (q.per_sm > 1 && row * 2 * q.per_sm > kRowBytes) --q.per_sm;
   q.depth = (int)std::max<size_t>(1, std::min<size_t>(4, kRowBytes / (row * q.per_sm)));
   q.smem = row * q.depth;
