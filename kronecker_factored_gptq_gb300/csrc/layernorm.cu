@@ -112,8 +112,9 @@ struct Rows {
   __device__ __forceinline__ void start(int64_t first, void* smem) {
     if constexpr (kAhead) {
       next = first;
-      slot = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)tid * 16u;
       bytes = slot_bytes() * (uint32_t)depth;
+      slot = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)tid * 16u +
+             (tpr == 32 ? (threadIdx.x >> 5) * bytes : 0u);       // one row per warp, or per block
       for (int p = 0; p < depth - 1; ++p) copy();
     }
   }
@@ -240,8 +241,8 @@ __device__ __forceinline__ void params(Vec<float, V>& g, Vec<float, V>& b, const
 }
 
 template <typename TX, int V, int NV, bool kBlock, int MAXB>
-__global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ NormArgs p) {
-  constexpr bool kAhead = kBlock && V > 1;
+__global__ void __launch_bounds__(MAXB, V == 1 && MAXB <= 512 ? 2 : 1) norm_kernel(const __grid_constant__ NormArgs p) {
+  constexpr bool kAhead = V > 1;
   extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ Norm
     for (int i = 0; i < NV; ++i) params(gk[i], bk[i], p, (tid + i * tpr) * V);
   }
   // R rows at a time: their sums share the barriers and the shuffles' latency
-  constexpr int R = kAhead ? 2 : 1;
+  constexpr int R = kBlock && kAhead ? 2 : 1;
   for (int64_t row = row0; row < p.T; row += R * step) {
     float f[R][NV][V];
     float sum[R], sq[R];
@@ -359,8 +360,8 @@ __global__ void __launch_bounds__(MAXB) norm_kernel(const __grid_constant__ Norm
 __device__ __forceinline__ float norm_h(float x, float mu, float r) { return (x - mu) * r; }
 
 template <typename TX, int V, int NV, bool kBlock, int MAXB>
-__global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad_kernel(const __grid_constant__ NormArgs p) {
-  constexpr bool kAhead = kBlock && V > 1;
+__global__ void __launch_bounds__(MAXB, MAXB <= 256 || V == 1 ? (MAXB <= 512 ? 2 : 1) : 1) norm_grad_kernel(const __grid_constant__ NormArgs p) {
+  constexpr bool kAhead = V > 1;
   extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad
   rows.depth = p.depth;
   rows.start(lead, dsm);
   // R rows at a time: their sums share the barrier and the shuffles' latency
-  constexpr int R = kAhead && MAXB <= 512 ? 2 : 1;
+  constexpr int R = kBlock && kAhead && MAXB <= 512 ? 2 : 1;
   float mu_next[R], r_next[R];
   auto stats = [&](int64_t row) {
 #pragma unroll
@@ -512,8 +513,9 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 && kBlock ? 2 : 1) norm_grad
       }
     }
   } else {
-    // the warps of the block add theirs one after the other
+    // the warps of the block add theirs one after the other, where the rows were
     float* sum = reinterpret_cast<float*>(dsm);     // [2][d]
+    __syncthreads();
     for (int w = 0; w < rows_at_once; ++w) {
       if ((int)(threadIdx.x >> 5) == w) {
 #pragma unroll
@@ -642,13 +644,19 @@ NormPlan norm_plan(int64_t d, int dtype, bool aligned, int arrays) {
   q.v = (aligned && d % wide == 0) ? wide : 1;
   const int64_t vecs = d / q.v;
   // columns per thread: 32 forward, 16 backward (two sums per column live in
-  // registers there), 32 once a block of 896 threads is too small for that
-  const int most = q.v == 1 ? 16 : arrays == 1 || vecs > 16 / q.v * 896 ? 32 / q.v : 16 / q.v;
-  q.per_sm = arrays == 1 ? 8 : 4;
-  if (vecs <= 128 / q.v * (q.v == 1 ? 4 : 8)) {        // 512 odd columns, 1024 others
+  // registers there), 32 once a block of 896 threads is too small for that; of
+  // rows that are read by elements 8, or 16 for the longest
+  const int most = q.v == 1 ? (vecs > 8 * 1024 ? 16 : 8)
+                            : arrays == 1 || vecs > 16 / q.v * 896 ? 32 / q.v : 16 / q.v;
+  if (vecs <= 32 * (q.v == 1 ? 8 : 32 / q.v)) {        // 256 odd columns, 1024 others: a warp per row
     q.threads = 256;
-    q.nv = q.v == 1 ? 16 : 32 / q.v;
-    q.smem = arrays == 2 ? (size_t)(2 * d) * 4 : 0;    // the warps' sums
+    q.nv = q.v == 1 ? 8 : 32 / q.v;
+    q.per_sm = arrays == 1 ? 4 : 2;
+    if (q.v > 1) {
+      q.depth = 3;
+      q.smem = (size_t)8 * q.depth * arrays * q.nv * 32 * 16;
+    }
+    if (arrays == 2) q.smem = std::max(q.smem, (size_t)(2 * d) * 4);    // the warps' sums
     return q;
   }
   q.block = true;
@@ -658,15 +666,16 @@ NormPlan norm_plan(int64_t d, int dtype, bool aligned, int arrays) {
     return q;
   }
   q.nv = most;
-  q.threads = (int)(((vecs + q.nv - 1) / q.nv + 31) / 32 * 32);
+  // a row of 32 threads would be taken for a warp's
+  q.threads = std::max(64, (int)(((vecs + q.nv - 1) / q.nv + 31) / 32 * 32));
   if (q.v == 1) {
-    q.per_sm = arrays == 1 ? 4 : 2;
+    q.per_sm = std::max(1, 1024 / q.threads);
     return q;
   }
   // blocks per SM: what the registers allow (128 a thread), fewer for long rows; as many rows
   // ahead as fit beside that
   const size_t row = (size_t)arrays * q.nv * q.threads * 16;
-  q.per_sm = std::max(1, std::min(arrays == 1 ? 8 : 2, 512 / q.threads));
+  q.per_sm = std::max(1, std::min(arrays == 1 ? 8 : 4, 512 / q.threads));
   while (q.per_sm > 1 && row * 2 * q.per_sm > kRowBytes) --q.per_sm;
   q.depth = (int)std::max<size_t>(1, std::min<size_t>(4, kRowBytes / (row * q.per_sm)));
   q.smem = row * q.depth;
@@ -693,10 +702,11 @@ cudaError_t launch_norm(K k, const NormPlan& q, const NormArgs& a, std::atomic<u
 template <typename TX, int W>
 cudaError_t run_fwd(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
   constexpr int N = 32 / W;
-  static std::atomic<unsigned long long> d[7];
+  static std::atomic<unsigned long long> d[8];
   if (q.nv == 0) return launch_norm(norm_long_kernel<TX>, q, a, d[0], s);
-  if (q.v == 1 && !q.block) return launch_norm(norm_kernel<TX, 1, 16, false, 256>, q, a, d[1], s);
-  if (q.v == 1 && q.threads <= 512) return launch_norm(norm_kernel<TX, 1, 16, true, 512>, q, a, d[2], s);
+  if (q.v == 1 && !q.block) return launch_norm(norm_kernel<TX, 1, 8, false, 256>, q, a, d[1], s);
+  if (q.v == 1 && q.threads <= 512) return launch_norm(norm_kernel<TX, 1, 8, true, 512>, q, a, d[2], s);
+  if (q.v == 1 && q.nv == 8) return launch_norm(norm_kernel<TX, 1, 8, true, 1024>, q, a, d[7], s);
   if (q.v == 1) return launch_norm(norm_kernel<TX, 1, 16, true, 1024>, q, a, d[3], s);
   if (!q.block) return launch_norm(norm_kernel<TX, W, N, false, 256>, q, a, d[4], s);
   if (q.threads <= 512) return launch_norm(norm_kernel<TX, W, N, true, 512>, q, a, d[5], s);
@@ -705,10 +715,11 @@ cudaError_t run_fwd(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
 template <typename TX, int W>
 cudaError_t run_grad(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
   constexpr int N = 16 / W;
-  static std::atomic<unsigned long long> d[9];
+  static std::atomic<unsigned long long> d[10];
   if (q.nv == 0) return launch_norm(norm_grad_long_kernel<TX>, q, a, d[0], s);
-  if (q.v == 1 && !q.block) return launch_norm(norm_grad_kernel<TX, 1, 16, false, 256>, q, a, d[1], s);
-  if (q.v == 1 && q.threads <= 512) return launch_norm(norm_grad_kernel<TX, 1, 16, true, 512>, q, a, d[2], s);
+  if (q.v == 1 && !q.block) return launch_norm(norm_grad_kernel<TX, 1, 8, false, 256>, q, a, d[1], s);
+  if (q.v == 1 && q.threads <= 512) return launch_norm(norm_grad_kernel<TX, 1, 8, true, 512>, q, a, d[2], s);
+  if (q.v == 1 && q.nv == 8) return launch_norm(norm_grad_kernel<TX, 1, 8, true, 1024>, q, a, d[9], s);
   if (q.v == 1) return launch_norm(norm_grad_kernel<TX, 1, 16, true, 1024>, q, a, d[3], s);
   if (!q.block) return launch_norm(norm_grad_kernel<TX, W, 2 * N, false, 256>, q, a, d[4], s);
   if (q.nv == 2 * N) return launch_norm(norm_grad_kernel<TX, W, 2 * N, true, 1024>, q, a, d[5], s);

@@ -54,8 +54,21 @@ bool linear_args(const void* x, int64_t T, int dtype, const bakron_packed* w, co
   return true;
 }
 
+// Which forward kernel: a few tokens read in place (or staged at once, fp32)
+// by blocks of 16 or 32 rows; more of them shared by larger blocks; the tcgen05
+// kernel beyond.  fp32 tokens are three times the operand: at 8192 x 8192 and 8
+// tokens the few-token kernel, staging them in parts, took 51 us.
+enum Kernel { kFew, kMid, kMany };
+Kernel forward_kernel(const LinearArgs& a) {
+  if (a.dtype == BAKRON_F32) {
+    if (a.T > kFewTokens) return kMany;
+    return a.T * a.w.nc * 128 * 6 <= 160 * 1024 ? kFew : kMid;
+  }
+  return a.T <= kFewTokens ? kFew : a.T <= kMidTokens ? kMid : kMany;
+}
+
 size_t workspace_bytes(const LinearArgs& a, bool grad) {
-  if (!grad && a.T <= kFewTokens) return 0;
+  if (!grad && forward_kernel(a) == kFew) return 0;
   const int64_t K = grad ? a.w.m : a.w.n;
   return (size_t)(a.dtype == BAKRON_F32 ? 3 : 1) * (size_t)a.T * (size_t)((K + 127) / 128 * 128) * 2;
 }
@@ -66,9 +79,11 @@ bakron_status run_linear(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, vo
   if (need > 0 && (!ws || !aligned_to(ws, 256) || ws_bytes < need)) return BAKRON_ERR_INVALID_ARG;
   a.ws = ws;
   cudaStream_t s = (cudaStream_t)stream;
-  if (!grad && a.T <= kFewTokens)
-    return launch_status(launch_linear_few(a, s));
-  if (!grad && a.T <= kMidTokens && a.dtype != BAKRON_F32) return launch_status(launch_linear_mid(a, s));
+  if (!grad) {
+    const Kernel k = forward_kernel(a);
+    if (k == kFew) return launch_status(launch_linear_few(a, s));
+    if (k == kMid) return launch_status(launch_linear_mid(a, s));
+  }
   if (!prop_tc_supported()) return BAKRON_ERR_UNSUPPORTED;
   return launch_status(grad ? launch_linear_grad(a, s) : launch_linear_fwd(a, s));
 }

@@ -15,8 +15,8 @@ struct LinearArgs {
   void* ws;
 };
 
-// Tokens up to which bakron_linear runs linear_few_kernel, and, of 16-bit
-// types, linear_mid_kernel.
+// Tokens up to which bakron_linear runs linear_few_kernel (fp32: or, for long
+// rows, linear_mid_kernel), and, of 16-bit types, linear_mid_kernel.
 constexpr int64_t kFewTokens = 16;
 constexpr int64_t kMidTokens = 64;
 

@@ -1,4 +1,5 @@
-// bakron_linear for some tens of tokens: Y = X V^T with 9 to 64 rows of X.
+// bakron_linear for some tens of tokens: Y = X V^T with up to 64 rows of X (16 of
+// fp32, which count three times).
 //
 // Each code still meets few enough tokens that its bytes count (m n / 2), but
 // now the activations, read again by every block of rows, would be more than
@@ -263,6 +264,12 @@ cudaError_t by_tokens(const LinearArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_linear_mid(const LinearArgs& a, cudaStream_t s) {
+  if (a.dtype == BAKRON_F32) {
+    const bool wide = a.w.ng == 1 || a.w.g % 128 == 0;
+    if (a.T <= 8)
+      return wide ? run<float, __nv_bfloat16, 3, 1, 1>(a, s) : run<float, __nv_bfloat16, 3, 1, 4>(a, s);
+    return wide ? run<float, __nv_bfloat16, 3, 2, 1>(a, s) : run<float, __nv_bfloat16, 3, 2, 4>(a, s);
+  }
   return a.dtype == BAKRON_BF16 ? by_tokens<__nv_bfloat16>(a, s) : by_tokens<__half>(a, s);
 }
 
