@@ -15,6 +15,13 @@
 // dgamma and dbeta grow in registers and leave the block once, into a row of the
 // workspace; a second launch adds the blocks' rows in a fixed order (no atomics,
 // so the bits do not depend on the run).
+//
+// Rows that do not begin on 16 bytes (an odd d, or an odd address): a warp copies
+// the aligned 16-byte pieces that hold its columns, a thread moves its columns
+// into place out of two of them, and the results are exchanged through shared
+// memory so that they leave by whole words in order.  (Copies of 4 bytes, which
+// need no moving, took 172 us instead of
+// @@ for the gradient of 8192 x 4097 bf16.)
 #include <algorithm>
 #include <type_traits>
 
@@ -37,6 +44,7 @@ struct NormArgs {
   const float* rstd_in;
   float* part;           // [blocks][2][d], NULL without weight gradients
   int depth;             // slots of rows in shared memory
+  bool vectors;          // gamma and beta on 32 bytes
 };
 
 constexpr int kMaxWarps = 32;
@@ -79,74 +87,224 @@ struct alignas(sizeof(TX) * V) Vec {
   TX v[V];
 };
 
-// The rows of a block (or warp) from memory, V elements at a time: loaded when
-// asked for (kAhead false), or copied to shared memory `depth` - 1 rows ahead.
-template <typename TX, int V, int NV, int ARRAYS, bool kAhead>
+// The 16 bytes that begin `at` bytes into 32 (at < 16, the same for the whole warp).
+template <int ES>
+__device__ __forceinline__ uint4 window(const uint4& a, const uint4& b, uint32_t at) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int k = 0; k < 6; ++k) w[k] = at & 8 ? w[k + 2] : w[k];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) w[k] = at & 4 ? w[k + 1] : w[k];
+  if constexpr (ES == 2) {
+    const uint32_t bits = (at & 2) * 8;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], bits);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 ld_piece(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(at)
+               : "memory");
+  return u;
+}
+
+// Shared memory of a warp's columns of one array's row, and of its results, when
+// rows have any alignment.
+template <int NV>
+constexpr uint32_t kWarpRow = NV * 512 + 16;
+constexpr uint32_t kWarpOut = 512;
+
+// The rows of a block (or warp), copied to shared memory `depth` - 1 rows
+// ahead.  kShift: rows of any alignment.
+template <typename TX, int V, int NV, int ARRAYS, bool kBlock, bool kShift>
 struct Rows {
   const TX* src[ARRAYS];
   int64_t d, step, T;
   int64_t next;             // next row to copy
-  uint32_t slot, bytes;     // this thread's place in a slot; bytes of all slots
+  uint32_t slot, bytes;     // the slots of this block (warp), and their bytes
+  uint32_t mine;            // this thread's place in them
   uint32_t fill = 0, read = 0;
   int tid, tpr, depth;
 
-  __device__ __forceinline__ uint32_t slot_bytes() const { return (uint32_t)(ARRAYS * NV * tpr) * 16u; }
+  // The vectors of a thread; a warp has neighbouring ones when it shares pieces.
+  __device__ __forceinline__ int vec(int i) const {
+    return kShift ? (tid & ~31) * NV + (tid & 31) + i * 32 : tid + i * tpr;
+  }
+  __device__ __forceinline__ uint32_t array_bytes() const {
+    return kShift ? (uint32_t)(tpr >> 5) * kWarpRow<NV> : (uint32_t)(NV * tpr) * 16u;
+  }
+  __device__ __forceinline__ uint32_t slot_bytes() const { return ARRAYS * array_bytes(); }
+  // Bytes by which a row misses a 16-byte boundary.
+  __device__ __forceinline__ uint32_t past(const TX* row) const { return (uint32_t)(uintptr_t)row & 15u; }
+
+  // A warp's pieces of one array: those of its columns, whatever lies beside
+  // them in the first and the last, zeros past the row's end.
+  __device__ __forceinline__ void copy_pieces(const TX* row, bool first_row, uint32_t to) {
+    const int lane = tid & 31, c0 = (tid & ~31) * NV * V;
+    const uint32_t shift = past(row);
+    const char* from = reinterpret_cast<const char*>(row + c0) - shift + lane * 16;
+    const int left = ((int)d - c0) * (int)sizeof(TX) + (int)shift;     // bytes from piece 0 on
+    to += (tid >> 5) * kWarpRow<NV> + lane * 16;
+    if (left >= (int)kWarpRow<NV> && !first_row) {
+#pragma unroll
+      for (int i = 0; i <= NV; ++i)
+        if (i < NV || lane == 0)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512)
+                       : "memory");
+    } else if (left > 0) {
+#pragma unroll
+      for (int i = 0; i <= NV; ++i) {
+        const int at = lane * 16 + i * 512;
+        if (i == NV && lane > 0) break;
+        if (at == 0 && first_row && shift && c0 == 0) {
+          // the array's first elements: what is before them is not ours
+          for (int b = (int)shift; b < min(16, left); b += sizeof(TX)) {
+            if constexpr (sizeof(TX) == 2)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + b), "h"(*reinterpret_cast<const uint16_t*>(from + b))
+                           : "memory");
+            else
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + b), "r"(*reinterpret_cast<const uint32_t*>(from + b))
+                           : "memory");
+          }
+          for (int b = max((int)shift, left); b < 16; b += sizeof(TX)) {
+            if constexpr (sizeof(TX) == 2)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + b), "h"((uint16_t)0) : "memory");
+            else
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + b), "r"(0u) : "memory");
+          }
+          continue;
+        }
+        const int n = max(0, min(16, left - at));
+        // (nothing is read from the address that goes with n = 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 512),
+                     "l"(n ? from + i * 512 : from - lane * 16), "r"(n)
+                     : "memory");
+      }
+    }
+  }
   __device__ __forceinline__ void copy() {
     if (next < T) {
 #pragma unroll
-      for (int k = 0; k < ARRAYS; ++k)
+      for (int k = 0; k < ARRAYS; ++k) {
+        if constexpr (kShift) {
+          copy_pieces(src[k] + next * d, next == 0, slot + fill + k * array_bytes());
+        } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (tid + i * tpr) * V;
-          if (c < (int)d)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             slot + fill + (uint32_t)((k * NV + i) * tpr) * 16u),
-                         "l"(src[k] + next * d + c)
-                         : "memory");
+          for (int i = 0; i < NV; ++i) {
+            const int c = vec(i) * V;
+            if (c < (int)d)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                               mine + fill + (uint32_t)((k * NV + i) * tpr) * 16u),
+                           "l"(src[k] + next * d + c)
+                           : "memory");
+          }
         }
+      }
       next += step;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     fill = fill + slot_bytes() == bytes ? 0 : fill + slot_bytes();
   }
   __device__ __forceinline__ void start(int64_t first, void* smem) {
-    if constexpr (kAhead) {
-      next = first;
-      bytes = slot_bytes() * (uint32_t)depth;
-      slot = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)tid * 16u +
-             (tpr == 32 ? (threadIdx.x >> 5) * bytes : 0u);       // one row per warp, or per block
-      for (int p = 0; p < depth - 1; ++p) copy();
-    }
+    next = first;
+    bytes = slot_bytes() * (uint32_t)depth;
+    slot = (uint32_t)__cvta_generic_to_shared(smem) + (kBlock ? 0u : (threadIdx.x >> 5) * bytes);
+    mine = slot + (kShift ? (tid >> 5) * kWarpRow<NV> + (tid & 31) * 16u : tid * 16u);
+    for (int p = 0; p < depth - 1; ++p) copy();
   }
   // Row `row`, the successor of the one asked for before.
   __device__ __forceinline__ void get(int64_t row, Vec<TX, V> (&v)[ARRAYS][NV]) {
-    if constexpr (kAhead) {
-      copy();
-      // `depth` is 1 to 4
-      if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-      else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-      else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-      else asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
+    if constexpr (kShift) __syncwarp();     // the slot to be filled has been read
+    copy();
+    // `depth` is 1 to 4
+    if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if constexpr (kShift) __syncwarp();     // the other lanes' pieces
 #pragma unroll
-    for (int k = 0; k < ARRAYS; ++k)
+    for (int k = 0; k < ARRAYS; ++k) {
+      const uint32_t shift = kShift ? past(src[k] + row * d) : 0u;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (tid + i * tpr) * V;
-        if (c < (int)d) {
-          if constexpr (kAhead) {
-            uint4 u;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                         : "r"(slot + read + (uint32_t)((k * NV + i) * tpr) * 16u)
-                         : "memory");
-            v[k][i] = *reinterpret_cast<const Vec<TX, V>*>(&u);
-          } else {
-            v[k][i] = *reinterpret_cast<const Vec<TX, V>*>(src[k] + row * d + c);
-          }
+        if (vec(i) * V < (int)d) {
+          const uint32_t at = kShift ? mine + read + k * array_bytes() + i * 512u
+                                     : mine + read + (uint32_t)((k * NV + i) * tpr) * 16u;
+          uint4 u = ld_piece(at);
+          if constexpr (kShift) u = window<sizeof(TX)>(u, ld_piece(at + 16u), shift);
+          v[k][i] = *reinterpret_cast<const Vec<TX, V>*>(&u);
         }
       }
-    if constexpr (kAhead) read = read + slot_bytes() == bytes ? 0 : read + slot_bytes();
+    }
+    read = read + slot_bytes() == bytes ? 0 : read + slot_bytes();
+  }
+};
+
+// A row of results, vector by vector in the order of Rows::vec.  With kShift all
+// lanes of a warp come here for every i, whether they have columns or not, and
+// `stage` is the warp's kWarpOut bytes of shared memory.
+template <typename TX, int V, int NV, bool kShift>
+struct RowOut {
+  TX* y;                 // the row
+  uint32_t stage;
+  int d;
+  uint32_t before = 0;   // the last word of this lane's vector before
+
+  __device__ __forceinline__ RowOut(TX* row, int64_t d_, uint32_t stage_) : y(row), stage(stage_), d((int)d_) {}
+  __device__ __forceinline__ void put(int i, int vec, const Vec<TX, V>& o) {
+    const int c = vec * V;
+    if constexpr (!kShift) {
+      *reinterpret_cast<Vec<TX, V>*>(y + c) = o;
+      return;
+    }
+    const int lane = threadIdx.x & 31;
+    if (c - lane * V >= d) return;       // the whole warp
+    uint4 u = *reinterpret_cast<const uint4*>(&o);
+    uint32_t half = 0;
+    if constexpr (sizeof(TX) == 2) {
+      half = ((uint32_t)(uintptr_t)y >> 1) & 1u;
+      if (half) {      // one column on: the lane's first is the last of the lane before
+        const uint32_t p = __shfl_sync(0xffffffffu, lane == 31 ? before : u.w, (lane + 31) & 31);
+        before = u.w;
+        u.w = __funnelshift_l(u.z, u.w, 16);
+        u.z = __funnelshift_l(u.y, u.z, 16);
+        u.y = __funnelshift_l(u.x, u.y, 16);
+        u.x = __funnelshift_l(p, u.x, 16);
+      }
+    }
+    __syncwarp();      // the vector before has been read
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 16), "r"(u.x), "r"(u.y),
+                 "r"(u.z), "r"(u.w)
+                 : "memory");
+    __syncwarp();
+    constexpr int N = 4 / sizeof(TX);                          // columns of a word
+    const int c0 = c - lane * (V - N) - (int)half;             // of this lane's first word
+    uint32_t* to = reinterpret_cast<uint32_t*>(y + c0);
+    const bool inside = (i > 0 || !half) && c + (32 - lane) * V <= d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(stage + lane * 4 + j * 128) : "memory");
+      if (inside || (c0 + j * 32 * N + N <= d && !(half && i == 0 && j == 0 && lane == 0))) {
+        to[j * 32] = w;
+      } else if constexpr (N == 2) {
+        // the first or the last column of a word
+        const int a = c0 + j * 64;
+        TX* one = y + a;
+        if (half && i == 0 && j == 0 && lane == 0) {
+          if (a + 1 < d) *reinterpret_cast<uint16_t*>(one + 1) = (uint16_t)(w >> 16);
+        } else if (a < d) {
+          *reinterpret_cast<uint16_t*>(one) = (uint16_t)w;
+        }
+      }
+    }
+    // the last column of the warp begins a word that is not its own
+    if constexpr (N == 2)
+      if (half && lane == 31 && (i == NV - 1 || c + V == d) && c + V - 1 < d) y[c + V - 1] = o.v[V - 1];
   }
 };
 
@@ -185,7 +343,7 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // V elements to and from fp32, two at a time for the 16-bit types.
 template <typename TX, int V>
 __device__ __forceinline__ void widen(float (&f)[V], const Vec<TX, V>& v) {
-  if constexpr (V > 1 && sizeof(TX) == 2) {
+  if constexpr (sizeof(TX) == 2) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(&v);
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) {
@@ -200,12 +358,12 @@ __device__ __forceinline__ void widen(float (&f)[V], const Vec<TX, V>& v) {
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = to_float(v.v[e]);
+    for (int e = 0; e < V; ++e) f[e] = v.v[e];
   }
 }
 template <typename TX, int V>
 __device__ __forceinline__ void narrow(Vec<TX, V>& v, const float (&f)[V]) {
-  if constexpr (V > 1 && sizeof(TX) == 2) {
+  if constexpr (sizeof(TX) == 2) {
     uint32_t* u = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) {
@@ -219,30 +377,36 @@ __device__ __forceinline__ void narrow(Vec<TX, V>& v, const float (&f)[V]) {
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) v.v[e] = from_float<TX>(f[e]);
+    for (int e = 0; e < V; ++e) v.v[e] = f[e];
   }
 }
 
-// gamma and beta of V columns (1 and 0 where there are none).
+// V values of gamma or beta (`none` where there is no array, or no column).
+template <int V, bool kShift>
+__device__ __forceinline__ Vec<float, V> param(const float* g, float none, int c, int d, bool vectors) {
+  Vec<float, V> r;
+  if (g && (kShift ? vectors && c + V <= d : c < d)) {
+    r = *reinterpret_cast<const Vec<float, V>*>(g + c);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.v[e] = kShift && g && c + e < d ? g[c + e] : none;
+  }
+  return r;
+}
+
+// Columns past the row's end become `v` (they are 0 as copied, which is right for
+// every sum but that of the squared deviations).
 template <int V>
-__device__ __forceinline__ void params(Vec<float, V>& g, Vec<float, V>& b, const NormArgs& p, int c) {
-  if (p.gamma && c < (int)p.d) {
-    g = *reinterpret_cast<const Vec<float, V>*>(p.gamma + c);
-  } else {
+__device__ __forceinline__ void fill_tail(float (&f)[V], int c, int d, float v) {
+  if (c + V > d) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) g.v[e] = 1.f;
-  }
-  if (p.beta && c < (int)p.d) {
-    b = *reinterpret_cast<const Vec<float, V>*>(p.beta + c);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) b.v[e] = 0.f;
+    for (int e = 0; e < V; ++e)
+      if (c + e >= d) f[e] = v;
   }
 }
 
-template <typename TX, int V, int NV, bool kBlock, int MAXB>
-__global__ void __launch_bounds__(MAXB, V == 1 && MAXB <= 512 ? 2 : 1) norm_kernel(const __grid_constant__ NormArgs p) {
-  constexpr bool kAhead = V > 1;
+template <typename TX, int V, int NV, bool kBlock, bool kShift, int MAXB>
+__global__ void __launch_bounds__(MAXB, MAXB <= 256 ? 2 : 1) norm_kernel(const __grid_constant__ NormArgs p) {
   extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
@@ -253,7 +417,9 @@ __global__ void __launch_bounds__(MAXB, V == 1 && MAXB <= 512 ? 2 : 1) norm_kern
   const int64_t step = (int64_t)gridDim.x * rows_at_once;
   const float inv_d = 1.f / (float)p.d;
   const int d = (int)p.d;
-  Rows<TX, V, NV, 1, kAhead> rows;
+  // R rows at a time: their sums share the barriers and the shuffles' latency
+  constexpr int R = kBlock && MAXB <= 512 ? 2 : 1;
+  Rows<TX, V, NV, 1, kBlock, kShift> rows;
   rows.src[0] = static_cast<const TX*>(p.x);
   rows.d = p.d;
   rows.step = step;
@@ -262,15 +428,8 @@ __global__ void __launch_bounds__(MAXB, V == 1 && MAXB <= 512 ? 2 : 1) norm_kern
   rows.tpr = tpr;
   rows.depth = p.depth;
   rows.start(row0, dsm);
-  // gamma and beta stay in registers when there is room
-  constexpr bool kKeep = NV * V <= 16;
-  Vec<float, V> gk[kKeep ? NV : 1], bk[kKeep ? NV : 1];
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) params(gk[i], bk[i], p, (tid + i * tpr) * V);
-  }
-  // R rows at a time: their sums share the barriers and the shuffles' latency
-  constexpr int R = kBlock && kAhead ? 2 : 1;
+  const uint32_t stage = rows.slot + rows.bytes * (kBlock ? 1 : rows_at_once - (threadIdx.x >> 5)) +
+                         (threadIdx.x >> 5) * kWarpOut;     // after all slots
   for (int64_t row = row0; row < p.T; row += R * step) {
     float f[R][NV][V];
     float sum[R], sq[R];
@@ -279,21 +438,17 @@ __global__ void __launch_bounds__(MAXB, V == 1 && MAXB <= 512 ? 2 : 1) norm_kern
     for (int q = 0; q < R; ++q) {
       Vec<TX, V> v[1][NV];
       rows.get(row + q * step, v);
-      sum[q] = sq[q] = 0.f;
       p2[q] = f2(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if ((tid + i * tpr) * V < d) {
+        const int c = rows.vec(i) * V;
+        if (c < d) {
           widen(f[q][i], v[0][i]);
-          if constexpr (V == 1) {
-            sum[q] += f[q][i][0];
-          } else {
 #pragma unroll
-            for (int e = 0; e < V; e += 2) p2[q] = add2(p2[q], F2{f[q][i][e], f[q][i][e + 1]});
-          }
+          for (int e = 0; e < V; e += 2) p2[q] = add2(p2[q], F2{f[q][i][e], f[q][i][e + 1]});
         }
       }
-      if constexpr (V > 1) sum[q] = p2[q].x + p2[q].y;
+      sum[q] = p2[q].x + p2[q].y;
     }
     row_sums<kBlock, R>(sum, red, slot);
 #pragma unroll
@@ -303,22 +458,19 @@ __global__ void __launch_bounds__(MAXB, V == 1 && MAXB <= 512 ? 2 : 1) norm_kern
       p2[q] = f2(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if ((tid + i * tpr) * V < d) {
-          if constexpr (V == 1) {
-            f[q][i][0] -= mu;
-            sq[q] = fmaf(f[q][i][0], f[q][i][0], sq[q]);
-          } else {
+        const int c = rows.vec(i) * V;
+        if (c < d) {
+          if constexpr (kShift) fill_tail(f[q][i], c, d, mu);
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              const F2 t = add2(F2{f[q][i][e], f[q][i][e + 1]}, f2(-mu));
-              p2[q] = fma2(t, t, p2[q]);
-              f[q][i][e] = t.x;
-              f[q][i][e + 1] = t.y;
-            }
+          for (int e = 0; e < V; e += 2) {
+            const F2 t = add2(F2{f[q][i][e], f[q][i][e + 1]}, f2(-mu));
+            p2[q] = fma2(t, t, p2[q]);
+            f[q][i][e] = t.x;
+            f[q][i][e + 1] = t.y;
           }
         }
       }
-      if constexpr (V > 1) sq[q] = p2[q].x + p2[q].y;
+      sq[q] = p2[q].x + p2[q].y;
     }
     row_sums<kBlock, R>(sq, red, slot);
 #pragma unroll
@@ -330,38 +482,32 @@ __global__ void __launch_bounds__(MAXB, V == 1 && MAXB <= 512 ? 2 : 1) norm_kern
         if (p.mean) p.mean[at] = sum[q];
         if (p.rstd) p.rstd[at] = r;
       }
-      TX* y = static_cast<TX*>(p.y) + at * p.d;
+      RowOut<TX, V, NV, kShift> out(static_cast<TX*>(p.y) + at * p.d, p.d, stage);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (tid + i * tpr) * V;
+        const int c = rows.vec(i) * V;
+        if (!kShift && c >= d) continue;
+        Vec<TX, V> o;
         if (c < d) {
-          if constexpr (!kKeep) params(gk[0], bk[0], p, c);
-          const Vec<float, V>&g = gk[kKeep ? i : 0], &b = bk[kKeep ? i : 0];
-          Vec<TX, V> o;
-          if constexpr (V == 1) {
-            f[q][i][0] = fmaf(f[q][i][0] * r, g.v[0], b.v[0]);
-          } else {
+          const Vec<float, V> g = param<V, kShift>(p.gamma, 1.f, c, d, p.vectors);
+          const Vec<float, V> b = param<V, kShift>(p.beta, 0.f, c, d, p.vectors);
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              const F2 t = fma2(mul2(F2{f[q][i][e], f[q][i][e + 1]}, f2(r)), F2{g.v[e], g.v[e + 1]},
-                                F2{b.v[e], b.v[e + 1]});
-              f[q][i][e] = t.x;
-              f[q][i][e + 1] = t.y;
-            }
+          for (int e = 0; e < V; e += 2) {
+            const F2 t = fma2(mul2(F2{f[q][i][e], f[q][i][e + 1]}, f2(r)), F2{g.v[e], g.v[e + 1]},
+                              F2{b.v[e], b.v[e + 1]});
+            f[q][i][e] = t.x;
+            f[q][i][e + 1] = t.y;
           }
           narrow(o, f[q][i]);
-          *reinterpret_cast<Vec<TX, V>*>(y + c) = o;
         }
+        out.put(i, rows.vec(i), o);
       }
     }
   }
 }
 
-__device__ __forceinline__ float norm_h(float x, float mu, float r) { return (x - mu) * r; }
-
-template <typename TX, int V, int NV, bool kBlock, int MAXB>
-__global__ void __launch_bounds__(MAXB, MAXB <= 256 || V == 1 ? (MAXB <= 512 ? 2 : 1) : 1) norm_grad_kernel(const __grid_constant__ NormArgs p) {
-  constexpr bool kAhead = V > 1;
+template <typename TX, int V, int NV, bool kBlock, bool kShift, int MAXB>
+__global__ void __launch_bounds__(MAXB, MAXB <= 256 ? 2 : 1) norm_grad_kernel(const __grid_constant__ NormArgs p) {
   extern __shared__ __align__(16) uint8_t dsm[];
   __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
@@ -372,19 +518,9 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 || V == 1 ? (MAXB <= 512 ? 2
   const int64_t step = (int64_t)gridDim.x * rows_at_once;
   const float inv_d = 1.f / (float)p.d;
   const int d = (int)p.d;
-  // gamma stays in registers when there is room
-  constexpr bool kKeep = NV * V <= 16 && MAXB <= 512;
-  Vec<float, V> gk[kKeep ? NV : 1], unused;
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) params(gk[i], unused, p, (tid + i * tpr) * V);
-  }
-  float dg[NV][V], db[NV][V];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < V; ++e) dg[i][e] = db[i][e] = 0.f;
-  Rows<TX, V, NV, 2, kAhead> rows;
+  // R rows at a time: their sums share the barrier and the shuffles' latency
+  constexpr int R = kBlock && MAXB <= 512 ? 2 : 1;
+  Rows<TX, V, NV, 2, kBlock, kShift> rows;
   rows.src[0] = static_cast<const TX*>(p.x);
   rows.src[1] = static_cast<const TX*>(p.dy);
   rows.d = p.d;
@@ -393,9 +529,21 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 || V == 1 ? (MAXB <= 512 ? 2
   rows.tid = tid;
   rows.tpr = tpr;
   rows.depth = p.depth;
+  // gamma stays in registers when there is room
+  constexpr bool kKeep = NV * V <= 16 && MAXB <= 512;
+  Vec<float, V> gk[kKeep ? NV : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) gk[i] = param<V, kShift>(p.gamma, 1.f, rows.vec(i) * V, d, p.vectors);
+  }
+  float dg[NV][V], db[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < V; ++e) dg[i][e] = db[i][e] = 0.f;
   rows.start(lead, dsm);
-  // R rows at a time: their sums share the barrier and the shuffles' latency
-  constexpr int R = kBlock && kAhead && MAXB <= 512 ? 2 : 1;
+  const uint32_t stage = rows.slot + rows.bytes * (kBlock ? 1 : rows_at_once - (threadIdx.x >> 5)) +
+                         (threadIdx.x >> 5) * kWarpOut;     // after all slots
   float mu_next[R], r_next[R];
   auto stats = [&](int64_t row) {
 #pragma unroll
@@ -422,75 +570,63 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 || V == 1 ? (MAXB <= 512 ? 2
     for (int q = 0; q < R; ++q) {
       rows.get(row + q * step, v[q]);
       const bool there = row + q * step < p.T;
-      float s1 = 0.f, s2 = 0.f;
       F2 t1 = f2(0.f), t2 = f2(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (tid + i * tpr) * V;
+        const int c = rows.vec(i) * V;
         if (c < d && there) {
-          if constexpr (!kKeep) params(gk[0], unused, p, c);
+          if constexpr (!kKeep) gk[0] = param<V, kShift>(p.gamma, 1.f, c, d, p.vectors);
           const Vec<float, V>& g = gk[kKeep ? i : 0];
           float fx[V], fw[V];
           widen(fx, v[q][0][i]);
           widen(fw, v[q][1][i]);
-          if constexpr (V == 1) {
-            const float h = norm_h(fx[0], mu[q], r[q]), w = fw[0], a = w * g.v[0];
-            s1 += a;
-            s2 = fmaf(a, h, s2);
-            dg[i][0] = fmaf(w, h, dg[i][0]);
-            db[i][0] += w;
-          } else {
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              const F2 h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu[q])), f2(r[q])), w = F2{fw[e], fw[e + 1]};
-              const F2 a = mul2(w, F2{g.v[e], g.v[e + 1]});
-              t1 = add2(t1, a);
-              t2 = fma2(a, h, t2);
-              const F2 x = fma2(w, h, F2{dg[i][e], dg[i][e + 1]}), z = add2(F2{db[i][e], db[i][e + 1]}, w);
-              dg[i][e] = x.x;
-              dg[i][e + 1] = x.y;
-              db[i][e] = z.x;
-              db[i][e + 1] = z.y;
-            }
+          for (int e = 0; e < V; e += 2) {
+            const F2 h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu[q])), f2(r[q])), w = F2{fw[e], fw[e + 1]};
+            const F2 a = mul2(w, F2{g.v[e], g.v[e + 1]});
+            t1 = add2(t1, a);
+            t2 = fma2(a, h, t2);
+            const F2 x = fma2(w, h, F2{dg[i][e], dg[i][e + 1]}), z = add2(F2{db[i][e], db[i][e + 1]}, w);
+            dg[i][e] = x.x;
+            dg[i][e + 1] = x.y;
+            db[i][e] = z.x;
+            db[i][e + 1] = z.y;
           }
         }
       }
-      sums[2 * q] = V > 1 ? t1.x + t1.y : s1;
-      sums[2 * q + 1] = V > 1 ? t2.x + t2.y : s2;
+      sums[2 * q] = t1.x + t1.y;
+      sums[2 * q + 1] = t2.x + t2.y;
     }
     row_sums<kBlock, 2 * R>(sums, red, slot);
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       const int64_t at = row + q * step;
       if (at >= p.T) break;
-      TX* dx = static_cast<TX*>(p.y) + at * p.d;
+      RowOut<TX, V, NV, kShift> out(static_cast<TX*>(p.y) + at * p.d, p.d, stage);
       // dX = r a - (r m1) - h (r m2): three constants of the row
       const float m1 = r[q] * (sums[2 * q] * inv_d), m2 = r[q] * (sums[2 * q + 1] * inv_d);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (tid + i * tpr) * V;
+        const int c = rows.vec(i) * V;
+        if (!kShift && c >= d) continue;
+        Vec<TX, V> o;
         if (c < d) {
-          if constexpr (!kKeep) params(gk[0], unused, p, c);
+          if constexpr (!kKeep) gk[0] = param<V, kShift>(p.gamma, 1.f, c, d, p.vectors);
           const Vec<float, V>& g = gk[kKeep ? i : 0];
-          Vec<TX, V> o;
           float fx[V], fw[V], fo[V];
           widen(fx, v[q][0][i]);
           widen(fw, v[q][1][i]);
-          if constexpr (V == 1) {
-            fo[0] = fmaf(-norm_h(fx[0], mu[q], r[q]), m2, fmaf(r[q], fw[0] * g.v[0], -m1));
-          } else {
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              const F2 h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu[q])), f2(r[q]));
-              const F2 a = mul2(F2{fw[e], fw[e + 1]}, F2{g.v[e], g.v[e + 1]});
-              const F2 x = fma2(h, f2(-m2), fma2(a, f2(r[q]), f2(-m1)));
-              fo[e] = x.x;
-              fo[e + 1] = x.y;
-            }
+          for (int e = 0; e < V; e += 2) {
+            const F2 h = mul2(add2(F2{fx[e], fx[e + 1]}, f2(-mu[q])), f2(r[q]));
+            const F2 a = mul2(F2{fw[e], fw[e + 1]}, F2{g.v[e], g.v[e + 1]});
+            const F2 x = fma2(h, f2(-m2), fma2(a, f2(r[q]), f2(-m1)));
+            fo[e] = x.x;
+            fo[e + 1] = x.y;
           }
           narrow(o, fo);
-          *reinterpret_cast<Vec<TX, V>*>(dx + c) = o;
         }
+        out.put(i, rows.vec(i), o);
       }
     }
   }
@@ -499,39 +635,48 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 || V == 1 ? (MAXB <= 512 ? 2
   if constexpr (kBlock) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(tid + i * tpr) * V;
-      if (c < p.d) {
-        Vec<float, V> a, b;
+      const int c = rows.vec(i) * V;
+      if constexpr (kShift) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (c + e < d) {
+            o[c + e] = dg[i][e];
+            o[p.d + c + e] = db[i][e];
+          }
+      } else if (c < d) {
+        Vec<float, V> g, b;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          a.v[e] = dg[i][e];
+          g.v[e] = dg[i][e];
           b.v[e] = db[i][e];
         }
-        *reinterpret_cast<Vec<float, V>*>(o + c) = a;
-        if constexpr (V == 1) o[p.d + c] = b.v[0];
-        else *reinterpret_cast<Vec<float, V>*>(o + p.d + c) = b;
+        *reinterpret_cast<Vec<float, V>*>(o + c) = g;
+        *reinterpret_cast<Vec<float, V>*>(o + p.d + c) = b;
       }
     }
   } else {
-    // the warps of the block add theirs one after the other, where the rows were
-    float* sum = reinterpret_cast<float*>(dsm);     // [2][d]
+    // the warps' sums where their rows were, one line per column of a vector
+    // (its length keeps both sides free of bank conflicts), then added in order
+    constexpr int kLine = 32 + 32 / V, kWarp = 2 * NV * V * kLine;
+    float* sum = reinterpret_cast<float*>(dsm);
     __syncthreads();
-    for (int w = 0; w < rows_at_once; ++w) {
-      if ((int)(threadIdx.x >> 5) == w) {
+    float* mine = sum + (threadIdx.x >> 5) * kWarp + tid;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const int64_t c = (int64_t)(tid + i * tpr) * V + e;
-            if (c < p.d) {
-              sum[c] = (w ? sum[c] : 0.f) + dg[i][e];
-              sum[p.d + c] = (w ? sum[p.d + c] : 0.f) + db[i][e];
-            }
-          }
+      for (int e = 0; e < V; ++e) {
+        mine[(i * V + e) * kLine] = dg[i][e];
+        mine[(NV * V + i * V + e) * kLine] = db[i][e];
       }
-      __syncthreads();
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
+      const int col = c < d ? c : c - d, vec = col / V;
+      const float* at = sum + ((c < d ? 0 : NV * V) + vec / 32 * V + col % V) * kLine + vec % 32;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v += at[w * kWarp];
+      o[c] = v;
     }
-    for (int64_t c = threadIdx.x; c < 2 * p.d; c += blockDim.x) o[c] = sum[c];
   }
 }
 
@@ -625,60 +770,65 @@ __global__ void __launch_bounds__(512) norm_join_kernel(const float* __restrict_
   }
 }
 
-// How a shape runs: vector width, vectors per thread, threads per row, and for
-// the block-per-row kernels the rows in flight.
+// How a shape runs: vectors per thread, threads per row, and the rows in flight.
 struct NormPlan {
-  int v, nv;        // nv 0: the long-row kernels
+  int nv;           // 0: the long-row kernels
   bool block;       // one block per row, else one warp
+  bool shift;       // rows of any alignment
   int threads;      // of a block
   int depth, per_sm;
   size_t smem;
 };
 
-// Shared memory per SM that the rows in flight may take (of 228 KB).
-constexpr size_t kRowBytes = 200 * 1024;
+// Shared memory per SM that the rows in flight may take (of 228 KB), and one row.
+constexpr size_t kRowBytes = 200 * 1024, kMaxRow = 224 * 1024;
 
-NormPlan norm_plan(int64_t d, int dtype, bool aligned, int arrays) {
+NormPlan norm_plan(int64_t T, int64_t d, int dtype, bool aligned, int arrays) {
   NormPlan q = {};
-  const int wide = dtype == BAKRON_F32 ? 4 : 8;
-  q.v = (aligned && d % wide == 0) ? wide : 1;
-  const int64_t vecs = d / q.v;
+  const int v = dtype == BAKRON_F32 ? 4 : 8;
+  q.shift = !aligned || d % v != 0;
+  const int64_t vecs = (d + v - 1) / v;
+  const size_t extra = q.shift ? (size_t)arrays * 16 : 0, out = q.shift ? kWarpOut : 0;   // per warp
   // columns per thread: 32 forward, 16 backward (two sums per column live in
-  // registers there), 32 once a block of 896 threads is too small for that; of
-  // rows that are read by elements 8, or 16 for the longest
-  const int most = q.v == 1 ? (vecs > 8 * 1024 ? 16 : 8)
-                            : arrays == 1 || vecs > 16 / q.v * 896 ? 32 / q.v : 16 / q.v;
-  if (vecs <= 32 * (q.v == 1 ? 8 : 32 / q.v)) {        // 256 odd columns, 1024 others: a warp per row
+  // registers there), 32 once a block of 896 threads is too small for that
+  const int most = arrays == 1 || vecs > 16 / v * 896 ? 32 / v : 16 / v;
+  const bool few = T <= sm_count() && vecs > 32 && vecs <= 1024;
+  if (vecs <= 32 * (32 / v) && !few) {        // 1024 columns: a warp per row
     q.threads = 256;
-    q.nv = q.v == 1 ? 8 : 32 / q.v;
+    q.nv = 32 / v;
     q.per_sm = arrays == 1 ? 4 : 2;
-    if (q.v > 1) {
-      q.depth = 3;
-      q.smem = (size_t)8 * q.depth * arrays * q.nv * 32 * 16;
-    }
-    if (arrays == 2) q.smem = std::max(q.smem, (size_t)(2 * d) * 4);    // the warps' sums
+    q.depth = 3;
+    q.smem = (size_t)8 * (q.depth * (arrays * q.nv * 32 * 16 + extra) + out);
+    // (the warps' sums need 8 x 2 x 32 x (32 + 32 / v) floats, less than this)
     return q;
   }
   q.block = true;
-  if (vecs > (int64_t)1024 * most) {
+  if (few) {
+    // one row per block at most: its latency counts, which a vector per thread keeps
+    // shortest (37 x 1111 fp32: @@ us, 8 with eight vectors)
+    q.nv = 1;
+    q.threads = (int)((vecs + 31) / 32 * 32);
+    q.per_sm = 1;
+    q.depth = 1;
+    q.smem = (size_t)arrays * q.threads * 16 + (extra + out) * (q.threads / 32);
+    return q;
+  }
+  const int threads = (int)std::min<int64_t>(2048, ((vecs + most - 1) / most + 31) / 32 * 32);
+  const size_t row = (size_t)arrays * most * threads * 16 + extra * (threads / 32);
+  const size_t fixed = out * (threads / 32);
+  if (threads > 1024 || row + fixed > kMaxRow) {
     q.threads = 1024;
     q.per_sm = 2;
     return q;
   }
   q.nv = most;
-  // a row of 32 threads would be taken for a warp's
-  q.threads = std::max(64, (int)(((vecs + q.nv - 1) / q.nv + 31) / 32 * 32));
-  if (q.v == 1) {
-    q.per_sm = std::max(1, 1024 / q.threads);
-    return q;
-  }
+  q.threads = threads;
   // blocks per SM: what the registers allow (128 a thread), fewer for long rows; as many rows
   // ahead as fit beside that
-  const size_t row = (size_t)arrays * q.nv * q.threads * 16;
   q.per_sm = std::max(1, std::min(arrays == 1 ? 8 : 4, 512 / q.threads));
-  while (q.per_sm > 1 && row * 2 * q.per_sm > kRowBytes) --q.per_sm;
-  q.depth = (int)std::max<size_t>(1, std::min<size_t>(4, kRowBytes / (row * q.per_sm)));
-  q.smem = row * q.depth;
+  while (q.per_sm > 1 && (row * 2 + fixed) * q.per_sm > kRowBytes) --q.per_sm;
+  q.depth = (int)std::max<size_t>(1, std::min<size_t>(4, (kRowBytes / q.per_sm - fixed) / row));
+  q.smem = row * q.depth + fixed;
   return q;
 }
 
@@ -699,33 +849,37 @@ cudaError_t launch_norm(K k, const NormPlan& q, const NormArgs& a, std::atomic<u
   return cudaGetLastError();
 }
 
-template <typename TX, int W>
+template <typename TX, int W, bool kShift>
 cudaError_t run_fwd(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
   constexpr int N = 32 / W;
-  static std::atomic<unsigned long long> d[8];
-  if (q.nv == 0) return launch_norm(norm_long_kernel<TX>, q, a, d[0], s);
-  if (q.v == 1 && !q.block) return launch_norm(norm_kernel<TX, 1, 8, false, 256>, q, a, d[1], s);
-  if (q.v == 1 && q.threads <= 512) return launch_norm(norm_kernel<TX, 1, 8, true, 512>, q, a, d[2], s);
-  if (q.v == 1 && q.nv == 8) return launch_norm(norm_kernel<TX, 1, 8, true, 1024>, q, a, d[7], s);
-  if (q.v == 1) return launch_norm(norm_kernel<TX, 1, 16, true, 1024>, q, a, d[3], s);
-  if (!q.block) return launch_norm(norm_kernel<TX, W, N, false, 256>, q, a, d[4], s);
-  if (q.threads <= 512) return launch_norm(norm_kernel<TX, W, N, true, 512>, q, a, d[5], s);
-  return launch_norm(norm_kernel<TX, W, N, true, 1024>, q, a, d[6], s);
+  static std::atomic<unsigned long long> d[4];
+  if (q.nv == 1) return launch_norm(norm_kernel<TX, W, 1, true, kShift, 1024>, q, a, d[3], s);
+  if (!q.block) return launch_norm(norm_kernel<TX, W, N, false, kShift, 256>, q, a, d[0], s);
+  if (q.threads <= 512) return launch_norm(norm_kernel<TX, W, N, true, kShift, 512>, q, a, d[1], s);
+  return launch_norm(norm_kernel<TX, W, N, true, kShift, 1024>, q, a, d[2], s);
+}
+template <typename TX, int W>
+cudaError_t run_fwd(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
+  static std::atomic<unsigned long long> d;
+  if (q.nv == 0) return launch_norm(norm_long_kernel<TX>, q, a, d, s);
+  return q.shift ? run_fwd<TX, W, true>(q, a, s) : run_fwd<TX, W, false>(q, a, s);
+}
+template <typename TX, int W, bool kShift>
+cudaError_t run_grad(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
+  constexpr int N = 16 / W;
+  static std::atomic<unsigned long long> d[6];
+  if (q.nv == 1) return launch_norm(norm_grad_kernel<TX, W, 1, true, kShift, 1024>, q, a, d[5], s);
+  if (!q.block) return launch_norm(norm_grad_kernel<TX, W, 2 * N, false, kShift, 256>, q, a, d[0], s);
+  if (q.nv == 2 * N) return launch_norm(norm_grad_kernel<TX, W, 2 * N, true, kShift, 1024>, q, a, d[1], s);
+  if (q.threads <= 256) return launch_norm(norm_grad_kernel<TX, W, N, true, kShift, 256>, q, a, d[2], s);
+  if (q.threads <= 512) return launch_norm(norm_grad_kernel<TX, W, N, true, kShift, 512>, q, a, d[3], s);
+  return launch_norm(norm_grad_kernel<TX, W, N, true, kShift, 896>, q, a, d[4], s);
 }
 template <typename TX, int W>
 cudaError_t run_grad(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
-  constexpr int N = 16 / W;
-  static std::atomic<unsigned long long> d[10];
-  if (q.nv == 0) return launch_norm(norm_grad_long_kernel<TX>, q, a, d[0], s);
-  if (q.v == 1 && !q.block) return launch_norm(norm_grad_kernel<TX, 1, 8, false, 256>, q, a, d[1], s);
-  if (q.v == 1 && q.threads <= 512) return launch_norm(norm_grad_kernel<TX, 1, 8, true, 512>, q, a, d[2], s);
-  if (q.v == 1 && q.nv == 8) return launch_norm(norm_grad_kernel<TX, 1, 8, true, 1024>, q, a, d[9], s);
-  if (q.v == 1) return launch_norm(norm_grad_kernel<TX, 1, 16, true, 1024>, q, a, d[3], s);
-  if (!q.block) return launch_norm(norm_grad_kernel<TX, W, 2 * N, false, 256>, q, a, d[4], s);
-  if (q.nv == 2 * N) return launch_norm(norm_grad_kernel<TX, W, 2 * N, true, 1024>, q, a, d[5], s);
-  if (q.threads <= 256) return launch_norm(norm_grad_kernel<TX, W, N, true, 256>, q, a, d[6], s);
-  if (q.threads <= 512) return launch_norm(norm_grad_kernel<TX, W, N, true, 512>, q, a, d[7], s);
-  return launch_norm(norm_grad_kernel<TX, W, N, true, 896>, q, a, d[8], s);
+  static std::atomic<unsigned long long> d;
+  if (q.nv == 0) return launch_norm(norm_grad_long_kernel<TX>, q, a, d, s);
+  return q.shift ? run_grad<TX, W, true>(q, a, s) : run_grad<TX, W, false>(q, a, s);
 }
 
 bool norm_args_ok(int64_t T, int64_t d, int dtype) {
@@ -736,7 +890,7 @@ bool norm_args_ok(int64_t T, int64_t d, int dtype) {
 size_t grad_bytes(int64_t T, int64_t d) {
   int64_t rows = 0;
   for (int dt : {BAKRON_F32, BAKRON_BF16})
-    for (bool al : {false, true}) rows = std::max(rows, norm_blocks(norm_plan(d, dt, al, 2), T));
+    for (bool al : {false, true}) rows = std::max(rows, norm_blocks(norm_plan(T, d, dt, al, 2), T));
   return (size_t)(rows * 2 * d) * sizeof(float);
 }
 
@@ -763,7 +917,8 @@ extern "C" bakron_status bakron_layernorm(const void* X, int64_t T, int64_t d, i
   a.mean = mean;
   a.rstd = rstd;
   const bool al = aligned_to(X, 16) && aligned_to(Y, 16) && aligned_to(gamma, 32) && aligned_to(beta, 32);
-  const NormPlan q = norm_plan(d, dtype, al, 1);
+  const NormPlan q = norm_plan(T, d, dtype, al, 1);
+  a.vectors = aligned_to(gamma, 32) && aligned_to(beta, 32);
   a.depth = q.depth;
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = dtype == BAKRON_F32    ? run_fwd<float, 4>(q, a, s)
@@ -809,7 +964,8 @@ extern "C" bakron_status bakron_layernorm_grad(const void* dY, const void* X, in
   a.rstd_in = rstd;
   a.part = dgamma ? static_cast<float*>(ws) : nullptr;
   const bool al = aligned_to(X, 16) && aligned_to(dY, 16) && aligned_to(dX, 16) && aligned_to(gamma, 32);
-  const NormPlan q = norm_plan(d, dtype, al, 2);
+  const NormPlan q = norm_plan(T, d, dtype, al, 2);
+  a.vectors = aligned_to(gamma, 32);
   a.depth = q.depth;
   const cudaError_t e = dtype == BAKRON_F32    ? run_grad<float, 4>(q, a, s)
                         : dtype == BAKRON_BF16 ? run_grad<__nv_bfloat16, 8>(q, a, s)

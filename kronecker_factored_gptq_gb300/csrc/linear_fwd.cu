@@ -86,6 +86,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 
+// Two fp32 values with one instruction: of short groups, whose accumulators are
+// read most often, these additions are what the epilogue is bound by.
+__device__ __forceinline__ void add2(uint32_t& x, uint32_t& y, uint32_t a, uint32_t b) {
+  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n"
+      " mov.b64 {%0, %1}, p;\n}\n"
+      : "+r"(x), "+r"(y)
+      : "r"(a), "r"(b));
+}
+__device__ __forceinline__ void fma2(float& x, float& y, float s, uint32_t a, uint32_t b) {
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n mov.b64 r, {%3, %4};\n"
+      " fma.rn.f32x2 p, q, r, p;\n mov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(s), "r"(a), "r"(b));
+}
+
 struct Bars {
   unsigned long long full_b[kMaxStages], empty_b[kMaxStages], full_a[kWStages], empty_a[kWStages];
   unsigned long long acc_full[2], acc_empty[2], done;
@@ -350,37 +365,27 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
           const uint32_t ws = seq & 1;
           go = wait_or_abort(fb + 8u * (uint32_t)rg.s, rg.parity, &bars.abort, a.status) &&
                wait_or_abort(fa + 8u * ws, (seq >> 1) & 1, &bars.abort, a.status);
-          // the accumulators of the chunk's first two units: unit u - 2 has been read
-          if (u >= 2) {
-            go = go && wait_or_abort(ae + 8u * (u & 1), ((u >> 1) & 1) ^ 1u, &bars.abort, a.status);
-            if (UPC > 1) go = go && wait_or_abort(ae + 8u * ((u + 1) & 1), (((u + 1) >> 1) & 1) ^ 1u, &bars.abort, a.status);
-          }
-          go = __all_sync(0xffffffffu, go);
-          if (!go) break;
           fence_after_sync();
           const uint64_t db = desc_b0 + (uint32_t)rg.s * stage16;
           const uint32_t ta = tmem_a + ws * 64u;
 #pragma unroll
-          for (int q4 = 0; q4 < UPC; q4 += 2) {
-            if (q4 == 2) {                    // units of 32 columns: two more
-              go = wait_or_abort(ae + 8u * ((u + 2) & 1), (((u + 2) >> 1) & 1) ^ 1u, &bars.abort, a.status) &&
-                   wait_or_abort(ae + 8u * ((u + 3) & 1), (((u + 3) >> 1) & 1) ^ 1u, &bars.abort, a.status);
-              go = __all_sync(0xffffffffu, go);
-              if (!go) break;
-              fence_after_sync();
-            }
+          for (int i = 0; i < UPC; ++i) {
+            const uint32_t v = u + i, buf = v & 1;
+            // the accumulator: unit v - 2 has been read
+            go = go && (v < 2 || wait_or_abort(ae + 8u * buf, ((v >> 1) & 1) ^ 1u, &bars.abort, a.status));
+            go = __all_sync(0xffffffffu, go);
+            if (!go) break;
+            fence_after_sync();
             if (elect_one()) {
+              const uint32_t d = tmem + buf * acc_cols;
 #pragma unroll
-              for (int j = q4 * KU; j < (UPC > 1 ? (q4 + 2) * KU : 8); ++j) {
-                const uint32_t buf = (u + j / KU) & 1;
-                const uint32_t d = tmem + buf * acc_cols;
+              for (int j = i * KU; j < (i + 1) * KU; ++j)
 #pragma unroll
                 for (int q = 0; q < TX; ++q)
                   mma_f16_ts(q == 0 ? d : d + (uint32_t)a.N, ta + j * 8,
                              db + ((j / 4) * half16 + q * plane16 + (j % 4) * 2), idesc, j % KU == 0 && q <= 1 ? 0u : 1u);
-                if (j % KU == KU - 1) mma_commit(af + 8u * buf);
-              }
-              if (q4 + 2 >= UPC) {
+              mma_commit(af + 8u * buf);
+              if (i == UPC - 1) {
                 mma_commit(eb + 8u * (uint32_t)rg.s);
                 mma_commit(ea + 8u * ws);
               }
@@ -433,22 +438,25 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
         if (!ok) break;
         fence_after_sync();
         const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (u_all & 1) * acc_cols + (uint32_t)col0;
+        // 32 columns at a time where registers allow: fewer round trips to TMEM
+        constexpr int LD = TX == 1 && NC <= 64 ? 32 : 16;
 #pragma unroll
-        for (int g = 0; g < NC / 16; ++g) {
-          if (g * 16 < ncols) {
-            uint32_t v[16];
-            tmem_ld16(ta + g * 16, v);
+        for (int g = 0; g < NC / LD; ++g) {
+          if (g * LD < ncols) {
+            uint32_t v[LD];
+            tmem_ld16(ta + g * LD, *reinterpret_cast<uint32_t(*)[16]>(v));
+            if constexpr (LD == 32) tmem_ld16(ta + g * LD + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
             if constexpr (TX > 1) {
               uint32_t c[16];
               tmem_ld16(ta + (uint32_t)a.N + g * 16, c);
               tmem_ld_wait();
 #pragma unroll
-              for (int t = 0; t < 16; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) + __uint_as_float(c[t]));
+              for (int t = 0; t < 16; t += 2) add2(v[t], v[t + 1], c[t], c[t + 1]);
             } else {
               tmem_ld_wait();
             }
 #pragma unroll
-            for (int t = 0; t < 16; ++t) acc[g * 16 + t] = fmaf(s, __uint_as_float(v[t]), acc[g * 16 + t]);
+            for (int t = 0; t < LD; t += 2) fma2(acc[g * LD + t], acc[g * LD + t + 1], s, v[t], v[t + 1]);
           }
         }
         fence_before_sync();
@@ -564,11 +572,10 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
 
 // A unit ends where a group does: 128, 64 or 32 columns.
 template <typename TO, typename H, int TX, int NC, int EW>
-cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
-  if (a.w.ng > 1 && a.w.g % 128 != 0)
-    return a.w.g % 64 == 0 ? run_unit<TO, H, TX, NC, EW, 4>(a, N, s) : run_unit<TO, H, TX, NC, EW, 2>(a, N, s);
-  return run_unit<TO, H, TX, NC, EW, 8>(a, N, s);
+cudaError_t run_narrow(const LinearArgs& a, int N, cudaStream_t s) {
+  return a.w.g % 64 == 0 ? run_unit<TO, H, TX, NC, EW, 4>(a, N, s) : run_unit<TO, H, TX, NC, EW, 2>(a, N, s);
 }
+bool narrow_groups(const LinearArgs& a) { return a.w.ng > 1 && a.w.g % 128 != 0; }
 
 // Tokens per tile, a multiple of 32: the fewest tokens' worth of rounds, each
 // with a cost of its own of about 64 tokens.
@@ -588,15 +595,20 @@ int tokens_per_tile(int64_t T, int64_t tiles_m, int most) {
 
 template <typename TO>
 cudaError_t run16(const LinearArgs& a, cudaStream_t s) {
-  return run<TO, TO, 1, 96, 8>(a, tokens_per_tile(a.T, (a.w.m + 127) / 128, 192), s);
+  const int64_t tiles_m = (a.w.m + 127) / 128;
+  if (narrow_groups(a)) return run_narrow<TO, TO, 1, 64, 8>(a, tokens_per_tile(a.T, tiles_m, 128), s);
+  return run_unit<TO, TO, 1, 96, 8, 8>(a, tokens_per_tile(a.T, tiles_m, 192), s);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s) {
   switch (a.dtype) {
-    case BAKRON_F32:
-      return run<float, __nv_bfloat16, 3, 64, 4>(a, (int)std::min<int64_t>(64, (a.T + 31) / 32 * 32), s);
+    case BAKRON_F32: {
+      const int N = (int)std::min<int64_t>(64, (a.T + 31) / 32 * 32);
+      if (narrow_groups(a)) return run_narrow<float, __nv_bfloat16, 3, 64, 4>(a, N, s);
+      return run_unit<float, __nv_bfloat16, 3, 64, 4, 8>(a, N, s);
+    }
     case BAKRON_BF16: return run16<__nv_bfloat16>(a, s);
     default: return run16<__half>(a, s);
   }

@@ -213,3 +213,40 @@ def test_refusals():
         kb.bakron_layernorm_grad(x, x, None, mean[:3], rstd)
     with pytest.raises(ValueError):
         kb.bakron_layernorm_grad(x, x, None, mean, rstd, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,d", [(1, 1), (3, 7), (9, 130), (700, 37), (40, 255), (30, 1023), (5, 1026),
+                                 (400, 1111), (20, 2049), (7, 4100), (9, 9999), (3, 14335)])
+@pytest.mark.parametrize("offsets", [(0, 0, 0), (1, 3, 5), (6, 4, 0)])
+def test_rows_of_any_alignment(T, d, offsets, dtype):
+    """Inputs and outputs at different places inside 16 bytes, NaN around the
+    inputs (nothing of them may count), guards around the outputs."""
+    kb = _kb()
+    x, dy, gamma, beta = _case(T, d, dtype, T + d)
+
+    def put(t, k, pad):
+        b = torch.full((t.numel() + 24,), pad, dtype=t.dtype, device="cuda")
+        v = b[8 + k:8 + k + t.numel()].view(t.shape)
+        v.copy_(t)
+        return b, v
+
+    _, x = put(x, offsets[0], float("nan"))
+    _, dy = put(dy, offsets[1], float("nan"))
+    ybuf, y = put(x, offsets[2], 7.0)
+    dbuf, dx = put(x, offsets[1], 7.0)
+    _, mean, rstd = kb.bakron_layernorm(x, gamma, beta, EPS, out=y)
+    check_forward(y, mean, rstd, x, gamma, beta, dtype)
+    _, dgamma, dbeta = kb.bakron_layernorm_grad(dy, x, gamma, mean, rstd, out=dx)
+    check_backward(dx, dgamma, dbeta, dy, x, gamma, mean, rstd, dtype)
+    for buf, v, k in ((ybuf, y, offsets[2]), (dbuf, dx, offsets[1])):
+        assert (buf[:8 + k] == 7).all() and (buf[8 + k + v.numel():] == 7).all()
+
+
+@pytest.mark.parametrize("d", [28000, 28700, 32768])
+def test_fp32_rows_near_the_shared_memory_limit(d):
+    kb = _kb()
+    x, dy, gamma, beta = _case(3, d, torch.float32, d)
+    y, mean, rstd = kb.bakron_layernorm(x, gamma, beta, EPS)
+    check_forward(y, mean, rstd, x, gamma, beta, torch.float32)
+    check_backward(*kb.bakron_layernorm_grad(dy, x, gamma, mean, rstd), dy, x, gamma, mean, rstd, torch.float32)
