@@ -57,18 +57,29 @@ bool linear_args(const void* x, int64_t T, int dtype, const bakron_packed* w, co
 // Which forward kernel: a few tokens read in place (or staged at once, fp32)
 // by blocks of 16 or 32 rows; more of them shared by larger blocks; the tcgen05
 // kernel beyond.  fp32 tokens are three times the operand: at 8192 x 8192 and 8
-// tokens the few-token kernel, staging them in parts, took 51 us.
+// tokens the few-token kernel, staging them in parts, took 51 us, the second 23.
 enum Kernel { kFew, kMid, kMany };
 Kernel forward_kernel(const LinearArgs& a) {
   if (a.dtype == BAKRON_F32) {
     if (a.T > kFewTokens) return kMany;
     return a.T * a.w.nc * 128 * 6 <= 160 * 1024 ? kFew : kMid;
   }
-  return a.T <= kFewTokens ? kFew : a.T <= kMidTokens ? kMid : kMany;
+  if (a.T <= kFewTokens) return kFew;
+  if (a.T <= kMidTokens / 2) return kMid;
+  if (a.T > kMidTokens) return kMany;
+  // Between 33 and 64 tokens: microseconds by what was measured of the two, the
+  // second by the codes, the third by a block's chunks, which cost more when
+  // they hold more groups (bf16, 48 tokens, second and third: 8192 x 8192 29.5 and
+  // 25.4, with groups of 64 44 and 39, of 32 44 and 71; 14336 x 4096, whose 112
+  // tiles leave SMs idle, 25.6 and 23.8, 33 and 38, 34 and 71).
+  const bool narrow = a.w.ng > 1 && a.w.g % 128 != 0;
+  const double mid = 1e-6 * (double)(a.w.mp * a.w.nc * 128) * (narrow ? 0.55 : 0.38) * (a.T <= 48 ? 1.0 : 1.3);
+  const double many = (double)linear_fwd_steps(a) * (!narrow ? 0.57 : a.w.g % 64 == 0 ? 1.05 : 2.05);
+  return mid < many ? kMid : kMany;
 }
 
 size_t workspace_bytes(const LinearArgs& a, bool grad) {
-  if (!grad && forward_kernel(a) == kFew) return 0;
+  if (!grad && a.T <= kFewTokens && forward_kernel(a) == kFew) return 0;
   const int64_t K = grad ? a.w.m : a.w.n;
   return (size_t)(a.dtype == BAKRON_F32 ? 3 : 1) * (size_t)a.T * (size_t)((K + 127) / 128 * 128) * 2;
 }

@@ -15,8 +15,8 @@ struct LinearArgs {
   void* ws;
 };
 
-// Tokens up to which bakron_linear runs linear_few_kernel (fp32: or, for long
-// rows, linear_mid_kernel), and, of 16-bit types, linear_mid_kernel.
+// Tokens up to which bakron_linear may run linear_few_kernel and
+// linear_mid_kernel.
 constexpr int64_t kFewTokens = 16;
 constexpr int64_t kMidTokens = 64;
 
@@ -30,6 +30,7 @@ cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_
 
 // tcgen05 products for many tokens, and the gradient for any number.
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);
+int64_t linear_fwd_steps(const LinearArgs& a);    // 128-column chunks that its busiest block takes (16-bit x)
 cudaError_t launch_linear_grad(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace bakron

@@ -28,7 +28,7 @@
 // A stage is a whole chunk, of weights (64 TMEM columns) and of activations: what the
 // issuing warp waits and commits per stage costs it some 400 cycles, so stages of
 // half a chunk kept the tensor core waiting for it.  TMEM: two accumulators of N
-// columns, then two stages of weights.
+// columns, then four stages of weights (two where N is above 128).
 //
 // Every mbarrier wait is bounded (clock64 budget); a block whose wait runs
 // out records BAKRON_ERR_TIMEOUT in the device's status word, stops issuing,
@@ -47,7 +47,7 @@ using namespace tc;
 
 namespace {
 
-constexpr int kWStages = 2;                  // of weights in TMEM, 64 columns each
+constexpr int kWStages = 4;                  // of weights in TMEM, 64 columns each, at most
 constexpr int kMaxStages = 8;                // of activations in shared memory
 constexpr int kSlots = 3;                    // chunks of codes per weights warp, in flight and at hand
 constexpr uint32_t kSlotBytes = 32 * 64;     // 32 rows x 128 columns of codes
@@ -64,6 +64,7 @@ struct FwdArgs {
   int chunks;         // 128-wide K chunks
   int N;              // tokens per tile, a multiple of 32
   int stages;
+  int wstages;        // 4 where TMEM has room, else 2: a power of two
   int* status;
 };
 
@@ -195,7 +196,9 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, Bars& b
 #pragma unroll
   for (int p = 0; p < kSlots - 1; ++p) copy();
   uint32_t z = zeros(tile_now, c_now, m_now);
-  uint32_t parity = 1;       // of the stages' previous use; a fresh barrier passes
+  uint32_t seq = (uint32_t)group;      // chunk of the block
+  const uint32_t last_stage = (uint32_t)a.wstages - 1;
+  const int log_stages = a.wstages == 4 ? 2 : 1;
   while (tile_now < a.tiles) {
     copy();
     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
@@ -214,6 +217,7 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, Bars& b
     c_now += 2;
     settle(tile_now, c_now, m_now);
     z = zeros(tile_now, c_now, m_now);
+    const uint32_t ws = seq & last_stage;        // (a fresh barrier passes the wait for its previous use)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t v[32];
@@ -232,16 +236,16 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, Bars& b
         }
       }
       if (h == 0) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(empty + 8u * group, parity, &bars.abort, a.status))) goto out;
+        if (!__all_sync(0xffffffffu, wait_or_abort(empty + 8u * ws, ((seq >> log_stages) & 1) ^ 1u, &bars.abort, a.status))) goto out;
         fence_after_sync();
       }
-      tmem_st32(tmem_a + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(group * 64 + h * 32), v);
+      tmem_st32(tmem_a + ((uint32_t)(quarter * 32) << 16) + ws * 64u + (uint32_t)(h * 32), v);
     }
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(full + 8u * group);
-    parity ^= 1;
+    if (lane == 0) mbar_arrive(full + 8u * ws);
+    seq += 2;
   }
 out:
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -358,13 +362,15 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       constexpr int UPC = 8 / KU;             // units of a chunk
       uint32_t u = 0;                         // units begun
       uint32_t seq = 0;                       // chunks begun
+      const uint32_t last_stage = (uint32_t)a.wstages - 1;
+      const int log_stages = a.wstages == 4 ? 2 : 1;
       bool go = true;
       Ring rg;
       for (int64_t tile = k.tile; tile < a.tiles && go; tile += k.step) {
         for (int c = k.c0; c < k.c1; ++c) {
-          const uint32_t ws = seq & 1;
+          const uint32_t ws = seq & last_stage;
           go = wait_or_abort(fb + 8u * (uint32_t)rg.s, rg.parity, &bars.abort, a.status) &&
-               wait_or_abort(fa + 8u * ws, (seq >> 1) & 1, &bars.abort, a.status);
+               wait_or_abort(fa + 8u * ws, (seq >> log_stages) & 1, &bars.abort, a.status);
           fence_after_sync();
           const uint64_t db = desc_b0 + (uint32_t)rg.s * stage16;
           const uint32_t ta = tmem_a + ws * 64u;
@@ -515,6 +521,14 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   }
 }
 
+// Blocks per tile: as many as there are SMs without a tile, two chunks each at
+// least.
+int blocks_per_tile(int64_t tiles, int64_t chunks) {
+  int S = 1;
+  while (S < 8 && tiles * 2 * S <= sm_count() && chunks >= 4 * S) S *= 2;
+  return S;
+}
+
 template <typename TO, typename H, int TX, int NC, int EW, int KU>
 cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
   auto k = linear_fwd_kernel<TO, H, TX, NC, EW, KU>;
@@ -529,6 +543,7 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
   t.N = N;
   const uint32_t stage = TX * (uint32_t)N * 256u;
   t.stages = (int)std::min<uint32_t>(kMaxStages, kRing / stage);
+  t.wstages = (TX == 1 ? 2 : 4) * N + 4 * 64 <= 512 ? 4 : 2;
   t.status = async_status_word();
   if (!t.status) return cudaErrorInvalidSymbol;
   // activations: as they are when TMA can read them, else as planes
@@ -545,10 +560,7 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
   }
   CUtensorMap map;
   if (!make_map16(&map, x, rows, ldx, N, std::is_same<H, __nv_bfloat16>::value)) return cudaErrorInvalidValue;
-  // blocks per tile: as many as there are SMs without a tile, two chunks each at
-  // least
-  int S = 1;
-  while (S < 8 && t.tiles * 2 * S <= sm_count() && t.chunks >= 4 * S) S *= 2;
+  const int S = blocks_per_tile(t.tiles, t.chunks);
   static std::atomic<unsigned long long> done;
   const size_t smem = (size_t)t.stages * stage + kCodes + 1024;
   cudaError_t e = ensure_smem_limit((const void*)k, kRing + kCodes + 1024, done);
@@ -577,30 +589,40 @@ cudaError_t run_narrow(const LinearArgs& a, int N, cudaStream_t s) {
 }
 bool narrow_groups(const LinearArgs& a) { return a.w.ng > 1 && a.w.g % 128 != 0; }
 
-// Tokens per tile, a multiple of 32: the fewest tokens' worth of rounds, each
-// with a cost of its own of about 64 tokens.
-int tokens_per_tile(int64_t T, int64_t tiles_m, int most) {
+// Tokens per tile, a multiple of 32: a chunk costs about as much as 500 tokens
+// besides its own (measured: 985 cycles at 64 tokens, 1270 at 192).
+int tokens_per_tile(const LinearArgs& a, int most) {
+  const int64_t tiles_m = (a.w.m + 127) / 128;
   int best = most;
   double cost = 0.0;
-  for (int n = most; n >= 64 || n == most; n -= 32) {
-    const double rounds = (double)((tiles_m * ((T + n - 1) / n) + sm_count() - 1) / sm_count());
-    const double c = rounds * (n + 64);
+  for (int n = most; n >= 32; n -= 32) {
+    if (n > a.T + 31 && n > 32) continue;
+    const int64_t tiles = tiles_m * ((a.T + n - 1) / n);
+    const int S = blocks_per_tile(tiles, a.w.nc);
+    const double rounds = S > 1 ? 1.0 : (double)((tiles + sm_count() - 1) / sm_count());
+    const double c = rounds * (n + 500) / S;
     if (cost == 0.0 || c < cost) {
       cost = c;
       best = n;
     }
   }
-  return (int)std::min<int64_t>(best, (T + 31) / 32 * 32);
+  return best;
 }
 
 template <typename TO>
 cudaError_t run16(const LinearArgs& a, cudaStream_t s) {
-  const int64_t tiles_m = (a.w.m + 127) / 128;
-  if (narrow_groups(a)) return run_narrow<TO, TO, 1, 64, 8>(a, tokens_per_tile(a.T, tiles_m, 128), s);
-  return run_unit<TO, TO, 1, 96, 8, 8>(a, tokens_per_tile(a.T, tiles_m, 192), s);
+  if (narrow_groups(a)) return run_narrow<TO, TO, 1, 64, 8>(a, tokens_per_tile(a, 128), s);
+  return run_unit<TO, TO, 1, 96, 8, 8>(a, tokens_per_tile(a, 192), s);
 }
 
 }  // namespace
+
+int64_t linear_fwd_steps(const LinearArgs& a) {
+  const int N = tokens_per_tile(a, narrow_groups(a) ? 128 : 192);
+  const int64_t tiles = (a.w.m + 127) / 128 * ((a.T + N - 1) / N);
+  const int S = blocks_per_tile(tiles, a.w.nc);
+  return S > 1 ? (a.w.nc + S - 1) / S : (tiles + sm_count() - 1) / sm_count() * a.w.nc;
+}
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s) {
   switch (a.dtype) {

@@ -205,6 +205,7 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
     f.ld = kp;
     f.cols = (int)kp;
   }
+  static_assert(8 * qm::Pipe<1, NS, kDepth>::kBytes + (size_t)kDepth * TERMS * 8 * NT * kPitch <= kSmem);
   static std::atomic<unsigned long long> done;
   cudaError_t e = ensure_smem_limit((const void*)k, kSmem, done);
   if (e != cudaSuccess) return e;
@@ -212,7 +213,10 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
   // 256-column step of 16 warps, a quarter of which a step costs whatever its
   // warps, and 8 of which a round of blocks costs to start and to join.
   const int64_t tiles = a.w.mp / 16, np = (a.w.nc + 1) / 2;
-  int warps = 16, S = 1;
+  auto ring = [&](int w) {
+    return (size_t)w * qm::Pipe<1, NS, kDepth>::kBytes + (size_t)kDepth * TERMS * a.T * kPitch;
+  };
+  int warps = 8, S = 1;      // whose memory always fits
   double best = 0.0;
   for (int c = 1; c <= 8 && c <= np; c *= 2) {
     static std::atomic<int> fit[4];            // row groups at once, by c = 1, 2, 4, 8 (0: not asked yet)
@@ -229,6 +233,7 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
       f_c.store(at_once, std::memory_order_relaxed);
     }
     for (int w = kMaxWarps; w >= 8; --w) {
+      if (ring(w) > kSmem) continue;
       const int64_t groups = (tiles + w - 1) / w;
       const double rounds = (double)((groups + at_once - 1) / at_once);
       const double cost = rounds * ((double)((np + c - 1) / c) * (w / 16.0 + 0.25) + 8.0);
@@ -240,8 +245,7 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
     }
   }
   f.S = S;
-  const size_t smem = std::max<size_t>((size_t)warps * qm::Pipe<1, NS, kDepth>::kBytes + (size_t)kDepth * TERMS * a.T * kPitch,
-                                       S > 1 ? (size_t)a.T * 16 * warps * 4 : 0);
+  const size_t smem = std::max<size_t>(ring(warps), S > 1 ? (size_t)a.T * 16 * warps * 4 : 0);
   Launch q = cluster_config(32 * warps, smem, S, (unsigned)((tiles + warps - 1) / warps * S), s);
   count_launch();
   return cudaLaunchKernelEx(&q.cfg, k, f);

@@ -279,3 +279,16 @@ def test_linear_grad_against_differences():
             d = ((g.double() * (a @ V.T)).sum() - (g.double() * (b @ V.T)).sum()) / 2e-3
             tol = bound(mag[t, j], product_depth(m, 6), torch.float32, d) + 1e-9
             assert abs(dx[t, j].item() - d.item()) <= tol
+
+
+@pytest.mark.parametrize("T,m,n,group,dtype", [
+    (64, 8192, 256, 32, torch.bfloat16), (49, 8192, 1000, 96, torch.float16), (50, 19456, 256, 96, torch.bfloat16),
+    (33, 8192, 256, 128, torch.bfloat16), (48, 4100, 700, 64, torch.float16), (16, 8192, 1800, 32, torch.float32),
+    (16, 19456, 1800, 0, torch.float32), (9, 4096, 4000, 128, torch.float32), (1, 2000, 28000, 64, torch.float32)])
+def test_linear_of_many_rows(T, m, n, group, dtype):
+    """Enough rows that blocks are as large as they get."""
+    kb = _kb()
+    codes, scale, zero, qmin, qmax = random_weight((m, n), group, True, T + m)
+    w = kb.bakron_pack(codes, scale, qmin, qmax, zero=zero, group=group)
+    x = _x(T, n, dtype, 1)
+    check_linear(kb.bakron_linear(x, w), x, value(codes, scale, zero, group), dtype)
