@@ -4,9 +4,9 @@
 //   h = silu(gate_e x) * (up_e x),   y_t = sum over its experts of q (w_out_e h).
 //
 // The layer is bound by the bytes of the experts that any token chose: every
-// expert's matrices are read once for all its tokens.  Two launches:
+// expert's matrices are read once for all its tokens.  Three launches, or four:
 //
-// moe_route_kernel forms the logits, one block per expert and 8 tokens.  (Formed
+// moe_route_kernel forms the logits, one block per expert and two tokens.  (Formed
 // by every block of the next launch instead, the same rows went to all SMs and
 // took 58 us at 16 tokens x 8 experts x 4096 and 5.6 us at 1 x 32 x 1024; this
 // launch, chained to the next without a gap, takes about 3.)
@@ -22,12 +22,14 @@
 //
 // moe_out_kernel.  A block owns 256 rows of y (32 per warp) and a run of the list
 // of (chosen expert, chunk of f); the expert's tokens are again the columns, and
-// their sums are added to per-token sums in shared memory when the expert changes.
-// The blocks that share rows leave their sums in the workspace; the last of
-// them to arrive (a counter that the launch before cleared) adds them in rank order,
-// so nothing depends on who was last.  (As clusters of 16 with the sums in
-// distributed shared memory not all blocks fitted at once: 184 us against 122 at 16
-// tokens x 8 experts of 4096 x 14336.)
+// their sums go to the block's part of the workspace when the expert changes (kept
+// in shared memory instead, 32 tokens' sums left room for one block per SM).
+// The blocks that share rows are joined in rank order: for up to four tokens by
+// the last of them to arrive (a counter that the launch before cleared), so
+// nothing depends on who was last; for more by moe_join_kernel, as one block
+// per row group took some 25 us to read the sums of 32 tokens.
+// (As clusters of 16 with the sums in distributed shared memory not all blocks fitted
+// at once: 184 us against 122 at 16 tokens x 8 experts of 4096 x 14336.)
 #include <algorithm>
 #include <type_traits>
 
@@ -41,14 +43,16 @@ namespace {
 constexpr int kInWarps = 16, kInThreads = 32 * kInWarps;
 constexpr int kOutWarps = 8, kOutThreads = 32 * kOutWarps;
 constexpr int kOutRows = 32 * kOutWarps;
-constexpr int kRouteWarps = 8, kRouteTokens = 8;
+constexpr int kRouteWarps = 8, kRouteTokens = 2;
+constexpr int kLastTokens = 4;                  // up to which moe_out_kernel joins its blocks' sums itself
 constexpr int kMaxTokens = BAKRON_MOE_TOKENS;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 1024;
 constexpr int kDepthIn = 2, kDepthOut = 2;      // slots of two chunks per warp
 template <int NS>
 constexpr uint32_t kInX = NS == 1 ? 64 * 1024 : 48 * 1024;     // shared memory for an expert's tokens
-constexpr uint32_t kOutX = 24 * 1024;    // and for their h
+template <int NS>
+constexpr uint32_t kOutX = NS == 1 ? 40 * 1024 : 28 * 1024;    // and for their h: two blocks per SM
 // Tokens of one launch: fp32 ones take three times the room.
 constexpr int launch_tokens(int terms) { return terms == 1 ? kMaxTokens : kMaxTokens / 2; }
 
@@ -66,7 +70,7 @@ struct MoeArgs {
   uint32_t* who;        // [na]: bit t set where token t chose the expert
   uint8_t* slot;        // [na][T]: which of its choices
   float* logits;        // [T][E]
-  int* arrived;         // [row groups of y]
+  int* arrived;         // [row groups of y], for up to kLastTokens tokens
   float* part;          // [row groups][S][T][256]
   int row_groups, S;    // blocks per row group of y
   void* y;
@@ -106,6 +110,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const __gri
   float acc[kRouteTokens];
 #pragma unroll
   for (int t = 0; t < kRouteTokens; ++t) acc[t] = 0.f;
+#pragma unroll 2
   for (int64_t c = 8 * threadIdx.x; c < a.d; c += 8 * 32 * kRouteWarps) {
     float w[8];
     load8(w, r + c, a.vec_ok != 0, a.d - c);
@@ -459,13 +464,40 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// Rows 4 i .. 4 i + 3 (over the tokens) of a row group of y: its blocks' sums in
+// rank order.
+template <typename TX>
+__device__ __forceinline__ void join_sums(const MoeArgs& a, int rg, int i) {
+  const int n4 = a.T * kOutRows / 4;
+  const float4* all = reinterpret_cast<const float4*>(a.part) + (int64_t)rg * a.S * n4 + i;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < a.S; k0 += 8) {       // eight blocks' sums on their way at a time
+    float4 p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      p[k] = k0 + k < a.S ? __ldcg(all + (int64_t)(k0 + k) * n4) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v.x += p[k].x;
+      v.y += p[k].y;
+      v.z += p[k].z;
+      v.w += p[k].w;
+    }
+  }
+  const int64_t row = (int64_t)rg * kOutRows + 4 * i % kOutRows;
+  TX* o = static_cast<TX*>(a.y) + (int64_t)(4 * i / kOutRows) * a.d + row;
+  if (row < a.d) o[0] = from_float<TX>(v.x);
+  if (row + 1 < a.d) o[1] = from_float<TX>(v.y);
+  if (row + 2 < a.d) o[2] = from_float<TX>(v.z);
+  if (row + 3 < a.d) o[3] = from_float<TX>(v.w);
+}
+
 template <typename TX, int HT, int NS>
 __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_constant__ MoeArgs a) {
   constexpr int kWarps = kOutWarps, kThreads = kOutThreads;
   using P = qm::Pipe<2, NS, kDepthOut>;
   extern __shared__ __align__(16) uint8_t dsm[];
   uint8_t* hs = dsm + kWarps * P::kBytes;
-  float* sums = reinterpret_cast<float*>(hs + kOutX);       // [T][256]: the block's rows of y
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.S, rank = blockIdx.x % S, rg = blockIdx.x / S;
   __shared__ int last;
@@ -476,12 +508,14 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
   const int nc = (int)a.wo.nc;
   const int units = na * nc;                                // (expert, chunk)
   const int u0 = (int)((int64_t)units * rank / S), u1 = (int)((int64_t)units * (rank + 1) / S);
-  for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) sums[i] = 0.f;
+  // the block's sums [T][256]; a thread adds to what it wrote itself
+  float* mine = a.part + ((int64_t)rg * S + rank) * a.T * kOutRows;
+  uint32_t seen = 0;                                        // tokens that have sums
 
   // chunks of an expert's h that are staged at a time, of `part` chunks in all:
   // an even number, unless it is all of them or there is room for one only
   auto slab_of = [&](int ai, int part) {
-    const int room = (int)((kOutX / (uint32_t)(HT * __popc(a.who[ai])) - 64) / 256);
+    const int room = (int)((kOutX<NS> / (uint32_t)(HT * __popc(a.who[ai])) - 64) / 256);
     return room >= part ? part : max(1, room & ~1);
   };
   const int64_t rows[2] = {row0 + 32 * warp, row0 + 32 * warp + 16};
@@ -566,68 +600,48 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
         pipe.release();
       }
     }
-    // to the tokens' sums; a warp's rows are its own
-    __syncwarp();
+    // to the tokens' sums
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 8 * j + 2 * (lane & 3) + (i & 1);
+      for (int i = 0; i < 2; ++i) {
+        const int c = 8 * j + 2 * (lane & 3) + i;
         if (c < cnt) {
           const int t = nth_bit(who, c);
+          float* to = mine + t * kOutRows + 32 * warp + (lane >> 2);
+          const bool more = seen >> t & 1;
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            sums[t * kOutRows + 32 * warp + 16 * q + (lane >> 2) + 8 * (i >> 1)] += tot[q][j][i];
+          for (int q = 0; q < 4; ++q) {
+            const float v = tot[q >> 1][j][i + 2 * (q & 1)];
+            to[8 * q] = more ? to[8 * q] + v : v;
+          }
         }
       }
-    __syncwarp();
     };
     by_columns(live, chunks_of);
+    seen |= who;
     u += c1 - c0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-
-  TX* y = static_cast<TX*>(a.y);
-  if (S == 1) {
-    for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads) {
-      const int64_t row = row0 + i % kOutRows;
-      if (row < a.d) y[(int64_t)(i / kOutRows) * a.d + row] = from_float<TX>(sums[i]);
-    }
-    return;
-  }
-  const int n4 = a.T * kOutRows / 4;
-  float4* mine = reinterpret_cast<float4*>(a.part) + ((int64_t)rg * S + rank) * n4;
-  for (int i = threadIdx.x; i < n4; i += kThreads) mine[i] = reinterpret_cast<const float4*>(sums)[i];
+  for (int i = threadIdx.x; i < a.T * kOutRows; i += kThreads)
+    if (!(seen >> (i / kOutRows) & 1)) mine[i] = 0.f;
+  if (a.T > kLastTokens) return;             // moe_join_kernel follows
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = atomicAdd(&a.arrived[rg], 1) == S - 1;
   __syncthreads();
   if (!last) return;
   __threadfence();
-  const float4* all = reinterpret_cast<const float4*>(a.part) + (int64_t)rg * S * n4;
-  for (int i = threadIdx.x; i < n4; i += kThreads) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < S; k0 += 8) {       // eight blocks' sums on their way at a time
-      float4 p[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        p[k] = k0 + k < S ? __ldcg(all + (int64_t)(k0 + k) * n4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v.x += p[k].x;
-        v.y += p[k].y;
-        v.z += p[k].z;
-        v.w += p[k].w;
-      }
-    }
-    const int64_t row = row0 + 4 * i % kOutRows;
-    TX* o = y + (int64_t)(4 * i / kOutRows) * a.d + row;
-    if (row < a.d) o[0] = from_float<TX>(v.x);
-    if (row + 1 < a.d) o[1] = from_float<TX>(v.y);
-    if (row + 2 < a.d) o[2] = from_float<TX>(v.z);
-    if (row + 3 < a.d) o[3] = from_float<TX>(v.w);
-  }
+  for (int i = threadIdx.x; i < a.T * kOutRows / 4; i += kThreads) join_sums<TX>(a, rg, i);
+}
+
+// One block per row group and 256 groups of four rows of a token.
+template <typename TX>
+__global__ void __launch_bounds__(kOutThreads) moe_join_kernel(const __grid_constant__ MoeArgs a) {
+  const int i = blockIdx.y * kOutThreads + threadIdx.x;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (i < a.T * kOutRows / 4) join_sums<TX>(a, blockIdx.x, i);
 }
 
 // Blocks that share a row group of y: two blocks per SM in all, each with a
@@ -643,15 +657,16 @@ cudaError_t run(MoeArgs& a, cudaStream_t s) {
   auto k1 = moe_in_kernel<TX, H, TERMS, HT, NS>;
   auto k2 = moe_out_kernel<TX, HT, NSO>;
   static_assert(kInX<NS> / (TERMS * launch_tokens(TERMS)) >= 2 * 256 + 64, "two chunks of every token fit");
-  static_assert(kOutX / (HT * launch_tokens(TERMS)) >= 256 + 64, "one chunk of every token's h fits");
+  static_assert(kOutX<NSO> / (HT * launch_tokens(TERMS)) >= 256 + 64, "one chunk of every token's h fits");
   constexpr size_t pipes = kInWarps * (size_t)qm::Pipe<2, NS, kDepthIn>::kBytes;
   static_assert(kInWarps * (kMaxTokens / 8) * 4 * 32 * 4 <= kInX<NS>, "the joins fit the tokens' area");
   constexpr size_t in_bytes = std::max(pipes + kInX<NS>, (size_t)(kMaxTokens + 1) * kMaxExperts * 4);
-  const size_t out_bytes = kOutWarps * (size_t)qm::Pipe<2, NSO, kDepthOut>::kBytes + kOutX + (size_t)a.T * kOutRows * 4;
+  constexpr size_t out_bytes = kOutWarps * (size_t)qm::Pipe<2, NSO, kDepthOut>::kBytes + kOutX<NSO>;
+  static_assert(2 * (out_bytes + 1024 + 64) <= 228 * 1024, "two blocks per SM");
   static std::atomic<unsigned long long> done, done2;
   cudaError_t e = ensure_smem_limit((const void*)k1, in_bytes, done);
   if (e == cudaSuccess)
-    e = ensure_smem_limit((const void*)k2, out_bytes - (size_t)a.T * kOutRows * 4 + (size_t)kMaxTokens * kOutRows * 4, done2);
+    e = ensure_smem_limit((const void*)k2, out_bytes, done2);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
@@ -662,7 +677,7 @@ cudaError_t run(MoeArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)a.E, (unsigned)((a.T + kRouteTokens - 1) / kRouteTokens));
   cfg.blockDim = dim3(32 * kRouteWarps);
-  count_launch(3);
+  count_launch(a.T > kLastTokens ? 4 : 3);
   e = cudaLaunchKernelEx(&cfg, moe_route_kernel<TX>, a);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)sm_count());    // one block per SM
@@ -673,7 +688,11 @@ cudaError_t run(MoeArgs& a, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(a.row_groups * a.S));
   cfg.blockDim = dim3(kOutThreads);
   cfg.dynamicSmemBytes = out_bytes;
-  return cudaLaunchKernelEx(&cfg, k2, a);
+  e = cudaLaunchKernelEx(&cfg, k2, a);
+  if (e != cudaSuccess || a.T <= kLastTokens) return e;
+  cfg.gridDim = dim3((unsigned)a.row_groups, (unsigned)((a.T * kOutRows / 4 + kOutThreads - 1) / kOutThreads));
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, moe_join_kernel<TX>, a);
 }
 
 template <typename TX, typename H, int TERMS, int HT>
