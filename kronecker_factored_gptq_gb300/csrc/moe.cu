@@ -283,8 +283,16 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
   const int i_lo = (int)(items * blockIdx.x / gridDim.x), i_hi = (int)(items * (blockIdx.x + 1) / gridDim.x);
   const int nc = (int)a.wi.nc;
   const int np = (nc + 1) / 2;             // pairs of chunks
+  auto segment_end = [&](int it) { return min(i_hi, (it / tiles + 1) * tiles); };
+  // warps per item: as many as the run's fullest expert leaves without one
+  int most = 1;
+  for (int it = i_lo; it < i_hi;) {
+    const int end = segment_end(it);
+    most = max(most, end - it);
+    it = end;
+  }
   int G = 1;
-  while (G < kWarps && (i_hi - i_lo) * 2 * G <= kWarps && np >= 2 * G) G *= 2;
+  while (2 * G * most <= kWarps && 2 * G <= np) G *= 2;
   const int group = warp / G, part = warp % G, groups = kWarps / G;
   const int c_lo = np * part / G * 2, c_hi = min(nc, np * (part + 1) / G * 2);
 
@@ -297,7 +305,6 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
     qm::tile_ref<2>(t, a.wi, R.active[ai], rows, lane);
   };
   // a warp's items: group, group + groups, ... of each expert's part of the run
-  auto segment_end = [&](int it) { return min(i_hi, (it / tiles + 1) * tiles); };
   auto next_item = [&](int it, int seg_end) { return it + groups < seg_end ? it + groups : -1; };
   qm::TileRef<2> t_ahead, t_now;
   int seg_a = i_lo, seg_a_end = i_lo < i_hi ? segment_end(i_lo) : i_lo;   // where the copies are
