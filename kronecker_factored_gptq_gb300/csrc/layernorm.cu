@@ -20,8 +20,13 @@
 // the aligned 16-byte pieces that hold its columns, a thread moves its columns
 // into place out of two of them, and the results are exchanged through shared
 // memory so that they leave by whole words in order.  (Copies of 4 bytes, which
-// need no moving, took 172 us instead of
-// @@ for the gradient of 8192 x 4097 bf16.)
+// need no moving, took 172 us instead of 113 for the gradient of 8192 x 4097 bf16;
+// one column per load took 165.)
+//
+// Measured, forward and gradient: 8192 x 4096 bf16 31 and 42 us (4.3 and 4.8 TB/s; the bytes
+// at 6.68 TB/s 20 and 30), 2048 x 14336 fp16 31 and 61 (one row at a time, 64 registers a
+// thread), 8192 x 1024 8.6 and 20, 8192 x 4097 64 and 113 (instructions per column),
+// 37 x 1111 fp32 2.9 and 5.8 (launches and latency).
 #include <algorithm>
 #include <type_traits>
 
@@ -805,7 +810,7 @@ NormPlan norm_plan(int64_t T, int64_t d, int dtype, bool aligned, int arrays) {
   q.block = true;
   if (few) {
     // one row per block at most: its latency counts, which a vector per thread keeps
-    // shortest (37 x 1111 fp32: @@ us, 8 with eight vectors)
+    // shortest (37 x 1111 fp32 forward: 2.9 us, 8 with eight vectors)
     q.nv = 1;
     q.threads = (int)((vecs + 31) / 32 * 32);
     q.per_sm = 1;

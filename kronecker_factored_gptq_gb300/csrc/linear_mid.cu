@@ -8,7 +8,9 @@
 // activations that the block copies into shared memory; its codes go the way
 // of the few-token kernel (qmma.cuh).  Both are asynchronous copies a few
 // steps ahead, one barrier a step.  The matrix instructions of 8 tokens each are the
-// next bound: 8 NT per 16 x 128 codes.
+// next bound: 8 NT per 16 x 128 codes, each about 16 cycles of an SM's quarter.
+// Measured: 32 tokens of 8192 x 8192 bf16 24 us, 48 of 14336 x 4096 fp16 with groups of
+// 64 33 us (the codes' bytes alone: 5.4 us).
 //
 // Warps per block W and blocks per row group S (a cluster that splits the columns
 // and adds the sums in rank order through distributed shared memory) are chosen
