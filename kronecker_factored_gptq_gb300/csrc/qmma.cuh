@@ -207,10 +207,14 @@ __device__ __forceinline__ void set_zeros(Chunk16<NS> (&f)[RT], const uint32_t (
 // tot[r][j] += products of the chunk of row tile r with column tile j.  fetch(j, q, s): this thread's 8 columns 32 s + 8 t .. of
 // term q of its activation row in column tile j.  A warp's instructions, not the
 // matrix pipe, are what a chunk costs, so two row tiles share a fetch where they can.
+// Three terms are fp32 activations: the matrix instructions cut their sums off instead
+// of rounding, so the two small terms have a sum of their own and the large one
+// is cut off a third as often.
 template <typename H, int TERMS, int RT, int NT, int NS, typename Fetch>
 __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chunk16<NS> (&f)[RT],
                                               bool has_zero, int zu, Fetch fetch) {
-  float acc[RT][NT][4];
+  constexpr bool kApart = TERMS == 3;
+  float acc[RT][NT][4], low[kApart ? RT : 1][kApart ? NT : 1][4];
   uint32_t off[RT][2];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -233,8 +237,10 @@ __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chu
         const uint4 x = fetch(j, q, s);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          mma16816<H>(acc[r][j], q == 0 && (s == 0 || NS == 4), a[r][0], b[r][0], a[r][1], b[r][1], x.x, x.y);
-          mma16816<H>(acc[r][j], false, a[r][2], b[r][2], a[r][3], b[r][3], x.z, x.w);
+          float(&to)[4] = kApart && q > 0 ? low[kApart ? r : 0][kApart ? j : 0] : acc[r][j];
+          const bool first = q <= (kApart ? 1 : 0) && (s == 0 || NS == 4);
+          mma16816<H>(to, first, a[r][0], b[r][0], a[r][1], b[r][1], x.x, x.y);
+          mma16816<H>(to, false, a[r][2], b[r][2], a[r][3], b[r][3], x.z, x.w);
         }
       }
     }
@@ -244,6 +250,10 @@ __device__ __forceinline__ void chunk_product(float (&tot)[RT][NT][4], const Chu
         const float s0 = f[r].s[0][NS == 4 ? s : 0], s1 = f[r].s[1][NS == 4 ? s : 0];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
+          if constexpr (kApart) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][j][i] += low[r][j][i];
+          }
           tot[r][j][0] = fmaf(s0, acc[r][j][0], tot[r][j][0]);
           tot[r][j][1] = fmaf(s0, acc[r][j][1], tot[r][j][1]);
           tot[r][j][2] = fmaf(s1, acc[r][j][2], tot[r][j][2]);
