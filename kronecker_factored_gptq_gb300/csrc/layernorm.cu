@@ -895,7 +895,9 @@ bool norm_args_ok(int64_t T, int64_t d, int dtype) {
 size_t grad_bytes(int64_t T, int64_t d) {
   int64_t rows = 0;
   for (int dt : {BAKRON_F32, BAKRON_BF16})
-    for (bool al : {false, true}) rows = std::max(rows, norm_blocks(norm_plan(T, d, dt, al, 2), T));
+    for (bool al : {false, true})
+      for (int64_t t : {T, std::min<int64_t>(T, sm_count())})      // fewer rows may take more blocks
+        rows = std::max(rows, norm_blocks(norm_plan(t, d, dt, al, 2), t));
   return (size_t)(rows * 2 * d) * sizeof(float);
 }
 

@@ -250,3 +250,15 @@ def test_fp32_rows_near_the_shared_memory_limit(d):
     y, mean, rstd = kb.bakron_layernorm(x, gamma, beta, EPS)
     check_forward(y, mean, rstd, x, gamma, beta, torch.float32)
     check_backward(*kb.bakron_layernorm_grad(dy, x, gamma, mean, rstd), dy, x, gamma, mean, rstd, torch.float32)
+
+
+@pytest.mark.parametrize("d", [64, 1000, 1111])
+def test_a_workspace_serves_fewer_rows(d):
+    kb = _kb()
+    ws = kb.layernorm_grad_workspace(400, d)
+    for T in (400, 200, 150, 9, 1):
+        assert kb.layernorm_grad_workspace_size(T, d) <= ws.numel()
+        x, dy, gamma, beta = _case(T, d, torch.float32, T)
+        _, mean, rstd = kb.bakron_layernorm(x, gamma, beta, EPS)
+        got = kb.bakron_layernorm_grad(dy, x, gamma, mean, rstd, workspace=ws)
+        check_backward(*got, dy, x, gamma, mean, rstd, torch.float32)
