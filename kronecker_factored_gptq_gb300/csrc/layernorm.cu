@@ -14,7 +14,9 @@
 // same columns of every row that its block takes, so the sums over rows of
 // dgamma and dbeta grow in registers and leave the block once, into a row of the
 // workspace; a second launch adds the blocks' rows in a fixed order (no atomics,
-// so the bits do not depend on the run).
+// so the bits do not depend on the run).  Up to a row per SM, each row has a block, and
+// blocks of their own sum the columns beside them (37 x 1111 fp32: 3.4 us, 6.1 with the
+// second launch).
 //
 // Rows that do not begin on 16 bytes (an odd d, or an odd address): a warp copies
 // the aligned 16-byte pieces that hold its columns, a thread moves its columns
@@ -24,9 +26,9 @@
 // one column per load took 165.)
 //
 // Measured, forward and gradient: 8192 x 4096 bf16 31 and 42 us (4.3 and 4.8 TB/s; the bytes
-// at 6.68 TB/s 20 and 30), 2048 x 14336 fp16 31 and 61 (one row at a time, 64 registers a
-// thread), 8192 x 1024 8.6 and 20, 8192 x 4097 64 and 113 (instructions per column),
-// 37 x 1111 fp32 2.9 and 5.8 (launches and latency).
+// at 6.68 TB/s 20 and 30), 2048 x 14336 fp16 31 and 53 (one block per SM, one row at a
+// time), 8192 x 1024 8.6 and 20, 8192 x 4097 64 and 113 (instructions per column),
+// 37 x 1111 fp32 2.9 and 3.4 (launch and latency).
 #include <algorithm>
 #include <type_traits>
 
@@ -47,7 +49,9 @@ struct NormArgs {
   float* rstd;
   const float* mean_in;
   const float* rstd_in;
-  float* part;           // [blocks][2][d], NULL without weight gradients
+  float* part;           // [blocks][2][d], NULL without weight gradients or with few rows
+  float* dgamma;         // of few rows
+  float* dbeta;
   int depth;             // slots of rows in shared memory
   bool vectors;          // gamma and beta on 32 bytes
 };
@@ -511,9 +515,43 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 ? 2 : 1) norm_kernel(const _
   }
 }
 
+// dgamma and dbeta of 32 columns over few rows: a warp takes every W-th row, the
+// warps' sums are added in order.  mean and rstd are given, so this needs nothing of
+// the rows' own blocks and runs beside them.
+template <typename TX>
+__device__ __forceinline__ void column_sums(const NormArgs& p, int block, float* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t c = (int64_t)block * 32 + lane;
+  const TX* x = static_cast<const TX*>(p.x) + c;
+  const TX* dy = static_cast<const TX*>(p.dy) + c;
+  float g = 0.f, b = 0.f;
+  if (c < p.d) {
+#pragma unroll 8
+    for (int64_t t = warp; t < p.T; t += warps) {
+      const float w = to_float(dy[t * p.d]), h = (to_float(x[t * p.d]) - p.mean_in[t]) * p.rstd_in[t];
+      g = fmaf(w, h, g);
+      b += w;
+    }
+  }
+  sum[warp * 64 + lane] = g;
+  sum[warp * 64 + 32 + lane] = b;
+  __syncthreads();
+  if (warp < 2 && c < p.d) {
+    float v = 0.f;
+    for (int w = 0; w < warps; ++w) v += sum[w * 64 + threadIdx.x];
+    (warp == 0 ? p.dgamma : p.dbeta)[c] = v;
+  }
+}
+
 template <typename TX, int V, int NV, bool kBlock, bool kShift, int MAXB>
 __global__ void __launch_bounds__(MAXB, MAXB <= 256 ? 2 : 1) norm_grad_kernel(const __grid_constant__ NormArgs p) {
   extern __shared__ __align__(16) uint8_t dsm[];
+  if constexpr (NV == 1) {        // few rows, one per block; the blocks after them sum columns
+    if (blockIdx.x >= p.T) {
+      column_sums<TX>(p, (int)(blockIdx.x - p.T), reinterpret_cast<float*>(dsm));
+      return;
+    }
+  }
   __shared__ float red[2][4][kMaxWarps];
   int slot = 0;
   const int tid = kBlock ? threadIdx.x : threadIdx.x & 31;
@@ -535,7 +573,7 @@ __global__ void __launch_bounds__(MAXB, MAXB <= 256 ? 2 : 1) norm_grad_kernel(co
   rows.tpr = tpr;
   rows.depth = p.depth;
   // gamma stays in registers when there is room
-  constexpr bool kKeep = NV * V <= 16 && MAXB <= 512;
+  constexpr bool kKeep = NV * V <= 16 && MAXB <= 640;
   Vec<float, V> gk[kKeep ? NV : 1];
   if constexpr (kKeep) {
 #pragma unroll
@@ -812,7 +850,7 @@ NormPlan norm_plan(int64_t T, int64_t d, int dtype, bool aligned, int arrays) {
     // one row per block at most: its latency counts, which a vector per thread keeps
     // shortest (37 x 1111 fp32 forward: 2.9 us, 8 with eight vectors)
     q.nv = 1;
-    q.threads = (int)((vecs + 31) / 32 * 32);
+    q.threads = (int)std::max<int64_t>(256, (vecs + 31) / 32 * 32);
     q.per_sm = 1;
     q.depth = 1;
     q.smem = (size_t)arrays * q.threads * 16 + (extra + out) * (q.threads / 32);
@@ -833,6 +871,9 @@ NormPlan norm_plan(int64_t T, int64_t d, int dtype, bool aligned, int arrays) {
   q.per_sm = std::max(1, std::min(arrays == 1 ? 8 : 4, 512 / q.threads));
   while (q.per_sm > 1 && (row * 2 + fixed) * q.per_sm > kRowBytes) --q.per_sm;
   q.depth = (int)std::max<size_t>(1, std::min<size_t>(4, (kRowBytes / q.per_sm - fixed) / row));
+  // gamma is read from memory by blocks this large, and stays in the L1 cache beside
+  // two rows, not three (2048 x 14336 fp16: 53 us, 57)
+  if (arrays == 2 && q.threads > 640) q.depth = std::min(q.depth, 2);
   q.smem = row * q.depth + fixed;
   return q;
 }
@@ -844,13 +885,13 @@ int64_t norm_blocks(const NormPlan& q, int64_t T) {
 
 template <typename K>
 cudaError_t launch_norm(K k, const NormPlan& q, const NormArgs& a, std::atomic<unsigned long long>& done,
-                        cudaStream_t s) {
+                        cudaStream_t s, int64_t more_blocks = 0) {
   if (q.smem > 46 * 1024) {      // beyond the default of 48 KB with the static part
     const cudaError_t e = ensure_smem_limit((const void*)k, 226 * 1024, done);
     if (e != cudaSuccess) return e;
   }
   count_launch();
-  k<<<(unsigned)norm_blocks(q, a.T), q.threads, q.smem, s>>>(a);
+  k<<<(unsigned)(norm_blocks(q, a.T) + more_blocks), q.threads, q.smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -872,12 +913,14 @@ cudaError_t run_fwd(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
 template <typename TX, int W, bool kShift>
 cudaError_t run_grad(const NormPlan& q, const NormArgs& a, cudaStream_t s) {
   constexpr int N = 16 / W;
-  static std::atomic<unsigned long long> d[6];
-  if (q.nv == 1) return launch_norm(norm_grad_kernel<TX, W, 1, true, kShift, 1024>, q, a, d[5], s);
+  static std::atomic<unsigned long long> d[7];
+  if (q.nv == 1)
+    return launch_norm(norm_grad_kernel<TX, W, 1, true, kShift, 1024>, q, a, d[5], s, a.dgamma ? (a.d + 31) / 32 : 0);
   if (!q.block) return launch_norm(norm_grad_kernel<TX, W, 2 * N, false, kShift, 256>, q, a, d[0], s);
   if (q.nv == 2 * N) return launch_norm(norm_grad_kernel<TX, W, 2 * N, true, kShift, 1024>, q, a, d[1], s);
   if (q.threads <= 256) return launch_norm(norm_grad_kernel<TX, W, N, true, kShift, 256>, q, a, d[2], s);
   if (q.threads <= 512) return launch_norm(norm_grad_kernel<TX, W, N, true, kShift, 512>, q, a, d[3], s);
+  if (q.threads <= 640) return launch_norm(norm_grad_kernel<TX, W, N, true, kShift, 640>, q, a, d[6], s);
   return launch_norm(norm_grad_kernel<TX, W, N, true, kShift, 896>, q, a, d[4], s);
 }
 template <typename TX, int W>
@@ -969,16 +1012,21 @@ extern "C" bakron_status bakron_layernorm_grad(const void* dY, const void* X, in
   a.y = dX;
   a.mean_in = mean;
   a.rstd_in = rstd;
-  a.part = dgamma ? static_cast<float*>(ws) : nullptr;
   const bool al = aligned_to(X, 16) && aligned_to(dY, 16) && aligned_to(dX, 16) && aligned_to(gamma, 32);
   const NormPlan q = norm_plan(T, d, dtype, al, 2);
   a.vectors = aligned_to(gamma, 32);
   a.depth = q.depth;
+  if (q.nv == 1) {
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+  } else if (dgamma) {
+    a.part = static_cast<float*>(ws);
+  }
   const cudaError_t e = dtype == BAKRON_F32    ? run_grad<float, 4>(q, a, s)
                         : dtype == BAKRON_BF16 ? run_grad<__nv_bfloat16, 8>(q, a, s)
                                                : run_grad<__half, 8>(q, a, s);
   if (e != cudaSuccess) return launch_status(e);
-  if (dgamma) {
+  if (a.part) {
     count_launch();
     norm_join_kernel<<<(unsigned)((2 * d + 31) / 32), 512, 0, s>>>(a.part, norm_blocks(q, T), d, dgamma,
                                                                      dbeta);

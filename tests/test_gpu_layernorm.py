@@ -262,3 +262,17 @@ def test_a_workspace_serves_fewer_rows(d):
         _, mean, rstd = kb.bakron_layernorm(x, gamma, beta, EPS)
         got = kb.bakron_layernorm_grad(dy, x, gamma, mean, rstd, workspace=ws)
         check_backward(*got, dy, x, gamma, mean, rstd, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,d", [(152, 300), (153, 300), (150, 1111), (100, 4096), (31, 8000), (152, 5001), (40, 10240),
+                                 (300, 10000), (200, 9500)])
+def test_few_rows_and_blocks_of_several_sizes(T, d, dtype):
+    kb = _kb()
+    x, dy, gamma, beta = _case(T, d, dtype, T * d)
+    y, mean, rstd = kb.bakron_layernorm(x, gamma, beta, EPS)
+    check_forward(y, mean, rstd, x, gamma, beta, dtype)
+    got = kb.bakron_layernorm_grad(dy, x, gamma, mean, rstd)
+    check_backward(*got, dy, x, gamma, mean, rstd, dtype)
+    again = kb.bakron_layernorm_grad(dy, x, gamma, mean, rstd)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
