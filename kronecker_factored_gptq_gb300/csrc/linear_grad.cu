@@ -28,9 +28,9 @@
 //   warp 2: allocates and frees TMEM;  warps 4-11: weights;  warps 12-15: epilogue.
 //
 // Measured: 2048 tokens of 4096 x 14336 bf16 in 210 us, 1.15 PFLOP/s, bound by the
-// issuing warp's waits and by the warps that transpose; 333 tokens of 1000 x 1300 fp32 27 us and
-// 1024 of 4096 x 4096 fp32 443 us, bound by the warps that split each weight
-// into its terms.
+// issuing warp's waits and by the warps that transpose; 333 tokens of 1000 x 1300 fp32 23 us and
+// 1024 of 4096 x 4096 fp32 332 us, bound by the warps that split each weight into
+// its terms (with a branch for infinite weights there 27 and 443 us).
 //
 // Every mbarrier wait is bounded (clock64 budget); a block whose wait runs
 // out records BAKRON_ERR_TIMEOUT in the device's status word, stops issuing,
@@ -84,6 +84,17 @@ __device__ __forceinline__ float2 unpack2(uint32_t p, __nv_bfloat16) {
 }
 __device__ __forceinline__ float2 unpack2(uint32_t p, __half) {
   return __half22float2(*reinterpret_cast<const __half2*>(&p));
+}
+
+// Two weights in three exact bf16 terms each, as pairs.  No weight is NaN; an
+// infinite one (of a scale near the largest float) is its first term.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  const auto top = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); };
+  const auto tops = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); };
+  hi = tops(x, y);
+  const float rx = fabsf(x) < INFINITY ? x - top(x) : 0.f, ry = fabsf(y) < INFINITY ? y - top(y) : 0.f;
+  mid = tops(rx, ry);
+  lo = tops(rx - top(rx), ry - top(ry));
 }
 
 struct Bars {
@@ -201,11 +212,7 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
             if constexpr (TW == 1) {
               o[0][p] = pack2(f.x, f.y, H());
             } else {
-              float x3[3], y3[3];
-              split3(f.x, x3[0], x3[1], x3[2]);
-              split3(f.y, y3[0], y3[1], y3[2]);
-#pragma unroll
-              for (int q = 0; q < TW; ++q) o[q][p] = (uint32_t)bf16_bits(x3[q]) | (uint32_t)bf16_bits(y3[q]) << 16;
+              split_pair(f.x, f.y, o[0][p], o[1][p], o[2][p]);
             }
           }
 #pragma unroll
