@@ -11,8 +11,8 @@
 // transpose: a thread takes 4 rows x 32 columns of codes; one byte permutation
 // brings the same columns of two rows next to each other, and each column's 4
 // rows leave as 8 bytes of a 128-byte line of the operand.  Two warps share a
-// step of 64 rows, so that a stage is filled by 2 warps while 6 others fill the next
-// ones.
+// step of 64 rows (four with three terms), so that a stage is filled by them
+// while the other weights' warps fill the next ones.
 //
 // 16-bit dY: the whole sum stays in TMEM (a chain of K / 16 additions that cut
 // off, at most 2^-23 of the partial sum each, against the 2^-9 or 2^-12 of the result's
@@ -28,9 +28,9 @@
 //   warp 2: allocates and frees TMEM;  warps 4-11: weights;  warps 12-15: epilogue.
 //
 // Measured: 2048 tokens of 4096 x 14336 bf16 in 210 us, 1.15 PFLOP/s, bound by the
-// issuing warp's waits and by the warps that transpose; 333 tokens of 1000 x 1300 fp32 23 us and
-// 1024 of 4096 x 4096 fp32 332 us, bound by the warps that split each weight into
-// its terms (with a branch for infinite weights there 27 and 443 us).
+// issuing warp's waits and by the warps that transpose; 333 tokens of 1000 x 1300 fp32 21.5 us
+// and 1024 of 4096 x 4096 fp32 279 us, bound by the warps that split each weight into its
+// terms (with a branch for infinite weights there 27 and 443 us).
 //
 // Every mbarrier wait is bounded (clock64 budget); a block whose wait runs
 // out records BAKRON_ERR_TIMEOUT in the device's status word, stops issuing,
@@ -110,41 +110,62 @@ struct Work {
   int k0, k1;
 };
 
-// What a thread holds of a step: 4 rows x 32 columns of codes and the rows'
+// Warps that fill a stage, and the 32-column parts that one of their threads takes.
+// Splitting into terms is long, and three stages of such weights are all that fits:
+// with two warps a stage, two of the eight had none (1024 x 4096 x 4096: 279 us, 332).
+template <int TW>
+constexpr int kStepWarps = TW == 1 ? 2 : 4;
+template <int TW>
+constexpr int kParts = TW == 1 ? 4 : 2;
+
+// What a thread holds of a step: 4 rows x 32 (16) columns of codes and the rows'
 // grid for the columns' groups (one group, or one per 32 columns).
-template <int NS>
+template <int SN, int NS>
 struct Codes {
-  uint4 q[4];
-  float4 sc[NS];
-  uint32_t z[NS];
+  uint32_t q[4][SN];
+  float4 sc[NS < SN ? NS : SN];
+  uint32_t z[NS < SN ? NS : SN];
 };
 
 template <typename H, int TW, int NS>
 __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& bars, uint32_t ring,
                                         uint32_t stage_bytes, int warp, int lane) {
   const PackedView& w = a.w;
-  const int pair = warp >> 1;
-  const int t = 2 * (warp & 1) + (lane >> 4), hh = (lane >> 3) & 1, rb = lane & 7;
-  const int turn = min(4, a.stages);    // pairs of warps at work: a wait tells a stage's
-  if (pair >= turn) return;             // uses apart by one bit, so none may be two ahead
+  constexpr int W = kStepWarps<TW>, SN = kParts<TW>, G = NS < SN ? NS : SN;
+  const int group = warp / W, hh = (lane >> 3) & 1, rb = lane & 7;
+  // word 4 t + s of a row: t by warp and lane, or t by warp and half of s by lane
+  const int t = SN == 4 ? 2 * (warp & 1) + (lane >> 4) : warp & 3;
+  const int s0 = SN == 4 ? 0 : 2 * (lane >> 4);
+  const int turn = min(8 / W, a.stages);    // groups of warps at work: a wait tells a stage's
+  if (group >= turn) return;                // uses apart by one bit, so none may be two ahead
   const uint32_t full = smem_u32(bars.full), empty = smem_u32(bars.empty);
   const int64_t nb = w.mp / 8;
   const int n = k.k1 - k.k0;
-  auto load = [&](Codes<NS>& c, int64_t tile, int m, int i) {
+  auto load = [&](Codes<SN, NS>& c, int64_t tile, int m, int i) {
     const int64_t b = (int64_t)(k.k0 + i) * 8 + rb;
     const bool live = tile < a.tiles && b < nb;
-    const uint8_t* src = w.codes + ((live ? b : 0) * w.nc + (live ? m : 0)) * kBlockBytes + hh * 256 + t * 16;
+    const uint8_t* src = w.codes + ((live ? b : 0) * w.nc + (live ? m : 0)) * kBlockBytes + hh * 256 + t * 16 + s0 * 4;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      c.q[r] = make_uint4(0, 0, 0, 0);
-      if (live) c.q[r] = ld_codes(src + r * 64);
+      for (int e = 0; e < SN; ++e) c.q[r][e] = 0;
+      if (live) {
+        if constexpr (SN == 4) {
+          const uint4 u = ld_codes(src + r * 64);
+          c.q[r][0] = u.x;
+          c.q[r][1] = u.y;
+          c.q[r][2] = u.z;
+          c.q[r][3] = u.w;
+        } else {
+          asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(c.q[r][0]), "=r"(c.q[r][1]) : "l"(src + r * 64));
+        }
+      }
     }
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < G; ++s) {
       c.sc[s] = make_float4(0.f, 0.f, 0.f, 0.f);
       c.z[s] = 0;
       if (live) {
-        const int64_t at = grid_row(w, 0, b * 8 + hh * 4) + grid_group(w, (uint32_t)m * 128u + 32 * s) * 16;
+        const int64_t at = grid_row(w, 0, b * 8 + hh * 4) + grid_group(w, (uint32_t)m * 128u + 32 * (s0 + s)) * 16;
         asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
                      : "=f"(c.sc[s].x), "=f"(c.sc[s].y), "=f"(c.sc[s].z), "=f"(c.sc[s].w)
                      : "l"(w.scale + at));
@@ -152,9 +173,9 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
       }
     }
   };
-  // this pair's steps over all tiles: every turn-th
+  // this group's steps over all tiles: every turn-th
   int64_t tile = k.tile;
-  int m = (int)(tile % a.tiles_m), i = pair;
+  int m = (int)(tile % a.tiles_m), i = group;
   auto settle = [&]() {
     if (i < n) return;
     while (i >= n && tile < a.tiles) {
@@ -164,12 +185,12 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
     m = (int)(tile % a.tiles_m);
   };
   settle();
-  Codes<NS> c;
+  Codes<SN, NS> c;
   load(c, tile, m, i);
   Ring rg;
-  rg.advance(pair, a.stages);
+  rg.advance(group, a.stages);
   while (tile < a.tiles) {
-    const Codes<NS> now = c;
+    const Codes<SN, NS> now = c;
     i += turn;
     settle();
     load(c, tile, m, i);
@@ -179,8 +200,8 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
     float sc[4];
     uint32_t off[2];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (s < NS) {
+    for (int s = 0; s < SN; ++s) {
+      if (s < G) {
         sc[0] = now.sc[s].x; sc[1] = now.sc[s].y; sc[2] = now.sc[s].z; sc[3] = now.sc[s].w;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -191,8 +212,7 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
       }
       uint32_t word[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        word[r] = s == 0 ? now.q[r].x : s == 1 ? now.q[r].y : s == 2 ? now.q[r].z : now.q[r].w;
+      for (int r = 0; r < 4; ++r) word[r] = now.q[r][s];
 #pragma unroll
       for (int odd = 0; odd < 2; ++odd) {
         uint32_t tr[2];
@@ -200,7 +220,7 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
         for (int p = 0; p < 2; ++p) tr[p] = __byte_perm(word[2 * p], word[2 * p + 1], odd ? 0x7632 : 0x5410);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int col = 32 * s + 8 * t + 2 * e + odd;
+          const int col = 32 * (s0 + s) + 8 * t + 2 * e + odd;
           const uint32_t at = sa + (uint32_t)col * 128u + (uint32_t)((rb ^ (2 * e + odd)) << 4);
           uint32_t o[TW][2];
 #pragma unroll
@@ -262,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     bars.abort = 0;
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(smem_u32(&bars.full[s]), 3);          // the copies and two warps of weights
+      mbar_init(smem_u32(&bars.full[s]), 1 + kStepWarps<TW>);     // the copies and the weights' warps
       mbar_init(smem_u32(&bars.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
