@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
     } else if (warp == 1) {
       // ---------------- MMA issuer: the warp waits together, one lane issues.
       // A single warp's dependent instructions, not the tensor core, bound
-      // this loop when it is long, so everything is fixed per K chunk of two
-      // stages: where units begin and end, and the descriptors' offsets.
+      // this loop when it is long, so everything is fixed per K chunk:
+      // where units begin and end, and the descriptors' offsets.
       const uint32_t idesc = idesc_f16<H>(a.N);
       const uint64_t desc_b0 = desc_sw128(ring);
       const uint32_t stage16 = stage_bytes >> 4, half16 = half_bytes >> 4, plane16 = plane_b >> 4;
