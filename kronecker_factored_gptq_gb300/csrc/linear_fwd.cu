@@ -496,6 +496,9 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
     if constexpr (kSplit) role_end<THREADS, 96>(true, warp);
   }
   __syncwarp();
+  // the wait below begins when the roles have ended: its budget is for the last
+  // products, not for all of the block's tiles
+  __syncthreads();
 
   // all MMAs must have completed before TMEM is freed and the ring is reused
   if (warp == 2) {
