@@ -396,7 +396,8 @@ typedef struct {
  * most 2^38.
  * Layout of data, with mp = m rounded up to 16, np = n rounded up to 128 and
  * groups = ceil(n / group):
- *   256 bytes            status word of the packing, otherwise unused;
+ *   256 bytes            status word of the packing; at byte 128 the largest scale
+ *     (float); otherwise unused;
  *   codes, count mp np / 2 bytes: blocks of 8 rows x 128 columns (512 bytes)
  *     in row-major order of blocks; inside a block row by row, 64 bytes each;
  *     word 4 t + s (32 bits; s, t = 0..3) of a row holds columns 32 s + 8 t
@@ -428,7 +429,11 @@ bakron_status bakron_linear(const void* X, int64_t T, int dtype, const bakron_pa
                             void* ws, size_t ws_bytes, void* stream);
 /* The gradient of bakron_linear for its activations (the weights are
  * frozen): dX = dY V, dY T x m, dX T x n.  For 16-bit dY each value of V is
- * rounded to dY's type before the product; for fp32 it is not. */
+ * rounded to dY's type before the product; for fp32 it is not.  The scales
+ * may be of any size: a power of two is taken out of them before that, so
+ * that for fp16 a value keeps its 11 bits while its scale is at least 2^-25 of
+ * the matrix's largest one (2^-21 without zero points where |c| exceeds 15),
+ * and below is off by at most 2^-36 (2^-32) of that scale. */
 bakron_status bakron_linear_grad_workspace_size(const bakron_packed* w, int64_t T, int dtype,
                                                 size_t* bytes);
 bakron_status bakron_linear_grad(const void* dY, int64_t T, int dtype, const bakron_packed* w,

@@ -38,6 +38,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <type_traits>
 
 #include "linear_tc.cuh"
@@ -64,6 +65,7 @@ struct GradArgs {
   int steps;          // K steps of 64 rows
   int N;              // tokens per tile, a multiple of 32
   int stages;
+  int most;           // no |c - z| is larger
   int* status;
 };
 
@@ -84,6 +86,26 @@ __device__ __forceinline__ float2 unpack2(uint32_t p, __nv_bfloat16) {
 }
 __device__ __forceinline__ float2 unpack2(uint32_t p, __half) {
   return __half22float2(*reinterpret_cast<const __half2*>(&p));
+}
+
+// The power of two that the scales take on their way into the operand, and its
+// inverse, which the sums take on their way out: V itself need not be in the
+// range of the operand's type, or of fp32.  fp16: the largest weight comes next to
+// the largest number, so that a weight keeps its 11 bits down to 2^-25 (2^-21 where
+// |c - z| exceeds 15) of the largest scale.  bf16 (and its terms): a factor only
+// where a weight could overflow or the last of three terms lose bits.
+template <typename H>
+__device__ __forceinline__ void operand_range(const GradArgs& a, float& in, float& out) {
+  const float top = __ldg(a.w.largest);
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;
+  int p = 0;
+  if (top > 0.f) {
+    if (std::is_same<H, __half>::value) p = max(-126, min(126, (a.most <= 15 ? 11 : 7) - e));
+    else if (e > 119) p = 119 - e;
+    else if (e < -90) p = -90 - e;
+  }
+  in = __uint_as_float((uint32_t)(127 + p) << 23);
+  out = __uint_as_float((uint32_t)(127 - p) << 23);
 }
 
 // Two weights in three exact bf16 terms each, as pairs.  No weight is NaN; an
@@ -140,6 +162,8 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
   if (group >= turn) return;                // uses apart by one bit, so none may be two ahead
   const uint32_t full = smem_u32(bars.full), empty = smem_u32(bars.empty);
   const int64_t nb = w.mp / 8;
+  float range_in, range_out;
+  operand_range<H>(a, range_in, range_out);
   const int n = k.k1 - k.k0;
   auto load = [&](Codes<SN, NS>& c, int64_t tile, int m, int i) {
     const int64_t b = (int64_t)(k.k0 + i) * 8 + rb;
@@ -202,7 +226,10 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
 #pragma unroll
     for (int s = 0; s < SN; ++s) {
       if (s < G) {
-        sc[0] = now.sc[s].x; sc[1] = now.sc[s].y; sc[2] = now.sc[s].z; sc[3] = now.sc[s].w;
+        sc[0] = now.sc[s].x * range_in;
+        sc[1] = now.sc[s].y * range_in;
+        sc[2] = now.sc[s].z * range_in;
+        sc[3] = now.sc[s].w * range_in;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const float z0 = w.zero ? (float)((now.z[s] >> (16 * p)) & 255u) : (float)w.zu;
@@ -304,6 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
   grid_dep_wait();
   grid_dep_launch();
+  float range_in, range_out;
+  operand_range<H>(a, range_in, range_out);
 
   if (warp == 0) {
     // ---------------- incoming gradients
@@ -423,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // lane = output column: the 32 lanes write 32 consecutive elements
 #pragma unroll
               for (int t = 0; t < 32; ++t)
-                if (t0 + g + t < a.T) y[(int64_t)(g + t) * a.w.n] = from_float<TO>(v[t]);
+                if (t0 + g + t < a.T) y[(int64_t)(g + t) * a.w.n] = from_float<TO>(v[t] * range_out);
             }
           }
         } else {
@@ -448,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < NC; ++t) {
           if (t < a.N) {
             if (S > 1) part[t * 128 + quarter * 32 + lane] = acc[t];
-            else if (ok && row < a.w.n && t0 + t < a.T) y[(int64_t)t * a.w.n] = from_float<TO>(acc[t]);
+            else if (ok && row < a.w.n && t0 + t < a.T) y[(int64_t)t * a.w.n] = from_float<TO>(acc[t] * range_out);
           }
         }
       }
@@ -485,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row >= a.w.n || t0 + c >= a.T) continue;
       float v = 0.f;
       for (int q = 0; q < S; ++q) v += cluster.map_shared_rank(part, q)[c * 128 + r];
-      static_cast<TO*>(a.y)[(t0 + c) * a.w.n + row] = from_float<TO>(v);
+      static_cast<TO*>(a.y)[(t0 + c) * a.w.n + row] = from_float<TO>(v * range_out);
     }
     __syncwarp();
     cluster.sync();   // no block leaves while its sums are read
@@ -504,6 +533,7 @@ cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
   t.tiles = (int64_t)t.tiles_m * ((a.T + N - 1) / N);
   t.steps = (int)((K + 63) / 64);
   t.N = N;
+  t.most = a.w.zero ? 15 : std::max(std::abs(a.w.zu), std::abs(15 - a.w.zu));
   const uint32_t stage = TW * kABytes + TX * (uint32_t)N * 128u;
   t.stages = (int)std::min<uint32_t>(kMaxStages, kRing / stage);
   t.status = async_status_word();

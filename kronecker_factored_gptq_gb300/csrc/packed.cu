@@ -46,13 +46,15 @@ __global__ void pack_codes_kernel(const int8_t* __restrict__ codes, int64_t coun
 }
 
 // scale[e][i][k] -> [e][i / 16][k][i % 16], 0 on the padding rows; zero points likewise
-// as bytes z - qmin.
+// as bytes z - qmin.  The bits of positive floats are ordered as they are, so the largest
+// scale is a maximum of whole numbers, whatever the order.
 __global__ void pack_grid_kernel(const float* __restrict__ scale, const float* __restrict__ zero,
                                  int64_t count, int64_t m, int64_t mp, int64_t ng, float qmin,
                                  float qmax, float* __restrict__ so, uint8_t* __restrict__ zo,
-                                 DevStatus* st) {
+                                 unsigned* __restrict__ largest, DevStatus* st) {
   const int64_t total = count * ng * mp;
   bool bad = false, badz = false;
+  unsigned top = 0;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t b = i / 16, k = b % ng, r = (b / ng) % (mp / 16) * 16 + i % 16, e = i / (mp * ng);
@@ -61,7 +63,8 @@ __global__ void pack_grid_kernel(const float* __restrict__ scale, const float* _
     if (r < m) {
       const int64_t at = (e * m + r) * ng + k;
       s = scale[at];
-      bad |= !(s > 0.f) || !isfinite(s);
+      if (s > 0.f && isfinite(s)) top = max(top, __float_as_uint(s));
+      else bad = true;
       if (zero) {
         const float v = zero[at];
         const bool wrong = !(v >= qmin && v <= qmax) || rintf(v) != v;
@@ -72,6 +75,8 @@ __global__ void pack_grid_kernel(const float* __restrict__ scale, const float* _
     so[i] = s;
     if (zero) zo[i] = z;
   }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) atomicMax(largest, top);
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) set_status(st, BAKRON_ERR_NONFINITE);
   if (__any_sync(0xffffffffu, badz) && (threadIdx.x & 31) == 0) set_status(st, BAKRON_ERR_CODE_RANGE);
 }
@@ -161,7 +166,8 @@ extern "C" bakron_status bakron_pack(const int8_t* codes, const float* scale, co
       codes, count, m, n, L.mp, L.nc, qmin, qmax, reinterpret_cast<uint32_t*>(p + L.codes), st);
   pack_grid_kernel<<<grid_words(count * L.ng * L.mp), 256, 0, s>>>(
       scale, zero, count, m, L.mp, L.ng, (float)qmin, (float)qmax,
-      reinterpret_cast<float*>(p + L.scale), zero ? p + L.zero : nullptr, st);
+      reinterpret_cast<float*>(p + L.scale), zero ? p + L.zero : nullptr,
+      reinterpret_cast<unsigned*>(p + kPackLargest), st);
   if (cudaGetLastError() != cudaSuccess) return BAKRON_ERR_CUDA;
   DevStatus host;
   if (cudaMemcpyAsync(&host, st, sizeof(host), cudaMemcpyDeviceToHost, s) != cudaSuccess ||

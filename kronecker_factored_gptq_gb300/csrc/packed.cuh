@@ -21,6 +21,7 @@
 namespace bakron {
 
 constexpr size_t kPackHeader = 256;
+constexpr size_t kPackLargest = 128;  // in the header: the largest scale
 constexpr int kBlockBytes = 512;      // 8 rows x 128 columns
 constexpr int64_t kMaxPackedDim = int64_t(1) << 20;
 constexpr int64_t kMaxPackedCodes = int64_t(1) << 38;
@@ -62,6 +63,7 @@ struct PackedView {
   const float* scale;     // [count][mp / 16][ng][16]
   const uint8_t* zero;    // likewise, or NULL: every zero point is `zu`
   int zu;                 // -qmin
+  const float* largest;   // the largest scale of all (0: not known)
   int64_t count, m, n, mp, nc, ng, g;
   uint64_t g_mul;         // floor(2^40 / g) + 1: k / g = (k g_mul) >> 40 for k, g <= 2^20
 };
@@ -77,6 +79,7 @@ inline bool packed_view(const bakron_packed* w, PackedView* v) {
   v->scale = reinterpret_cast<const float*>(p + L.scale);
   v->zero = w->has_zero ? p + L.zero : nullptr;
   v->zu = -w->qmin;
+  v->largest = reinterpret_cast<const float*>(p + kPackLargest);
   v->count = w->count;
   v->m = w->m;
   v->n = w->n;
