@@ -57,6 +57,7 @@ constexpr int kMaxStages = 8;
 
 struct GradArgs {
   PackedView w;
+  const void* dy;
   void* y;
   int64_t T;          // tokens
   int64_t plane;      // token rows per plane of dY's map
@@ -117,6 +118,43 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   const float rx = fabsf(x) < INFINITY ? x - top(x) : 0.f, ry = fabsf(y) < INFINITY ? y - top(y) : 0.f;
   mid = tops(rx, ry);
   lo = tops(rx - top(rx), ry - top(ry));
+}
+
+// fp32 dY: what infinities and NaN of token t's gradient bring to output column j
+// of this lane (the warp's lanes: 32 columns, one token).  An infinite gradient is
+// its first term alone; its products with the weights' second and third terms, which
+// are often exact zeros, are NaN where the formula has an infinity.  So a sum that
+// is not finite is formed anew from the gradients that are not and
+// the signs of their weights; false when there are none (a sum that overflowed).
+__device__ __noinline__ bool nonfinite_part(const GradArgs& a, int64_t t, int64_t j, float& sum) {
+  const PackedView& w = a.w;
+  const int lane = threadIdx.x & 31, in = (int)(j & 127), k = in & 7;
+  const float* dy = static_cast<const float*>(a.dy) + t * w.m;
+  const uint8_t* word = w.codes + (j >> 7) * kBlockBytes + (((in >> 3) & 3) * 4 + (in >> 5)) * 4;
+  const int shift = 4 * (k >> 1) + 16 * (k & 1);
+  const uint32_t group = grid_group(w, (uint32_t)j) * 16;
+  bool found = false;
+  sum = 0.f;
+  constexpr int Q = 8;
+  for (int64_t i0 = 0; i0 < w.m; i0 += 32 * Q) {
+    float v[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) v[q] = i0 + 32 * q + lane < w.m ? dy[i0 + 32 * q + lane] : 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      uint32_t which = __ballot_sync(0xffffffffu, !(fabsf(v[q]) < INFINITY));
+      found |= which != 0;
+      for (; which != 0; which &= which - 1) {
+        const int b = __ffs((int)which) - 1;
+        const int64_t i = i0 + 32 * q + b;
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(word + (i >> 3) * w.nc * kBlockBytes + (i & 7) * 64);
+        const int z = w.zero ? w.zero[grid_row(w, 0, i) + group] : w.zu;
+        sum = fmaf(__shfl_sync(0xffffffffu, v[q], b), (float)((int)((u >> shift) & 15u) - z), sum);
+      }
+    }
+    if (__all_sync(0xffffffffu, sum != sum)) break;
+  }
+  return found;
 }
 
 struct Bars {
@@ -425,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t af = smem_u32(&bars.acc_full[0]), ae = smem_u32(&bars.acc_empty[0]);
     float* part = reinterpret_cast<float*>(dsm + (ring - base_raw));   // S > 1: [column][row], in the idle ring
     uint32_t u_all = 0;
-    bool ok = true;
+    bool ok = true, off = false;             // off: a sum of this lane is not finite
     for (int64_t tile = k.tile; tile < a.tiles && ok; tile += k.step) {
       const int64_t row = (tile % a.tiles_m) * 128 + quarter * 32 + lane;
       const int64_t t0 = tile / a.tiles_m * a.N;
@@ -476,8 +514,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < NC; ++t) {
           if (t < a.N) {
+            if (!(fabsf(acc[t]) < INFINITY)) off = true;
             if (S > 1) part[t * 128 + quarter * 32 + lane] = acc[t];
             else if (ok && row < a.w.n && t0 + t < a.T) y[(int64_t)t * a.w.n] = from_float<TO>(acc[t] * range_out);
+          }
+        }
+      }
+    }
+    if constexpr (!kWhole) {
+      // after the last tile, when no other warp waits for this one any more
+      if (S == 1 && ok && __any_sync(0xffffffffu, off)) {
+        for (int64_t tile = k.tile; tile < a.tiles; tile += k.step) {
+          const int64_t row = (tile % a.tiles_m) * 128 + quarter * 32 + lane, t0 = tile / a.tiles_m * a.N;
+          for (int64_t t = t0; t < min(t0 + a.N, a.T); ++t) {
+            TO* y = static_cast<TO*>(a.y) + t * a.w.n + row;
+            const bool bad = row < a.w.n && !(fabsf(*y) < INFINITY);
+            float v;
+            if (__any_sync(0xffffffffu, bad) && nonfinite_part(a, t, row, v) && bad) *y = v;
           }
         }
       }
@@ -511,10 +564,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;
     const int64_t row = (k.tile % a.tiles_m) * 128 + r, t0 = k.tile / a.tiles_m * a.N;
     for (int c = rank + S * (threadIdx.x >> 7); c < a.N; c += S * (kThreads / 128)) {
-      if (row >= a.w.n || t0 + c >= a.T) continue;
+      if (t0 + c >= a.T) continue;           // the whole warp
       float v = 0.f;
       for (int q = 0; q < S; ++q) v += cluster.map_shared_rank(part, q)[c * 128 + r];
-      static_cast<TO*>(a.y)[(t0 + c) * a.w.n + row] = from_float<TO>(v * range_out);
+      const bool live = row < a.w.n;
+      float out = v * range_out;
+      if constexpr (TX > 1) {
+        const bool off = live && !(fabsf(v) < INFINITY);
+        float f;
+        if (__any_sync(0xffffffffu, off) && nonfinite_part(a, t0 + c, row, f) && off) out = f;
+      }
+      if (live) static_cast<TO*>(a.y)[(t0 + c) * a.w.n + row] = from_float<TO>(out);
     }
     __syncwarp();
     cluster.sync();   // no block leaves while its sums are read
@@ -527,6 +587,7 @@ cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
   const int64_t K = a.w.m;
   GradArgs t = {};
   t.w = a.w;
+  t.dy = a.x;
   t.y = a.y;
   t.T = a.T;
   t.tiles_m = (int)((a.w.n + 127) / 128);

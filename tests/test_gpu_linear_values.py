@@ -21,6 +21,58 @@ def _dy(T, m, dtype, seed):
     return torch.randn((T, m), generator=g).to(dtype).cuda()
 
 
+def formula(dy, V):
+    """sum_i dy_ti V_ij in fp64, term by term, so that infinities and NaN
+    meet every weight of their row as written."""
+    out = torch.zeros((dy.shape[0], V.shape[1]), dtype=torch.float64, device=dy.device)
+    for i in range(dy.shape[1]):
+        out += dy[:, i:i + 1].double() * V[i:i + 1]
+    return out
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,m,n,group,asym", [
+    (9, 100, 300, 0, False), (40, 600, 257, 32, True), (70, 1100, 130, 128, True), (700, 64, 4200, 96, False)])
+def test_infinities_and_nan_as_in_the_formula(T, m, n, group, asym, dtype):
+    """Scales are powers of two and codes small, so every weight fits in one
+    bf16 term: the second and third terms of an fp32 product are exact zeros,
+    which an infinite gradient must not meet."""
+    kb = _kb()
+    codes, scale, zero, qmin, qmax = random_weight((m, n), group, asym, T + m)
+    scale = torch.exp2(torch.round(torch.log2(scale)))
+    w = kb.bakron_pack(codes, scale, qmin, qmax, zero=zero, group=group)
+    V = value(codes, scale, zero, group)
+    dy = _dy(T, m, dtype, n)
+    inf = float("inf")
+    dy[1, m // 2] = inf
+    dy[2, 3] = -inf
+    dy[3, 0] = inf
+    dy[3, m - 1] = inf
+    dy[4, 5] = inf
+    dy[4, 6] = -inf
+    dy[5, m - 2] = float("nan")
+    dy[T - 1, 7] = inf
+    dx = kb.bakron_linear_grad(dy, w)
+    ref = formula(dy, V)
+    assert torch.equal(torch.isnan(dx), torch.isnan(ref))
+    assert torch.equal(dx == inf, ref == inf) and torch.equal(dx == -inf, ref == -inf)
+    ok = torch.isfinite(ref)
+    tol = bound(dy.double().abs().nan_to_num(0, 0, 0) @ V.abs(), product_depth(m, terms=6), dtype, ref)
+    assert ((dx.double() - ref).abs()[ok] <= tol[ok]).all()
+    kb.bakron_async_status()
+
+
+def test_a_sum_that_overflows_stays_infinite():
+    kb = _kb()
+    codes = torch.full((40, 130), 7, dtype=torch.int8, device="cuda")
+    w = kb.bakron_pack(codes, torch.ones((40, 1), device="cuda"), -8, 7)
+    dy = torch.full((5, 40), 3e38, device="cuda")
+    dy[1] = -dy[1]
+    dy[2] = 1.0
+    dx = kb.bakron_linear_grad(dy, w)
+    assert (dx[0] == float("inf")).all() and (dx[1] == float("-inf")).all() and (dx[2] == 280).all()
+
+
 # Scales over the whole range that bakron_pack takes, with gradients for which the results are finite and
 # normal: (log2 of the scales' middle, spread in octaves either way, log2 of dY).
 RANGES = {torch.float16: [(13, 1, -13), (20, 2, -22), (-16, 2, 6), (-26, 3, 10), (-4, 8, 0)],
