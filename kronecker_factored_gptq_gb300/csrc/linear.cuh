@@ -24,9 +24,10 @@ cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_mid(const LinearArgs& a, cudaStream_t s);
 
 // x (T x K of dtype, any alignment) -> planes [terms][T][kp] of 16-bit terms (1,
-// or 3 for fp32), zeros past K; out is 16-byte aligned, kp a multiple of 8.
+// or 3 for fp32), zeros past K; out is 16-byte aligned, kp a multiple of 8.  `near`: the
+// terms are rounded instead of cut off (split3_near).
 cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_t kp, void* out,
-                          cudaStream_t s);
+                          cudaStream_t s, bool near = false);
 
 // tcgen05 products for many tokens, and the gradient for any number.
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);

@@ -5,7 +5,8 @@
 // sum, so the operand holds the value s (u - z): rounded once to dY's type for 16-bit dY
 // (the exact operands of the forward product would need a scaled copy of dY per
 // group, and as much rounding of that), in three exact bf16 terms for fp32 dY (with
-// three of dY; six products, those whose weight is at least 2^-16).
+// three of dY; six products: the three left out are at most 2^-24 of the whole, as the
+// terms are rounded; cut off they came to 2^-21, always towards zero).
 //
 // The packed words run along the columns, so the operand (rows along K) is their
 // transpose: a thread takes 4 rows x 32 columns of codes; one byte permutation
@@ -109,15 +110,15 @@ __device__ __forceinline__ void operand_range(const GradArgs& a, float& in, floa
   out = __uint_as_float((uint32_t)(127 - p) << 23);
 }
 
-// Two weights in three exact bf16 terms each, as pairs.  No weight is NaN; an
-// infinite one (of a scale near the largest float) is its first term.
+// Two weights in three exact bf16 terms each, as pairs, the first two rounded to
+// nearest (split3_near); operand_range keeps them below 2^127.
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  const auto top = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); };
-  const auto tops = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); };
-  hi = tops(x, y);
-  const float rx = fabsf(x) < INFINITY ? x - top(x) : 0.f, ry = fabsf(y) < INFINITY ? y - top(y) : 0.f;
-  mid = tops(rx, ry);
-  lo = tops(rx - top(rx), ry - top(ry));
+  hi = pack2(x, y, __nv_bfloat16());
+  const float2 h = unpack2(hi, __nv_bfloat16());
+  const float rx = x - h.x, ry = y - h.y;
+  mid = pack2(rx, ry, __nv_bfloat16());
+  const float2 m = unpack2(mid, __nv_bfloat16());
+  lo = __byte_perm(__float_as_uint(rx - m.x), __float_as_uint(ry - m.y), 0x7632);
 }
 
 // fp32 dY: what infinities and NaN of token t's gradient bring to output column j
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int qw = 0; qw < TW; ++qw)
 #pragma unroll
               for (int qx = 0; qx < TX; ++qx) {
-                if (qw + qx > 2) continue;   // below 2^-24 of the product
+                if (qw + qx > 2) continue;   // together at most 2^-24 (1 + 2^-9) of the product
                 const bool large = qw == 0 && qx == 0;
                 mma_f16(large ? d : d + (uint32_t)a.N, da + (uint32_t)(qw * (kABytes >> 4) + j * 2),
                         db + (qx * plane16 + j * 2), idesc, begin && j == 0 && (large || (qw == 0 && qx == 1)) ? 0u : 1u);
@@ -605,7 +606,7 @@ cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
   t.plane = a.T;
   if (TX != 1 || !aligned_to(a.x, 16) || K % 8 != 0) {
     const int64_t kp = (K + 127) / 128 * 128;
-    const cudaError_t e = launch_planes(a.x, a.dtype, a.T, K, kp, a.ws, s);
+    const cudaError_t e = launch_planes(a.x, a.dtype, a.T, K, kp, a.ws, s, true);
     if (e != cudaSuccess) return e;
     x = a.ws;
     ldx = kp;

@@ -205,6 +205,17 @@ __device__ __forceinline__ void split3(float x, float& hi, float& mid, float& lo
   lo = r - mid;
 }
 
+// The same sum with hi and mid rounded to nearest instead of cut off: mid is at
+// most 2^-8 and lo 2^-17 of the power of two below |x| (cut off: 2^-7 and 2^-15),
+// where products of small terms are left out.  Cut where rounding would overflow.
+__device__ __forceinline__ void split3_near(float x, float& hi, float& mid, float& lo) {
+  if ((__float_as_uint(x) & 0x7fffffffu) >= 0x7f7f8000u) return split3(x, hi, mid, lo);
+  hi = __bfloat162float(__float2bfloat16_rn(x));
+  const float r = x - hi;
+  mid = __bfloat162float(__float2bfloat16_rn(r));
+  lo = r - mid;
+}
+
 // The top half of a float that is a bf16.
 __device__ __forceinline__ uint16_t bf16_bits(float x) {
   return (uint16_t)(__float_as_uint(x) >> 16);

@@ -101,3 +101,25 @@ def test_scales_of_any_size(T, m, n, group, asym, dtype, mid, spread, mag):
     assert torch.isfinite(dx).all()
     worst = ((dx.double() - ref).abs() / tol).max().item()
     assert worst <= 1.0, "error %.3g times the bound" % worst
+
+
+def test_products_of_full_precision():
+    """One product per output (m = 1).  With x = hi + mid + lo in rounded bf16
+    terms mid is at most 2^-8 and lo at most 2^-17 of the power of two below x, so the
+    three products left out are at most 2^-24 (1 + 2^-9) of the whole; the two
+    sums' addition rounds once more, 2^-24."""
+    kb = _kb()
+    g = torch.Generator(device="cpu").manual_seed(4)
+    n, T = 4, 4000
+    for trial in range(4):
+        s = torch.exp2(4 * torch.rand((1, 1), generator=g)).cuda()
+        dy = torch.exp2(4 * torch.rand((T, 1), generator=g)).cuda()
+        if trial == 0:
+            s.fill_(1 + 2.0 ** -7 - 2.0 ** -23)
+            dy[:10] = 1 + 2.0 ** -7 - 2.0 ** -23
+        codes = torch.ones((1, n), dtype=torch.int8, device="cuda")
+        w = kb.bakron_pack(codes, s, -8, 7)
+        dx = kb.bakron_linear_grad(dy, w)
+        ref = dy.double() * s.double() * torch.ones((1, n), device="cuda").double()
+        worst = ((dx.double() - ref).abs() / ref).max().item()
+        assert worst <= 2.1 * U, "error %.3g of 2^-24" % (worst / U)
