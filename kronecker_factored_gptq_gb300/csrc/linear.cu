@@ -81,6 +81,9 @@ Kernel forward_kernel(const LinearArgs& a) {
 
 size_t workspace_bytes(const LinearArgs& a, bool grad) {
   if (!grad && a.T <= kFewTokens && forward_kernel(a) == kFew) return 0;
+  if (grad && a.dtype != BAKRON_F32 && a.w.m > grad_chain(a.dtype) && a.T > 0)
+    return grad_planes_bytes(a) +
+           (size_t)sm_count() * (size_t)std::min<int64_t>(kGradTokens, (a.T + 31) / 32 * 32) * 128 * sizeof(float);
   const int64_t K = grad ? a.w.m : a.w.n;
   return (size_t)(a.dtype == BAKRON_F32 ? 3 : 1) * (size_t)a.T * (size_t)((K + 127) / 128 * 128) * 2;
 }

@@ -20,6 +20,15 @@ struct LinearArgs {
 constexpr int64_t kFewTokens = 16;
 constexpr int64_t kMidTokens = 64;
 
+// Rows of the gradient's sum (16-bit dY) that stay in one accumulator; more need
+// room for it in the workspace, behind dY's planes: N x 128 floats per block.
+__host__ __device__ constexpr int64_t grad_chain(int dtype) { return dtype == BAKRON_F16 ? 4096 : 32768; }
+constexpr int64_t kGradTokens = 256;     // N at most
+inline size_t grad_planes_bytes(const LinearArgs& a) {
+  const size_t b = (size_t)(a.dtype == BAKRON_F32 ? 3 : 1) * (size_t)a.T * (size_t)((a.w.m + 127) / 128 * 128) * 2;
+  return (b + 255) / 256 * 256;
+}
+
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_mid(const LinearArgs& a, cudaStream_t s);
 

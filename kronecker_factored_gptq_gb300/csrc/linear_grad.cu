@@ -15,10 +15,11 @@
 // step of 64 rows (four with three terms), so that a stage is filled by them
 // while the other weights' warps fill the next ones.
 //
-// 16-bit dY: the whole sum stays in TMEM (a chain of K / 16 additions that cut
-// off, at most 2^-23 of the partial sum each, against the 2^-9 or 2^-12 of the result's
-// and the weights' rounding), and two accumulators let the epilogue write one
-// tile while the next is summed.  fp32 dY: the sum is cut after every 128 rows and
+// 16-bit dY: the sum over 4096 rows (bf16: 32768) stays in TMEM, a chain of one addition
+// per 16 rows that cuts off at most 2^-23 of the partial sum: 2^-15 (2^-12) in all, an eighth
+// of the result's own rounding.  Longer sums are added from such chains in fp32, by way of
+// the workspace (fp16, 1024 tokens of 14336 x 4096: 127 us, one chain 119).  Two accumulators
+// let the epilogue take one while the next is summed.  fp32 dY: the sum is cut after every 128 rows and
 // added in fp32 registers, and the five small products have an accumulator of
 // their own, so that the large one is cut off 8 times a unit instead of 48 (error
 // of a 333 x 1000 x 1300 product against 64 bits: with one accumulator 1.3e-6).
@@ -68,6 +69,7 @@ struct GradArgs {
   int N;              // tokens per tile, a multiple of 32
   int stages;
   int most;           // no |c - z| is larger
+  float* sums;        // [block][N][128]: 16-bit dY, chains before the last
   int* status;
 };
 
@@ -313,12 +315,14 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
   }
 }
 
-// TX, TW: 16-bit terms of dY and of the weights (1 and 1: the sum stays in TMEM;
-// else it is cut every 128 rows); NS: groups per 128 columns.
+// TX, TW: 16-bit terms of dY and of the weights (1 and 1: the sum is cut every grad_chain
+// rows; else every 128); NS: groups per 128 columns.
 template <typename TO, typename H, int TX, int TW, int NS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_grad_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ GradArgs a) {
   constexpr bool kWhole = TW == 1;
+  // K steps of an accumulator's chain
+  constexpr int kChain = kWhole ? (int)(grad_chain(std::is_same<H, __half>::value ? BAKRON_F16 : BAKRON_BF16) / 64) : 2;
   constexpr int NC = 64;                     // columns in registers when the sum is cut
   extern __shared__ __align__(1024) unsigned char dsm[];
   __shared__ Bars bars;
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   k.k0 = 2 * (int)((int64_t)pairs * rank / S);
   k.k1 = 2 * (int)((int64_t)pairs * (rank + 1) / S);
   const int steps = k.k1 - k.k0;                      // per tile; even
-  const int units = kWhole ? 1 : steps / 2;
+  const int units = (steps + kChain - 1) / kChain;
   // accumulators: two of N columns, each with one for the small products beside it
   const uint32_t acc_cols = (kWhole ? 1u : 2u) * (uint32_t)a.N;
   uint32_t cols = 32;
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring rg;
     for (int64_t tile = k.tile; tile < a.tiles && go; tile += k.step) {
       for (int i = 0; i < steps; ++i) {
-        const bool begin = kWhole ? i == 0 : (i & 1) == 0, end = kWhole ? i == steps - 1 : (i & 1) != 0;
+        const bool begin = i % kChain == 0, end = i % kChain == kChain - 1 || i == steps - 1;
         if (begin) {
           // the accumulator's previous unit, u - 2, has been read
           if (u >= 2) go = wait_or_abort(ae + 8u * (u & 1), ((u >> 1) & 1) ^ 1u, &bars.abort, a.status);
@@ -484,6 +488,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 0; g < a.N; g += 32) {
             float v[32];
             tmem_ld32(ta + (uint32_t)g, v);
+            if (units > 1) {
+              // chains are added in fp32, rounded, by way of the workspace
+              float* sum = a.sums + ((int64_t)blockIdx.x * a.N + g) * 128 + quarter * 32 + lane;
+              if (u > 0) {
+#pragma unroll
+                for (int t = 0; t < 32; ++t) v[t] += sum[t * 128];
+              }
+              if (u < units - 1) {
+#pragma unroll
+                for (int t = 0; t < 32; ++t) sum[t * 128] = v[t];
+                continue;
+              }
+            }
             if (S > 1) {
 #pragma unroll
               for (int t = 0; t < 32; ++t) part[(g + t) * 128 + quarter * 32 + lane] = v[t];
@@ -618,6 +635,7 @@ cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
   // least
   int S = 1;
   while (S < 8 && t.tiles * 2 * S <= sm_count() && t.steps >= 8 * S) S *= 2;
+  if (a.dtype != BAKRON_F32 && a.w.m > grad_chain(a.dtype)) t.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + grad_planes_bytes(a));
   static std::atomic<unsigned long long> done;
   const size_t smem = (size_t)t.stages * stage + 1024;
   cudaError_t e = ensure_smem_limit((const void*)k, kRing + 1024, done);
@@ -666,8 +684,8 @@ cudaError_t launch_linear_grad(const LinearArgs& a, cudaStream_t s) {
   const int64_t tiles_m = (a.w.n + 127) / 128;
   switch (a.dtype) {
     case BAKRON_F32: return by_groups<float, __nv_bfloat16, 3, 3>(a, tokens_per_tile(a.T, tiles_m, 64), s);
-    case BAKRON_BF16: return by_groups<__nv_bfloat16, __nv_bfloat16, 1, 1>(a, tokens_per_tile(a.T, tiles_m, 256), s);
-    default: return by_groups<__half, __half, 1, 1>(a, tokens_per_tile(a.T, tiles_m, 256), s);
+    case BAKRON_BF16: return by_groups<__nv_bfloat16, __nv_bfloat16, 1, 1>(a, tokens_per_tile(a.T, tiles_m, kGradTokens), s);
+    default: return by_groups<__half, __half, 1, 1>(a, tokens_per_tile(a.T, tiles_m, kGradTokens), s);
   }
 }
 

@@ -123,3 +123,26 @@ def test_products_of_full_precision():
         ref = dy.double() * s.double() * torch.ones((1, n), device="cuda").double()
         worst = ((dx.double() - ref).abs() / ref).max().item()
         assert worst <= 2.1 * U, "error %.3g of 2^-24" % (worst / U)
+
+
+@pytest.mark.parametrize("T,m,n,dtype", [(64, 131072, 130, torch.float16), (300, 65600, 2048, torch.float16),
+                                         (1, 100000, 60, torch.float16), (40, 131072, 256, torch.bfloat16),
+                                         (600, 9000, 8200, torch.float16), (600, 33000, 8200, torch.bfloat16)])
+def test_long_sums(T, m, n, dtype):
+    """Sums of one sign over many rows: the tensor core cuts a sum off at
+    every addition (at most 2^-23 of it, one per 16 rows), so a chain of them is
+    at most 4096 rows long (bf16: 32768), 2^-15 (2^-12); the chains are added with
+    roundings of 2^-24."""
+    kb = _kb()
+    g = torch.Generator(device="cpu").manual_seed(T)
+    codes = torch.randint(1, 8, (m, n), generator=g, dtype=torch.int8).cuda()
+    w = kb.bakron_pack(codes, torch.full((m, 1), 2.0 ** -6, device="cuda"), -8, 7)     # V is exact
+    dy = (0.01 + 0.05 * torch.rand((T, m), generator=g)).to(dtype).cuda()
+    dx = kb.bakron_linear_grad(dy, w)
+    ref = dy.double() @ (codes.double() * 2.0 ** -6)
+    chain = 4096 if dtype == torch.float16 else 32768
+    err = (chain / 16 * 2.0 ** -23 + (m / chain + 8) * U) * ref
+    tol = err + HALF_ULP[dtype] * (ref + err) + TINY[dtype]
+    worst = ((dx.double() - ref).abs() / tol).max().item()
+    assert worst <= 1.0, "error %.3g times the bound" % worst
+    assert torch.equal(dx, kb.bakron_linear_grad(dy, w))
