@@ -17,8 +17,8 @@
 // that expert's tokens in shared memory; they are the columns of the matrix
 // instructions (qmma.cuh).  A warp takes whole items, or a part of the columns
 // of one when there are fewer items than warps.  h leaves multiplied by q, in two
-// bf16 terms (three for fp32), so that the second product sees it to 2^-16
-// (2^-24).
+// bf16 terms, rounded, so that the second product sees it to 2^-17 (cut off: 2^-15,
+// always towards zero); fp32's three terms hold it whole.
 //
 // moe_out_kernel.  A block owns 256 rows of y (32 per warp) and a run of the list
 // of (chosen expert, chunk of f); the expert's tokens are again the columns, and
@@ -462,7 +462,8 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
               const float g = tot[0][j][i];
               const float v = g / (1.f + expf(-g)) * tot[1][j][i] * R.weight[t][s];
               float p[3];
-              split3(v, p[0], p[1], p[2]);
+              if constexpr (HT == 2) split3_near(v, p[0], p[1], p[2]);
+              else split3(v, p[0], p[1], p[2]);
               uint8_t* o = a.h + ((int64_t)(t * a.k + s) * a.fp + row) * 2;
 #pragma unroll
               for (int q = 0; q < HT; ++q) *reinterpret_cast<uint16_t*>(o + q * a.h_plane) = bf16_bits(p[q]);

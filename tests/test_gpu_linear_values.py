@@ -146,3 +146,29 @@ def test_long_sums(T, m, n, dtype):
     worst = ((dx.double() - ref).abs() / tol).max().item()
     assert worst <= 1.0, "error %.3g times the bound" % worst
     assert torch.equal(dx, kb.bakron_linear_grad(dy, w))
+
+
+def test_experts_hidden_values_keep_sixteen_bits():
+    """One token, one expert, d = 1: h_i = 64 v_i exactly (silu(64) is 64, the routing weight 1), with v_i
+    set by a scale.  The second product adds h_i with + 1 for v = 1 + 2^-7 - 2^-23, whose bits below the
+    second bf16 term are all ones, and with - 1 for v = 1 + 2^-7, which one term holds.  Two rounded
+    terms leave at most 2^-17 of each h (two cut-off ones up to 2^-15, all of one sign)."""
+    kb = _kb()
+    f = 256
+    v = torch.full((f,), 1 + 2.0 ** -7, dtype=torch.float64)
+    v[::2] -= 2.0 ** -23
+    s_in = torch.cat([torch.full((f,), 64.0, dtype=torch.float64), v]).float().reshape(1, 2 * f, 1).cuda()
+    ones = torch.ones((1, 2 * f, 1), dtype=torch.int8, device="cuda")
+    w_in = kb.bakron_pack(ones, s_in, -8, 7)
+    sign = torch.ones((1, 1, f), dtype=torch.int8)
+    sign[..., 1::2] = -1
+    w_out = kb.bakron_pack(sign.cuda(), torch.ones((1, 1, 1), device="cuda"), -8, 7)
+    for dtype in DTYPES:
+        x = torch.ones((1, 1), dtype=dtype, device="cuda")
+        y = kb.bakron_moe(x, x, w_in, w_out, 1).double().item()
+        ref = (64 * v * sign.reshape(-1).double()).sum().item()
+        mag = (64 * v).sum().item()
+        err = (2.0 ** -17 + 2 * U * (product_depth(f) + 8)) * mag
+        # the products' own roundings are bounded apart from h's: the sums here are short and exact to 2^-23
+        tight = (2.0 ** -17 + 2.0 ** -22) * mag
+        assert abs(y - ref) <= min(err, tight) + HALF_ULP[dtype] * abs(ref) + TINY[dtype]
