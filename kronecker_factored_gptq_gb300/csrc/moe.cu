@@ -419,7 +419,9 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
         }
       }
       // the group's sums of gate and up (thread: rows lane / 4 and + 8, columns
-      // 2 (lane & 3) and + 1 of each column tile); the joins use the tokens' area
+      // 2 (lane & 3) and + 1 of each column tile); the joins use the tokens' area, which
+      // is free: G > 1 where no expert of the run has more items than there are
+      // groups, so this is the only round
       if (G > 1) {
         float* mine = reinterpret_cast<float*>(xs) + (size_t)warp * (NT * 4 * 32) + lane;
 #pragma unroll
@@ -437,13 +439,6 @@ __global__ void __launch_bounds__(kInThreads, 1) moe_in_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tot[q][j][i] += mine[(size_t)w * (NT * 4 * 32) + (j * 4 + i) * 32];
             }
-          }
-        }
-        if (rounds > 1) {      // the tokens are needed again
-          __syncthreads();
-          if (slab == nc) {
-            stage(0);
-            __syncthreads();
           }
         }
       }
