@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "packed.cuh"
+#include "rows_copy.h"
 
 namespace bakron {
 namespace {
@@ -150,15 +151,17 @@ struct Rows {
   // Bytes by which a row misses a 16-byte boundary.
   __device__ __forceinline__ uint32_t past(const TX* row) const { return (uint32_t)(uintptr_t)row & 15u; }
 
-  // A warp's pieces of one array: those of its columns, whatever lies beside
-  // them in the first and the last, zeros past the row's end.
-  __device__ __forceinline__ void copy_pieces(const TX* row, bool first_row, uint32_t to) {
+  // A warp's pieces of one array: those of its columns, with what lies in front of
+  // them in the first where that is the array's (piece_bytes), zeros past the
+  // row's end.  `front`: the array's bytes in front of the row, 16 for more.
+  __device__ __forceinline__ void copy_pieces(const TX* row, int front, uint32_t to) {
     const int lane = tid & 31, c0 = (tid & ~31) * NV * V;
     const uint32_t shift = past(row);
+    const int before = c0 > 0 ? 16 : front;
     const char* from = reinterpret_cast<const char*>(row + c0) - shift + lane * 16;
     const int left = ((int)d - c0) * (int)sizeof(TX) + (int)shift;     // bytes from piece 0 on
     to += (tid >> 5) * kWarpRow<NV> + lane * 16;
-    if (left >= (int)kWarpRow<NV> && !first_row) {
+    if (left >= (int)kWarpRow<NV> && before >= (int)shift) {
 #pragma unroll
       for (int i = 0; i <= NV; ++i)
         if (i < NV || lane == 0)
@@ -169,9 +172,10 @@ struct Rows {
       for (int i = 0; i <= NV; ++i) {
         const int at = lane * 16 + i * 512;
         if (i == NV && lane > 0) break;
-        if (at == 0 && first_row && shift && c0 == 0) {
-          // the array's first elements: what is before them is not ours
-          for (int b = (int)shift; b < min(16, left); b += sizeof(TX)) {
+        const PieceBytes p = piece_bytes(before, (int)shift, left, at);
+        if (p.from > 0) {
+          // the array begins inside this piece
+          for (int b = p.from; b < p.to; b += sizeof(TX)) {
             if constexpr (sizeof(TX) == 2)
               asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + b), "h"(*reinterpret_cast<const uint16_t*>(from + b))
                            : "memory");
@@ -179,7 +183,7 @@ struct Rows {
               asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + b), "r"(*reinterpret_cast<const uint32_t*>(from + b))
                            : "memory");
           }
-          for (int b = max((int)shift, left); b < 16; b += sizeof(TX)) {
+          for (int b = max(p.from, p.to); b < 16; b += sizeof(TX)) {
             if constexpr (sizeof(TX) == 2)
               asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + b), "h"((uint16_t)0) : "memory");
             else
@@ -187,7 +191,7 @@ struct Rows {
           }
           continue;
         }
-        const int n = max(0, min(16, left - at));
+        const int n = p.to;
         // (nothing is read from the address that goes with n = 0)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 512),
                      "l"(n ? from + i * 512 : from - lane * 16), "r"(n)
@@ -197,10 +201,11 @@ struct Rows {
   }
   __device__ __forceinline__ void copy() {
     if (next < T) {
+      const int front = next >= 16 ? 16 : min(16, (int)next * (int)d * (int)sizeof(TX));
 #pragma unroll
       for (int k = 0; k < ARRAYS; ++k) {
         if constexpr (kShift) {
-          copy_pieces(src[k] + next * d, next == 0, slot + fill + k * array_bytes());
+          copy_pieces(src[k] + next * d, front, slot + fill + k * array_bytes());
         } else {
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
