@@ -217,10 +217,27 @@ def _torch():
     return _TORCH
 
 
+def _device():
+    """Index of the current CUDA device, on which the library works."""
+    return _torch()._C._cuda_getDevice()
+
+
+def _elsewhere(index, name):
+    return ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, index, _device()))
+
+
+def _check_stream(stream):
+    index = getattr(stream, "device_index", None)
+    if index is not None and index != _device():
+        raise _elsewhere(index, "stream")
+
+
 def _dev(t, dtype, shape, name):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != _device():
+        raise _elsewhere(t.get_device(), name)
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if tuple(t.shape) != tuple(shape):
@@ -232,8 +249,11 @@ def _dev(t, dtype, shape, name):
 
 def _stream(stream):
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    else:
+        _check_stream(stream)
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def workspace_size(m, n, opts=None):
@@ -272,6 +292,10 @@ def prepare_workspace_size(n, m):
 def _ws(nbytes, workspace):
     torch = _torch()
     if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if workspace.get_device() != _device():
+            raise _elsewhere(workspace.get_device(), "workspace")
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError("workspace too small: need %d bytes" % nbytes)
         return workspace
@@ -554,15 +578,17 @@ def _dtypes():
 def _handle(stream):
     """cudaStream_t of ``stream``, or of the current stream."""
     if stream is not None:
+        _check_stream(stream)
         return stream.cuda_stream
-    c = _torch()._C
-    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return _torch()._C._cuda_getCurrentRawStream(_device())
 
 
 def _act(t, name, cols=None):
     """Checks an activation matrix; returns (rows, columns, bakron_dtype)."""
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != _device():
+        raise _elsewhere(t.get_device(), name)
     code = (_DTYPES or _dtypes()).get(t.dtype)
     if code is None:
         raise ValueError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
@@ -654,6 +680,8 @@ def bakron_pack(codes, scale, qmin, qmax, zero=None, group=None, stream=None):
 def bakron_unpack(w, stream=None):
     """V (float32) of a PackedWeight: the values the solver returned."""
     torch = _torch()
+    if w._index != _device():
+        raise _elsewhere(w._index, "the weight")
     V = torch.empty((w.count, w.m, w.n), dtype=torch.float32, device=w.device)
     _check(lib().bakron_unpack(w.ref, ctypes.c_void_p(V.data_ptr()), _stream(stream)), "bakron_unpack")
     return V[0] if w.count == 1 else V
@@ -803,13 +831,13 @@ def bakron_layernorm_grad(dy, x, gamma, mean, rstd, want_weight_grads=True, out=
     nb = 0
     if want_weight_grads:
         torch = _torch()
-        dg = torch.empty(d, dtype=torch.float32, device=x.device)
-        db = torch.empty(d, dtype=torch.float32, device=x.device)
-        gp, bp = dg.data_ptr(), db.data_ptr()
         nb = layernorm_grad_workspace_size(T, d)
         # kept until the call is enqueued, then the allocator may reuse it in stream order
         keep = _ws(nb, workspace)
         ws = keep.data_ptr()
+        dg = torch.empty(d, dtype=torch.float32, device=x.device)
+        db = torch.empty(d, dtype=torch.float32, device=x.device)
+        gp, bp = dg.data_ptr(), db.data_ptr()
     _check(lib().bakron_layernorm_grad(yp, x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"),
                                        _vec(mean, T, x, "mean"), _vec(rstd, T, x, "rstd"), dx.data_ptr(),
                                        gp, bp, ws, nb, _handle(stream)), "bakron_layernorm_grad")
