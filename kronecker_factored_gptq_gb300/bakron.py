@@ -217,9 +217,15 @@ def _torch():
     return _TORCH
 
 
+_DEVICE = None
+
+
 def _device():
     """Index of the current CUDA device, on which the library works."""
-    return _torch()._C._cuda_getDevice()
+    global _DEVICE
+    if _DEVICE is None:
+        _DEVICE = _torch()._C._cuda_getDevice
+    return _DEVICE()
 
 
 def _elsewhere(index, name):
@@ -575,20 +581,21 @@ def _dtypes():
     return _DTYPES
 
 
-def _handle(stream):
-    """cudaStream_t of ``stream``, or of the current stream."""
+def _handle(stream, index):
+    """cudaStream_t of ``stream``, or of the current stream of ``index``, the current device."""
     if stream is not None:
         _check_stream(stream)
         return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(_device())
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 def _act(t, name, cols=None):
-    """Checks an activation matrix; returns (rows, columns, bakron_dtype)."""
+    """Checks an activation matrix; returns (rows, columns, bakron_dtype, device)."""
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.get_device() != _device():
-        raise _elsewhere(t.get_device(), name)
+    index = t.get_device()
+    if index != _device():
+        raise _elsewhere(index, name)
     code = (_DTYPES or _dtypes()).get(t.dtype)
     if code is None:
         raise ValueError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
@@ -598,7 +605,7 @@ def _act(t, name, cols=None):
                          % (name, "columns" if cols is None else cols, tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return shape[0], shape[1], code
+    return shape[0], shape[1], code, index
 
 
 def _same(t, like, shape, name):
@@ -643,6 +650,10 @@ class PackedWeight:
         self._index = data.get_device()
         self._ws = {}
 
+    def _here(self):
+        if self._index != _device():
+            raise _elsewhere(self._index, "the weight")
+
     def _check(self, like, name):
         if like.get_device() != self._index:
             raise ValueError("%s must be on %s, the weight's device" % (name, self.device))
@@ -680,8 +691,7 @@ def bakron_pack(codes, scale, qmin, qmax, zero=None, group=None, stream=None):
 def bakron_unpack(w, stream=None):
     """V (float32) of a PackedWeight: the values the solver returned."""
     torch = _torch()
-    if w._index != _device():
-        raise _elsewhere(w._index, "the weight")
+    w._here()
     V = torch.empty((w.count, w.m, w.n), dtype=torch.float32, device=w.device)
     _check(lib().bakron_unpack(w.ref, ctypes.c_void_p(V.data_ptr()), _stream(stream)), "bakron_unpack")
     return V[0] if w.count == 1 else V
@@ -693,6 +703,11 @@ def bakron_async_status(stream=None):
 
 
 def linear_workspace_size(w, T, dtype, grad=False):
+    w._here()           # the size depends on the device's SM count
+    return _linear_ws_size(w, T, dtype, grad)
+
+
+def _linear_ws_size(w, T, dtype, grad):
     key = (T, dtype, grad)
     size = w._ws.get(key)
     if size is None:
@@ -716,14 +731,15 @@ def linear_workspace(w, T, dtype, grad=False):
 
 def _linear(fn, where, grad, x, w, out, workspace, stream):
     name = "dY" if grad else "X"
-    T, _, code = _act(x, name, w.m if grad else w.n)
+    T, _, code, dev = _act(x, name, w.m if grad else w.n)
     w._check(x, name)
     if w.count != 1:
         raise ValueError("%s takes a single matrix, got %d" % (where, w.count))
     y = _out(out, x, (T, w.n if grad else w.m), "out")
-    nb = linear_workspace_size(w, T, x.dtype, grad)
+    nb = _linear_ws_size(w, T, x.dtype, grad)
     ws = _ws(nb, workspace) if nb else None     # alive until the call is enqueued
-    st = fn(x.data_ptr(), T, code, w.ref, y.data_ptr(), None if ws is None else ws.data_ptr(), nb, _handle(stream))
+    st = fn(x.data_ptr(), T, code, w.ref, y.data_ptr(), None if ws is None else ws.data_ptr(), nb,
+            _handle(stream, dev))
     if st != OK:
         raise BakronError(st, where)
     return y
@@ -742,6 +758,11 @@ def bakron_linear_grad(dy, w, out=None, workspace=None, stream=None):
 
 
 def moe_workspace_size(w_in, w_out, T, top_k, dtype):
+    w_in._here()
+    return _moe_ws_size(w_in, w_out, T, top_k, dtype)
+
+
+def _moe_ws_size(w_in, w_out, T, top_k, dtype):
     key = (T, dtype, top_k, w_out.n)
     size = w_in._ws.get(key)
     if size is None:
@@ -766,7 +787,7 @@ def bakron_moe(x, router, w_in, w_out, top_k, renormalize=True, out=None, worksp
     """A mixture-of-experts layer: x (T, d), router (E, d) of x's type, w_in
     (E matrices of 2f x d: gate rows, then up rows), w_out (E of d x f).
     Returns (T, d) of x's type."""
-    T, d, code = _act(x, "X", w_in.n)
+    T, d, code, dev = _act(x, "X", w_in.n)
     if (w_in.count, w_out.m) != (w_out.count, d) or w_in.m != 2 * w_out.n:
         raise ValueError("w_in must hold E matrices of 2f x d and w_out E of d x f, got %d of %d x %d and "
                          "%d of %d x %d" % (w_in.count, w_in.m, w_in.n, w_out.count, w_out.m, w_out.n))
@@ -774,10 +795,10 @@ def bakron_moe(x, router, w_in, w_out, top_k, renormalize=True, out=None, worksp
     w_out._check(x, "X")
     rp = _same(router, x, (w_in.count, d), "router")
     y = _out(out, x, (T, d), "out")
-    nb = moe_workspace_size(w_in, w_out, T, top_k, x.dtype)
+    nb = _moe_ws_size(w_in, w_out, T, top_k, x.dtype)
     ws = _ws(nb, workspace)
     _check(lib().bakron_moe(x.data_ptr(), T, code, rp, w_in.ref, w_out.ref, int(top_k),
-                            1 if renormalize else 0, y.data_ptr(), ws.data_ptr(), nb, _handle(stream)),
+                            1 if renormalize else 0, y.data_ptr(), ws.data_ptr(), nb, _handle(stream, dev)),
            "bakron_moe")
     return y
 
@@ -786,7 +807,7 @@ def bakron_layernorm(x, gamma=None, beta=None, eps=1e-5, out=None, want_stats=Tr
     """Layer norm of the rows of x (T, d); gamma, beta (d,) float32 or None.
     Returns (y, mean, rstd); mean and rstd (T,) float32 feed the gradient
     (None without want_stats)."""
-    T, d, code = _act(x, "X")
+    T, d, code, dev = _act(x, "X")
     y = _out(out, x, (T, d), "out")
     mean = rstd = mp = rp = None
     if want_stats:
@@ -795,7 +816,7 @@ def bakron_layernorm(x, gamma=None, beta=None, eps=1e-5, out=None, want_stats=Tr
         rstd = torch.empty(T, dtype=torch.float32, device=x.device)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
     _check(lib().bakron_layernorm(x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"), _vec(beta, d, x, "beta"),
-                                  eps, y.data_ptr(), mp, rp, _handle(stream)), "bakron_layernorm")
+                                  eps, y.data_ptr(), mp, rp, _handle(stream, dev)), "bakron_layernorm")
     return y, mean, rstd
 
 
@@ -803,7 +824,9 @@ _NORM_WS = {}
 
 
 def layernorm_grad_workspace_size(T, d):
-    size = _NORM_WS.get((T, d))
+    """Bytes on the current device (they depend on its SM count)."""
+    key = (T, d, _device())
+    size = _NORM_WS.get(key)
     if size is None:
         b = ctypes.c_size_t(0)
         _check(lib().bakron_layernorm_grad_workspace_size(T, d, ctypes.byref(b)),
@@ -811,12 +834,12 @@ def layernorm_grad_workspace_size(T, d):
         size = b.value
         if len(_NORM_WS) > 256:
             _NORM_WS.clear()
-        _NORM_WS[(T, d)] = size
+        _NORM_WS[key] = size
     return size
 
 
 def layernorm_grad_workspace(T, d):
-    """A workspace for bakron_layernorm_grad of up to T rows of d."""
+    """A workspace for bakron_layernorm_grad of up to T rows of d, on the current device."""
     return _torch().empty(layernorm_grad_workspace_size(T, d), dtype=_torch().uint8, device="cuda")
 
 
@@ -824,7 +847,7 @@ def bakron_layernorm_grad(dy, x, gamma, mean, rstd, want_weight_grads=True, out=
                           stream=None):
     """Gradients of bakron_layernorm: returns (dx, dgamma, dbeta), dgamma and
     dbeta (d,) float32 (None without want_weight_grads)."""
-    T, d, code = _act(x, "X")
+    T, d, code, dev = _act(x, "X")
     yp = _same(dy, x, (T, d), "dY")
     dx = _out(out, x, (T, d), "out")
     dg = db = gp = bp = ws = None
@@ -840,7 +863,7 @@ def bakron_layernorm_grad(dy, x, gamma, mean, rstd, want_weight_grads=True, out=
         gp, bp = dg.data_ptr(), db.data_ptr()
     _check(lib().bakron_layernorm_grad(yp, x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"),
                                        _vec(mean, T, x, "mean"), _vec(rstd, T, x, "rstd"), dx.data_ptr(),
-                                       gp, bp, ws, nb, _handle(stream)), "bakron_layernorm_grad")
+                                       gp, bp, ws, nb, _handle(stream, dev)), "bakron_layernorm_grad")
     return dx, dg, db
 
 

@@ -218,12 +218,15 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
   auto ring = [&](int w) {
     return (size_t)w * qm::Pipe<1, NS, kDepth>::kBytes + (size_t)kDepth * TERMS * a.T * kPitch;
   };
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   int warps = 8, S = 1;      // whose memory always fits
   double best = 0.0;
   for (int c = 1; c <= 8 && c <= np; c *= 2) {
-    static std::atomic<int> fit[4];            // row groups at once, by c = 1, 2, 4, 8 (0: not asked yet)
-    std::atomic<int>& f_c = fit[c == 8 ? 3 : c / 2];
-    int at_once = f_c.load(std::memory_order_relaxed);
+    // row groups at once on each device, by c = 1, 2, 4, 8 (0: not asked yet)
+    static std::atomic<int> fit[64][4];
+    std::atomic<int>* const kept = dev < 64 ? &fit[dev][c == 8 ? 3 : c / 2] : nullptr;
+    int at_once = kept ? kept->load(std::memory_order_relaxed) : 0;
     if (at_once == 0) {
       at_once = sm_count();
       if (c > 1) {
@@ -232,7 +235,7 @@ cudaError_t run(const LinearArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
       }
       if (at_once < 1) at_once = 1;
-      f_c.store(at_once, std::memory_order_relaxed);
+      if (kept) kept->store(at_once, std::memory_order_relaxed);
     }
     for (int w = kMaxWarps; w >= 8; --w) {
       if (ring(w) > kSmem) continue;

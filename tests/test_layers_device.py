@@ -130,3 +130,23 @@ def test_packing_and_unpacking(device):
         kb.bakron_unpack(weight(1))
     with pytest.raises(ValueError, match="scale is on cuda:1"):
         kb.bakron_pack(on(0, 16, 32, dtype=torch.int8), scale, -8, 7)
+
+
+def test_norm_workspace_sizes_are_kept_per_device(device):
+    assert kb.layernorm_grad_workspace_size(5, 64) == 1000
+    device[0] = 1
+    assert kb.layernorm_grad_workspace_size(5, 64) == 2000
+    device[0] = 0
+    assert kb.layernorm_grad_workspace_size(5, 64) == 1000
+
+
+def test_workspace_sizes_are_asked_on_the_weights_device(device):
+    w, wi, wo = weight(1), weight(1, 2, 16, 64), weight(1, 2, 64, 8)
+    for ask in (lambda: kb.linear_workspace_size(w, 5, torch.float32),
+                lambda: kb.linear_workspace_size(w, 5, torch.float32, grad=True),
+                lambda: kb.moe_workspace_size(wi, wo, 5, 1, torch.float32)):
+        with pytest.raises(ValueError, match="current device"):
+            ask()
+        device[0] = 1
+        assert ask() == 64
+        device[0] = 0
