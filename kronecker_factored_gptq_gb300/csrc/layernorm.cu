@@ -30,6 +30,7 @@
 // time), 8192 x 1024 8.6 and 20, 8192 x 4097 64 and 113 (instructions per column),
 // 37 x 1111 fp32 2.9 and 3.4 (launch and latency).
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "packed.cuh"
@@ -939,6 +940,10 @@ bool norm_args_ok(int64_t T, int64_t d, int dtype) {
   return dtype_ok(dtype) && T >= 0 && T <= (int64_t(1) << 31) && d >= 1 && d <= (int64_t(1) << 20);
 }
 
+bool floats_aligned(std::initializer_list<const float*> all) {
+  return std::all_of(all.begin(), all.end(), [](const float* p) { return aligned_to(p, 4); });
+}
+
 // The alignment of the pointers and the type are not known to the size call.
 size_t grad_bytes(int64_t T, int64_t d) {
   int64_t rows = 0;
@@ -960,7 +965,8 @@ extern "C" bakron_status bakron_layernorm(const void* X, int64_t T, int64_t d, i
   if (!norm_args_ok(T, d, dtype) || !(eps >= 0.f)) return BAKRON_ERR_INVALID_ARG;
   if (T == 0) return BAKRON_OK;
   const size_t es = dtype_size(dtype);
-  if (!X || !Y || !aligned_to(X, es) || !aligned_to(Y, es)) return BAKRON_ERR_INVALID_ARG;
+  if (!X || !Y || !aligned_to(X, es) || !aligned_to(Y, es) || !floats_aligned({gamma, beta, mean, rstd}))
+    return BAKRON_ERR_INVALID_ARG;
   NormArgs a = {};
   a.x = X;
   a.T = T;
@@ -1004,7 +1010,7 @@ extern "C" bakron_status bakron_layernorm_grad(const void* dY, const void* X, in
   }
   const size_t es = dtype_size(dtype);
   if (!X || !dY || !dX || !mean || !rstd || !aligned_to(X, es) || !aligned_to(dY, es) ||
-      !aligned_to(dX, es))
+      !aligned_to(dX, es) || !floats_aligned({gamma, mean, rstd, dgamma, dbeta}))
     return BAKRON_ERR_INVALID_ARG;
   if (dgamma && (!ws || !aligned_to(ws, 256) || ws_bytes < grad_bytes(T, d)))
     return BAKRON_ERR_INVALID_ARG;

@@ -156,7 +156,8 @@ extern "C" bakron_status bakron_pack(const int8_t* codes, const float* scale, co
   if (!codes || !scale || !data || !pack_layout(count, m, n, group, zero != nullptr, &L))
     return BAKRON_ERR_INVALID_ARG;
   if (qmin < -128 || qmin > qmax || qmax > 127 || qmax - qmin > 15) return BAKRON_ERR_INVALID_ARG;
-  if (!aligned_to(data, 16) || data_bytes < L.total) return BAKRON_ERR_INVALID_ARG;
+  if (!aligned_to(data, 16) || data_bytes < L.total || !aligned_to(scale, 4) || !aligned_to(zero, 4))
+    return BAKRON_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   uint8_t* p = static_cast<uint8_t*>(data);
   DevStatus* st = reinterpret_cast<DevStatus*>(p);
@@ -178,7 +179,7 @@ extern "C" bakron_status bakron_pack(const int8_t* codes, const float* scale, co
 
 extern "C" bakron_status bakron_unpack(const bakron_packed* w, float* V, void* stream) {
   PackedView v;
-  if (!V || !packed_view(w, &v)) return BAKRON_ERR_INVALID_ARG;
+  if (!V || !aligned_to(V, 4) || !packed_view(w, &v)) return BAKRON_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   count_launch();
   unpack_kernel<<<grid_words(v.count * v.mp * v.nc * 16), 256, 0, s>>>(v, V);
