@@ -9,7 +9,7 @@ namespace {
 
 // x (T x K, any alignment) -> planes [TERMS][T][kp] of 16-bit terms, zeros
 // past K: the activations as the tensor map wants them.
-template <typename TX, int TERMS, bool kNear>
+template <typename TX, int TERMS, bool kGrad>
 __global__ void __launch_bounds__(256) planes_kernel(const TX* __restrict__ x, int64_t T, int64_t K,
                                                      int64_t kp, uint16_t* __restrict__ out) {
   const int64_t per = kp / 8, total = T * per;
@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(256) planes_kernel(const TX* __restrict__ x, i
           v[0] = *reinterpret_cast<const uint16_t*>(p);
         } else {
           float f[3];
-          if constexpr (kNear) split3_near(to_float(*p), f[0], f[1], f[2]);
+          if constexpr (kGrad) split3_grad(to_float(*p), f[0], f[1], f[2]);
           else split3(to_float(*p), f[0], f[1], f[2]);
 #pragma unroll
           for (int q = 0; q < 3; ++q) v[q] = bf16_bits(f[q]);
@@ -106,13 +106,13 @@ bakron_status run_linear(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, vo
 }  // namespace
 
 cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_t kp, void* out,
-                          cudaStream_t s, bool near) {
+                          cudaStream_t s, bool grad) {
   const int64_t total = T * kp / 8;
   const unsigned g = (unsigned)std::max<int64_t>(1, std::min<int64_t>((total + 255) / 256, (int64_t)sm_count() * 16));
   uint16_t* o = static_cast<uint16_t*>(out);
   count_launch();
   const float* f = static_cast<const float*>(x);
-  if (dtype == BAKRON_F32 && near) planes_kernel<float, 3, true><<<g, 256, 0, s>>>(f, T, K, kp, o);
+  if (dtype == BAKRON_F32 && grad) planes_kernel<float, 3, true><<<g, 256, 0, s>>>(f, T, K, kp, o);
   else if (dtype == BAKRON_F32) planes_kernel<float, 3, false><<<g, 256, 0, s>>>(f, T, K, kp, o);
   else planes_kernel<uint16_t, 1, false><<<g, 256, 0, s>>>(static_cast<const uint16_t*>(x), T, K, kp, o);
   return cudaGetLastError();

@@ -33,10 +33,10 @@ cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_mid(const LinearArgs& a, cudaStream_t s);
 
 // x (T x K of dtype, any alignment) -> planes [terms][T][kp] of 16-bit terms (1,
-// or 3 for fp32), zeros past K; out is 16-byte aligned, kp a multiple of 8.  `near`: the
-// terms are rounded instead of cut off (split3_near).
+// or 3 for fp32), zeros past K; out is 16-byte aligned, kp a multiple of 8.  `grad`: the
+// terms of the gradient's dY (split3_grad).
 cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_t kp, void* out,
-                          cudaStream_t s, bool near = false);
+                          cudaStream_t s, bool grad = false);
 
 // tcgen05 products for many tokens, and the gradient for any number.
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);

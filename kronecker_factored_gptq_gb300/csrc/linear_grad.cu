@@ -59,7 +59,6 @@ constexpr int kMaxStages = 8;
 
 struct GradArgs {
   PackedView w;
-  const void* dy;
   void* y;
   int64_t T;          // tokens
   int64_t plane;      // token rows per plane of dY's map
@@ -123,43 +122,6 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   lo = __byte_perm(__float_as_uint(rx - m.x), __float_as_uint(ry - m.y), 0x7632);
 }
 
-// fp32 dY: what infinities and NaN of token t's gradient bring to output column j
-// of this lane (the warp's lanes: 32 columns, one token).  An infinite gradient is
-// its first term alone; its products with the weights' second and third terms, which
-// are often exact zeros, are NaN where the formula has an infinity.  So a sum that
-// is not finite is formed anew from the gradients that are not and
-// the signs of their weights; false when there are none (a sum that overflowed).
-__device__ __noinline__ bool nonfinite_part(const GradArgs& a, int64_t t, int64_t j, float& sum) {
-  const PackedView& w = a.w;
-  const int lane = threadIdx.x & 31, in = (int)(j & 127), k = in & 7;
-  const float* dy = static_cast<const float*>(a.dy) + t * w.m;
-  const uint8_t* word = w.codes + (j >> 7) * kBlockBytes + (((in >> 3) & 3) * 4 + (in >> 5)) * 4;
-  const int shift = 4 * (k >> 1) + 16 * (k & 1);
-  const uint32_t group = grid_group(w, (uint32_t)j) * 16;
-  bool found = false;
-  sum = 0.f;
-  constexpr int Q = 8;
-  for (int64_t i0 = 0; i0 < w.m; i0 += 32 * Q) {
-    float v[Q];
-#pragma unroll
-    for (int q = 0; q < Q; ++q) v[q] = i0 + 32 * q + lane < w.m ? dy[i0 + 32 * q + lane] : 0.f;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      uint32_t which = __ballot_sync(0xffffffffu, !(fabsf(v[q]) < INFINITY));
-      found |= which != 0;
-      for (; which != 0; which &= which - 1) {
-        const int b = __ffs((int)which) - 1;
-        const int64_t i = i0 + 32 * q + b;
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(word + (i >> 3) * w.nc * kBlockBytes + (i & 7) * 64);
-        const int z = w.zero ? w.zero[grid_row(w, 0, i) + group] : w.zu;
-        sum = fmaf(__shfl_sync(0xffffffffu, v[q], b), (float)((int)((u >> shift) & 15u) - z), sum);
-      }
-    }
-    if (__all_sync(0xffffffffu, sum != sum)) break;
-  }
-  return found;
-}
-
 struct Bars {
   unsigned long long full[kMaxStages], empty[kMaxStages];
   unsigned long long acc_full[2], acc_empty[2], done;
@@ -203,8 +165,6 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
   if (group >= turn) return;                // uses apart by one bit, so none may be two ahead
   const uint32_t full = smem_u32(bars.full), empty = smem_u32(bars.empty);
   const int64_t nb = w.mp / 8;
-  float range_in, range_out;
-  operand_range<H>(a, range_in, range_out);
   const int n = k.k1 - k.k0;
   auto load = [&](Codes<SN, NS>& c, int64_t tile, int m, int i) {
     const int64_t b = (int64_t)(k.k0 + i) * 8 + rb;
@@ -252,6 +212,8 @@ __device__ __forceinline__ void weights(const GradArgs& a, const Work& k, Bars& 
   settle();
   Codes<SN, NS> c;
   load(c, tile, m, i);
+  float range_in, range_out;
+  operand_range<H>(a, range_in, range_out);
   Ring rg;
   rg.advance(group, a.stages);
   while (tile < a.tiles) {
@@ -374,8 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
   grid_dep_wait();
   grid_dep_launch();
-  float range_in, range_out;
-  operand_range<H>(a, range_in, range_out);
 
   if (warp == 0) {
     // ---------------- incoming gradients
@@ -445,7 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int qw = 0; qw < TW; ++qw)
 #pragma unroll
               for (int qx = 0; qx < TX; ++qx) {
-                if (qw + qx > 2) continue;   // together at most 2^-24 (1 + 2^-9) of the product
+                // together at most 2^-24 (1 + 2^-9) of the product; the last term of dY, which
+                // holds its infinities, meets the first of the weights alone (split3_grad)
+                if (qw + qx > 2) continue;
                 const bool large = qw == 0 && qx == 0;
                 mma_f16(large ? d : d + (uint32_t)a.N, da + (uint32_t)(qw * (kABytes >> 4) + j * 2),
                         db + (qx * plane16 + j * 2), idesc, begin && j == 0 && (large || (qw == 0 && qx == 1)) ? 0u : 1u);
@@ -467,8 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const uint32_t af = smem_u32(&bars.acc_full[0]), ae = smem_u32(&bars.acc_empty[0]);
     float* part = reinterpret_cast<float*>(dsm + (ring - base_raw));   // S > 1: [column][row], in the idle ring
+    float range_in, range_out;
+    operand_range<H>(a, range_in, range_out);
     uint32_t u_all = 0;
-    bool ok = true, off = false;             // off: a sum of this lane is not finite
+    bool ok = true;
     for (int64_t tile = k.tile; tile < a.tiles && ok; tile += k.step) {
       const int64_t row = (tile % a.tiles_m) * 128 + quarter * 32 + lane;
       const int64_t t0 = tile / a.tiles_m * a.N;
@@ -532,23 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < NC; ++t) {
           if (t < a.N) {
-            if (!(fabsf(acc[t]) < INFINITY)) off = true;
             if (S > 1) part[t * 128 + quarter * 32 + lane] = acc[t];
             else if (ok && row < a.w.n && t0 + t < a.T) y[(int64_t)t * a.w.n] = from_float<TO>(acc[t] * range_out);
-          }
-        }
-      }
-    }
-    if constexpr (!kWhole) {
-      // after the last tile, when no other warp waits for this one any more
-      if (S == 1 && ok && __any_sync(0xffffffffu, off)) {
-        for (int64_t tile = k.tile; tile < a.tiles; tile += k.step) {
-          const int64_t row = (tile % a.tiles_m) * 128 + quarter * 32 + lane, t0 = tile / a.tiles_m * a.N;
-          for (int64_t t = t0; t < min(t0 + a.N, a.T); ++t) {
-            TO* y = static_cast<TO*>(a.y) + t * a.w.n + row;
-            const bool bad = row < a.w.n && !(fabsf(*y) < INFINITY);
-            float v;
-            if (__any_sync(0xffffffffu, bad) && nonfinite_part(a, t, row, v) && bad) *y = v;
           }
         }
       }
@@ -577,22 +526,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (S > 1) {
     // each block adds up and writes every S-th column
     float* part = reinterpret_cast<float*>(dsm + (ring - base_raw));
+    float range_in, range_out;
+    operand_range<H>(a, range_in, range_out);
     __syncwarp();
     cluster.sync();
     const int r = threadIdx.x & 127;
     const int64_t row = (k.tile % a.tiles_m) * 128 + r, t0 = k.tile / a.tiles_m * a.N;
     for (int c = rank + S * (threadIdx.x >> 7); c < a.N; c += S * (kThreads / 128)) {
-      if (t0 + c >= a.T) continue;           // the whole warp
+      if (row >= a.w.n || t0 + c >= a.T) continue;
       float v = 0.f;
       for (int q = 0; q < S; ++q) v += cluster.map_shared_rank(part, q)[c * 128 + r];
-      const bool live = row < a.w.n;
-      float out = v * range_out;
-      if constexpr (TX > 1) {
-        const bool off = live && !(fabsf(v) < INFINITY);
-        float f;
-        if (__any_sync(0xffffffffu, off) && nonfinite_part(a, t0 + c, row, f) && off) out = f;
-      }
-      if (live) static_cast<TO*>(a.y)[(t0 + c) * a.w.n + row] = from_float<TO>(out);
+      static_cast<TO*>(a.y)[(t0 + c) * a.w.n + row] = from_float<TO>(v * range_out);
     }
     __syncwarp();
     cluster.sync();   // no block leaves while its sums are read
@@ -605,7 +549,6 @@ cudaError_t run(const LinearArgs& a, int N, cudaStream_t s) {
   const int64_t K = a.w.m;
   GradArgs t = {};
   t.w = a.w;
-  t.dy = a.x;
   t.y = a.y;
   t.T = a.T;
   t.tiles_m = (int)((a.w.n + 127) / 128);

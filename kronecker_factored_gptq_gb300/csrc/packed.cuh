@@ -216,6 +216,17 @@ __device__ __forceinline__ void split3_near(float x, float& hi, float& mid, floa
   lo = r - mid;
 }
 
+// split3_near for the gradient's dY, whose last term is multiplied with the weights'
+// first terms only: there an infinity or NaN meets what the formula has, zero where the
+// weight is, and not the exact zeros that the weights' other terms often are.
+__device__ __forceinline__ void split3_grad(float x, float& hi, float& mid, float& lo) {
+  split3_near(x, hi, mid, lo);
+  if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) {
+    lo = hi;
+    hi = 0.f;
+  }
+}
+
 // The top half of a float that is a bf16.
 __device__ __forceinline__ uint16_t bf16_bits(float x) {
   return (uint16_t)(__float_as_uint(x) >> 16);
