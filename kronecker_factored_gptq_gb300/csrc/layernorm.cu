@@ -25,10 +25,13 @@
 // need no moving, took 172 us instead of 113 for the gradient of 8192 x 4097 bf16;
 // one column per load took 165.)
 //
-// Measured, forward and gradient: 8192 x 4096 bf16 31 and 42 us (4.3 and 4.8 TB/s; the bytes
-// at 6.68 TB/s 20 and 30), 2048 x 14336 fp16 31 and 53 (one block per SM, one row at a
-// time), 8192 x 1024 8.6 and 20, 8192 x 4097 64 and 113 (instructions per column),
-// 37 x 1111 fp32 2.9 and 3.4 (launch and latency).
+// Measured, forward and gradient: 8192 x 4096 bf16 31 and 43 us (4.3 and 4.7 TB/s; the bytes
+// at 6.68 TB/s 20 and 30), 2048 x 14336 fp16 32 and 54 (one block per SM, one row at a
+// time), 8192 x 1024 8.7 and 19, 8192 x 4097 65 and 115 (instructions per column),
+// 37 x 1111 fp32 3.0 and 3.2 (launch and latency).  Past 14336 columns a
+// thread of the gradient holds 32 columns, in a kernel that is compiled for 1024 threads and
+// spills at its 64 registers (9 % of the executed instructions): 2048 x 14344 fp16 117,
+// 2048 x 16384 bf16 126.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>

@@ -70,9 +70,12 @@ Kernel forward_kernel(const LinearArgs& a) {
   if (a.T > kMidTokens) return kMany;
   // Between 33 and 64 tokens: microseconds by what was measured of the two, the
   // second by the codes, the third by a block's chunks, which cost more when
-  // they hold more groups (bf16, 48 tokens, second and third: 8192 x 8192 29.5 and
-  // 25.4, with groups of 64 44 and 39, of 32 44 and 71; 14336 x 4096, whose 112
-  // tiles leave SMs idle, 25.6 and 23.8, 33 and 38, 34 and 71).
+  // they hold more groups (bf16, second and third, groups of 128, 64 and 32;
+  // 48 tokens of 8192 x 8192: 29.4 and 25.1, 41.5 and 39.2, 42.0 and 71.2; of 14336 x 4096,
+  // whose 112 tiles leave SMs idle: 25.7 and 23.7, 31.6 and 38.2, 32.3 and 70.9; 64 tokens
+  // of 8192 x 8192: 36.4 and 25.7, 55.3 and 39.8, 55.8 and 72.1).  Fitted to large
+  // layers: of small ones it overrates the second (48 tokens of 4096 x 4096, groups of 64:
+  // 13.7, and it takes the third's 14.9; of 2048 x 8192, groups of 128: 13.2 and 21.9).
   const bool narrow = a.w.ng > 1 && a.w.g % 128 != 0;
   const double mid = 1e-6 * (double)(a.w.mp * a.w.nc * 128) * (narrow ? 0.55 : 0.38) * (a.T <= 48 ? 1.0 : 1.3);
   const double many = (double)linear_fwd_steps(a) * (!narrow ? 0.57 : a.w.g % 64 == 0 ? 1.05 : 2.05);

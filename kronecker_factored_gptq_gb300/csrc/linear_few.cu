@@ -4,9 +4,10 @@
 // once and used for at most 16 tokens, so the codes' bytes bound the kernel
 // (m n / 2; at 8192 x 8192 33.6 MB, 5.0 us at 6.68 TB/s); the products run on
 // warp-level matrix instructions (qmma.cuh), which cost a fraction of that.  Measured:
-// 1 token of 8192 x 8192 bf16 10.3 us (3.3 TB/s), 16 tokens 16 us; 1 token of 1024 x 1024
-// 1.7 us and 7 of 1000 x 1111 fp32 4.4 us, which are launch and latency.  What bounds
-// the large ones is the instructions per code (some 350 per 32 x 128 codes).
+// 1 token of 8192 x 8192 bf16 10.4 us (3.3 TB/s), 16 tokens 16 us; 1 token of 1024 x 1024
+// 1.8 us and 7 of 1000 x 1111 fp32 4.3 us, which are launch and latency.  What bounds
+// the large ones is the latency of a warp's dependent instructions (some 350 per 32 x 128
+// codes): 44 % of the issue slots and a fifth of the warps an SM could hold are in use.
 //
 // A block takes 16 or 32 rows; its 8 warps take the 128-column chunks of the rows in
 // turn, each with several chunks on their way, and add their partial sums in

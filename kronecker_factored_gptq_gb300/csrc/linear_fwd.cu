@@ -30,12 +30,14 @@
 // half a chunk kept the tensor core waiting for it.  TMEM: two accumulators of N
 // columns, then four stages of weights (two where N is above 128).
 //
-// Measured: 2048 tokens of 8192 x 8192 bf16 in 208 us, 1.32 PFLOP/s; 48 tokens 24 us.  A
+// Measured: 2048 tokens of 8192 x 8192 bf16 in 206 us in a graph of one weight (1.34
+// PFLOP/s) and 215 among calls on several; 48 tokens 25 us; fp32, 1024 tokens of 4096 x 4096 103 us
+// and 2048 of 8192 x 8192 648 us (three products: 1.27 PFLOP/s).  A
 // chunk takes 1270 cycles at 192 tokens, of which the tensor core works 768: the
 // issuing warp's waits, one after the other, are the rest; few tokens do not make it
 // shorter than 985, what eight warps need to turn a chunk's codes into
 // operands.  With groups of 32 columns an accumulator goes to and fro every 32
-// columns, 650 cycles each (1024 tokens of 4096 x 4096: 88 us, groups of 128: 45).  Tried and
+// columns, 650 cycles each (1024 tokens of 4096 x 4096: 102 us, groups of 128: 44).  Tried and
 // slower: one wait of three lanes on the three barriers (208 -> 260 us), the scales
 // copied ahead to shared memory (208 -> 234).
 //

@@ -18,7 +18,8 @@
 // 16-bit dY: the sum over 4096 rows (bf16: 32768) stays in TMEM, a chain of one addition
 // per 16 rows that cuts off at most 2^-23 of the partial sum: 2^-15 (2^-12) in all, an eighth
 // of the result's own rounding.  Longer sums are added from such chains in fp32, by way of
-// the workspace (fp16, 1024 tokens of 14336 x 4096: 127 us, one chain 119).  Two accumulators
+// the workspace (fp16, 1024 tokens of 14336 x 4096 in four chains 116 us, bf16 in one 107;
+// 512 of 65536 x 4096 in 16 and 2 chains 483 and 441).  Two accumulators
 // let the epilogue take one while the next is summed.  fp32 dY: the sum is cut after every 128 rows and
 // added in fp32 registers, and the five small products have an accumulator of
 // their own, so that the large one is cut off 8 times a unit instead of 48 (error
@@ -28,11 +29,15 @@
 // part of the rows of one, joined over a cluster through distributed shared memory):
 //   warp 0: TMA producer of dY;  warp 1: issues the tcgen05.mma (M 128, K 16);
 //   warp 2: allocates and frees TMEM;  warps 4-11: weights;  warps 12-15: epilogue.
+// The scales enter and leave by a power of two (operand_range), so that V may be of any
+// size in any type.
 //
-// Measured: 2048 tokens of 4096 x 14336 bf16 in 210 us, 1.15 PFLOP/s, bound by the
-// issuing warp's waits and by the warps that transpose; 333 tokens of 1000 x 1300 fp32 21.5 us
-// and 1024 of 4096 x 4096 fp32 279 us, bound by the warps that split each weight into its
-// terms (with a branch for infinite weights there 27 and 443 us).
+// Measured: 2048 tokens of 4096 x 14336 bf16 in 204 us in a graph of one weight (1.18
+// PFLOP/s) and 215 among calls on several, bound by the issuing warp's waits and by the
+// warps that transpose; 333 tokens of 1000 x 1300 fp32 21 us and 1024 of 4096 x 4096 fp32
+// 257 us (groups of 32: 280), bound by the warps that split each weight into its terms
+// (with a branch for infinite weights there 27 and 443 us; code for them behind the
+// sums, even where no call reached it, 272).
 //
 // Every mbarrier wait is bounded (clock64 budget); a block whose wait runs
 // out records BAKRON_ERR_TIMEOUT in the device's status word, stops issuing,

@@ -32,10 +32,15 @@
 // (As clusters of 16 with the sums in distributed shared memory not all blocks fitted
 // at once: 184 us against 122 at 16 tokens x 8 experts of 4096 x 14336.)
 //
-// Measured: 16 tokens, 8 experts of 4096 x 14336, two each, bf16: 232 us, of which the two
-// products 129 and 106 alone, against 111 for the experts' bytes: the instructions
-// per code bound them, as in the few-token product.  One token, 4 of 32 experts of
-// 1024 x 704: 27 us, latencies of the launches and of the selection.
+// Measured: 16 tokens, 8 experts of 4096 x 14336, two each, bf16: 231 to 262 us by routing
+// (an expert with more than eight tokens takes the loop for two column tiles), of which
+// the two products about 130 and 100 alone, against 111 for the experts' bytes: latency
+// and the instructions per code bound them, as in the few-token product (50 to 54 % of
+// the issue slots, 24 % of the warps).  All loops of a kernel share 128 registers and
+// spill; 2 to 3 % of the executed instructions are spills' there, 4 in fp32, 7 for one
+// token.  One token, 4 of 32 experts of 1024 x 704: 27 us, latencies of the launches and
+// of the selection.  Every 32 tokens read their experts again: 2048 tokens, 8 experts of
+// 4096 x 4096, take 8.4 ms.
 #include <algorithm>
 #include <type_traits>
 
@@ -517,7 +522,9 @@ __global__ void __launch_bounds__(kOutThreads, 2) moe_out_kernel(const __grid_co
   const int nc = (int)a.wo.nc;
   const int units = na * nc;                                // (expert, chunk)
   const int u0 = (int)((int64_t)units * rank / S), u1 = (int)((int64_t)units * (rank + 1) / S);
-  // the block's sums [T][256]; a thread adds to what it wrote itself
+  // the block's sums [T][256].  A token is another column, and so another lane's, for each
+  // expert; what its sums were is seen because the warps meet (__syncthreads) when the
+  // next expert's h is staged
   float* mine = a.part + ((int64_t)rg * S + rank) * a.T * kOutRows;
   uint32_t seen = 0;                                        // tokens that have sums
 

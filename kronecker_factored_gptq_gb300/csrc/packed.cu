@@ -1,7 +1,8 @@
 // bakron_pack / bakron_unpack: 4-bit codes into the layout of the products
-// (packed.cuh) and back to values.  Both run once per layer; they are bound
-// by HBM (one byte read and half a byte written per code, and the reverse
-// with four bytes written).
+// (packed.cuh) and back to values.  Both run once per layer and were left
+// simple: eight one-byte loads (stores of four bytes) a thread.  A call that
+// ends with its status read back: 8192 x 8192 144 to 158 us to pack (the bytes at 6.68 TB/s:
+// 15), 210 to 216 to unpack (45).
 #include <algorithm>
 
 #include "packed.cuh"

@@ -16,8 +16,8 @@
 // A is the exact integer u - z; the group's sum comes out of the tensor core
 // in fp32 (at most 128 products, so no long chain of its additions) and is
 // scaled and added to the running sum with fp32 FMAs.  fp32 activations are
-// three bf16 terms whose sum is exact (split3); their products go into the
-// same group sum.
+// three bf16 terms whose sum is exact (split3); the products of the two small
+// ones have a group sum of their own (chunk_product).
 #pragma once
 
 #include "packed.cuh"
