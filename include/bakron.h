@@ -349,8 +349,9 @@ bakron_status bakron_quantize_noalloc(const float* W, int64_t m, int64_t n,
 /* ------------------------------------------------ quantised layers in use
  *
  * The calls below run the layers that the solver has quantised: products
- * with the packed codes in both directions, a mixture-of-experts layer over
- * packed experts, and the layer norm in front of them with its gradients.
+ * with the packed codes in both directions, their activations, a mixture-of-experts
+ * layer over packed experts (at once for few tokens, or in its steps for any number and for
+ * gradients), and the layer norm in front of them with its gradients.
  * They differ from the solver's calls in two points:
  *  - activations are fp32, bf16 or fp16 (bakron_dtype; one type per call),
  *    still dense, row-major and contiguous, at any address that is a multiple
@@ -438,6 +439,74 @@ bakron_status bakron_linear_grad_workspace_size(const bakron_packed* w, int64_t 
                                                 size_t* bytes);
 bakron_status bakron_linear_grad(const void* dY, int64_t T, int dtype, const bakron_packed* w,
                                  void* dX, void* ws, size_t ws_bytes, void* stream);
+
+/* Activations a(z): none (z), relu (max(z, 0)), gelu (z Phi(z), Phi the normal
+ * distribution), gelu_tanh (0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))), silu
+ * (z / (1 + exp(-z))). */
+typedef enum {
+  BAKRON_ACT_NONE = 0, BAKRON_ACT_RELU = 1, BAKRON_ACT_GELU = 2, BAKRON_ACT_GELU_TANH = 3, BAKRON_ACT_SILU = 4
+} bakron_activation;
+
+/* bakron_linear with an epilogue: Z = X V^T + bias, Y = residual + a(Z).  bias: m
+ * floats, nullable; residual: T x m of type dtype, nullable; pre: T x m of type dtype,
+ * nullable, receives Z (which the gradient of a needs).  All in fp32 on the product's sum;
+ * Y and Z are each rounded once, Y from Z's fp32 value.  ws as for bakron_linear. */
+bakron_status bakron_linear_act(const void* X, int64_t T, int dtype, const bakron_packed* w,
+                                const float* bias, int act, const void* residual, void* Y, void* pre,
+                                void* ws, size_t ws_bytes, void* stream);
+/* Y = a(Z), Y and Z T x m.  gated: Z is T x 2 m, each row m gates G, then m values U (the
+ * order of bakron_moe's w_in), and Y = a(G) U.  1 <= m <= 2^20. */
+bakron_status bakron_act(const void* Z, int64_t T, int64_t m, int dtype, int act, int gated, void* Y,
+                         void* stream);
+/* Gradients of bakron_act, and of bakron_linear_act towards Z and bias (its residual's is dY):
+ * dZ = dY a'(Z); gated: dG = dY U a'(G), dU = dY a(G).  relu'(0) = 0.  dbias: the sum of dZ's
+ * fp32 values over the rows, m (gated: 2 m) floats, nullable; T = 0 writes zeros to it.  ws: device,
+ * 256-byte aligned, bakron_act_grad_workspace_size bytes for the number of columns of Z, not
+ * read without dbias. */
+bakron_status bakron_act_grad_workspace_size(int64_t T, int64_t columns, size_t* bytes);
+bakron_status bakron_act_grad(const void* dY, const void* Z, int64_t T, int64_t m, int dtype, int act,
+                              int gated, void* dZ, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* The steps of a mixture-of-experts layer for any number of tokens, and their gradients.
+ *
+ * bakron_sort_tokens: choice (T x k) holds the experts that each token has chosen, integers of
+ * choice_bytes 4 or 8.  The choices are ordered by expert, those of an expert as they come
+ * in choice: offsets (E + 1) are the boundaries of the experts' rows in that order,
+ * place (T x k) the row of each choice.  A choice outside 0 .. E - 1 (padding) has
+ * no row: its place is -1.  E <= 1024, k <= 32, T k <= 2^28.
+ * In the calls below a place outside 0 .. R - 1 has no row; no row is the place of two choices. */
+bakron_status bakron_sort_tokens(const void* choice, int choice_bytes, int64_t T, int k, int E,
+                                 int32_t* offsets, int32_t* place, void* stream);
+/* rows[place_tj] = X_t, or weight_tj X_t (weight: T x k floats, nullable).  X is T x d, rows R x
+ * d; rows that are no choice's place are left as they were.  1 <= d <= 2^20, R <= 2^28.  With
+ * weight this is the gradient of bakron_combine towards its rows. */
+bakron_status bakron_dispatch(const void* X, int64_t T, int64_t d, int dtype, const int32_t* place, int k,
+                              const float* weight, void* rows, int64_t R, void* stream);
+/* Y_t = sum over j of weight_tj rows[place_tj] (weight nullable: 1), summed in fp32 in the order of j
+ * and rounded once; 0 where a token has no row.  Without weight this is the gradient of
+ * bakron_dispatch. */
+bakron_status bakron_combine(const void* rows, int64_t R, int64_t d, int dtype, const int32_t* place, int64_t T,
+                             int k, const float* weight, void* Y, void* stream);
+/* Both gradients of bakron_combine: drows[place_tj] = weight_tj dY_t (other rows left as they were),
+ * dweight_tj = the product of rows[place_tj] and dY_t (0 for a choice without a row). */
+bakron_status bakron_combine_grad(const void* dY, const void* rows, int64_t R, int64_t d, int dtype,
+                                  const int32_t* place, int64_t T, int k, const float* weight, void* drows,
+                                  float* dweight, void* stream);
+/* The experts' products over sorted rows: for every matrix e of w (E = w->count <= 1024),
+ *   Y_r = X_r V_e^T   for offsets[e] <= r < offsets[e + 1],
+ * X R x n, Y R x m of type dtype, offsets E + 1 integers on the device, ascending from 0 to at most
+ * R (others are taken as the nearest that are).  Rows of no expert are not read as rows and
+ * left as they were in Y.  The arithmetic is bakron_linear's; one launch, whatever the experts have.
+ * ws: device, 256-byte aligned, bakron_experts_workspace_size bytes (grad 1: for the gradient),
+ * which serve fewer rows too. */
+bakron_status bakron_experts_workspace_size(const bakron_packed* w, int64_t R, int dtype, int grad,
+                                            size_t* bytes);
+bakron_status bakron_experts(const void* X, int64_t R, int dtype, const bakron_packed* w,
+                             const int32_t* offsets, void* Y, void* ws, size_t ws_bytes, void* stream);
+/* Its gradient towards the rows: dX_r = dY_r V_e, in bakron_linear_grad's arithmetic; the scales' power
+ * of two is taken from the largest scale of all experts. */
+bakron_status bakron_experts_grad(const void* dY, int64_t R, int dtype, const bakron_packed* w,
+                                  const int32_t* offsets, void* dX, void* ws, size_t ws_bytes, void* stream);
 
 /* A mixture-of-experts layer for a few tokens.  X is T x d; router (E x d)
  * has X's type; w_in holds E matrices of 2 f x d, rows 0..f-1 the gate and

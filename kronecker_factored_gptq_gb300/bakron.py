@@ -31,11 +31,14 @@ EXPORTS = ["bakron_default_opts", "bakron_status_string", "bakron_version", "bak
            "bakron_pack", "bakron_unpack", "bakron_linear_workspace_size", "bakron_linear",
            "bakron_linear_grad_workspace_size", "bakron_linear_grad", "bakron_moe_workspace_size",
            "bakron_moe", "bakron_layernorm", "bakron_layernorm_grad_workspace_size",
-           "bakron_layernorm_grad"]
+           "bakron_layernorm_grad", "bakron_linear_act", "bakron_act", "bakron_act_grad_workspace_size",
+           "bakron_act_grad", "bakron_sort_tokens", "bakron_dispatch", "bakron_combine", "bakron_combine_grad",
+           "bakron_experts_workspace_size", "bakron_experts", "bakron_experts_grad"]
 FACTORS_KFAC = 0
 FACTORS_SHAMPOO = 1
 F32, BF16, F16 = 0, 1, 2      # bakron_dtype
 MOE_TOKENS = 32               # tokens that bakron_moe takes together
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}      # bakron_activation
 
 
 class PhaseTimes(ctypes.Structure):
@@ -132,6 +135,18 @@ def lib():
     L.bakron_layernorm.argtypes = [vp, i64, i64, ctypes.c_int, vp, vp, f32, vp, vp, vp, vp]
     L.bakron_layernorm_grad_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
     L.bakron_layernorm_grad.argtypes = [vp, vp, i64, i64, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    num = ctypes.c_int
+    L.bakron_linear_act.argtypes = [vp, i64, num, pk, vp, num, vp, vp, vp, vp, sz, vp]
+    L.bakron_act.argtypes = [vp, i64, i64, num, num, num, vp, vp]
+    L.bakron_act_grad_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    L.bakron_act_grad.argtypes = [vp, vp, i64, i64, num, num, num, vp, vp, vp, sz, vp]
+    L.bakron_sort_tokens.argtypes = [vp, num, i64, num, num, vp, vp, vp]
+    L.bakron_dispatch.argtypes = [vp, i64, i64, num, vp, num, vp, vp, i64, vp]
+    L.bakron_combine.argtypes = [vp, i64, i64, num, vp, i64, num, vp, vp, vp]
+    L.bakron_combine_grad.argtypes = [vp, vp, i64, i64, num, vp, i64, num, vp, vp, vp, vp]
+    L.bakron_experts_workspace_size.argtypes = [pk, i64, num, num, ctypes.POINTER(sz)]
+    L.bakron_experts.argtypes = [vp, i64, num, pk, vp, vp, vp, sz, vp]
+    L.bakron_experts_grad.argtypes = [vp, i64, num, pk, vp, vp, vp, sz, vp]
     for f in ("bakron_schedule_export", "bakron_workspace_size", "bakron_prepare_workspace_size", "bakron_rowscale",
               "bakron_prepare", "bakron_quantize", "bakron_quantize_antidiag",
               "bakron_quantize_noalloc", "bakron_factors_workspace_size", "bakron_factors",
@@ -141,7 +156,10 @@ def lib():
               "bakron_unpack", "bakron_linear_workspace_size", "bakron_linear",
               "bakron_linear_grad_workspace_size", "bakron_linear_grad",
               "bakron_moe_workspace_size", "bakron_moe", "bakron_layernorm",
-              "bakron_layernorm_grad_workspace_size", "bakron_layernorm_grad"):
+              "bakron_layernorm_grad_workspace_size", "bakron_layernorm_grad",
+              "bakron_linear_act", "bakron_act", "bakron_act_grad_workspace_size", "bakron_act_grad",
+              "bakron_sort_tokens", "bakron_dispatch", "bakron_combine", "bakron_combine_grad",
+              "bakron_experts_workspace_size", "bakron_experts", "bakron_experts_grad"):
         getattr(L, f).restype = ctypes.c_int
     _LIB = L
     return L
@@ -755,6 +773,257 @@ def bakron_linear_grad(dy, w, out=None, workspace=None, stream=None):
     """dX = dY V, the gradient of bakron_linear for its activations: dy
     (T, m); returns (T, n) of dy's type."""
     return _linear(lib().bakron_linear_grad, "bakron_linear_grad", True, dy, w, out, workspace, stream)
+
+
+def _activation(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(ACTIVATIONS), act))
+    return code
+
+
+def bakron_linear_act(x, w, bias=None, act="none", residual=None, want_pre=False, out=None, pre=None,
+                      workspace=None, stream=None):
+    """Z = X V^T + bias, Y = residual + act(Z): x (T, n), w a PackedWeight of one m x n
+    matrix, bias (m,) float32 or None, act a name of ACTIVATIONS, residual (T, m) of x's
+    type or None.  Returns (Y, Z), both (T, m) of x's type; Z is None without want_pre.
+    The workspace is bakron_linear's (linear_workspace)."""
+    T, _, code, dev = _act(x, "X", w.n)
+    w._check(x, "X")
+    if w.count != 1:
+        raise ValueError("bakron_linear_act takes a single matrix, got %d" % w.count)
+    kind = _activation(act)
+    y = _out(out, x, (T, w.m), "out")
+    rp = None if residual is None else _same(residual, x, (T, w.m), "residual")
+    if want_pre:
+        pre = _out(pre, x, (T, w.m), "pre")
+    elif pre is not None:
+        raise ValueError("pre is given but not wanted (want_pre)")
+    nb = _linear_ws_size(w, T, x.dtype, False)
+    ws = _ws(nb, workspace) if nb else None     # alive until the call is enqueued
+    st = lib().bakron_linear_act(x.data_ptr(), T, code, w.ref, _vec(bias, w.m, x, "bias"), kind, rp, y.data_ptr(),
+                                 None if pre is None else pre.data_ptr(), None if ws is None else ws.data_ptr(), nb,
+                                 _handle(stream, dev))
+    if st != OK:
+        raise BakronError(st, "bakron_linear_act")
+    return y, pre
+
+
+def _gates(z, gated, name="Z"):
+    """Checks Z of an activation; returns (T, columns of Y, bakron_dtype, device)."""
+    T, cols, code, dev = _act(z, name)
+    if cols < 1 or (gated and cols % 2):
+        raise ValueError("%s must have %s, got %d" % (name, "an even number of columns" if gated else "columns", cols))
+    return T, cols // 2 if gated else cols, code, dev
+
+
+def bakron_act(z, act, gated=False, out=None, stream=None):
+    """act(z) for z (T, m); gated: z is (T, 2m), gates first, and the result
+    act(gates) * rest, (T, m)."""
+    T, m, code, dev = _gates(z, gated)
+    kind = _activation(act)
+    y = _out(out, z, (T, m), "out")
+    _check(lib().bakron_act(z.data_ptr(), T, m, code, kind, 1 if gated else 0, y.data_ptr(), _handle(stream, dev)),
+           "bakron_act")
+    return y
+
+
+_ACT_WS = {}
+
+
+def act_grad_workspace_size(T, columns):
+    """Bytes on the current device (they depend on its SM count)."""
+    key = (T, columns, _device())
+    size = _ACT_WS.get(key)
+    if size is None:
+        b = ctypes.c_size_t(0)
+        _check(lib().bakron_act_grad_workspace_size(T, columns, ctypes.byref(b)), "bakron_act_grad_workspace_size")
+        size = b.value
+        if len(_ACT_WS) > 256:
+            _ACT_WS.clear()
+        _ACT_WS[key] = size
+    return size
+
+
+def act_grad_workspace(T, columns):
+    """A workspace for bakron_act_grad with the bias's gradient of up to T rows, Z having
+    that many columns, on the current device; None when none is needed."""
+    nb = act_grad_workspace_size(T, columns)
+    return _torch().empty(nb, dtype=_torch().uint8, device="cuda") if nb else None
+
+
+def bakron_act_grad(dy, z, act, gated=False, want_bias_grad=False, out=None, workspace=None, stream=None):
+    """Gradients of bakron_act (and of bakron_linear_act towards Z and bias): returns
+    (dz, dbias), dz of z's shape, dbias (columns of z,) float32, the sum of dz over the
+    rows (None without want_bias_grad)."""
+    T, m, code, dev = _gates(z, gated)
+    kind = _activation(act)
+    yp = _same(dy, z, (T, m), "dY")
+    cols = z.shape[1]
+    dz = _out(out, z, (T, cols), "out")
+    db = ws = bp = wp = None
+    nb = 0
+    if want_bias_grad:
+        nb = act_grad_workspace_size(T, cols)
+        ws = _ws(nb, workspace) if nb else None
+        wp = None if ws is None else ws.data_ptr()
+        db = _torch().empty(cols, dtype=_torch().float32, device=z.device)
+        bp = db.data_ptr()
+    _check(lib().bakron_act_grad(yp, z.data_ptr(), T, m, code, kind, 1 if gated else 0, dz.data_ptr(), bp, wp, nb,
+                                 _handle(stream, dev)), "bakron_act_grad")
+    return dz, db
+
+
+# ---- mixture of experts in steps: any number of tokens, and gradients
+
+
+def _ints(t, shape, index, name):
+    """Device address of an int32 tensor of that shape on device `index`."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.get_device() != index or \
+            tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s on cuda:%d" % (name, tuple(shape), index))
+    return t.data_ptr()
+
+
+def bakron_sort_tokens(choice, experts, out=None, stream=None):
+    """choice (T, k), int32 or int64: the experts each token has chosen (any other number: no
+    expert).  Returns (offsets, place), int32: the rows of expert e are offsets[e] ..
+    offsets[e + 1] - 1 in the order by expert, and choice (t, j) has row place[t, j], -1 for none."""
+    torch = _torch()
+    if not isinstance(choice, torch.Tensor) or not choice.is_cuda or choice.dim() != 2 or \
+            choice.dtype not in (torch.int32, torch.int64) or not choice.is_contiguous():
+        raise ValueError("choice must be a contiguous int32 or int64 CUDA tensor of shape (tokens, choices)")
+    dev = choice.get_device()
+    if dev != _device():
+        raise _elsewhere(dev, "choice")
+    T, k = choice.shape
+    if not 1 <= k <= 32 or not 1 <= experts <= 1024:
+        raise ValueError("up to 32 choices of a token and 1024 experts, got %d and %d" % (k, experts))
+    if out is None:
+        out = (torch.empty(experts + 1, dtype=torch.int32, device=choice.device),
+               torch.empty((T, k), dtype=torch.int32, device=choice.device))
+    offsets, place = out
+    _check(lib().bakron_sort_tokens(choice.data_ptr(), choice.element_size(), T, k, int(experts),
+                                    _ints(offsets, (experts + 1,), dev, "offsets"), _ints(place, (T, k), dev, "place"),
+                                    _handle(stream, dev)), "bakron_sort_tokens")
+    return offsets, place
+
+
+def _placed(place, index, T=None):
+    """Checks places (of T tokens); returns (address, tokens, choices per token)."""
+    if not isinstance(place, _torch().Tensor) or place.dim() != 2 or (T is not None and place.shape[0] != T):
+        raise ValueError("place must be an int32 tensor of shape (%s, choices)" % ("tokens" if T is None else T))
+    return (_ints(place, place.shape, index, "place"),) + tuple(place.shape)
+
+
+def _weights(weight, place, index, name="weight", optional=False):
+    """Address of a float32 tensor of the places' shape; None for None if that is allowed."""
+    if weight is None and optional:
+        return None
+    torch = _torch()
+    if not isinstance(weight, torch.Tensor) or weight.dtype != torch.float32 or not weight.is_cuda or \
+            weight.get_device() != index or weight.shape != place.shape or not weight.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of shape %s on cuda:%d" % (name, tuple(place.shape), index))
+    return weight.data_ptr()
+
+
+def bakron_dispatch(x, place, weight=None, out=None, stream=None):
+    """rows[place[t, j]] = x[t], or weight[t, j] * x[t]: x (T, d), place (T, k) from
+    bakron_sort_tokens, weight (T, k) float32 or None.  Returns rows, (T k, d) or ``out`` of any
+    number of rows; rows that no choice has are left as they were (``out`` None: not
+    initialised)."""
+    T, d, code, dev = _act(x, "X")
+    pp, _, k = _placed(place, dev, T)
+    wp = _weights(weight, place, dev, optional=True)
+    R = out.shape[0] if isinstance(out, _torch().Tensor) and out.dim() == 2 else T * k
+    rows = _out(out, x, (R, d), "out")
+    _check(lib().bakron_dispatch(x.data_ptr(), T, d, code, pp, k, wp, rows.data_ptr(), R, _handle(stream, dev)),
+           "bakron_dispatch")
+    return rows
+
+
+def bakron_combine(rows, place, weight=None, out=None, stream=None):
+    """y[t] = the sum over j of weight[t, j] * rows[place[t, j]] (weight None: 1), (T, d).
+    Without weight the gradient of bakron_dispatch."""
+    R, d, code, dev = _act(rows, "rows")
+    pp, T, k = _placed(place, dev)
+    wp = _weights(weight, place, dev, optional=True)
+    y = _out(out, rows, (T, d), "out")
+    _check(lib().bakron_combine(rows.data_ptr(), R, d, code, pp, T, k, wp, y.data_ptr(), _handle(stream, dev)),
+           "bakron_combine")
+    return y
+
+
+def bakron_combine_grad(dy, rows, place, weight, out=None, stream=None):
+    """Gradients of bakron_combine: returns (drows, dweight), of the shapes of rows and weight
+    (float32).  Rows of drows that no choice has are left as they were (``out`` None: not
+    initialised)."""
+    T, d, code, dev = _act(dy, "dY")
+    R = rows.shape[0] if isinstance(rows, _torch().Tensor) and rows.dim() == 2 else 0
+    rp = _same(rows, dy, (R, d), "rows")
+    pp, _, k = _placed(place, dev, T)
+    wp = _weights(weight, place, dev)
+    if out is None:
+        out = (None, _torch().empty_like(weight))
+    drows, dweight = _out(out[0], dy, (R, d), "drows"), out[1]
+    _check(lib().bakron_combine_grad(dy.data_ptr(), rp, R, d, code, pp, T, k, wp, drows.data_ptr(),
+                                     _weights(dweight, place, dev, "dweight"), _handle(stream, dev)),
+           "bakron_combine_grad")
+    return drows, dweight
+
+
+def experts_workspace_size(w, R, dtype, grad=False):
+    w._here()           # the size depends on the device's SM count
+    return _experts_ws_size(w, R, dtype, grad)
+
+
+def _experts_ws_size(w, R, dtype, grad):
+    key = ("experts", R, dtype, grad)
+    size = w._ws.get(key)
+    if size is None:
+        b = ctypes.c_size_t(0)
+        _check(lib().bakron_experts_workspace_size(w.ref, R, _dtypes()[dtype], 1 if grad else 0, ctypes.byref(b)),
+               "bakron_experts_workspace_size")
+        size = b.value
+        if len(w._ws) > 64:
+            w._ws.clear()
+        w._ws[key] = size
+    return size
+
+
+def experts_workspace(w, R, dtype, grad=False):
+    """A workspace for bakron_experts (or its gradient) of up to R rows."""
+    nb = experts_workspace_size(w, R, dtype, grad)
+    return _torch().empty(nb, dtype=_torch().uint8, device=w.device)
+
+
+def _experts(fn, where, grad, x, w, offsets, out, workspace, stream):
+    name = "dY" if grad else "X"
+    R, _, code, dev = _act(x, name, w.m if grad else w.n)
+    w._check(x, name)
+    op = _ints(offsets, (w.count + 1,), dev, "offsets")
+    y = _out(out, x, (R, w.n if grad else w.m), "out")
+    nb = _experts_ws_size(w, R, x.dtype, grad)
+    ws = _ws(nb, workspace)
+    st = fn(x.data_ptr(), R, code, w.ref, op, y.data_ptr(), ws.data_ptr(), nb, _handle(stream, dev))
+    if st != OK:
+        raise BakronError(st, where)
+    return y
+
+
+def bakron_experts(x, w, offsets, out=None, workspace=None, stream=None):
+    """Y[r] = X[r] V_e^T for the rows offsets[e] <= r < offsets[e + 1] of every expert: x (R, n)
+    sorted by expert (bakron_dispatch), w a PackedWeight of E m x n matrices, offsets (E + 1,)
+    int32 from bakron_sort_tokens.  Returns (R, m) of x's type; rows of no expert are left as they
+    were (``out`` None: not initialised)."""
+    return _experts(lib().bakron_experts, "bakron_experts", False, x, w, offsets, out, workspace, stream)
+
+
+def bakron_experts_grad(dy, w, offsets, out=None, workspace=None, stream=None):
+    """dX[r] = dY[r] V_e, the gradient of bakron_experts for its rows: dy (R, m); returns (R, n)
+    of dy's type."""
+    return _experts(lib().bakron_experts_grad, "bakron_experts_grad", True, dy, w, offsets, out, workspace, stream)
 
 
 def moe_workspace_size(w_in, w_out, T, top_k, dtype):

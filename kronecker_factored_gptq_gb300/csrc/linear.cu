@@ -2,7 +2,7 @@
 // of kernel.
 #include <algorithm>
 
-#include "linear.cuh"
+#include "linear_tc.cuh"
 
 namespace bakron {
 namespace {
@@ -43,15 +43,17 @@ __global__ void __launch_bounds__(256) planes_kernel(const TX* __restrict__ x, i
 
 // Arguments both directions share; T = 0 is a valid call that does nothing.
 bool linear_args(const void* x, int64_t T, int dtype, const bakron_packed* w, const void* y,
-                 LinearArgs* a) {
+                 LinearArgs* a, bool experts = false) {
   if (!dtype_ok(dtype) || T < 0 || T > (int64_t(1) << 28) || !packed_view(w, &a->w)) return false;
-  if (a->w.count != 1) return false;
+  if (!experts && a->w.count != 1) return false;
   if (T > 0 && (!x || !y || !aligned_to(x, dtype_size(dtype)) || !aligned_to(y, dtype_size(dtype))))
     return false;
   a->x = x;
   a->y = const_cast<void*>(y);
   a->T = T;
   a->dtype = dtype;
+  a->epi = {};
+  a->offsets = nullptr;
   return true;
 }
 
@@ -82,8 +84,8 @@ Kernel forward_kernel(const LinearArgs& a) {
   return mid < many ? kMid : kMany;
 }
 
-size_t workspace_bytes(const LinearArgs& a, bool grad) {
-  if (!grad && a.T <= kFewTokens && forward_kernel(a) == kFew) return 0;
+size_t workspace_bytes(const LinearArgs& a, bool grad, bool experts = false) {
+  if (!grad && !experts && a.T <= kFewTokens && forward_kernel(a) == kFew) return 0;
   if (grad && a.dtype != BAKRON_F32 && a.w.m > grad_chain(a.dtype) && a.T > 0)
     return grad_planes_bytes(a) +
            (size_t)sm_count() * (size_t)std::min<int64_t>(kGradTokens, (a.T + 31) / 32 * 32) * 128 * sizeof(float);
@@ -91,19 +93,42 @@ size_t workspace_bytes(const LinearArgs& a, bool grad) {
   return (size_t)(a.dtype == BAKRON_F32 ? 3 : 1) * (size_t)a.T * (size_t)((K + 127) / 128 * 128) * 2;
 }
 
-bakron_status run_linear(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, void* stream) {
+enum class Call { kLinear, kAct, kGrad };
+
+bakron_status run_linear(LinearArgs& a, Call call, void* ws, size_t ws_bytes, void* stream) {
   if (a.T == 0) return BAKRON_OK;
+  const bool grad = call == Call::kGrad, act = call == Call::kAct;
   const size_t need = workspace_bytes(a, grad);
   if (need > 0 && (!ws || !aligned_to(ws, 256) || ws_bytes < need)) return BAKRON_ERR_INVALID_ARG;
   a.ws = ws;
   cudaStream_t s = (cudaStream_t)stream;
   if (!grad) {
     const Kernel k = forward_kernel(a);
-    if (k == kFew) return launch_status(launch_linear_few(a, s));
-    if (k == kMid) return launch_status(launch_linear_mid(a, s));
+    if (k == kFew) return launch_status(act ? launch_linear_act_few(a, s) : launch_linear_few(a, s));
+    if (k == kMid) return launch_status(act ? launch_linear_act_mid(a, s) : launch_linear_mid(a, s));
   }
   if (!prop_tc_supported()) return BAKRON_ERR_UNSUPPORTED;
-  return launch_status(grad ? launch_linear_grad(a, s) : launch_linear_fwd(a, s));
+  return launch_status(grad ? launch_linear_grad(a, s) : act ? launch_linear_act_fwd(a, s) : launch_linear_fwd(a, s));
+}
+
+// Experts' products: the rows of x that belong to them are known on the device alone, so
+// the tcgen05 kernels take every number of rows.
+bool experts_args(const void* x, int64_t R, int dtype, const bakron_packed* w, const int32_t* offsets,
+                  const void* y, LinearArgs* a) {
+  if (!linear_args(x, R, dtype, w, y, a, true) || a->w.count > kMaxGroupedExperts) return false;
+  if (R > 0 && (!offsets || !aligned_to(offsets, 4))) return false;
+  a->offsets = offsets;
+  return true;
+}
+
+bakron_status run_experts(LinearArgs& a, bool grad, void* ws, size_t ws_bytes, void* stream) {
+  if (a.T == 0) return BAKRON_OK;
+  const size_t need = workspace_bytes(a, grad, true);
+  if (!ws || !aligned_to(ws, 256) || ws_bytes < need) return BAKRON_ERR_INVALID_ARG;
+  a.ws = ws;
+  if (!prop_tc_supported()) return BAKRON_ERR_UNSUPPORTED;
+  cudaStream_t s = (cudaStream_t)stream;
+  return launch_status(grad ? launch_experts_grad(a, s) : launch_experts_fwd(a, s));
 }
 
 }  // namespace
@@ -137,7 +162,7 @@ extern "C" bakron_status bakron_linear(const void* X, int64_t T, int dtype, cons
                                        void* Y, void* ws, size_t ws_bytes, void* stream) {
   LinearArgs a;
   if (!linear_args(X, T, dtype, w, Y, &a)) return BAKRON_ERR_INVALID_ARG;
-  return run_linear(a, false, ws, ws_bytes, stream);
+  return run_linear(a, Call::kLinear, ws, ws_bytes, stream);
 }
 
 extern "C" bakron_status bakron_linear_grad_workspace_size(const bakron_packed* w, int64_t T,
@@ -153,5 +178,41 @@ extern "C" bakron_status bakron_linear_grad(const void* dY, int64_t T, int dtype
                                             size_t ws_bytes, void* stream) {
   LinearArgs a;
   if (!linear_args(dY, T, dtype, w, dX, &a)) return BAKRON_ERR_INVALID_ARG;
-  return run_linear(a, true, ws, ws_bytes, stream);
+  return run_linear(a, Call::kGrad, ws, ws_bytes, stream);
+}
+
+extern "C" bakron_status bakron_linear_act(const void* X, int64_t T, int dtype, const bakron_packed* w,
+                                           const float* bias, int act, const void* residual, void* Y,
+                                           void* pre, void* ws, size_t ws_bytes, void* stream) {
+  LinearArgs a;
+  if (!linear_args(X, T, dtype, w, Y, &a) || !act_ok(act)) return BAKRON_ERR_INVALID_ARG;
+  const size_t es = dtype_size(dtype);
+  if (!aligned_to(bias, 4) || !aligned_to(residual, es) || !aligned_to(pre, es)) return BAKRON_ERR_INVALID_ARG;
+  a.epi = {bias, residual, pre, act};
+  return run_linear(a, Call::kAct, ws, ws_bytes, stream);
+}
+
+extern "C" bakron_status bakron_experts_workspace_size(const bakron_packed* w, int64_t R, int dtype, int grad,
+                                                       size_t* bytes) {
+  LinearArgs a;
+  if (!bytes || (grad != 0 && grad != 1) || !experts_args(w, R, dtype, w, reinterpret_cast<const int32_t*>(w), w, &a))
+    return BAKRON_ERR_INVALID_ARG;
+  *bytes = workspace_bytes(a, grad != 0, true);
+  return BAKRON_OK;
+}
+
+extern "C" bakron_status bakron_experts(const void* X, int64_t R, int dtype, const bakron_packed* w,
+                                        const int32_t* offsets, void* Y, void* ws, size_t ws_bytes,
+                                        void* stream) {
+  LinearArgs a;
+  if (!experts_args(X, R, dtype, w, offsets, Y, &a)) return BAKRON_ERR_INVALID_ARG;
+  return run_experts(a, false, ws, ws_bytes, stream);
+}
+
+extern "C" bakron_status bakron_experts_grad(const void* dY, int64_t R, int dtype, const bakron_packed* w,
+                                             const int32_t* offsets, void* dX, void* ws, size_t ws_bytes,
+                                             void* stream) {
+  LinearArgs a;
+  if (!experts_args(dY, R, dtype, w, offsets, dX, &a)) return BAKRON_ERR_INVALID_ARG;
+  return run_experts(a, true, ws, ws_bytes, stream);
 }

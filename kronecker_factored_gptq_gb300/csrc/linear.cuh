@@ -2,6 +2,7 @@
 // kernels.
 #pragma once
 
+#include "act.cuh"
 #include "packed.cuh"
 
 namespace bakron {
@@ -13,7 +14,11 @@ struct LinearArgs {
   int dtype;
   PackedView w;
   void* ws;
+  Epilogue epi;         // bakron_linear_act
+  const int* offsets;   // experts: boundaries of their rows of x, w.count + 1
 };
+
+constexpr int kMaxGroupedExperts = 1024;      // of bakron_experts
 
 // Tokens up to which bakron_linear may run linear_few_kernel and
 // linear_mid_kernel.
@@ -31,6 +36,8 @@ inline size_t grad_planes_bytes(const LinearArgs& a) {
 
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_mid(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_act_few(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_act_mid(const LinearArgs& a, cudaStream_t s);
 
 // x (T x K of dtype, any alignment) -> planes [terms][T][kp] of 16-bit terms (1,
 // or 3 for fp32), zeros past K; out is 16-byte aligned, kp a multiple of 8.  `grad`: the
@@ -42,5 +49,8 @@ cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);
 int64_t linear_fwd_steps(const LinearArgs& a);    // 128-column chunks that its busiest block takes (16-bit x)
 cudaError_t launch_linear_grad(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_act_fwd(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_experts_fwd(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_experts_grad(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace bakron

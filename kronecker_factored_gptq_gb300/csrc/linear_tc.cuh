@@ -2,6 +2,9 @@
 // instructions, TMEM access, waits and the position in a ring of stages.
 #pragma once
 
+#include <algorithm>
+
+#include "act.cuh"
 #include "linear.cuh"
 #include "tc_common.cuh"
 
@@ -74,6 +77,119 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p != 0;
+}
+
+
+// What a tcgen05 product computes: Y = X V^T, the same with bakron_linear_act's
+// epilogue, or the experts' products over rows sorted by expert (and likewise their
+// gradients).
+enum Product { kPlain, kWithAct, kExperts };
+
+// A tile of the output: 128 rows m of expert e's matrix, tokens t0 to end.
+struct Place {
+  int m, e;
+  int64_t t0, end;
+};
+
+constexpr int kTileThreads = 512;            // that fill an experts' table
+constexpr int kTileBounds = 4;               // boundaries each
+constexpr uint32_t kTableBytes = 2 * (kMaxGroupedExperts + 1) * 4;
+static_assert(kTileThreads * kTileBounds > kMaxGroupedExperts);
+
+// The tiles of a product.  Experts: `bounds` are the boundaries of their rows, `first`
+// their first token tiles (e = 0 .. E, in shared memory).
+template <Product P>
+struct Tiles {
+  int64_t tiles;        // of the output
+  int tiles_m, N;
+  int64_t T;
+  const int* bounds;
+  const int* first;
+  int E;
+
+  __device__ __forceinline__ Place at(int64_t tile) const {
+    if constexpr (P != kExperts) {
+      return Place{(int)(tile % tiles_m), 0, tile / tiles_m * N, T};
+    } else {
+      const int tt = (int)(tile / tiles_m);
+      int e = 0, hi = E;                     // the last expert whose first tile is at most tt
+      while (hi - e > 1) {
+        const int mid = (e + hi) >> 1;
+        if (first[mid] <= tt) e = mid;
+        else hi = mid;
+      }
+      return Place{(int)(tile % tiles_m), e, bounds[e] + (int64_t)(tt - first[e]) * N, bounds[e + 1]};
+    }
+  }
+};
+
+// Token tiles of N: at most, as each expert's rows may end within one, and
+// likely, where tokens are spread about evenly.
+inline int64_t token_tiles(const LinearArgs& a, int N) {
+  return (a.T + N - 1) / N + (a.offsets ? std::min<int64_t>(a.w.count, a.T) : 0);
+}
+inline int64_t likely_tiles(const LinearArgs& a, int N) {
+  if (!a.offsets) return (a.T + N - 1) / N;
+  const int64_t live = std::min<int64_t>(a.w.count, a.T);
+  return std::max<int64_t>(live, a.T / N + (live + 1) / 2);
+}
+
+// Fills an experts' table from their offsets (device, E + 1), a block of at least
+// kTileThreads threads together; returns the number of token tiles.  An offset below an earlier
+// one or outside 0 .. T counts as the nearest that is not: whatever the offsets, every
+// tile lies inside the rows and no two share one.
+__device__ inline int expert_tiles(const int* offsets, int E, int T, int N, int* bounds, int* first,
+                                   int (*sums)[kTileThreads / 32]) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool in = tid < kTileThreads;
+  int v[kTileBounds], most = 0;
+#pragma unroll
+  for (int i = 0; i < kTileBounds; ++i) {
+    const int b = kTileBounds * tid + i;
+    v[i] = in && b <= E ? min(max(__ldg(offsets + b), 0), T) : 0;
+    most = v[i] = max(v[i], most);
+  }
+  int up = most;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up = max(up, u);
+  }
+  if (in && lane == 31) sums[0][warp] = up;
+  int before = __shfl_up_sync(0xffffffffu, up, 1);
+  if (lane == 0) before = 0;
+  __syncthreads();
+  if (in) {
+    for (int w = 0; w < warp; ++w) before = max(before, sums[0][w]);
+#pragma unroll
+    for (int i = 0; i < kTileBounds; ++i)
+      if (kTileBounds * tid + i <= E) bounds[kTileBounds * tid + i] = max(before, v[i]);
+  }
+  __syncthreads();
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kTileBounds; ++i) {
+    const int e = kTileBounds * tid + i;
+    v[i] = sum;
+    if (in && e < E) sum += (bounds[e + 1] - bounds[e] + N - 1) / N;
+  }
+  up = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += u;
+  }
+  if (in && lane == 31) sums[1][warp] = up;
+  before = up - sum;
+  __syncthreads();
+  if (in) {
+    for (int w = 0; w < warp; ++w) before += sums[1][w];
+#pragma unroll
+    for (int i = 0; i < kTileBounds; ++i)
+      if (kTileBounds * tid + i <= E) first[kTileBounds * tid + i] = before + v[i];
+  }
+  __syncthreads();
+  return first[E];
 }
 
 }  // namespace tc
