@@ -60,37 +60,39 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const __grid_constant__ A
           if constexpr (kGrad) d[i] = *reinterpret_cast<const W*>(dy + row * a.m);
         }
       }
+      by_act(a.act, [&](auto A) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int64_t row = r + (int64_t)i * ry;
-        if (row < r1) {
-          W o, p;
+        for (int i = 0; i < kRows; ++i) {
+          const int64_t row = r + (int64_t)i * ry;
+          if (row < r1) {
+            W o, p;
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float x = to_float(g[i].v[e]);
-            if constexpr (!kGrad) {
-              float y = activate<TX>(x, a.act);
-              if constexpr (kGated) y *= to_float(u[i].v[e]);
-              o.v[e] = from_float<TX>(y);
-            } else {
-              float f, slope;
-              activate_slope<TX>(x, a.act, f, slope);
-              float q = to_float(d[i].v[e]);
-              if constexpr (kGated) {
-                const float t = q * f;
-                p.v[e] = from_float<TX>(t);
-                if constexpr (kSums) sum[V + e] += t;
-                q *= to_float(u[i].v[e]);
+            for (int e = 0; e < V; ++e) {
+              const float x = to_float(g[i].v[e]);
+              if constexpr (!kGrad) {
+                float y = activate<TX, A>(x);
+                if constexpr (kGated) y *= to_float(u[i].v[e]);
+                o.v[e] = from_float<TX>(y);
+              } else {
+                float f, slope;
+                activate_slope<TX, A>(x, f, slope);
+                float q = to_float(d[i].v[e]);
+                if constexpr (kGated) {
+                  const float t = q * f;
+                  p.v[e] = from_float<TX>(t);
+                  if constexpr (kSums) sum[V + e] += t;
+                  q *= to_float(u[i].v[e]);
+                }
+                q *= slope;
+                o.v[e] = from_float<TX>(q);
+                if constexpr (kSums) sum[e] += q;
               }
-              q *= slope;
-              o.v[e] = from_float<TX>(q);
-              if constexpr (kSums) sum[e] += q;
             }
+            *reinterpret_cast<W*>(out + row * oc) = o;
+            if constexpr (kGated && kGrad) *reinterpret_cast<W*>(out + row * oc + a.m) = p;
           }
-          *reinterpret_cast<W*>(out + row * oc) = o;
-          if constexpr (kGated && kGrad) *reinterpret_cast<W*>(out + row * oc + a.m) = p;
         }
-      }
+      });
     }
   }
   if constexpr (kSums) {

@@ -5,6 +5,8 @@
 // cancel for negative z.
 #pragma once
 
+#include <type_traits>
+
 #include "packed.cuh"
 
 namespace bakron {
@@ -38,38 +40,60 @@ __device__ __forceinline__ float exp_for(float x) {
 
 inline bool act_ok(int act) { return act >= BAKRON_ACT_NONE && act <= BAKRON_ACT_SILU; }
 
+// Calls f with the activation as a constant: the choice is made once for many values.
+template <typename F>
+__device__ __forceinline__ void by_act(int act, F f) {
+  switch (act) {
+    case BAKRON_ACT_NONE: return f(std::integral_constant<int, BAKRON_ACT_NONE>());
+    case BAKRON_ACT_RELU: return f(std::integral_constant<int, BAKRON_ACT_RELU>());
+    case BAKRON_ACT_GELU: return f(std::integral_constant<int, BAKRON_ACT_GELU>());
+    case BAKRON_ACT_GELU_TANH: return f(std::integral_constant<int, BAKRON_ACT_GELU_TANH>());
+    default: return f(std::integral_constant<int, BAKRON_ACT_SILU>());
+  }
+}
+
 // a(z), for a result of type T.
-template <typename T>
-__device__ __forceinline__ float activate(float z, int act) {
-  if (act == BAKRON_ACT_NONE) return z;
-  if (act == BAKRON_ACT_RELU) return z < 0.f ? 0.f : z;       // NaN stays
-  if (act == BAKRON_ACT_GELU) return 0.5f * z * erfcf(-kSqrtHalf * z);
-  float p, rest;
-  sigmoid<T>(act == BAKRON_ACT_GELU_TANH ? z * fmaf(kTanh3, z * z, kTanh1) : z, p, rest);
-  return z * p;
+template <typename T, int A>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (A == BAKRON_ACT_NONE) {
+    return z;
+  } else if constexpr (A == BAKRON_ACT_RELU) {
+    return z < 0.f ? 0.f : z;                                 // NaN stays
+  } else if constexpr (A == BAKRON_ACT_GELU) {
+    return 0.5f * z * erfcf(-kSqrtHalf * z);
+  } else {
+    float p, rest;
+    sigmoid<T>(A == BAKRON_ACT_GELU_TANH ? z * fmaf(kTanh3, z * z, kTanh1) : z, p, rest);
+    return z * p;
+  }
 }
 
 // a(z) and a'(z).  The values of finite z are finite: z^2 is kept below what would meet a
 // factor of zero as infinity.
-template <typename T>
-__device__ __forceinline__ void activate_slope(float z, int act, float& a, float& slope) {
-  if (act == BAKRON_ACT_NONE) {
+template <typename T, int A>
+__device__ __forceinline__ void activate_slope(float z, float& a, float& slope) {
+  if constexpr (A == BAKRON_ACT_NONE) {
     a = z;
     slope = 1.f;
-  } else if (act == BAKRON_ACT_RELU) {
+  } else if constexpr (A == BAKRON_ACT_RELU) {
     a = z < 0.f ? 0.f : z;
     slope = z > 0.f ? 1.f : z <= 0.f ? 0.f : z;               // NaN stays
-  } else if (act == BAKRON_ACT_GELU) {
+  } else if constexpr (A == BAKRON_ACT_GELU) {
     const float p = 0.5f * erfcf(-kSqrtHalf * z);
     a = z * p;
     slope = fmaf(z * exp_for<T>(-0.5f * z * z), kInvSqrt2Pi, p);
   } else {
-    const bool tanh = act == BAKRON_ACT_GELU_TANH;
-    const float zz = fminf(z * z, 1e30f);
     float s, rest;
-    sigmoid<T>(tanh ? z * fmaf(kTanh3, zz, kTanh1) : z, s, rest);
-    a = z * s;
-    slope = fmaf(a * rest, tanh ? fmaf(3.f * kTanh3, zz, kTanh1) : 1.f, s);
+    if constexpr (A == BAKRON_ACT_GELU_TANH) {
+      const float zz = fminf(z * z, 1e30f);
+      sigmoid<T>(z * fmaf(kTanh3, zz, kTanh1), s, rest);
+      a = z * s;
+      slope = fmaf(a * rest, fmaf(3.f * kTanh3, zz, kTanh1), s);
+    } else {
+      sigmoid<T>(z, s, rest);
+      a = z * s;
+      slope = fmaf(a, rest, s);
+    }
   }
 }
 
@@ -88,7 +112,7 @@ __device__ __forceinline__ void put(T* y, const Epilogue& e, int64_t at, int64_t
   if constexpr (kAct) {
     if (e.bias) v += __ldg(e.bias + col);
     if (e.pre) static_cast<T*>(e.pre)[at] = from_float<T>(v);
-    v = activate<T>(v, e.act);
+    by_act(e.act, [&](auto A) { v = activate<T, A>(v); });
     if (e.residual) v += to_float(static_cast<const T*>(e.residual)[at]);
   }
   *y = from_float<T>(v);

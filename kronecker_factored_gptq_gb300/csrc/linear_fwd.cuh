@@ -117,6 +117,83 @@ __device__ __forceinline__ void fma2(float& x, float& y, float s, uint32_t a, ui
       : "f"(s), "r"(a), "r"(b));
 }
 
+// 16 registers of each lane to 16 TMEM columns of its row.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16};" ::"r"(taddr),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+      : "memory");
+}
+
+// 8 TMEM columns of each lane's row.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+constexpr int kFinish = 8;
+// bakron_linear_act's epilogue for a warp's sums, 32 rows (a lane each) x n tokens, that lie in
+// TMEM: kFinish tokens at a time in a loop whose code stays small.  (Unrolled over all 96 tokens that a
+// thread's registers hold, the code did not fit the instruction cache: 2048 tokens of 8192 x 8192
+// 344 us with an activation alone, 500 with residuals, loaded one by one.)  The residuals of the next ones
+// are on their way while these are finished.
+template <typename TO>
+__device__ __forceinline__ void finish(const FwdArgs& a, uint32_t ta, int n, int64_t y0, int64_t row) {
+  const bool live = row < a.w.m;
+  const float bias = a.epi.bias && live ? __ldg(a.epi.bias + row) : 0.f;
+  const TO* res = static_cast<const TO*>(a.epi.residual) + y0;
+  TO* pre = static_cast<TO*>(a.epi.pre) + y0;
+  TO* y = static_cast<TO*>(a.y) + y0;
+  const bool with_res = a.epi.residual != nullptr, with_pre = a.epi.pre != nullptr;
+  const int mine = live ? n : 0;
+  by_act(a.epi.act, [&](auto A) {
+    TO r[kFinish], next[kFinish] = {};
+    auto fetch = [&](int g) {
+      if (!with_res) return;
+#pragma unroll
+      for (int t = 0; t < kFinish; ++t) {
+        if (g + t < mine) next[t] = __ldg(res);
+        res += a.w.m;
+      }
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int g = 0; g < n; g += kFinish) {
+      uint32_t v[kFinish];
+      tmem_ld8(ta + (uint32_t)g, v);
+#pragma unroll
+      for (int t = 0; t < kFinish; ++t) r[t] = next[t];
+      fetch(g + kFinish);
+      tmem_ld_wait();
+      // values first, then the stores: a condition around each would line them up
+      TO z[kFinish], o[kFinish];
+#pragma unroll
+      for (int t = 0; t < kFinish; ++t) {
+        const float f = __uint_as_float(v[t]) + bias;
+        z[t] = from_float<TO>(f);
+        float q = activate<TO, A>(f);
+        if (with_res) q += to_float(r[t]);
+        o[t] = from_float<TO>(q);
+      }
+      if (with_pre) {
+#pragma unroll
+        for (int t = 0; t < kFinish; ++t) {
+          if (g + t < mine) *pre = z[t];
+          pre += a.w.m;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kFinish; ++t) {
+        if (g + t < mine) *y = o[t];
+        y += a.w.m;
+      }
+    }
+  });
+}
+
 struct Bars {
   unsigned long long full_b[kMaxStages], empty_b[kMaxStages], full_a[kWStages], empty_a[kWStages];
   unsigned long long acc_full[2], acc_empty[2], done;
@@ -471,6 +548,16 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
         if (!live || u >= units) return 0.f;
         return ld_ahead(scale_row + grid_group(a.w, (uint32_t)(k.c0 * 128 + u * (KU * 16))) * 16);
       };
+      if (P == kWithAct && S == 1 && a.epi.residual) {
+        // the residuals of the tile on their way into L2: a lane per token, 32 rows' bytes
+        const int64_t first = row - lane, last = min(first + 31, a.w.m - 1);
+        for (int t = lane; first < a.w.m && t < ncols && t0 + t < at.end; t += 32) {
+          const TO* p = static_cast<const TO*>(a.epi.residual) + (t0 + t) * a.w.m;
+          for (int64_t c = first; c <= last; c += 32 / sizeof(TO))
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p + last));
+        }
+      }
       float s_next = scale_of(0);
       for (int u = 0; u < units; ++u, ++u_all) {
         const float s = s_next;
@@ -501,6 +588,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
             for (int t = 0; t < LD; t += 2) fma2(acc[g * LD + t], acc[g * LD + t + 1], s, v[t], v[t + 1]);
           }
         }
+        if (P == kWithAct && S == 1 && u == units - 1) break;      // read, but still needed
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(ae + 8u * (u_all & 1));
@@ -512,14 +600,25 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
 #pragma unroll
         for (int t = 0; t < NC; ++t)
           if (t < ncols) part[(col0 + t) * 128 + quarter * 32 + lane] = acc[t];
+      } else if (P == kWithAct) {
+        if (!ok) break;
+        // the sums pass through the accumulator that was read last
+        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (u_all & 1) * acc_cols + (uint32_t)col0;
+#pragma unroll
+        for (int g = 0; g < NC; g += 16)
+          if (g < ncols) tmem_st16(ta + g, acc + g);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        finish<TO>(a, ta, (int)min((int64_t)ncols, at.end - t0), t0 * a.w.m + row, row);
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ae + 8u * (u_all & 1));
+        ++u_all;
       } else if (ok && row < a.w.m) {
         // lane = output column: the 32 lanes write 32 consecutive elements
-        const int64_t y0 = t0 * a.w.m + row;
-        TO* y = static_cast<TO*>(a.y) + y0;
+        TO* y = static_cast<TO*>(a.y) + t0 * a.w.m + row;
 #pragma unroll
         for (int t = 0; t < NC; ++t)
-          if (t < ncols && t0 + t < at.end)
-            put<TO, P == kWithAct>(y + (int64_t)t * a.w.m, a.epi, y0 + (int64_t)t * a.w.m, row, acc[t]);
+          if (t < ncols && t0 + t < at.end) y[(int64_t)t * a.w.m] = from_float<TO>(acc[t]);
       }
     }
     if constexpr (kSplit) role_end<THREADS, 96>(true, warp);

@@ -230,29 +230,32 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
 template <typename TX, int VB>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ RowArgs a) {
   using P = Piece<TX, VB>;
-  constexpr int kAtOnce = 4, kWide = kVecs / 2;
+  constexpr int kAtOnce = 2;
   const int lane = threadIdx.x & 31;
-  const int64_t units = a.T * a.parts;
-  for (int64_t u = blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5); u < units;
-       u += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int64_t t = u / a.parts, v0 = (u - t * a.parts) * (32 * kWide) + lane;
-    int at;
-    float w;
-    load_choices(a, t, lane, at, w);
-    float sum[kWide][P::V];
+  const int64_t units = a.T * a.parts, step = (int64_t)gridDim.x * (kThreads / 32);
+  int64_t u = blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5);
+  int at_next = -1;
+  float w_next = 1.f;
+  if (u < units) load_choices(a, u / a.parts, lane, at_next, w_next);
+  for (; u < units; u += step) {
+    const int64_t t = u / a.parts, v0 = (u - t * a.parts) * (32 * kVecs) + lane;
+    const int at = at_next;
+    const float w = w_next;
+    if (u + step < units) load_choices(a, (u + step) / a.parts, lane, at_next, w_next);
+    float sum[kVecs][P::V];
 #pragma unroll
-    for (int i = 0; i < kWide; ++i)
+    for (int i = 0; i < kVecs; ++i)
 #pragma unroll
       for (int e = 0; e < P::V; ++e) sum[i][e] = 0.f;
     for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
-      P x[kAtOnce][kWide];
+      P x[kAtOnce][kVecs];
       int64_t r[kAtOnce];
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
         r[q] = __shfl_sync(0xffffffffu, at, (j0 + q) & 31);
         if (j0 + q >= a.k) r[q] = -1;
 #pragma unroll
-        for (int i = 0; i < kWide; ++i)
+        for (int i = 0; i < kVecs; ++i)
           if (r[q] >= 0 && v0 + 32 * i < a.vecs) x[q][i] = load<TX, VB>(a.in, r[q] * a.vecs + v0 + 32 * i);
       }
 #pragma unroll
@@ -260,14 +263,14 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
         const float f = __shfl_sync(0xffffffffu, w, (j0 + q) & 31);
         if (r[q] < 0) continue;
 #pragma unroll
-        for (int i = 0; i < kWide; ++i)
+        for (int i = 0; i < kVecs; ++i)
 #pragma unroll
           for (int e = 0; e < P::V; ++e)
             if (v0 + 32 * i < a.vecs) sum[i][e] = fmaf(f, to_float(x[q][i].v[e]), sum[i][e]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kWide; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
       if (v0 + 32 * i >= a.vecs) continue;
       P o;
 #pragma unroll
@@ -363,8 +366,7 @@ enum class Op { kDispatch, kCombine, kCombineGrad };
 template <typename TX, int VB>
 cudaError_t launch_rows(RowArgs& a, Op op, cudaStream_t s) {
   a.vecs = a.d * (int64_t)sizeof(TX) / VB;
-  const int per = 32 * (op == Op::kCombine ? kVecs / 2 : kVecs);
-  a.parts = (a.vecs + per - 1) / per;
+  a.parts = (a.vecs + 32 * kVecs - 1) / (32 * kVecs);
   const int64_t most = (int64_t)sm_count() * 64;
   const unsigned blocks = (unsigned)std::min<int64_t>(most, (a.T * a.parts + kThreads / 32 - 1) / (kThreads / 32));
   count_launch();
