@@ -880,8 +880,8 @@ def bakron_act_grad(dy, z, act, gated=False, want_bias_grad=False, out=None, wor
 def _ints(t, shape, index, name):
     """Device address of an int32 tensor of that shape on device `index`."""
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.get_device() != index or \
-            tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.get_device() != index or t.shape != shape or \
+            not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of shape %s on cuda:%d" % (name, tuple(shape), index))
     return t.data_ptr()
 
@@ -892,7 +892,7 @@ def bakron_sort_tokens(choice, experts, out=None, stream=None):
     offsets[e + 1] - 1 in the order by expert, and choice (t, j) has row place[t, j], -1 for none."""
     torch = _torch()
     if not isinstance(choice, torch.Tensor) or not choice.is_cuda or choice.dim() != 2 or \
-            choice.dtype not in (torch.int32, torch.int64) or not choice.is_contiguous():
+            (choice.dtype != torch.int64 and choice.dtype != torch.int32) or not choice.is_contiguous():
         raise ValueError("choice must be a contiguous int32 or int64 CUDA tensor of shape (tokens, choices)")
     dev = choice.get_device()
     if dev != _device():
@@ -911,20 +911,22 @@ def bakron_sort_tokens(choice, experts, out=None, stream=None):
 
 
 def _placed(place, index, T=None):
-    """Checks places (of T tokens); returns (address, tokens, choices per token)."""
-    if not isinstance(place, _torch().Tensor) or place.dim() != 2 or (T is not None and place.shape[0] != T):
-        raise ValueError("place must be an int32 tensor of shape (%s, choices)" % ("tokens" if T is None else T))
-    return (_ints(place, place.shape, index, "place"),) + tuple(place.shape)
-
-
-def _weights(weight, place, index, name="weight", optional=False):
-    """Address of a float32 tensor of the places' shape; None for None if that is allowed."""
-    if weight is None and optional:
-        return None
+    """Checks places (of T tokens); returns (address, their shape)."""
     torch = _torch()
-    if not isinstance(weight, torch.Tensor) or weight.dtype != torch.float32 or not weight.is_cuda or \
-            weight.get_device() != index or weight.shape != place.shape or not weight.is_contiguous():
-        raise ValueError("%s must be a contiguous float32 tensor of shape %s on cuda:%d" % (name, tuple(place.shape), index))
+    shape = place.shape if isinstance(place, torch.Tensor) else ()
+    if len(shape) != 2 or (T is not None and shape[0] != T) or place.dtype != torch.int32 or \
+            place.get_device() != index or not place.is_contiguous():
+        raise ValueError("place must be a contiguous int32 tensor of shape (%s, choices) on cuda:%d"
+                         % ("tokens" if T is None else T, index))
+    return place.data_ptr(), shape
+
+
+def _weights(weight, shape, index, name="weight"):
+    """Address of a float32 tensor of the places' shape."""
+    torch = _torch()
+    if not isinstance(weight, torch.Tensor) or weight.dtype != torch.float32 or weight.get_device() != index or \
+            weight.shape != shape or not weight.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of shape %s on cuda:%d" % (name, tuple(shape), index))
     return weight.data_ptr()
 
 
@@ -934,8 +936,9 @@ def bakron_dispatch(x, place, weight=None, out=None, stream=None):
     number of rows; rows that no choice has are left as they were (``out`` None: not
     initialised)."""
     T, d, code, dev = _act(x, "X")
-    pp, _, k = _placed(place, dev, T)
-    wp = _weights(weight, place, dev, optional=True)
+    pp, shape = _placed(place, dev, T)
+    k = shape[1]
+    wp = None if weight is None else _weights(weight, shape, dev)
     R = out.shape[0] if isinstance(out, _torch().Tensor) and out.dim() == 2 else T * k
     rows = _out(out, x, (R, d), "out")
     _check(lib().bakron_dispatch(x.data_ptr(), T, d, code, pp, k, wp, rows.data_ptr(), R, _handle(stream, dev)),
@@ -947,8 +950,9 @@ def bakron_combine(rows, place, weight=None, out=None, stream=None):
     """y[t] = the sum over j of weight[t, j] * rows[place[t, j]] (weight None: 1), (T, d).
     Without weight the gradient of bakron_dispatch."""
     R, d, code, dev = _act(rows, "rows")
-    pp, T, k = _placed(place, dev)
-    wp = _weights(weight, place, dev, optional=True)
+    pp, shape = _placed(place, dev)
+    T, k = shape
+    wp = None if weight is None else _weights(weight, shape, dev)
     y = _out(out, rows, (T, d), "out")
     _check(lib().bakron_combine(rows.data_ptr(), R, d, code, pp, T, k, wp, y.data_ptr(), _handle(stream, dev)),
            "bakron_combine")
@@ -962,13 +966,13 @@ def bakron_combine_grad(dy, rows, place, weight, out=None, stream=None):
     T, d, code, dev = _act(dy, "dY")
     R = rows.shape[0] if isinstance(rows, _torch().Tensor) and rows.dim() == 2 else 0
     rp = _same(rows, dy, (R, d), "rows")
-    pp, _, k = _placed(place, dev, T)
-    wp = _weights(weight, place, dev)
+    pp, shape = _placed(place, dev, T)
+    wp = _weights(weight, shape, dev)
     if out is None:
         out = (None, _torch().empty_like(weight))
     drows, dweight = _out(out[0], dy, (R, d), "drows"), out[1]
-    _check(lib().bakron_combine_grad(dy.data_ptr(), rp, R, d, code, pp, T, k, wp, drows.data_ptr(),
-                                     _weights(dweight, place, dev, "dweight"), _handle(stream, dev)),
+    _check(lib().bakron_combine_grad(dy.data_ptr(), rp, R, d, code, pp, T, shape[1], wp, drows.data_ptr(),
+                                     _weights(dweight, shape, dev, "dweight"), _handle(stream, dev)),
            "bakron_combine_grad")
     return drows, dweight
 

@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "act.cuh"
+#include "piece.cuh"
 
 namespace bakron {
 namespace {
@@ -27,14 +28,9 @@ struct ActArgs {
   float* sums;          // [row blocks][columns of z], or dbias
 };
 
-template <typename TX, int V>
-struct alignas(sizeof(TX) * V) Vec {
-  TX v[V];
-};
-
 template <typename TX, int V, bool kGated, bool kGrad, bool kSums>
-__global__ void __launch_bounds__(kThreads) act_kernel(const __grid_constant__ ActArgs a) {
-  using W = Vec<TX, V>;
+__global__ void __launch_bounds__(kThreads, kSums ? 3 : 4) act_kernel(const __grid_constant__ ActArgs a) {
+  using W = Piece<TX, V * (int)sizeof(TX)>;
   constexpr int kRows = kGated ? 2 : 4;
   constexpr int NS = kSums ? (kGated ? 2 : 1) * V : 1;
   const int tx = threadIdx.x & (a.cx - 1), ty = threadIdx.x / a.cx, ry = kThreads / a.cx;
@@ -65,31 +61,36 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const __grid_constant__ A
         for (int i = 0; i < kRows; ++i) {
           const int64_t row = r + (int64_t)i * ry;
           if (row < r1) {
-            W o, p;
+            W o;
+            float vo[V], vp[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              const float x = to_float(g[i].v[e]);
+              const float x = g[i].get(e);
               if constexpr (!kGrad) {
                 float y = activate<TX, A>(x);
-                if constexpr (kGated) y *= to_float(u[i].v[e]);
-                o.v[e] = from_float<TX>(y);
+                if constexpr (kGated) y *= u[i].get(e);
+                vo[e] = y;
               } else {
                 float f, slope;
                 activate_slope<TX, A>(x, f, slope);
-                float q = to_float(d[i].v[e]);
+                float q = d[i].get(e);
                 if constexpr (kGated) {
                   const float t = q * f;
-                  p.v[e] = from_float<TX>(t);
+                  vp[e] = t;
                   if constexpr (kSums) sum[V + e] += t;
-                  q *= to_float(u[i].v[e]);
+                  q *= u[i].get(e);
                 }
                 q *= slope;
-                o.v[e] = from_float<TX>(q);
+                vo[e] = q;
                 if constexpr (kSums) sum[e] += q;
               }
             }
+            o.set(vo);
             *reinterpret_cast<W*>(out + row * oc) = o;
-            if constexpr (kGated && kGrad) *reinterpret_cast<W*>(out + row * oc + a.m) = p;
+            if constexpr (kGated && kGrad) {
+              o.set(vp);
+              *reinterpret_cast<W*>(out + row * oc + a.m) = o;
+            }
           }
         }
       });
@@ -132,7 +133,9 @@ __global__ void __launch_bounds__(512) act_join_kernel(const float* __restrict__
   }
 }
 
-// Row blocks: as many as fill the SMs eight times, but four rows for each thread at least.
+// Row blocks: as many as fill the SMs eight times, but four rows for each thread at least, and one
+// block as long as a thread then has eight at most: a second launch, which joins the blocks' sums,
+// costs more (37 x 1111 fp32).
 struct Grid {
   int cx;
   int64_t strips, blocks;
@@ -144,6 +147,10 @@ Grid act_grid(int64_t T, int64_t m, int V) {
   while (g.cx < 32 && g.cx < vecs) g.cx *= 2;
   g.strips = (vecs + g.cx - 1) / g.cx;
   const int64_t rows = (int64_t)4 * (kThreads / g.cx);
+  if (T <= 2 * rows) {
+    g.blocks = 1;
+    return g;
+  }
   g.blocks = std::max<int64_t>(1, std::min<int64_t>((T + rows - 1) / rows, (int64_t)sm_count() * 8 / g.strips));
   return g;
 }

@@ -18,7 +18,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "packed.cuh"
+#include "piece.cuh"
 
 namespace bakron {
 
@@ -29,6 +29,8 @@ namespace {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 32;              // of a token: a lane each
 constexpr int64_t kMaxRows = int64_t(1) << 28;
+constexpr int kMaxBlocks = 8;                // of the sort: a cluster
+constexpr int kKept = 8;                     // choices of a lane at a time
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 
 // ---------------------------------------------------------------- sort
@@ -57,18 +59,34 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
   // runs of whole 32s
   const int steps = (a.n + 31) / 32, w = rank * warps + warp, W = C * warps;
   const int lo = (int)((int64_t)steps * w / W) * 32, hi = min(a.n, (int)((int64_t)steps * (w + 1) / W) * 32);
+  // the run's first choices stay in registers for the second walk
+  int kept[kKept];
+#pragma unroll
+  for (int q = 0; q < kKept; ++q) {
+    const int i = lo + 32 * q + lane;
+    const I e = i < hi ? choice[i] : (I)-1;
+    kept[q] = e >= 0 && e < E ? (int)e : -1;
+  }
+#pragma unroll
+  for (int q = 0; q < kKept; ++q)
+    if (kept[q] >= 0) atomicAdd(&mine[kept[q]], 1);
 #pragma unroll 4
-  for (int i = lo + lane; i < hi; i += 32) {
+  for (int i = lo + 32 * kKept + lane; i < hi; i += 32) {
     const I e = choice[i];
     if (e >= 0 && e < E) atomicAdd(&mine[(int)e], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int sum = 0;
-    for (int v = 0; v < warps; ++v) {
-      const int c = count[v * E + e];
-      count[v * E + e] = sum;
-      sum += c;
+    for (int v0 = 0; v0 < warps; v0 += 8) {
+      int c[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) c[v] = v0 + v < warps ? count[(v0 + v) * E + e] : 0;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        if (v0 + v < warps) count[(v0 + v) * E + e] = sum;
+        sum += c[v];
+      }
     }
     total[e] = sum;
   }
@@ -80,10 +98,13 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     const int e = e0 + threadIdx.x;
     int all = 0, before = 0;
     if (e < E) {
-      for (int q = 0; q < C; ++q) {
-        const int c = q == rank ? total[e] : cluster.map_shared_rank(total, q)[e];
-        if (q < rank) before += c;
-        all += c;
+      int c[kMaxBlocks];
+#pragma unroll
+      for (int q = 0; q < kMaxBlocks; ++q) c[q] = q < C ? cluster.map_shared_rank(total, q)[e] : 0;
+#pragma unroll
+      for (int q = 0; q < kMaxBlocks; ++q) {
+        if (q < rank) before += c[q];
+        all += c[q];
       }
     }
     int up = all;
@@ -108,19 +129,29 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
   }
   if (rank == 0 && threadIdx.x == 0) a.offsets[E] = run;
   // (the barrier that ended the last turn is between first[] and its use)
-  for (int i = lo + lane; i - lane < hi; i += 32) {
-    const bool in = i < hi;
-    const I raw = in ? choice[i] : (I)-1;
-    const bool live = raw >= 0 && raw < E;
-    const int e = live ? (int)raw : -1;
+  auto put = [&](int i, int e) {
     const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const int rank_in = __popc(same & ((1u << lane) - 1));
+    const int lower = __popc(same & ((1u << lane) - 1));
     int at = -1;
-    if (live) at = first[e] + mine[e] + rank_in;
+    if (e >= 0) at = first[e] + mine[e] + lower;
     __syncwarp();
-    if (live && rank_in == 0) mine[e] += __popc(same);
+    if (e >= 0 && lower == 0) mine[e] += __popc(same);
     __syncwarp();
-    if (in) a.place[i] = at;
+    if (i < hi) a.place[i] = at;
+  };
+#pragma unroll
+  for (int q = 0; q < kKept; ++q)
+    if (lo + 32 * q < hi) put(lo + 32 * q + lane, kept[q]);
+  for (int i0 = lo + 32 * kKept; i0 < hi; i0 += 32 * kKept) {
+#pragma unroll
+    for (int q = 0; q < kKept; ++q) {
+      const int i = i0 + 32 * q + lane;
+      const I e = i < hi ? choice[i] : (I)-1;
+      kept[q] = e >= 0 && e < E ? (int)e : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kKept; ++q)
+      if (i0 + 32 * q < hi) put(i0 + 32 * q + lane, kept[q]);
   }
   __syncwarp();
   cluster.sync();                            // no block leaves while its totals are read
@@ -132,7 +163,7 @@ cudaError_t run_sort(const SortArgs& a, cudaStream_t s) {
   // a warp per 64 choices and a thread per expert; beyond 32 warps, more blocks
   const int warps = std::min(32, std::max({4, (a.n + 63) / 64, (a.E + 31) / 32}));
   int C = 1;
-  while (C < 8 && a.n > C * 32 * 64) C *= 2;
+  while (C < kMaxBlocks && a.n > C * 32 * 64) C *= 2;
   const size_t smem = (size_t)(warps + 2) * a.E * sizeof(int);
   static std::atomic<unsigned long long> done;
   if (smem > 46 * 1024) {
@@ -167,14 +198,9 @@ struct RowArgs {
   int k;
   int64_t vecs;         // of a row
   int64_t parts;        // warps' parts of a row
+  int narrow;           // T parts is below 2^32
 };
 
-// VB bytes of a row: V elements.
-template <typename TX, int VB>
-struct alignas(VB) Piece {
-  static constexpr int V = VB / sizeof(TX);
-  TX v[V];
-};
 template <typename TX, int VB>
 __device__ __forceinline__ Piece<TX, VB> load(const void* base, int64_t i) {
   return static_cast<const Piece<TX, VB>*>(base)[i];
@@ -182,6 +208,12 @@ __device__ __forceinline__ Piece<TX, VB> load(const void* base, int64_t i) {
 
 constexpr int kThreads = 256;
 constexpr int kVecs = 4;                     // of a lane at a time
+constexpr int kWide = 2;                     // where several rows are at hand
+
+// Unit u of a.parts a token: the token (division of 32 bits where the units fit).
+__device__ __forceinline__ int64_t token_of(const RowArgs& a, int64_t u) {
+  return a.narrow ? (int64_t)((uint32_t)u / (uint32_t)a.parts) : u / a.parts;
+}
 
 // A token's places and weights: lane j holds choice j (R where there is none).
 __device__ __forceinline__ void load_choices(const RowArgs& a, int64_t t, int lane, int& at, float& w) {
@@ -201,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
   const int64_t units = a.T * a.parts;
   for (int64_t u = blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5); u < units;
        u += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int64_t t = u / a.parts, v0 = (u - t * a.parts) * (32 * kVecs) + lane;
+    const int64_t t = token_of(a, u), v0 = (u - t * a.parts) * (32 * kVecs) + lane;
     int at;
     float w;
     load_choices(a, t, lane, at, w);
@@ -218,8 +250,10 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
         if (v0 + 32 * i >= a.vecs) continue;
         P o = x[i];
         if constexpr (kWeight) {
+          float v[P::V];
 #pragma unroll
-          for (int e = 0; e < P::V; ++e) o.v[e] = from_float<TX>(f * to_float(x[i].v[e]));
+          for (int e = 0; e < P::V; ++e) v[e] = f * x[i].get(e);
+          o.set(v);
         }
         static_cast<P*>(a.out)[r * a.vecs + v0 + 32 * i] = o;
       }
@@ -228,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
 }
 
 template <typename TX, int VB>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) combine_kernel(const __grid_constant__ RowArgs a) {
   using P = Piece<TX, VB>;
   constexpr int kAtOnce = 2;
   const int lane = threadIdx.x & 31;
@@ -236,45 +270,48 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
   int64_t u = blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5);
   int at_next = -1;
   float w_next = 1.f;
-  if (u < units) load_choices(a, u / a.parts, lane, at_next, w_next);
+  if (u < units) load_choices(a, token_of(a, u), lane, at_next, w_next);
   for (; u < units; u += step) {
-    const int64_t t = u / a.parts, v0 = (u - t * a.parts) * (32 * kVecs) + lane;
+    const int64_t t = token_of(a, u), v0 = (u - t * a.parts) * (32 * kWide) + lane;
     const int at = at_next;
     const float w = w_next;
-    if (u + step < units) load_choices(a, (u + step) / a.parts, lane, at_next, w_next);
-    float sum[kVecs][P::V];
+    if (u + step < units) load_choices(a, token_of(a, u + step), lane, at_next, w_next);
+    float sum[kWide][P::V];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
+    for (int i = 0; i < kWide; ++i)
 #pragma unroll
       for (int e = 0; e < P::V; ++e) sum[i][e] = 0.f;
     for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
-      P x[kAtOnce][kVecs];
-      int64_t r[kAtOnce];
+      P x[kAtOnce][kWide];
+      float f[kAtOnce];
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
-        r[q] = __shfl_sync(0xffffffffu, at, (j0 + q) & 31);
-        if (j0 + q >= a.k) r[q] = -1;
+        const int r = __shfl_sync(0xffffffffu, at, (j0 + q) & 31);
+        const bool there = r >= 0 && j0 + q < a.k;
+        f[q] = __shfl_sync(0xffffffffu, w, (j0 + q) & 31);
+        const P* row = static_cast<const P*>(a.in) + (int64_t)(there ? r : 0) * a.vecs + v0;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-          if (r[q] >= 0 && v0 + 32 * i < a.vecs) x[q][i] = load<TX, VB>(a.in, r[q] * a.vecs + v0 + 32 * i);
+        for (int i = 0; i < kWide; ++i) {
+          if (there && v0 + 32 * i < a.vecs) x[q][i] = row[32 * i];
+        }
+        if (!there) f[q] = 0.f;
+        if (!there) {
+#pragma unroll
+          for (int i = 0; i < kWide; ++i) x[q][i] = P{};
+        }
       }
 #pragma unroll
-      for (int q = 0; q < kAtOnce; ++q) {
-        const float f = __shfl_sync(0xffffffffu, w, (j0 + q) & 31);
-        if (r[q] < 0) continue;
+      for (int q = 0; q < kAtOnce; ++q)
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
+        for (int i = 0; i < kWide; ++i)
 #pragma unroll
-          for (int e = 0; e < P::V; ++e)
-            if (v0 + 32 * i < a.vecs) sum[i][e] = fmaf(f, to_float(x[q][i].v[e]), sum[i][e]);
-      }
+          for (int e = 0; e < P::V; ++e) sum[i][e] = fmaf(f[q], x[q][i].get(e), sum[i][e]);
     }
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < kWide; ++i) {
       if (v0 + 32 * i >= a.vecs) continue;
       P o;
-#pragma unroll
-      for (int e = 0; e < P::V; ++e) o.v[e] = from_float<TX>(sum[i][e]);
+      o.set(sum[i]);
       static_cast<P*>(a.out)[t * a.vecs + v0 + 32 * i] = o;
     }
   }
@@ -284,20 +321,23 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
 // token's choices, kAtOnce of them together; the products are joined over the lanes and then
 // the warps in a fixed order.
 template <typename TX, int VB, bool kBlock>
-__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) combine_grad_kernel(const __grid_constant__ RowArgs a) {
   using P = Piece<TX, VB>;
-  constexpr int kAtOnce = 4, kWide = 2;
+  constexpr int kAtOnce = 2;
   __shared__ float red[2][kAtOnce][kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t step = kBlock ? gridDim.x : (int64_t)gridDim.x * warps;
   const int first = kBlock ? threadIdx.x : lane, width = kBlock ? blockDim.x : 32;
-  int slot = 0;
-  for (int64_t t = kBlock ? blockIdx.x : blockIdx.x * (int64_t)warps + warp; t < a.T; t += step) {
-    int at;
-    float w;
-    load_choices(a, t, lane, at, w);
+  int slot = 0, at_next = -1;
+  float w_next = 1.f;
+  int64_t t = kBlock ? blockIdx.x : blockIdx.x * (int64_t)warps + warp;
+  if (t < a.T) load_choices(a, t, lane, at_next, w_next);
+  for (; t < a.T; t += step) {
+    const int at = at_next;
+    const float w = w_next;
+    if (t + step < a.T) load_choices(a, t + step, lane, at_next, w_next);
     for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
-      int64_t r[kAtOnce];
+      int r[kAtOnce];
       float f[kAtOnce], dot[kAtOnce];
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
@@ -315,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
           d[i] = load<TX, VB>(a.in, t * a.vecs + c);
 #pragma unroll
           for (int q = 0; q < kAtOnce; ++q)
-            if (r[q] >= 0) x[q][i] = load<TX, VB>(a.rows, r[q] * a.vecs + c);
+            if (r[q] >= 0) x[q][i] = load<TX, VB>(a.rows, (int64_t)r[q] * a.vecs + c);
         }
 #pragma unroll
         for (int i = 0; i < kWide; ++i) {
@@ -325,13 +365,15 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
           for (int q = 0; q < kAtOnce; ++q) {
             if (r[q] < 0) continue;
             P o;
+            float v[P::V];
 #pragma unroll
             for (int e = 0; e < P::V; ++e) {
-              const float g = to_float(d[i].v[e]);
-              dot[q] = fmaf(g, to_float(x[q][i].v[e]), dot[q]);
-              o.v[e] = from_float<TX>(f[q] * g);
+              const float g = d[i].get(e);
+              dot[q] = fmaf(g, x[q][i].get(e), dot[q]);
+              v[e] = f[q] * g;
             }
-            static_cast<P*>(a.out)[r[q] * a.vecs + c] = o;
+            o.set(v);
+            static_cast<P*>(a.out)[(int64_t)r[q] * a.vecs + c] = o;
           }
         }
       }
@@ -366,8 +408,11 @@ enum class Op { kDispatch, kCombine, kCombineGrad };
 template <typename TX, int VB>
 cudaError_t launch_rows(RowArgs& a, Op op, cudaStream_t s) {
   a.vecs = a.d * (int64_t)sizeof(TX) / VB;
-  a.parts = (a.vecs + 32 * kVecs - 1) / (32 * kVecs);
-  const int64_t most = (int64_t)sm_count() * 64;
+  const int per = 32 * (op == Op::kCombine ? kWide : kVecs);
+  a.parts = (a.vecs + per - 1) / per;
+  a.narrow = a.T * a.parts < (int64_t(1) << 32);
+  // dispatch_kernel's warps take a unit or few, the others loop, with the next choices on their way
+  const int64_t most = (int64_t)sm_count() * (op == Op::kDispatch ? 64 : 4);
   const unsigned blocks = (unsigned)std::min<int64_t>(most, (a.T * a.parts + kThreads / 32 - 1) / (kThreads / 32));
   count_launch();
   if (op == Op::kDispatch) {
