@@ -78,6 +78,7 @@ struct FwdArgs {
   int N;              // tokens per tile, a multiple of 32
   int stages;
   int wstages;        // 4 where TMEM has room, else 2: a power of two
+  int log_acc;        // each issuer has 1 << log_acc accumulators
   int* status;
   Epilogue epi;       // kWithAct
   const int* offsets; // kExperts
@@ -127,14 +128,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* r) {
       : "memory");
 }
 
-// 8 TMEM columns of each lane's row.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-
-constexpr int kFinish = 8;
+constexpr int kFinish = 16;
 // bakron_linear_act's epilogue for a warp's sums, 32 rows (a lane each) x n tokens, that lie in
 // TMEM: kFinish tokens at a time in a loop whose code stays small.  (Unrolled over all 96 tokens that a
 // thread's registers hold, the code did not fit the instruction cache: 2048 tokens of 8192 x 8192
@@ -163,7 +157,7 @@ __device__ __forceinline__ void finish(const FwdArgs& a, uint32_t ta, int n, int
 #pragma unroll 1
     for (int g = 0; g < n; g += kFinish) {
       uint32_t v[kFinish];
-      tmem_ld8(ta + (uint32_t)g, v);
+      tmem_ld16(ta + (uint32_t)g, v);
 #pragma unroll
       for (int t = 0; t < kFinish; ++t) r[t] = next[t];
       fetch(g + kFinish);
@@ -194,9 +188,11 @@ __device__ __forceinline__ void finish(const FwdArgs& a, uint32_t ta, int n, int
   });
 }
 
+constexpr int kMaxAcc = 4;                   // accumulators
+
 struct Bars {
-  unsigned long long full_b[kMaxStages], empty_b[kMaxStages], full_a[kWStages], empty_a[kWStages];
-  unsigned long long acc_full[2], acc_empty[2], done;
+  unsigned long long full_b[kMaxStages], empty_b[kMaxStages], full_a[2 * kWStages], empty_a[2 * kWStages];
+  unsigned long long acc_full[kMaxAcc], acc_empty[kMaxAcc], turn[2], done;
   uint32_t tmem;
   int abort;
 };
@@ -338,29 +334,42 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, const T
           for (int i = 0; i < 4; ++i) v[e * 16 + t * 4 + i] = p[i];
         }
       }
-      if (h == 0) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(empty + 8u * ws, ((seq >> log_stages) & 1) ^ 1u, &bars.abort, a.status))) goto out;
-        fence_after_sync();
-      }
+      if (!__all_sync(0xffffffffu, wait_or_abort(empty + 8u * (2 * ws + h), ((seq >> log_stages) & 1) ^ 1u, &bars.abort, a.status)))
+        goto out;
+      fence_after_sync();
       tmem_st32(tmem_a + ((uint32_t)(quarter * 32) << 16) + ws * 64u + (uint32_t)(h * 32), v);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8u * (2 * ws + h));
     }
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-    fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full + 8u * ws);
     seq += 2;
   }
 out:
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// Barriers of the epilogue's 256 threads; the second returns whether all of them say so.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 8, 256;" ::: "memory"); }
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 8, 256, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
 // TX: 16-bit terms of the activations; NC: columns per epilogue warp; EW:
-// epilogue warps; KU: accumulation unit in MMA steps of 16 (2, 4 or 8).
-template <typename TO, typename H, int TX, int NC, int EW, int KU, Product P>
+// epilogue warps; KU: accumulation unit in MMA steps of 16 (2, 4 or 8); SETS: sets of
+// epilogue warps that take the units in turn.
+template <typename TO, typename H, int TX, int NC, int EW, int KU, int SETS, Product P>
 __global__ void __launch_bounds__(32 * (12 + EW), 1)
     linear_fwd_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ FwdArgs a) {
   constexpr int THREADS = 32 * (12 + EW);
-  constexpr int PARTS = EW / 4;              // column parts of the epilogue
+  constexpr int PARTS = EW / 4 / SETS;       // column parts of the epilogue
   // 640 threads start with 96 registers each; the roles share them out
   // (8 x 136 + 8 x 72 + 4 x 64 warps' worth of 20 x 96)
   constexpr bool kSplit = EW == 8;
@@ -387,15 +396,16 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       mbar_init(smem_u32(&bars.full_b[s]), 1);
       mbar_init(smem_u32(&bars.empty_b[s]), 1);
     }
-    for (int s = 0; s < kWStages; ++s) {
+    for (int s = 0; s < 2 * kWStages; ++s) {         // halves
       mbar_init(smem_u32(&bars.full_a[s]), 4);       // the warps of a group
       mbar_init(smem_u32(&bars.empty_a[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kMaxAcc; ++b) {
       mbar_init(smem_u32(&bars.acc_full[b]), 1);
-      mbar_init(smem_u32(&bars.acc_empty[b]), EW);
+      mbar_init(smem_u32(&bars.acc_empty[b]), EW / SETS);
     }
-    mbar_init(smem_u32(&bars.done), 1);
+    for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&bars.turn[b]), 1);
+    mbar_init(smem_u32(&bars.done), 2);              // the issuers
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) {
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t acc_cols = (TX == 1 ? 1u : 2u) * (uint32_t)a.N;
-  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), tmem_a = tmem + 2u * acc_cols;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), tmem_a = tmem + (2u << a.log_acc) * acc_cols;
   grid_dep_wait();
   grid_dep_launch();
   Tiles<P> tiles = {a.tiles, a.tiles_m, a.N, a.T, nullptr, nullptr, 0};
@@ -460,61 +470,68 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
           }
         }
       }
-    } else if (warp == 1) {
-      // ---------------- MMA issuer: the warp waits together, one lane issues.
-      // A single warp's dependent instructions, not the tensor core, bound
-      // this loop when it is long, so everything is fixed per K chunk:
-      // where units begin and end, and the descriptors' offsets.
+    } else if (warp == 1 || warp == 3) {
+      // ---------------- MMA issuers, which take the chunks in turn: a warp waits together, one lane
+      // issues.  Their own instructions, not the tensor core, bounded a single issuer: what it
+      // waited for and issued one after the other.  Each has its accumulators and its stages of
+      // weights; the stages of activations are waited for in the order of the chunks (`turn`), so that
+      // a use of a stage is never mistaken for the one before.
+      const int me = warp >> 1;
       const uint32_t idesc = idesc_f16<H>(a.N);
       const uint64_t desc_b0 = desc_sw128(ring);
       const uint32_t stage16 = stage_bytes >> 4, half16 = half_bytes >> 4, plane16 = plane_b >> 4;
       const uint32_t fb = smem_u32(bars.full_b), eb = smem_u32(bars.empty_b);
       const uint32_t fa = smem_u32(bars.full_a), ea = smem_u32(bars.empty_a);
-      const uint32_t af = smem_u32(&bars.acc_full[0]), ae = smem_u32(&bars.acc_empty[0]);
-      constexpr int UPC = 8 / KU;             // units of a chunk
+      const uint32_t my_turn = smem_u32(&bars.turn[me]), other_turn = smem_u32(&bars.turn[me ^ 1]);
+      const uint32_t af = smem_u32(&bars.acc_full[me << a.log_acc]), ae = smem_u32(&bars.acc_empty[me << a.log_acc]);
+      const uint32_t tmem_me = tmem + ((uint32_t)me << a.log_acc) * acc_cols;
       uint32_t u = 0;                         // units begun
-      uint32_t seq = 0;                       // chunks begun
-      const uint32_t last_stage = (uint32_t)a.wstages - 1;
+      const uint32_t last_stage = (uint32_t)a.wstages - 1, last_acc = (1u << a.log_acc) - 1;
       const int log_stages = a.wstages == 4 ? 2 : 1;
-      bool go = true;
+      const int64_t chunks = k.tile < tiles.tiles ? ((tiles.tiles - 1 - k.tile) / k.step + 1) * (k.c1 - k.c0) : 0;
+      uint32_t turns = 0;
       Ring rg;
-      for (int64_t tile = k.tile; tile < tiles.tiles && go; tile += k.step) {
-        for (int c = k.c0; c < k.c1; ++c) {
-          const uint32_t ws = seq & last_stage;
-          go = wait_or_abort(fb + 8u * (uint32_t)rg.s, rg.parity, &bars.abort, a.status) &&
-               wait_or_abort(fa + 8u * ws, (seq >> log_stages) & 1, &bars.abort, a.status);
-          fence_after_sync();
-          const uint64_t db = desc_b0 + (uint32_t)rg.s * stage16;
-          const uint32_t ta = tmem_a + ws * 64u;
+      rg.advance(me, a.stages);
+      for (int64_t seq = me; seq < chunks; seq += 2) {
+        const uint32_t ws = (uint32_t)seq & last_stage;
+        bool go = seq == 0 || wait_or_abort(my_turn, (turns + (uint32_t)me + 1) & 1, &bars.abort, a.status);
+        ++turns;
+        go = go && wait_or_abort(fb + 8u * (uint32_t)rg.s, rg.parity, &bars.abort, a.status);
+        go = __all_sync(0xffffffffu, go);
+        if (!go) break;
+        if (lane == 0) mbar_arrive(other_turn);
+        const uint64_t db = desc_b0 + (uint32_t)rg.s * stage16;
+        const uint32_t ta = tmem_a + ws * 64u;
+        // halves of the chunk, each as soon as its weights are there; J steps at a time
+        constexpr int J = KU < 4 ? KU : 4;
 #pragma unroll
-          for (int i = 0; i < UPC; ++i) {
-            const uint32_t v = u + i, buf = v & 1;
-            // the accumulator: unit v - 2 has been read
-            go = go && (v < 2 || wait_or_abort(ae + 8u * buf, ((v >> 1) & 1) ^ 1u, &bars.abort, a.status));
-            go = __all_sync(0xffffffffu, go);
-            if (!go) break;
-            fence_after_sync();
-            if (elect_one()) {
-              const uint32_t d = tmem + buf * acc_cols;
-#pragma unroll
-              for (int j = i * KU; j < (i + 1) * KU; ++j)
-#pragma unroll
-                for (int q = 0; q < TX; ++q)
-                  mma_f16_ts(q == 0 ? d : d + (uint32_t)a.N, ta + j * 8,
-                             db + ((j / 4) * half16 + q * plane16 + (j % 4) * 2), idesc, j % KU == 0 && q <= 1 ? 0u : 1u);
-              mma_commit(af + 8u * buf);
-              if (i == UPC - 1) {
-                mma_commit(eb + 8u * (uint32_t)rg.s);
-                mma_commit(ea + 8u * ws);
-              }
-            }
-            __syncwarp();
-          }
+        for (int j0 = 0; j0 < 8; j0 += J) {
+          const int h = j0 / 4;
+          const uint32_t buf = u & last_acc, use = u >> a.log_acc;
+          if (j0 % 4 == 0)
+            go = go && wait_or_abort(fa + 8u * (2 * ws + h), (uint32_t)(seq >> log_stages) & 1, &bars.abort, a.status);
+          // the accumulator: its previous unit has been read
+          if (j0 % KU == 0) go = go && (use == 0 || wait_or_abort(ae + 8u * buf, (use & 1) ^ 1u, &bars.abort, a.status));
+          go = __all_sync(0xffffffffu, go);
           if (!go) break;
-          u += UPC;
-          ++seq;
-          rg.advance(1, a.stages);
+          fence_after_sync();
+          if (elect_one()) {
+            const uint32_t d = tmem_me + buf * acc_cols;
+#pragma unroll
+            for (int j = j0; j < j0 + J; ++j)
+#pragma unroll
+              for (int q = 0; q < TX; ++q)
+                mma_f16_ts(q == 0 ? d : d + (uint32_t)a.N, ta + j * 8,
+                           db + ((j / 4) * half16 + q * plane16 + (j % 4) * 2), idesc, j % KU == 0 && q <= 1 ? 0u : 1u);
+            if ((j0 + J) % KU == 0) mma_commit(af + 8u * buf);
+            if ((j0 + J) % 4 == 0) mma_commit(ea + 8u * (2 * ws + h));
+            if (j0 + J == 8) mma_commit(eb + 8u * (uint32_t)rg.s);
+          }
+          __syncwarp();
+          if ((j0 + J) % KU == 0) ++u;
         }
+        if (!go) break;
+        rg.advance(2, a.stages);
       }
       if (elect_one()) mma_commit(smem_u32(&bars.done));
       __syncwarp();
@@ -531,9 +548,12 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
     if constexpr (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const int quarter = warp & 3, ew = warp - 12;
     const int ncols = a.N / PARTS;           // a multiple of 16, at most NC
-    const int col0 = (ew / 4) * ncols;
+    const int set = SETS == 2 ? ew / 4 : 0, col0 = SETS == 2 ? 0 : (ew / 4) * ncols;
     const uint32_t af = smem_u32(&bars.acc_full[0]), ae = smem_u32(&bars.acc_empty[0]);
-    uint32_t u_all = 0;
+    // the next chunk's issuer, and the units read of each
+    constexpr uint32_t UPC = 8 / KU;
+    uint32_t who = 0, read[2] = {0, 0}, of_chunk = 0;
+    const uint32_t last_acc = (1u << a.log_acc) - 1;
     bool ok = true;
     for (int64_t tile = k.tile; tile < tiles.tiles && ok; tile += k.step) {
       const Place at = tiles.at(tile);
@@ -558,17 +578,21 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(p + last));
         }
       }
-      float s_next = scale_of(0);
-      for (int u = 0; u < units; ++u, ++u_all) {
-        const float s = s_next;
-        s_next = scale_of(u + 1);
-        ok = wait_or_abort(af + 8u * (u_all & 1), (u_all >> 1) & 1, &bars.abort, a.status);
+      uint32_t slot = 0;           // of the accumulator at hand
+      auto unit = [&](int u, float s) {
+        const uint32_t n_read = who == 0 ? read[0]++ : read[1]++;
+        slot = SETS == 2 ? 2 * who + (uint32_t)set : (who << a.log_acc) + (n_read & last_acc);
+        if (++of_chunk == UPC / SETS) {
+          of_chunk = 0;
+          who ^= 1;
+        }
+        ok = wait_or_abort(af + 8u * slot, (SETS == 2 ? n_read : n_read >> a.log_acc) & 1, &bars.abort, a.status);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (!ok) return;
         fence_after_sync();
-        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (u_all & 1) * acc_cols + (uint32_t)col0;
+        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + slot * acc_cols + (uint32_t)col0;
         // 32 columns at a time where registers allow: fewer round trips to TMEM
-        constexpr int LD = TX == 1 && NC <= 64 ? 32 : 16;
+        constexpr int LD = TX == 1 ? 32 : 16;
 #pragma unroll
         for (int g = 0; g < NC / LD; ++g) {
           if (g * LD < ncols) {
@@ -588,37 +612,89 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
             for (int t = 0; t < LD; t += 2) fma2(acc[g * LD + t], acc[g * LD + t + 1], s, v[t], v[t + 1]);
           }
         }
-        if (P == kWithAct && S == 1 && u == units - 1) break;      // read, but still needed
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ae + 8u * (u_all & 1));
+        // (the accumulator that was read last may still be needed)
+        if ((SETS == 1 && (P != kWithAct || S > 1)) || u < units - SETS) {
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ae + 8u * slot);
+        }
+      };
+      // this set's units: every SETS-th
+      float s_next = scale_of(set);
+      for (int u = set; u < units && ok; u += SETS) {
+        const float s = s_next;
+        s_next = scale_of(u + SETS);
+        unit(u, s);
+      }
+      const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + slot * acc_cols + (uint32_t)col0;
+      const int n = (int)max((int64_t)0, min((int64_t)ncols, at.end - t0));      // tokens of this warp
+      if constexpr (SETS == 2) {
+        // the second set's sums pass to the first through the accumulator that it read last
+        if (set == 1 && ok) {
+#pragma unroll
+          for (int g = 0; g < NC; g += 16)
+            if (g < ncols) tmem_st16(ta + g, acc + g);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          fence_before_sync();
+        }
+        ok = epilogue_all(ok);
+        if (!ok) break;
+        fence_after_sync();
+        if (set == 0) {
+#pragma unroll
+          for (int g = 0; g < NC; g += 16) {
+            if (g < ncols) {
+              uint32_t v[16];
+              tmem_ld16(ta + acc_cols + g, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int t = 0; t < 16; ++t) acc[g + t] += __uint_as_float(v[t]);
+            }
+          }
+        }
       }
       if (S > 1) {
         // this block's sums [column][row] into the ring, idle once the last
         // accumulator has been read
         float* part = reinterpret_cast<float*>(dsm + (ring - base_raw));
+        if (set == 0) {
 #pragma unroll
-        for (int t = 0; t < NC; ++t)
-          if (t < ncols) part[(col0 + t) * 128 + quarter * 32 + lane] = acc[t];
+          for (int t = 0; t < NC; ++t)
+            if (t < ncols) part[(col0 + t) * 128 + quarter * 32 + lane] = acc[t];
+        }
       } else if (P == kWithAct) {
         if (!ok) break;
         // the sums pass through the accumulator that was read last
-        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (u_all & 1) * acc_cols + (uint32_t)col0;
+        if (set == 0) {
 #pragma unroll
-        for (int g = 0; g < NC; g += 16)
-          if (g < ncols) tmem_st16(ta + g, acc + g);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        finish<TO>(a, ta, (int)min((int64_t)ncols, at.end - t0), t0 * a.w.m + row, row);
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ae + 8u * (u_all & 1));
-        ++u_all;
-      } else if (ok && row < a.w.m) {
+          for (int g = 0; g < NC; g += 16)
+            if (g < ncols) tmem_st16(ta + g, acc + g);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        const int64_t y0 = t0 * a.w.m + row;
+        if constexpr (SETS == 2) {
+          // each set finishes half of the tokens
+          fence_before_sync();
+          epilogue_sync();
+          fence_after_sync();
+          const int half = min(n, (ncols / 2 + kFinish - 1) / kFinish * kFinish);
+          if (set == 0) finish<TO>(a, ta, half, y0, row);
+          else finish<TO>(a, ta - acc_cols + half, n - half, y0 + (int64_t)half * a.w.m, row);
+        } else {
+          finish<TO>(a, ta, n, y0, row);
+        }
+      } else if (ok && set == 0 && row < a.w.m) {
         // lane = output column: the 32 lanes write 32 consecutive elements
         TO* y = static_cast<TO*>(a.y) + t0 * a.w.m + row;
 #pragma unroll
         for (int t = 0; t < NC; ++t)
-          if (t < ncols && t0 + t < at.end) y[(int64_t)t * a.w.m] = from_float<TO>(acc[t]);
+          if (t < n) y[(int64_t)t * a.w.m] = from_float<TO>(acc[t]);
+      }
+      if (SETS == 2 || (P == kWithAct && S == 1)) {
+        fence_before_sync();
+        __syncwarp();
+        if constexpr (SETS == 2) epilogue_sync();       // both sets have read both accumulators
+        if (lane == 0) mbar_arrive(ae + 8u * slot);
       }
     }
     if constexpr (kSplit) role_end<THREADS, 96>(true, warp);
@@ -672,9 +748,9 @@ int blocks_per_tile(int64_t tiles, int64_t chunks) {
   return S;
 }
 
-template <typename TO, typename H, int TX, int NC, int EW, int KU, Product P>
+template <typename TO, typename H, int TX, int NC, int EW, int KU, int SETS, Product P>
 cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
-  auto k = linear_fwd_kernel<TO, H, TX, NC, EW, KU, P>;
+  auto k = linear_fwd_kernel<TO, H, TX, NC, EW, KU, SETS, P>;
   const uint32_t table = P == kExperts ? 8u * (uint32_t)(a.w.count + 1) : 0u;    // the experts'
   const int64_t K = a.w.n;
   FwdArgs t = {};
@@ -687,7 +763,9 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
   t.N = N;
   const uint32_t stage = TX * (uint32_t)N * 256u;
   t.stages = (int)std::min<uint32_t>(kMaxStages, (kRing - table) / stage);
-  t.wstages = (TX == 1 ? 2 : 4) * N + 4 * 64 <= 512 ? 4 : 2;
+  // Short groups change accumulators within a chunk: two for each issuer.
+  t.log_acc = SETS == 2 ? 1 : 0;
+  t.wstages = (2 << t.log_acc) * (TX == 1 ? 1 : 2) * N + 4 * 64 <= 512 ? 4 : 2;
   t.epi = a.epi;
   t.offsets = a.offsets;
   t.status = async_status_word();
@@ -729,9 +807,9 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
 }
 
 // A unit ends where a group does: 128, 64 or 32 columns.
-template <typename TO, typename H, int TX, int NC, int EW, Product P>
+template <typename TO, typename H, int TX, int NC, Product P>
 cudaError_t run_narrow(const LinearArgs& a, int N, cudaStream_t s) {
-  return a.w.g % 64 == 0 ? run_unit<TO, H, TX, NC, EW, 4, P>(a, N, s) : run_unit<TO, H, TX, NC, EW, 2, P>(a, N, s);
+  return a.w.g % 64 == 0 ? run_unit<TO, H, TX, NC, 8, 4, 2, P>(a, N, s) : run_unit<TO, H, TX, NC, 8, 2, 2, P>(a, N, s);
 }
 bool narrow_groups(const LinearArgs& a) { return a.w.ng > 1 && a.w.g % 128 != 0; }
 
@@ -757,17 +835,21 @@ int tokens_per_tile(const LinearArgs& a, int most) {
 
 template <typename TO, Product P>
 cudaError_t run16(const LinearArgs& a, cudaStream_t s) {
-  if (narrow_groups(a)) return run_narrow<TO, TO, 1, 64, 8, P>(a, tokens_per_tile(a, 128), s);
-  return run_unit<TO, TO, 1, 96, 8, 8, P>(a, tokens_per_tile(a, 192), s);
+  if (narrow_groups(a)) return run_narrow<TO, TO, 1, 96, P>(a, tokens_per_tile(a, 96), s);
+  return run_unit<TO, TO, 1, 96, 8, 8, 1, P>(a, tokens_per_tile(a, 192), s);
 }
 
 template <Product P>
 cudaError_t forward(const LinearArgs& a, cudaStream_t s) {
   switch (a.dtype) {
     case BAKRON_F32: {
+      // three terms: few enough tokens for twice the accumulators
+      if (narrow_groups(a)) {
+        const int N = (int)std::min<int64_t>(48, (a.T + 15) / 16 * 16);
+        return run_narrow<float, __nv_bfloat16, 3, 48, P>(a, N, s);
+      }
       const int N = (int)std::min<int64_t>(64, (a.T + 31) / 32 * 32);
-      if (narrow_groups(a)) return run_narrow<float, __nv_bfloat16, 3, 64, 4, P>(a, N, s);
-      return run_unit<float, __nv_bfloat16, 3, 64, 4, 8, P>(a, N, s);
+      return run_unit<float, __nv_bfloat16, 3, 64, 4, 8, 1, P>(a, N, s);
     }
     case BAKRON_BF16: return run16<__nv_bfloat16, P>(a, s);
     default: return run16<__half, P>(a, s);
