@@ -79,6 +79,7 @@ struct FwdArgs {
   int stages;
   int wstages;        // 4 where TMEM has room, else 2: a power of two
   int log_acc;        // each issuer has 1 << log_acc accumulators
+  uint32_t group_mul; // floor(2^31 / (g / 32)) + 1: (32 c) / g = (c group_mul) >> 31 for c, g / 32 <= 2^15
   int* status;
   Epilogue epi;       // kWithAct
   const int* offsets; // kExperts
@@ -209,10 +210,10 @@ struct Work {
 // the epilogue has its registers) would take what the epilogue waits for.
 // PTX also wants the warps of a warpgroup to meet between two setmaxnreg.
 template <int THREADS, int REGS>
-__device__ __forceinline__ void role_end(bool epilogue, int warp) {
+__device__ __forceinline__ void role_end(bool epilogue, int warpgroup = 0) {
   __syncwarp();
   if (epilogue) {
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + (warp >> 2)) : "memory");
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + warpgroup) : "memory");
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
     asm volatile("bar.sync 7, %0;" ::"n"(THREADS) : "memory");
   } else {
@@ -536,13 +537,13 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       if (elect_one()) mma_commit(smem_u32(&bars.done));
       __syncwarp();
     }
-    if constexpr (kSplit) role_end<THREADS, 96>(false, warp);
+    if constexpr (kSplit) role_end<THREADS, 96>(false);
   } else if (warp < 12) {
     // ---------------- weights
     if constexpr (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const uint32_t codes = ring + (uint32_t)a.stages * stage_bytes + (uint32_t)(warp - 4) * (kSlots * kSlotBytes);
     weights<H, P>(a, k, tiles, bars, tmem_a, codes, (warp - 4) >> 2, warp & 3, lane);
-    if constexpr (kSplit) role_end<THREADS, 96>(false, warp);
+    if constexpr (kSplit) role_end<THREADS, 96>(false);
   } else {
     // ---------------- epilogue: running fp32 sums
     if constexpr (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
@@ -550,10 +551,12 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
     const int ncols = a.N / PARTS;           // a multiple of 16, at most NC
     const int set = SETS == 2 ? ew / 4 : 0, col0 = SETS == 2 ? 0 : (ew / 4) * ncols;
     const uint32_t af = smem_u32(&bars.acc_full[0]), ae = smem_u32(&bars.acc_empty[0]);
-    // the next chunk's issuer, and the units read of each
-    constexpr uint32_t UPC = 8 / KU;
-    uint32_t who = 0, read[2] = {0, 0}, of_chunk = 0;
-    const uint32_t last_acc = (1u << a.log_acc) - 1;
+    // A warp's instructions follow one another, several cycles each, and the time of a unit is their
+    // number: so where an accumulator is and which of its uses follows from the count alone.
+    uint32_t count = 0;
+    const uint32_t tmem_ep = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)set * acc_cols + (uint32_t)col0;
+    const uint32_t af_ep = af + 8u * (uint32_t)set, ae_ep = ae + 8u * (uint32_t)set;
+    static_assert(SETS == 2 ? KU < 8 : KU == 8);
     bool ok = true;
     for (int64_t tile = k.tile; tile < tiles.tiles && ok; tile += k.step) {
       const Place at = tiles.at(tile);
@@ -564,9 +567,10 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       const int64_t t0 = at.t0 + col0;
       const bool live = row < a.w.mp;
       const float* scale_row = a.w.scale + (live ? grid_row(a.w, at.e, row) : 0);
+      // (past the last unit the last group's; rows past the matrix take another row's)
       auto scale_of = [&](int u) {
-        if (!live || u >= units) return 0.f;
-        return ld_ahead(scale_row + grid_group(a.w, (uint32_t)(k.c0 * 128 + u * (KU * 16))) * 16);
+        const uint32_t col32 = (uint32_t)(k.c0 * 4 + u * (KU / 2));
+        return ld_ahead(scale_row + min(__umulhi(2 * col32, a.group_mul), (uint32_t)a.w.ng - 1) * 16);
       };
       if (P == kWithAct && S == 1 && a.epi.residual) {
         // the residuals of the tile on their way into L2: a lane per token, 32 rows' bytes
@@ -580,17 +584,15 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       }
       uint32_t slot = 0;           // of the accumulator at hand
       auto unit = [&](int u, float s) {
-        const uint32_t n_read = who == 0 ? read[0]++ : read[1]++;
-        slot = SETS == 2 ? 2 * who + (uint32_t)set : (who << a.log_acc) + (n_read & last_acc);
-        if (++of_chunk == UPC / SETS) {
-          of_chunk = 0;
-          who ^= 1;
-        }
-        ok = wait_or_abort(af + 8u * slot, (SETS == 2 ? n_read : n_read >> a.log_acc) & 1, &bars.abort, a.status);
+        // issuer 0's and 1's chunks in turn, a set's units of a chunk one after the other
+        const uint32_t turn = KU == 2 ? count >> 1 : count, use = KU == 2 ? count : count >> 1;
+        slot = SETS * (turn & 1);
+        ++count;
+        ok = wait_or_abort(af_ep + 8u * slot, use & 1, &bars.abort, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         fence_after_sync();
-        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + slot * acc_cols + (uint32_t)col0;
+        const uint32_t ta = tmem_ep + slot * acc_cols;
         // 32 columns at a time where registers allow: fewer round trips to TMEM
         constexpr int LD = TX == 1 ? 32 : 16;
 #pragma unroll
@@ -616,17 +618,30 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
         if ((SETS == 1 && (P != kWithAct || S > 1)) || u < units - SETS) {
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(ae + 8u * slot);
+          if (lane == 0) mbar_arrive(ae_ep + 8u * slot);
         }
       };
       // this set's units: every SETS-th
-      float s_next = scale_of(set);
-      for (int u = set; u < units && ok; u += SETS) {
-        const float s = s_next;
-        s_next = scale_of(u + SETS);
-        unit(u, s);
+      float s0 = scale_of(set);
+      if constexpr (SETS == 1) {
+        // scales two units ahead, each in a register of its own (moved, it would be waited for;
+        // for two sets the longer code costs more than it saves)
+        float s1 = scale_of(1);
+        for (int u = 0; u < units && ok; u += 2) {
+          unit(u, s0);
+          s0 = scale_of(u + 2);
+          if (u + 1 >= units || !ok) break;
+          unit(u + 1, s1);
+          s1 = scale_of(u + 3);
+        }
+      } else {
+        for (int u = set; u < units && ok; u += SETS) {
+          const float s = s0;
+          s0 = scale_of(u + SETS);
+          unit(u, s);
+        }
       }
-      const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + slot * acc_cols + (uint32_t)col0;
+      const uint32_t ta = tmem_ep + slot * acc_cols;
       const int n = (int)max((int64_t)0, min((int64_t)ncols, at.end - t0));      // tokens of this warp
       if constexpr (SETS == 2) {
         // the second set's sums pass to the first through the accumulator that it read last
@@ -694,10 +709,10 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
         fence_before_sync();
         __syncwarp();
         if constexpr (SETS == 2) epilogue_sync();       // both sets have read both accumulators
-        if (lane == 0) mbar_arrive(ae + 8u * slot);
+        if (lane == 0) mbar_arrive(ae_ep + 8u * slot);
       }
     }
-    if constexpr (kSplit) role_end<THREADS, 96>(true, warp);
+    if constexpr (kSplit) role_end<THREADS, 96>(true, ew >> 2);
   }
   __syncwarp();
   // the wait below begins when the roles have ended: its budget is for the last
@@ -765,6 +780,7 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
   t.stages = (int)std::min<uint32_t>(kMaxStages, (kRing - table) / stage);
   // Short groups change accumulators within a chunk: two for each issuer.
   t.log_acc = SETS == 2 ? 1 : 0;
+  t.group_mul = (uint32_t)((uint64_t(1) << 31) / (uint64_t)(a.w.g / 32) + 1);
   t.wstages = (2 << t.log_acc) * (TX == 1 ? 1 : 2) * N + 4 * 64 <= 512 ? 4 : 2;
   t.epi = a.epi;
   t.offsets = a.offsets;
@@ -806,21 +822,15 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k, map, t);
 }
 
-// A unit ends where a group does: 128, 64 or 32 columns.
-template <typename TO, typename H, int TX, int NC, Product P>
-cudaError_t run_narrow(const LinearArgs& a, int N, cudaStream_t s) {
-  return a.w.g % 64 == 0 ? run_unit<TO, H, TX, NC, 8, 4, 2, P>(a, N, s) : run_unit<TO, H, TX, NC, 8, 2, 2, P>(a, N, s);
-}
 bool narrow_groups(const LinearArgs& a) { return a.w.ng > 1 && a.w.g % 128 != 0; }
 
-// Tokens per tile, a multiple of 32: a chunk costs about as much as 500 tokens
-// besides its own (measured: 985 cycles at 64 tokens, 1270 at 192).
-int tokens_per_tile(const LinearArgs& a, int most) {
+// Tokens per tile, a multiple of `step`: a chunk costs about as much as 500 tokens besides its own.
+int tokens_per_tile(const LinearArgs& a, int most, int step) {
   const int64_t tiles_m = (a.w.m + 127) / 128;
   int best = most;
   double cost = 0.0;
-  for (int n = most; n >= 32; n -= 32) {
-    if (n > a.T + 31 && n > 32) continue;
+  for (int n = most; n >= step; n -= step) {
+    if (n > a.T + step - 1 && n > step) continue;
     const int64_t tiles = tiles_m * likely_tiles(a, n);
     const int S = blocks_per_tile(tiles_m * token_tiles(a, n), a.w.nc);
     const double rounds = S > 1 ? 1.0 : (double)((tiles + sm_count() - 1) / sm_count());
@@ -832,11 +842,18 @@ int tokens_per_tile(const LinearArgs& a, int most) {
   }
   return best;
 }
+inline int most_tokens(const LinearArgs& a) { return narrow_groups(a) ? 96 : 192; }      // of 16-bit x
+
+// Short groups: a unit ends where a group does, after 64 or 32 columns.
+template <typename TO, typename H, int TX, int NC, Product P>
+cudaError_t run_narrow(const LinearArgs& a, int N, cudaStream_t s) {
+  return a.w.g % 64 == 0 ? run_unit<TO, H, TX, NC, 8, 4, 2, P>(a, N, s) : run_unit<TO, H, TX, NC, 8, 2, 2, P>(a, N, s);
+}
 
 template <typename TO, Product P>
 cudaError_t run16(const LinearArgs& a, cudaStream_t s) {
-  if (narrow_groups(a)) return run_narrow<TO, TO, 1, 96, P>(a, tokens_per_tile(a, 96), s);
-  return run_unit<TO, TO, 1, 96, 8, 8, 1, P>(a, tokens_per_tile(a, 192), s);
+  const int N = tokens_per_tile(a, most_tokens(a), 32);
+  return narrow_groups(a) ? run_narrow<TO, TO, 1, 96, P>(a, N, s) : run_unit<TO, TO, 1, 96, 8, 8, 1, P>(a, N, s);
 }
 
 template <Product P>
@@ -844,12 +861,8 @@ cudaError_t forward(const LinearArgs& a, cudaStream_t s) {
   switch (a.dtype) {
     case BAKRON_F32: {
       // three terms: few enough tokens for twice the accumulators
-      if (narrow_groups(a)) {
-        const int N = (int)std::min<int64_t>(48, (a.T + 15) / 16 * 16);
-        return run_narrow<float, __nv_bfloat16, 3, 48, P>(a, N, s);
-      }
-      const int N = (int)std::min<int64_t>(64, (a.T + 31) / 32 * 32);
-      return run_unit<float, __nv_bfloat16, 3, 64, 4, 8, 1, P>(a, N, s);
+      if (narrow_groups(a)) return run_narrow<float, __nv_bfloat16, 3, 48, P>(a, tokens_per_tile(a, 48, 16), s);
+      return run_unit<float, __nv_bfloat16, 3, 64, 4, 8, 1, P>(a, tokens_per_tile(a, 64, 32), s);
     }
     case BAKRON_BF16: return run16<__nv_bfloat16, P>(a, s);
     default: return run16<__half, P>(a, s);
