@@ -68,19 +68,18 @@ Kernel forward_kernel(const LinearArgs& a) {
     return a.T * a.w.nc * 128 * 6 <= 160 * 1024 ? kFew : kMid;
   }
   if (a.T <= kFewTokens) return kFew;
-  if (a.T <= kMidTokens / 2) return kMid;
   if (a.T > kMidTokens) return kMany;
-  // Between 33 and 64 tokens: microseconds by what was measured of the two, the
-  // second by the codes, the third by a block's chunks, which cost more when
-  // they hold more groups (bf16, second and third, groups of 128, 64 and 32;
-  // 48 tokens of 8192 x 8192: 29.4 and 25.1, 41.5 and 39.2, 42.0 and 71.2; of 14336 x 4096,
-  // whose 112 tiles leave SMs idle: 25.7 and 23.7, 31.6 and 38.2, 32.3 and 70.9; 64 tokens
-  // of 8192 x 8192: 36.4 and 25.7, 55.3 and 39.8, 55.8 and 72.1).  Fitted to large
-  // layers: of small ones it overrates the second (48 tokens of 4096 x 4096, groups of 64:
-  // 13.7, and it takes the third's 14.9; of 2048 x 8192, groups of 128: 13.2 and 21.9).
+  // Microseconds by what was measured of the two, the second by the codes, the third by the chunks
+  // of a block, which cost more when they hold more groups (bf16, groups of 128, 64 and 32, second and
+  // third; 32 tokens of 8192 x 8192: 24.9 and 21.0, 30.2 and 23.3, 30.1 and 38.4; 48 tokens of 14336 x 4096:
+  // 25.9 and 19.2, 31.4 and 21.2, 31.6 and 38.0; 48 of 2048 x 8192: 13.3 and 13.6, 16.7 and 14.2, 16.7 and
+  // 17.8; 64 of 1000 x 4096: 9.0 and 9.5, 10.4 and 9.9, 10.4 and 11.7).
   const bool narrow = a.w.ng > 1 && a.w.g % 128 != 0;
-  const double mid = 1e-6 * (double)(a.w.mp * a.w.nc * 128) * (narrow ? 0.55 : 0.38) * (a.T <= 48 ? 1.0 : 1.3);
-  const double many = (double)linear_fwd_steps(a) * (!narrow ? 0.57 : a.w.g % 64 == 0 ? 1.05 : 2.05);
+  const double codes = 1e-6 * (double)(a.w.mp * a.w.nc * 128);
+  const double mid = a.T <= 32   ? 4.8 + codes * (narrow ? 0.345 : 0.29)
+                     : a.T <= 48 ? 4.5 + codes * (narrow ? 0.52 : 0.39)
+                                 : 6.0 + codes * (narrow ? 0.65 : 0.48);
+  const double many = 6.2 + (double)linear_fwd_steps(a) * (!narrow ? 0.46 : a.w.g % 64 == 0 ? 0.51 : 0.98);
   return mid < many ? kMid : kMany;
 }
 

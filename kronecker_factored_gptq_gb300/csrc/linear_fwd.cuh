@@ -755,11 +755,12 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   }
 }
 
-// Blocks per tile: as many as there are SMs without a tile, two chunks each at
-// least.
+// Blocks per tile: as many as there are SMs without a tile, two chunks each at least;
+// four at most (clusters of eight such blocks do not all fit at once: 48 tokens of 2048 x 8192
+// 20 us, in clusters of four 13.6).
 int blocks_per_tile(int64_t tiles, int64_t chunks) {
   int S = 1;
-  while (S < 8 && tiles * 2 * S <= sm_count() && chunks >= 4 * S) S *= 2;
+  while (S < 4 && tiles * 2 * S <= sm_count() && chunks >= 4 * S) S *= 2;
   return S;
 }
 

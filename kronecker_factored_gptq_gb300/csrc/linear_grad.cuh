@@ -130,6 +130,12 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   lo = __byte_perm(__float_as_uint(rx - m.x), __float_as_uint(ry - m.y), 0x7632);
 }
 
+// Tokens that a tile's products take: an expert's last tile is mostly not full.
+template <Product P>
+__device__ __forceinline__ int tokens_in(const Place& at, int N) {
+  return P == kExperts ? min(N, ((int)(at.end - at.t0) + 31) & ~31) : N;
+}
+
 struct Bars {
   unsigned long long full[kMaxStages], empty[kMaxStages];
   unsigned long long acc_full[2], acc_empty[2], done;
@@ -400,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer: the warp waits together, one lane issues
-    const uint32_t idesc = idesc_f16<H>(a.N);
+    uint32_t idesc = idesc_f16<H>(a.N);
     const uint64_t desc_a0 = desc_sw128(ring), desc_b0 = desc_sw128(ring + TW * kABytes);
     const uint32_t stage16 = stage_bytes >> 4, plane16 = plane_b >> 4;
     const uint32_t full = smem_u32(bars.full), empty = smem_u32(bars.empty);
@@ -409,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool go = true;
     Ring rg;
     for (int64_t tile = k.tile; tile < tiles.tiles && go; tile += k.step) {
+      if constexpr (P == kExperts) idesc = idesc_f16<H>(tokens_in<P>(tiles.at(tile), a.N));
       for (int i = 0; i < steps; ++i) {
         const bool begin = i % kChain == 0, end = i % kChain == kChain - 1 || i == steps - 1;
         if (begin) {
@@ -461,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Place at = tiles.at(tile);
       const int64_t row = (int64_t)at.m * 128 + quarter * 32 + lane;
       const int64_t t0 = at.t0;
+      const int N = tokens_in<P>(at, a.N);
       TO* y = static_cast<TO*>(a.y) + t0 * a.w.n + row;
       float acc[kWhole ? 1 : NC];
       if constexpr (!kWhole) {
@@ -474,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after_sync();
         const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (u_all & 1) * acc_cols;
         if constexpr (kWhole) {
-          for (int g = 0; g < a.N; g += 32) {
+          for (int g = 0; g < N; g += 32) {
             float v[32];
             tmem_ld32(ta + (uint32_t)g, v);
             if (units > 1) {
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int g = 0; g < NC / 16; ++g) {
-            if (g * 16 < a.N) {
+            if (g * 16 < N) {
               uint32_t v[16], c[16];
               tmem_ld16(ta + g * 16, v);
               tmem_ld16(ta + (uint32_t)a.N + g * 16, c);
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!kWhole) {
 #pragma unroll
         for (int t = 0; t < NC; ++t) {
-          if (t < a.N) {
+          if (t < N) {
             if (S > 1) part[t * 128 + quarter * 32 + lane] = acc[t];
             else if (ok && row < a.w.n && t0 + t < at.end) y[(int64_t)t * a.w.n] = from_float<TO>(acc[t] * range_out);
           }
