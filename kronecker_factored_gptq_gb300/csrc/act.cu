@@ -7,7 +7,10 @@
 // registers; kRows rows are loaded before the first is used.  A block's column sums are
 // joined in shared memory and go to its row of the workspace, which a second launch adds up in
 // a fixed order (no atomics: the bits do not depend on the run); with one block of rows they
-// are the result.
+// are the result.  The activation is chosen once for a thread's rows at hand, not per value.
+// Measured, gated silu of 2048 x 14336 bf16: 31 us (the bytes at 6.80 TB/s: 26), its gradient 48 (43); 37 x 1111
+// fp32 gelu 2.6 and with the bias's gradient 3.0 us: launch and latency.  Rows that do not begin on 16 bytes go
+// one element a thread.
 #include <algorithm>
 
 #include "act.cuh"

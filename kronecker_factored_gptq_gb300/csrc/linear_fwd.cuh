@@ -12,34 +12,40 @@
 //
 // The sum over a group (or over 128 columns of a longer one) goes into a fresh
 // accumulator, which the epilogue warps read, scale in fp32 and add to their
-// registers while the tensor core fills the other one: no rounding of the weights,
+// registers while the tensor core fills others: no rounding of the weights,
 // and no long chain of the tensor core's additions, which cut off instead of
 // rounding.  fp32 activations are three exact bf16 terms; the products of the two
 // small ones have an accumulator of their own.
 //
+// The same kernel runs bakron_linear_act (its epilogue, see finish()) and bakron_experts, whose
+// tiles are tokens of one expert each: a table of the experts' tiles is made from their offsets
+// by every block (expert_tiles), so that nothing about them need be known on the host.
+//
 // One block per SM, which takes output tiles in turn (or, when there are few, a
 // part of the columns of one, joined over a cluster through distributed shared memory):
 //   warp 0: TMA producer of the activations;
-//   warp 1: issues the tcgen05.mma (M 128, K 16 each);
+//   warps 1 and 3: issue the tcgen05.mma (M 128, K 16 each), 128-column chunks in turn;
 //   warp 2: allocates and frees TMEM;
 //   warps 4-11: weights, two groups of four (32 rows each) that take the
-//     128-column chunks in turn, codes copied asynchronously kAhead chunks ahead;
-//   the rest: epilogue, each 32 TMEM lanes x NC columns in fp32 registers.
-// A stage is a whole chunk, of weights (64 TMEM columns) and of activations: what the
-// issuing warp waits and commits per stage costs it some 400 cycles, so stages of
-// half a chunk kept the tensor core waiting for it.  TMEM: two accumulators of N
-// columns, then four stages of weights (two where N is above 128).
+//     chunks in turn, codes copied asynchronously kSlots - 1 of their chunks ahead;
+//   the rest: epilogue, each 32 TMEM lanes x NC columns in fp32 registers.  Where units are short, two
+//   sets of them take the units in turn and add their sums at the end of a tile.
+// Activations come by whole chunks, weights pass on by halves of one (32 TMEM columns), so that the
+// second half is unpacked while the first is multiplied.  TMEM: an accumulator of N columns for each
+// issuer (two of them for short groups), then four stages of weights (two where N is above 128, or 64).
 //
-// Measured: 2048 tokens of 8192 x 8192 bf16 in 206 us in a graph of one weight (1.34
-// PFLOP/s) and 215 among calls on several; 48 tokens 25 us; fp32, 1024 tokens of 4096 x 4096 103 us
-// and 2048 of 8192 x 8192 648 us (three products: 1.27 PFLOP/s).  A
-// chunk takes 1270 cycles at 192 tokens, of which the tensor core works 768: the
-// issuing warp's waits, one after the other, are the rest; few tokens do not make it
-// shorter than 985, what eight warps need to turn a chunk's codes into
-// operands.  With groups of 32 columns an accumulator goes to and fro every 32
-// columns, 650 cycles each (1024 tokens of 4096 x 4096: 102 us, groups of 128: 44).  Tried and
-// slower: one wait of three lanes on the three barriers (208 -> 260 us), the scales
-// copied ahead to shared memory (208 -> 234).
+// Measured: 2048 tokens of 8192 x 8192 bf16 in 174 us in a graph of two weights (1.58 PFLOP/s, 1.62 at
+// 4096 tokens); 48 tokens 22 us, of 14336 x 4096 19; fp32, 1024 tokens of 4096 x 4096 84 us and 2048 of
+// 8192 x 8192 507 us (three products: 1.63 PFLOP/s); experts, 4096 rows over 8 of 28672 x 4096 763 us (1.26
+// PFLOP/s: an expert's last tile is mostly not full), 256 rows over 32 of 1408 x 1024 33 us.  A chunk takes
+// 1040 cycles at 192 tokens, of which the tensor core works 816 (at cuBLAS's rate 950): with one issuing
+// warp, whose waits and instructions follow one another, it took 1270 (206 us), with weights passed on
+// by whole chunks 1100.  Few tokens do not make a chunk shorter than about 1000: a warp's instructions follow
+// one another, five or six cycles each, the epilogue's of a unit some 100 and the weights' of a chunk
+// some 300; twice as many weights warps changed nothing, more instructions in the epilogue (scales
+// prefetched into L2, four units ahead, copied to shared memory) made it slower.  Short groups: 2048 tokens
+// of 8192 x 8192 369 us in groups of 64; 1024 of 4096 x 4096 107 us in groups of 32, 64 in groups of 64, 38 in
+// groups of 128.
 //
 // Every mbarrier wait is bounded (clock64 budget); a block whose wait runs
 // out records BAKRON_ERR_TIMEOUT in the device's status word, stops issuing,
@@ -133,7 +139,8 @@ constexpr int kFinish = 16;
 // bakron_linear_act's epilogue for a warp's sums, 32 rows (a lane each) x n tokens, that lie in
 // TMEM: kFinish tokens at a time in a loop whose code stays small.  (Unrolled over all 96 tokens that a
 // thread's registers hold, the code did not fit the instruction cache: 2048 tokens of 8192 x 8192
-// 344 us with an activation alone, 500 with residuals, loaded one by one.)  The residuals of the next ones
+// 344 us with an activation alone, 500 with residuals, loaded one by one; now 200 and 216, the product
+// alone 174: 6000 and 10000 cycles a tile in which the tensor core mostly waits.)  The residuals of the next ones
 // are on their way while these are finished.
 template <typename TO>
 __device__ __forceinline__ void finish(const FwdArgs& a, uint32_t ta, int n, int64_t y0, int64_t row) {
@@ -224,7 +231,7 @@ __device__ __forceinline__ void role_end(bool epilogue, int warpgroup = 0) {
 
 // One chunk of codes at a time: 32 rows (a lane each) x 128 columns.
 template <typename H, Product P>
-__device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, const Tiles<P>& tiles, Bars& bars,
+__device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, const Tiles<P, FwdArgs>& tiles, Bars& bars,
                                         uint32_t tmem_a, uint32_t codes, int group, int quarter, int lane) {
   const PackedView& w = a.w;
   const bool narrow = w.ng > 1 && w.g % 128 != 0;
@@ -243,7 +250,7 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, const T
   const int n = k.c1 - k.c0;
   // the tile's row block and expert
   int m_ahead = 0, e_ahead = 0;
-  if (k.tile < tiles.tiles) {
+  if (k.tile < tiles.count()) {
     const Place p = tiles.at(k.tile);
     m_ahead = p.m;
     e_ahead = p.e;
@@ -251,11 +258,11 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, const T
   int m_now = m_ahead, e_now = e_ahead;
   auto settle = [&](int64_t& tile, int& c, int& m, int& e) {
     if (c < k.c1) return;
-    while (c >= k.c1 && tile < tiles.tiles) {
+    while (c >= k.c1 && tile < tiles.count()) {
       c -= n;
       tile += k.step;
     }
-    if (P == kExperts && tile >= tiles.tiles) return;
+    if (P == kExperts && tile >= tiles.count()) return;
     const Place p = tiles.at(tile);
     m = p.m;
     e = p.e;
@@ -264,7 +271,7 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, const T
   settle(tile_now, c_now, m_now, e_now);
   uint32_t fill = 0, read = 0;
   auto copy = [&]() {
-    if (tile_ahead < tiles.tiles) {
+    if (tile_ahead < tiles.count()) {
       const int64_t block = (int64_t)m_ahead * 16 + quarter * 4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -283,7 +290,7 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, const T
   };
   // the row's zero points of a chunk, a byte per 32 columns
   auto zeros = [&](int64_t tile, int c, int m, int e) -> uint32_t {
-    if (w.zero == nullptr || tile >= tiles.tiles) return 0u;
+    if (w.zero == nullptr || tile >= tiles.count()) return 0u;
     const int64_t row = (int64_t)m * 128 + quarter * 32 + lane;
     if (row >= w.mp) return 0u;
     const uint8_t* p = w.zero + grid_row(w, e, row);
@@ -299,7 +306,7 @@ __device__ __forceinline__ void weights(const FwdArgs& a, const Work& k, const T
   uint32_t seq = (uint32_t)group;      // chunk of the block
   const uint32_t last_stage = (uint32_t)a.wstages - 1;
   const int log_stages = a.wstages == 4 ? 2 : 1;
-  while (tile_now < tiles.tiles) {
+  while (tile_now < tiles.count()) {
     copy();
     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
     __syncwarp();
@@ -422,14 +429,14 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), tmem_a = tmem + (2u << a.log_acc) * acc_cols;
   grid_dep_wait();
   grid_dep_launch();
-  Tiles<P> tiles = {a.tiles, a.tiles_m, a.N, a.T, nullptr, nullptr, 0};
+  Tiles<P, FwdArgs> tiles = {a, 0, nullptr, nullptr, 0};
   if constexpr (P == kExperts) {
     __shared__ int sums[2][kTileThreads / 32];
     int* table = reinterpret_cast<int*>(dsm + (ring - base_raw) + (uint32_t)a.stages * stage_bytes + kCodes);
     tiles.E = (int)a.w.count;
     tiles.bounds = table;
     tiles.first = table + tiles.E + 1;
-    tiles.tiles = (int64_t)a.tiles_m * expert_tiles(a.offsets, tiles.E, (int)a.T, a.N, table, table + tiles.E + 1, sums);
+    tiles.own = (int64_t)a.tiles_m * expert_tiles(a.offsets, tiles.E, (int)a.T, a.N, table, table + tiles.E + 1, sums);
   }
 
   if (warp < 4) {
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       int64_t issued = 0;
       Ring rg;
       bool go = true;
-      for (int64_t tile = k.tile; tile < tiles.tiles && go; tile += k.step) {
+      for (int64_t tile = k.tile; tile < tiles.count() && go; tile += k.step) {
         const int64_t t0 = tiles.at(tile).t0;
         for (int c = k.c0; c < k.c1; ++c) {
           go = rg.first || wait_or_abort(empty + 8u * (uint32_t)rg.s, rg.parity ^ 1u, &bars.abort, a.status);
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       uint32_t u = 0;                         // units begun
       const uint32_t last_stage = (uint32_t)a.wstages - 1, last_acc = (1u << a.log_acc) - 1;
       const int log_stages = a.wstages == 4 ? 2 : 1;
-      const int64_t chunks = k.tile < tiles.tiles ? ((tiles.tiles - 1 - k.tile) / k.step + 1) * (k.c1 - k.c0) : 0;
+      const int64_t chunks = k.tile < tiles.count() ? ((tiles.count() - 1 - k.tile) / k.step + 1) * (k.c1 - k.c0) : 0;
       uint32_t turns = 0;
       Ring rg;
       rg.advance(me, a.stages);
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
     const uint32_t af_ep = af + 8u * (uint32_t)set, ae_ep = ae + 8u * (uint32_t)set;
     static_assert(SETS == 2 ? KU < 8 : KU == 8);
     bool ok = true;
-    for (int64_t tile = k.tile; tile < tiles.tiles && ok; tile += k.step) {
+    for (int64_t tile = k.tile; tile < tiles.count() && ok; tile += k.step) {
       const Place at = tiles.at(tile);
       float acc[NC];
 #pragma unroll
@@ -741,7 +748,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
     cluster.sync();
     const int r = threadIdx.x & 127;
     Place at = {};
-    if (k.tile < tiles.tiles) at = tiles.at(k.tile);
+    if (k.tile < tiles.count()) at = tiles.at(k.tile);
     const int64_t row = (int64_t)at.m * 128 + r;
     for (int c = rank + S * (threadIdx.x >> 7); c < a.N; c += S * (THREADS / 128)) {
       if (row >= a.w.m || at.t0 + c >= at.end) continue;

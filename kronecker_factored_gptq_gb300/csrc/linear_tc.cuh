@@ -98,27 +98,27 @@ static_assert(kTileThreads * kTileBounds > kMaxGroupedExperts);
 
 // The tiles of a product.  Experts: `bounds` are the boundaries of their rows, `first`
 // their first token tiles (e = 0 .. E, in shared memory).
-template <Product P>
+template <Product P, typename Args>
 struct Tiles {
-  int64_t tiles;        // of the output
-  int tiles_m, N;
-  int64_t T;
+  const Args& a;        // tiles (not for experts), tiles_m, N, T
+  int64_t own;          // tiles of the experts
   const int* bounds;
   const int* first;
   int E;
 
+  __device__ __forceinline__ int64_t count() const { return P == kExperts ? own : a.tiles; }
   __device__ __forceinline__ Place at(int64_t tile) const {
     if constexpr (P != kExperts) {
-      return Place{(int)(tile % tiles_m), 0, tile / tiles_m * N, T};
+      return Place{(int)(tile % a.tiles_m), 0, tile / a.tiles_m * a.N, a.T};
     } else {
-      const int tt = (int)(tile / tiles_m);
+      const int tt = (int)(tile / a.tiles_m);
       int e = 0, hi = E;                     // the last expert whose first tile is at most tt
       while (hi - e > 1) {
         const int mid = (e + hi) >> 1;
         if (first[mid] <= tt) e = mid;
         else hi = mid;
       }
-      return Place{(int)(tile % tiles_m), e, bounds[e] + (int64_t)(tt - first[e]) * N, bounds[e + 1]};
+      return Place{(int)(tile % a.tiles_m), e, bounds[e] + (int64_t)(tt - first[e]) * a.N, bounds[e + 1]};
     }
   }
 };

@@ -8,11 +8,17 @@
 // (expert, warp); then each warp walks through its run again, 32 choices at a time, and a choice's
 // place is its expert's next one plus the number of lower lanes with the same expert.  Only
 // whole numbers are added, and every place follows from the order of choice, so it is stable
-// and the same in every run.  What bounds it is latency.
+// and the same in every run.  What bounds it is the instructions of the warps' walks, some 200 a step of
+// 32 choices (one ballot a bit of the expert's number instead of the match was no faster): 64 choices 2.9 us,
+// 49152 of 64 experts 11 us in a cluster of eight blocks, 16 in one of four, 50 in one block.
 //
 // The others move rows and are bound by their bytes: a warp takes a part of a token's row and
 // every row of the token's choices, so that x (dy) is read once, whatever k.  They go through
-// choice order, in which the reads of x and the writes of y are consecutive.
+// choice order, in which the reads of x and the writes of y are consecutive.  Four blocks an SM, 64 registers a
+// thread, keep enough bytes in flight; with 128 and more combine took 93 to 123 us instead of 38.
+// Measured, bf16 rows of 4096 (the bytes at 6.80 TB/s): dispatch of 8192 tokens to 6 experts, 5 % padding, 71 us
+// (66); combine of 8192 x 2 38 us (30), its gradient 53 us (49).  Rows that do not begin on 16 bytes take pieces of
+// 8, 4 or 2 bytes.
 #include <cooperative_groups.h>
 
 #include <algorithm>
