@@ -10,7 +10,7 @@
 // are the result.  The activation is chosen once for a thread's rows at hand, not per value.
 // Measured, gated silu of 2048 x 14336 bf16: 31 us (the bytes at 6.80 TB/s: 26), its gradient 48 (43); 37 x 1111
 // fp32 gelu 2.6 and with the bias's gradient 3.0 us: launch and latency.  Rows that do not begin on 16 bytes go
-// one element a thread.
+// by pieces of 8, 4 or 2 bytes (2048 x 6144 bf16 silu 12 us; 6148, 6146 and 6145 columns 13, 16 and 24).
 #include <algorithm>
 
 #include "act.cuh"
@@ -34,7 +34,10 @@ struct ActArgs {
 template <typename TX, int V, bool kGated, bool kGrad, bool kSums>
 __global__ void __launch_bounds__(kThreads, kSums ? 3 : 4) act_kernel(const __grid_constant__ ActArgs a) {
   using W = Piece<TX, V * (int)sizeof(TX)>;
-  constexpr int kRows = kGated ? 2 : 4;
+  // rows at hand: more of narrow pieces (2048 x 6146 bf16 24 us with four, 16), but of single elements whose
+  // columns are summed (2048 x 6145: 38 us with eight, 33)
+  constexpr int VB = V * (int)sizeof(TX);
+  constexpr int kRows = VB == 16 ? (kGated ? 2 : 4) : VB == 8 || (V == 1 && kSums) ? 4 : 8;
   constexpr int NS = kSums ? (kGated ? 2 : 1) * V : 1;
   const int tx = threadIdx.x & (a.cx - 1), ty = threadIdx.x / a.cx, ry = kThreads / a.cx;
   const int64_t col = ((int64_t)blockIdx.x * a.cx + tx) * V;
@@ -190,9 +193,16 @@ cudaError_t by_gate(ActArgs& a, bool gated, bool grad, float* dbias, cudaStream_
 
 template <typename TX>
 cudaError_t by_vector(ActArgs& a, bool gated, bool grad, float* dbias, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(TX);
-  const bool whole = a.m % V == 0 && aligned_to(a.z, 16) && aligned_to(a.out, 16) && aligned_to(a.dy, 16);
-  return whole ? by_gate<TX, V>(a, gated, grad, dbias, s) : by_gate<TX, 1>(a, gated, grad, dbias, s);
+  // the widest pieces that rows and addresses allow
+  const uintptr_t all = (uintptr_t)(a.m * (int64_t)sizeof(TX)) | reinterpret_cast<uintptr_t>(a.z) |
+                        reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.dy);
+  constexpr int E = (int)sizeof(TX);
+  if (all % 16 == 0) return by_gate<TX, 16 / E>(a, gated, grad, dbias, s);
+  if (all % 8 == 0) return by_gate<TX, 8 / E>(a, gated, grad, dbias, s);
+  if constexpr (E == 2) {
+    if (all % 4 == 0) return by_gate<TX, 2>(a, gated, grad, dbias, s);
+  }
+  return by_gate<TX, 1>(a, gated, grad, dbias, s);
 }
 
 cudaError_t run_act(ActArgs& a, int dtype, bool gated, bool grad, float* dbias, cudaStream_t s) {
@@ -212,7 +222,7 @@ bool act_args_ok(int64_t T, int64_t m, int dtype, int act, int gated) {
 size_t act_grad_bytes(int64_t T, int64_t columns) {
   int64_t blocks = 0;
   for (int64_t m : {columns, (columns + 1) / 2})
-    for (int V : {1, 4, 8}) blocks = std::max(blocks, act_grid(T, m, V).blocks);
+    for (int V : {1, 2, 4, 8}) blocks = std::max(blocks, act_grid(T, m, V).blocks);
   return blocks > 1 ? (size_t)(blocks * columns) * sizeof(float) : 0;
 }
 

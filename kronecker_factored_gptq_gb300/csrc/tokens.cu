@@ -213,8 +213,12 @@ __device__ __forceinline__ Piece<TX, VB> load(const void* base, int64_t i) {
 }
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 4;                     // of a lane at a time
-constexpr int kWide = 2;                     // where several rows are at hand
+// Pieces of a lane at a time: 64 bytes where they are whole, and 32 where several rows are at hand;
+// more of the narrow ones (rows of 4097 bf16: combine of 4096 x 2 55 us, with two 91; rows of 4096 22).
+template <int VB>
+constexpr int kVecs = VB == 16 ? 4 : 8;
+template <int VB>
+constexpr int kWideOf = VB == 16 ? 2 : VB == 8 ? 4 : 8;
 
 // Unit u of a.parts a token: the token (division of 32 bits where the units fit).
 __device__ __forceinline__ int64_t token_of(const RowArgs& a, int64_t u) {
@@ -239,20 +243,20 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
   const int64_t units = a.T * a.parts;
   for (int64_t u = blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5); u < units;
        u += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int64_t t = token_of(a, u), v0 = (u - t * a.parts) * (32 * kVecs) + lane;
+    const int64_t t = token_of(a, u), v0 = (u - t * a.parts) * (32 * kVecs<VB>) + lane;
     int at;
     float w;
     load_choices(a, t, lane, at, w);
-    P x[kVecs];
+    P x[kVecs<VB>];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
+    for (int i = 0; i < kVecs<VB>; ++i)
       if (v0 + 32 * i < a.vecs) x[i] = load<TX, VB>(a.in, t * a.vecs + v0 + 32 * i);
     for (int j = 0; j < a.k; ++j) {
       const int64_t r = __shfl_sync(0xffffffffu, at, j);
       const float f = kWeight ? __shfl_sync(0xffffffffu, w, j) : 1.f;
       if (r < 0) continue;
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
+      for (int i = 0; i < kVecs<VB>; ++i) {
         if (v0 + 32 * i >= a.vecs) continue;
         P o = x[i];
         if constexpr (kWeight) {
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const __grid_constan
 template <typename TX, int VB>
 __global__ void __launch_bounds__(kThreads, 4) combine_kernel(const __grid_constant__ RowArgs a) {
   using P = Piece<TX, VB>;
-  constexpr int kAtOnce = 2;
+  constexpr int kAtOnce = 2, kWide = kWideOf<VB>;
   const int lane = threadIdx.x & 31;
   const int64_t units = a.T * a.parts, step = (int64_t)gridDim.x * (kThreads / 32);
   int64_t u = blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5);
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 4) combine_kernel(const __grid_const
 template <typename TX, int VB, bool kBlock>
 __global__ void __launch_bounds__(kThreads, 4) combine_grad_kernel(const __grid_constant__ RowArgs a) {
   using P = Piece<TX, VB>;
-  constexpr int kAtOnce = 2;
+  constexpr int kAtOnce = 2, kWide = kWideOf<VB>;
   __shared__ float red[2][kAtOnce][kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t step = kBlock ? gridDim.x : (int64_t)gridDim.x * warps;
@@ -414,7 +418,7 @@ enum class Op { kDispatch, kCombine, kCombineGrad };
 template <typename TX, int VB>
 cudaError_t launch_rows(RowArgs& a, Op op, cudaStream_t s) {
   a.vecs = a.d * (int64_t)sizeof(TX) / VB;
-  const int per = 32 * (op == Op::kCombine ? kWide : kVecs);
+  const int per = 32 * (op == Op::kCombine ? kWideOf<VB> : kVecs<VB>);
   a.parts = (a.vecs + per - 1) / per;
   a.narrow = a.T * a.parts < (int64_t(1) << 32);
   // dispatch_kernel's warps take a unit or few, the others loop, with the next choices on their way
