@@ -280,6 +280,41 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _side(stream):
+    """``stream`` as torch knows it when it is another than the current one, else None."""
+    _check_stream(stream)
+    torch = _torch()
+    if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(_device()):
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor that a call on ``stream`` (None: the current one) writes.  Memory from the
+    current stream's pool may still be read and written by work that is queued there, and would
+    be handed out again in that stream's order; so another stream gets memory of its own
+    pool, which once let go also waits for what the current stream has queued by then."""
+    torch = _torch()
+    side = None if stream is None else _side(stream)
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if t.is_cuda:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _keep(stream, *tensors):
+    """Tells the allocator that a call on ``stream`` uses the tensors (or None): let go after the
+    call, their memory is not handed out before the call has run."""
+    side = _side(stream)
+    if side is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(side)
+
+
 def workspace_size(m, n, opts=None):
     b = ctypes.c_size_t(0)
     _check(lib().bakron_workspace_size(m, n, ctypes.byref(opts) if opts else None, ctypes.byref(b)),
@@ -299,7 +334,7 @@ def bakron_plan_init(m, n, plan=None, stream=None):
     torch = _torch()
     nb = plan_size(m, n)
     if plan is None:
-        plan = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        plan = _empty(nb, torch.uint8, "cuda", stream)
     elif plan.numel() * plan.element_size() < nb:
         raise ValueError("plan buffer too small: need %d bytes" % nb)
     _check(lib().bakron_plan_init(m, n, ctypes.c_void_p(plan.data_ptr()), nb, _stream(stream)),
@@ -313,7 +348,7 @@ def prepare_workspace_size(n, m):
     return b.value
 
 
-def _ws(nbytes, workspace):
+def _ws(nbytes, workspace, stream):
     torch = _torch()
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
@@ -323,14 +358,14 @@ def _ws(nbytes, workspace):
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError("workspace too small: need %d bytes" % nbytes)
         return workspace
-    return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    return _empty(nbytes, torch.uint8, "cuda", stream)
 
 
 def bakron_rowscale(W, qmax, out=None, stream=None):
     torch = _torch()
     m, n = W.shape
     if out is None:
-        out = torch.empty(m, dtype=torch.float32, device=W.device)
+        out = _empty(m, torch.float32, W.device, stream)
     _check(lib().bakron_rowscale(_dev(W, torch.float32, (m, n), "W"), m, n, int(qmax),
                                  _dev(out, torch.float32, (m,), "scale"), _stream(stream)),
            "bakron_rowscale")
@@ -346,12 +381,12 @@ def bakron_prepare(A, damp_A, B=None, damp_B=0.0, want_L=False, workspace=None, 
     if out is not None:
         UA, UB = out
     else:
-        UA = torch.empty((n, n), dtype=torch.float32, device=A.device)
-        UB = None if B is None else torch.empty((m, m), dtype=torch.float32, device=A.device)
-    LA = torch.empty_like(UA) if want_L else None
-    LB = torch.empty_like(UB) if (want_L and B is not None) else None
+        UA = _empty((n, n), torch.float32, A.device, stream)
+        UB = None if B is None else _empty((m, m), torch.float32, A.device, stream)
+    LA = _empty((n, n), torch.float32, A.device, stream) if want_L else None
+    LB = _empty((m, m), torch.float32, A.device, stream) if (want_L and B is not None) else None
     nb = prepare_workspace_size(n, m)
-    ws = _ws(nb, workspace)
+    ws = _ws(nb, workspace, stream)
     info = (ctypes.c_int64 * 2)(-1, -1)
     st = lib().bakron_prepare(
         _dev(A, torch.float32, (n, n), "A"), n, float(damp_A),
@@ -375,13 +410,13 @@ def bakron_quantize(W, UA, UB, scale, qmin, qmax, want_preround=False, opts=None
     torch = _torch()
     m, n = W.shape
     if out is None:
-        V = torch.empty((m, n), dtype=torch.float32, device=W.device)
-        codes = torch.empty((m, n), dtype=torch.int8, device=W.device)
+        V = _empty((m, n), torch.float32, W.device, stream)
+        codes = _empty((m, n), torch.int8, W.device, stream)
     else:
         V, codes = out
-    pre = torch.empty((m, n), dtype=torch.float32, device=W.device) if want_preround else None
+    pre = _empty((m, n), torch.float32, W.device, stream) if want_preround else None
     nb = workspace_size(m, n, opts)
-    ws = _ws(nb, workspace)
+    ws = _ws(nb, workspace, stream)
     st = lib().bakron_quantize(
         _dev(W, torch.float32, (m, n), "W"), m, n,
         _dev(UA, torch.float32, (n, n), "UA"),
@@ -410,8 +445,8 @@ def bakron_grid_params(W, bits, asymmetric=False, group=None, stream=None):
     torch = _torch()
     m, n = W.shape
     ng = grid_groups(n, group)
-    scale = torch.empty((m, ng), dtype=torch.float32, device=W.device)
-    zero = torch.empty((m, ng), dtype=torch.float32, device=W.device)
+    scale = _empty((m, ng), torch.float32, W.device, stream)
+    zero = _empty((m, ng), torch.float32, W.device, stream)
     qmin, qmax = ctypes.c_int(0), ctypes.c_int(0)
     st = lib().bakron_grid_params(_dev(W, torch.float32, (m, n), "W"), m, n, int(bits),
                                   1 if asymmetric else 0, int(group or 0),
@@ -429,13 +464,13 @@ def bakron_quantize_grid(W, UA, UB, scale, zero, group, qmin, qmax, want_preroun
     m, n = W.shape
     ng = grid_groups(n, group)
     if out is None:
-        V = torch.empty((m, n), dtype=torch.float32, device=W.device)
-        codes = torch.empty((m, n), dtype=torch.int8, device=W.device)
+        V = _empty((m, n), torch.float32, W.device, stream)
+        codes = _empty((m, n), torch.int8, W.device, stream)
     else:
         V, codes = out
-    pre = torch.empty((m, n), dtype=torch.float32, device=W.device) if want_preround else None
+    pre = _empty((m, n), torch.float32, W.device, stream) if want_preround else None
     nb = workspace_size(m, n, opts)
-    ws = _ws(nb, workspace)
+    ws = _ws(nb, workspace, stream)
     st = lib().bakron_quantize_grid(
         _dev(W, torch.float32, (m, n), "W"), m, n, _dev(UA, torch.float32, (n, n), "UA"),
         None if UB is None else _dev(UB, torch.float32, (m, m), "UB"),
@@ -463,8 +498,8 @@ def bakron_quantize_batch(problems, opts=None, workspace=None, stream=None, outs
         m, n = W.shape
         ng = grid_groups(n, pr.get("group"))
         if outs is None:
-            V = torch.empty((m, n), dtype=torch.float32, device=W.device)
-            C = torch.empty((m, n), dtype=torch.int8, device=W.device)
+            V = _empty((m, n), torch.float32, W.device, stream)
+            C = _empty((m, n), torch.int8, W.device, stream)
         else:
             V, C = outs[k]
         UB, zero = pr.get("UB"), pr.get("zero")
@@ -481,7 +516,7 @@ def bakron_quantize_batch(problems, opts=None, workspace=None, stream=None, outs
     o = ctypes.byref(opts) if opts is not None else None
     _check(lib().bakron_batch_workspace_size(len(problems), arr, o, ctypes.byref(size)),
            "bakron_batch_workspace_size")
-    ws = _ws(size.value, workspace)
+    ws = _ws(size.value, workspace, stream)
     st = lib().bakron_quantize_batch(len(problems), arr, o, ctypes.c_void_p(ws.data_ptr()),
                                      size.value, _stream(stream))
     if st != OK:
@@ -496,11 +531,11 @@ def bakron_quantize_antidiag(W, UA, UB, scale, qmin, qmax, guide_codes=None, gui
     """Returns (V, codes, preround-or-None, overrides)."""
     torch = _torch()
     m, n = W.shape
-    V = torch.empty((m, n), dtype=torch.float32, device=W.device)
-    codes = torch.empty((m, n), dtype=torch.int8, device=W.device)
-    pre = torch.empty((m, n), dtype=torch.float32, device=W.device) if want_preround else None
+    V = _empty((m, n), torch.float32, W.device, stream)
+    codes = _empty((m, n), torch.int8, W.device, stream)
+    pre = _empty((m, n), torch.float32, W.device, stream) if want_preround else None
     nb = workspace_size(m, n, opts)
-    ws = _ws(nb, workspace)
+    ws = _ws(nb, workspace, stream)
     over = ctypes.c_int64(0)
     st = lib().bakron_quantize_antidiag(
         _dev(W, torch.float32, (m, n), "W"), m, n,
@@ -527,8 +562,8 @@ def bakron_quantize_noalloc(W, UA, UB, scale, qmin, qmax, out=None, stream=None)
     torch = _torch()
     m, n = W.shape
     if out is None:
-        V = torch.empty((m, n), dtype=torch.float32, device=W.device)
-        codes = torch.empty((m, n), dtype=torch.int8, device=W.device)
+        V = _empty((m, n), torch.float32, W.device, stream)
+        codes = _empty((m, n), torch.int8, W.device, stream)
     else:
         V, codes = out
     st = lib().bakron_quantize_noalloc(
@@ -558,12 +593,12 @@ def bakron_factors(X=None, G=None, mode=FACTORS_KFAC, want_A=True, want_B=True, 
     N = ref.shape[0]
     n = 0 if X is None else X.shape[1]
     m = 0 if G is None else G.shape[1]
-    A = torch.empty((n, n), dtype=torch.float32, device=ref.device) if (want_A and X is not None) else None
-    B = torch.empty((m, m), dtype=torch.float32, device=ref.device) if (want_B and G is not None) else None
+    A = _empty((n, n), torch.float32, ref.device, stream) if (want_A and X is not None) else None
+    B = _empty((m, m), torch.float32, ref.device, stream) if (want_B and G is not None) else None
     size = ctypes.c_size_t(0)
     _check(lib().bakron_factors_workspace_size(N, n, m, ctypes.byref(size)),
            "bakron_factors_workspace_size")
-    ws = _ws(size.value, workspace)
+    ws = _ws(size.value, workspace, stream)
     st = lib().bakron_factors(
         None if X is None else _dev(X, torch.float32, (N, n), "X"), N, n,
         None if G is None else _dev(G, torch.float32, (N, m), "G"), m, int(mode),
@@ -582,10 +617,10 @@ def bakron_factors(X=None, G=None, mode=FACTORS_KFAC, want_A=True, want_B=True, 
 # asked for its handle only.
 #
 # These calls only enqueue (bakron_pack and bakron_unpack excepted) on
-# ``stream``, or on the current stream.  Tensors allocated here belong to the
-# current stream as far as PyTorch's allocator knows; a caller who passes
-# another stream passes ``out`` and ``workspace`` too, or keeps the two
-# streams ordered.
+# ``stream``, or on the current stream.  On another stream than the current one the
+# caller orders the two where one reads what the other writes, as with any work on two
+# streams; the memory is looked after here: what a call allocates is of its stream
+# (_empty), and what it was given may be let go while it still runs (_keep).
 
 
 _DTYPES = {}
@@ -637,9 +672,9 @@ def _same(t, like, shape, name):
     return t.data_ptr()
 
 
-def _out(out, like, shape, name):
+def _out(out, like, shape, name, stream):
     if out is None:
-        return _torch().empty(shape, dtype=like.dtype, device=like.device)
+        return _empty(shape, like.dtype, like.device, stream)
     _same(out, like, shape, name)
     return out
 
@@ -700,7 +735,7 @@ def bakron_pack(codes, scale, qmin, qmax, zero=None, group=None, stream=None):
     args = (_dev(codes, torch.int8, lead + (n,), "codes"), _dev(scale, torch.float32, shape, "scale"),
             None if zero is None else _dev(zero, torch.float32, zero.shape if zero.shape == lead and ng == 1
                                            else lead + (ng,), "zero"))
-    data = torch.empty(size.value, dtype=torch.uint8, device=codes.device)
+    data = _empty(size.value, torch.uint8, codes.device, stream)
     _check(lib().bakron_pack(*args, count, m, n, int(group or 0), int(qmin), int(qmax),
                              ctypes.c_void_p(data.data_ptr()), size.value, _stream(stream)), "bakron_pack")
     return PackedWeight(data, count, m, n, int(group or 0), int(qmin), zero is not None)
@@ -710,7 +745,7 @@ def bakron_unpack(w, stream=None):
     """V (float32) of a PackedWeight: the values the solver returned."""
     torch = _torch()
     w._here()
-    V = torch.empty((w.count, w.m, w.n), dtype=torch.float32, device=w.device)
+    V = _empty((w.count, w.m, w.n), torch.float32, w.device, stream)
     _check(lib().bakron_unpack(w.ref, ctypes.c_void_p(V.data_ptr()), _stream(stream)), "bakron_unpack")
     return V[0] if w.count == 1 else V
 
@@ -753,13 +788,15 @@ def _linear(fn, where, grad, x, w, out, workspace, stream):
     w._check(x, name)
     if w.count != 1:
         raise ValueError("%s takes a single matrix, got %d" % (where, w.count))
-    y = _out(out, x, (T, w.n if grad else w.m), "out")
+    y = _out(out, x, (T, w.n if grad else w.m), "out", stream)
     nb = _linear_ws_size(w, T, x.dtype, grad)
-    ws = _ws(nb, workspace) if nb else None     # alive until the call is enqueued
+    ws = _ws(nb, workspace, stream) if nb else None
     st = fn(x.data_ptr(), T, code, w.ref, y.data_ptr(), None if ws is None else ws.data_ptr(), nb,
             _handle(stream, dev))
     if st != OK:
         raise BakronError(st, where)
+    if stream is not None:
+        _keep(stream, x, w.data, y, ws)
     return y
 
 
@@ -793,19 +830,21 @@ def bakron_linear_act(x, w, bias=None, act="none", residual=None, want_pre=False
     if w.count != 1:
         raise ValueError("bakron_linear_act takes a single matrix, got %d" % w.count)
     kind = _activation(act)
-    y = _out(out, x, (T, w.m), "out")
+    y = _out(out, x, (T, w.m), "out", stream)
     rp = None if residual is None else _same(residual, x, (T, w.m), "residual")
     if want_pre:
-        pre = _out(pre, x, (T, w.m), "pre")
+        pre = _out(pre, x, (T, w.m), "pre", stream)
     elif pre is not None:
         raise ValueError("pre is given but not wanted (want_pre)")
     nb = _linear_ws_size(w, T, x.dtype, False)
-    ws = _ws(nb, workspace) if nb else None     # alive until the call is enqueued
+    ws = _ws(nb, workspace, stream) if nb else None
     st = lib().bakron_linear_act(x.data_ptr(), T, code, w.ref, _vec(bias, w.m, x, "bias"), kind, rp, y.data_ptr(),
                                  None if pre is None else pre.data_ptr(), None if ws is None else ws.data_ptr(), nb,
                                  _handle(stream, dev))
     if st != OK:
         raise BakronError(st, "bakron_linear_act")
+    if stream is not None:
+        _keep(stream, x, w.data, bias, residual, y, pre, ws)
     return y, pre
 
 
@@ -822,9 +861,11 @@ def bakron_act(z, act, gated=False, out=None, stream=None):
     act(gates) * rest, (T, m)."""
     T, m, code, dev = _gates(z, gated)
     kind = _activation(act)
-    y = _out(out, z, (T, m), "out")
+    y = _out(out, z, (T, m), "out", stream)
     _check(lib().bakron_act(z.data_ptr(), T, m, code, kind, 1 if gated else 0, y.data_ptr(), _handle(stream, dev)),
            "bakron_act")
+    if stream is not None:
+        _keep(stream, z, y)
     return y
 
 
@@ -860,17 +901,19 @@ def bakron_act_grad(dy, z, act, gated=False, want_bias_grad=False, out=None, wor
     kind = _activation(act)
     yp = _same(dy, z, (T, m), "dY")
     cols = z.shape[1]
-    dz = _out(out, z, (T, cols), "out")
+    dz = _out(out, z, (T, cols), "out", stream)
     db = ws = bp = wp = None
     nb = 0
     if want_bias_grad:
         nb = act_grad_workspace_size(T, cols)
-        ws = _ws(nb, workspace) if nb else None
+        ws = _ws(nb, workspace, stream) if nb else None
         wp = None if ws is None else ws.data_ptr()
-        db = _torch().empty(cols, dtype=_torch().float32, device=z.device)
+        db = _empty(cols, _torch().float32, z.device, stream)
         bp = db.data_ptr()
     _check(lib().bakron_act_grad(yp, z.data_ptr(), T, m, code, kind, 1 if gated else 0, dz.data_ptr(), bp, wp, nb,
                                  _handle(stream, dev)), "bakron_act_grad")
+    if stream is not None:
+        _keep(stream, dy, z, dz, db, ws)
     return dz, db
 
 
@@ -901,12 +944,14 @@ def bakron_sort_tokens(choice, experts, out=None, stream=None):
     if not 1 <= k <= 32 or not 1 <= experts <= 1024:
         raise ValueError("up to 32 choices of a token and 1024 experts, got %d and %d" % (k, experts))
     if out is None:
-        out = (torch.empty(experts + 1, dtype=torch.int32, device=choice.device),
-               torch.empty((T, k), dtype=torch.int32, device=choice.device))
+        out = (_empty(experts + 1, torch.int32, choice.device, stream),
+               _empty((T, k), torch.int32, choice.device, stream))
     offsets, place = out
     _check(lib().bakron_sort_tokens(choice.data_ptr(), choice.element_size(), T, k, int(experts),
                                     _ints(offsets, (experts + 1,), dev, "offsets"), _ints(place, (T, k), dev, "place"),
                                     _handle(stream, dev)), "bakron_sort_tokens")
+    if stream is not None:
+        _keep(stream, choice, offsets, place)
     return offsets, place
 
 
@@ -940,9 +985,11 @@ def bakron_dispatch(x, place, weight=None, out=None, stream=None):
     k = shape[1]
     wp = None if weight is None else _weights(weight, shape, dev)
     R = out.shape[0] if isinstance(out, _torch().Tensor) and out.dim() == 2 else T * k
-    rows = _out(out, x, (R, d), "out")
+    rows = _out(out, x, (R, d), "out", stream)
     _check(lib().bakron_dispatch(x.data_ptr(), T, d, code, pp, k, wp, rows.data_ptr(), R, _handle(stream, dev)),
            "bakron_dispatch")
+    if stream is not None:
+        _keep(stream, x, place, weight, rows)
     return rows
 
 
@@ -953,9 +1000,11 @@ def bakron_combine(rows, place, weight=None, out=None, stream=None):
     pp, shape = _placed(place, dev)
     T, k = shape
     wp = None if weight is None else _weights(weight, shape, dev)
-    y = _out(out, rows, (T, d), "out")
+    y = _out(out, rows, (T, d), "out", stream)
     _check(lib().bakron_combine(rows.data_ptr(), R, d, code, pp, T, k, wp, y.data_ptr(), _handle(stream, dev)),
            "bakron_combine")
+    if stream is not None:
+        _keep(stream, rows, place, weight, y)
     return y
 
 
@@ -969,11 +1018,13 @@ def bakron_combine_grad(dy, rows, place, weight, out=None, stream=None):
     pp, shape = _placed(place, dev, T)
     wp = _weights(weight, shape, dev)
     if out is None:
-        out = (None, _torch().empty_like(weight))
-    drows, dweight = _out(out[0], dy, (R, d), "drows"), out[1]
+        out = (None, _empty(shape, weight.dtype, weight.device, stream))
+    drows, dweight = _out(out[0], dy, (R, d), "drows", stream), out[1]
     _check(lib().bakron_combine_grad(dy.data_ptr(), rp, R, d, code, pp, T, shape[1], wp, drows.data_ptr(),
                                      _weights(dweight, shape, dev, "dweight"), _handle(stream, dev)),
            "bakron_combine_grad")
+    if stream is not None:
+        _keep(stream, dy, rows, place, weight, drows, dweight)
     return drows, dweight
 
 
@@ -1007,12 +1058,14 @@ def _experts(fn, where, grad, x, w, offsets, out, workspace, stream):
     R, _, code, dev = _act(x, name, w.m if grad else w.n)
     w._check(x, name)
     op = _ints(offsets, (w.count + 1,), dev, "offsets")
-    y = _out(out, x, (R, w.n if grad else w.m), "out")
+    y = _out(out, x, (R, w.n if grad else w.m), "out", stream)
     nb = _experts_ws_size(w, R, x.dtype, grad)
-    ws = _ws(nb, workspace)
+    ws = _ws(nb, workspace, stream)
     st = fn(x.data_ptr(), R, code, w.ref, op, y.data_ptr(), ws.data_ptr(), nb, _handle(stream, dev))
     if st != OK:
         raise BakronError(st, where)
+    if stream is not None:
+        _keep(stream, x, w.data, offsets, y, ws)
     return y
 
 
@@ -1067,12 +1120,14 @@ def bakron_moe(x, router, w_in, w_out, top_k, renormalize=True, out=None, worksp
     w_in._check(x, "X")
     w_out._check(x, "X")
     rp = _same(router, x, (w_in.count, d), "router")
-    y = _out(out, x, (T, d), "out")
+    y = _out(out, x, (T, d), "out", stream)
     nb = _moe_ws_size(w_in, w_out, T, top_k, x.dtype)
-    ws = _ws(nb, workspace)
+    ws = _ws(nb, workspace, stream)
     _check(lib().bakron_moe(x.data_ptr(), T, code, rp, w_in.ref, w_out.ref, int(top_k),
                             1 if renormalize else 0, y.data_ptr(), ws.data_ptr(), nb, _handle(stream, dev)),
            "bakron_moe")
+    if stream is not None:
+        _keep(stream, x, router, w_in.data, w_out.data, y, ws)
     return y
 
 
@@ -1081,15 +1136,17 @@ def bakron_layernorm(x, gamma=None, beta=None, eps=1e-5, out=None, want_stats=Tr
     Returns (y, mean, rstd); mean and rstd (T,) float32 feed the gradient
     (None without want_stats)."""
     T, d, code, dev = _act(x, "X")
-    y = _out(out, x, (T, d), "out")
+    y = _out(out, x, (T, d), "out", stream)
     mean = rstd = mp = rp = None
     if want_stats:
         torch = _torch()
-        mean = torch.empty(T, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        mean = _empty(T, torch.float32, x.device, stream)
+        rstd = _empty(T, torch.float32, x.device, stream)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
     _check(lib().bakron_layernorm(x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"), _vec(beta, d, x, "beta"),
                                   eps, y.data_ptr(), mp, rp, _handle(stream, dev)), "bakron_layernorm")
+    if stream is not None:
+        _keep(stream, x, gamma, beta, y, mean, rstd)
     return y, mean, rstd
 
 
@@ -1122,21 +1179,22 @@ def bakron_layernorm_grad(dy, x, gamma, mean, rstd, want_weight_grads=True, out=
     dbeta (d,) float32 (None without want_weight_grads)."""
     T, d, code, dev = _act(x, "X")
     yp = _same(dy, x, (T, d), "dY")
-    dx = _out(out, x, (T, d), "out")
-    dg = db = gp = bp = ws = None
+    dx = _out(out, x, (T, d), "out", stream)
+    dg = db = gp = bp = keep = ws = None
     nb = 0
     if want_weight_grads:
         torch = _torch()
         nb = layernorm_grad_workspace_size(T, d)
-        # kept until the call is enqueued, then the allocator may reuse it in stream order
-        keep = _ws(nb, workspace)
+        keep = _ws(nb, workspace, stream)
         ws = keep.data_ptr()
-        dg = torch.empty(d, dtype=torch.float32, device=x.device)
-        db = torch.empty(d, dtype=torch.float32, device=x.device)
+        dg = _empty(d, torch.float32, x.device, stream)
+        db = _empty(d, torch.float32, x.device, stream)
         gp, bp = dg.data_ptr(), db.data_ptr()
     _check(lib().bakron_layernorm_grad(yp, x.data_ptr(), T, d, code, _vec(gamma, d, x, "gamma"),
                                        _vec(mean, T, x, "mean"), _vec(rstd, T, x, "rstd"), dx.data_ptr(),
                                        gp, bp, ws, nb, _handle(stream, dev)), "bakron_layernorm_grad")
+    if stream is not None:
+        _keep(stream, dy, x, gamma, mean, rstd, dx, dg, db, keep)
     return dx, dg, db
 
 
@@ -1159,13 +1217,13 @@ class Solver:
         self.stream = stream
         dev = "cuda"
         self.plan = bakron_plan_init(m, n, stream=stream)
-        self.ws_q = torch.empty(workspace_size(m, n, opts), dtype=torch.uint8, device=dev)
-        self.ws_p = torch.empty(prepare_workspace_size(n, m), dtype=torch.uint8, device=dev)
-        self.scale = torch.empty(m, dtype=torch.float32, device=dev)
-        self.UA = torch.empty((n, n), dtype=torch.float32, device=dev)
-        self.UB = torch.empty((m, m), dtype=torch.float32, device=dev)
-        self.V = torch.empty((m, n), dtype=torch.float32, device=dev)
-        self.codes = torch.empty((m, n), dtype=torch.int8, device=dev)
+        self.ws_q = _empty(workspace_size(m, n, opts), torch.uint8, dev, stream)
+        self.ws_p = _empty(prepare_workspace_size(n, m), torch.uint8, dev, stream)
+        self.scale = _empty(m, torch.float32, dev, stream)
+        self.UA = _empty((n, n), torch.float32, dev, stream)
+        self.UB = _empty((m, m), torch.float32, dev, stream)
+        self.V = _empty((m, n), torch.float32, dev, stream)
+        self.codes = _empty((m, n), torch.int8, dev, stream)
 
     def rowscale(self, W):
         return bakron_rowscale(W, self.qmax, out=self.scale, stream=self.stream)
