@@ -504,7 +504,9 @@ bakron_status bakron_experts_workspace_size(const bakron_packed* w, int64_t R, i
 bakron_status bakron_experts(const void* X, int64_t R, int dtype, const bakron_packed* w,
                              const int32_t* offsets, void* Y, void* ws, size_t ws_bytes, void* stream);
 /* Its gradient towards the rows: dX_r = dY_r V_e, in bakron_linear_grad's arithmetic; the scales' power
- * of two is taken from the largest scale of all experts. */
+ * of two is taken from the largest scale of all experts.  So in fp16 an expert's weights keep their 11
+ * bits down to 2^-25 of that scale (2^-21 where |c - z| can exceed 15) and are off by 2^-36 (2^-32) of it
+ * at most below: experts further apart than that want bf16, or a w each. */
 bakron_status bakron_experts_grad(const void* dY, int64_t R, int dtype, const bakron_packed* w,
                                   const int32_t* offsets, void* dX, void* ws, size_t ws_bytes, void* stream);
 
