@@ -48,6 +48,7 @@ cudaError_t launch_planes(const void* x, int dtype, int64_t T, int64_t K, int64_
 // tcgen05 products for many tokens, and the gradient for any number.
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);
 int64_t linear_fwd_steps(const LinearArgs& a);    // 128-column chunks that its busiest block takes (16-bit x)
+int linear_fwd_eights();                          // clusters of eight of its blocks that the current device runs at once
 cudaError_t launch_linear_grad(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_act_fwd(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_experts_fwd(const LinearArgs& a, cudaStream_t s);

@@ -762,12 +762,13 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   }
 }
 
-// Blocks per tile: as many as there are SMs without a tile, two chunks each at least;
-// four at most (clusters of eight such blocks do not all fit at once: 48 tokens of 2048 x 8192
-// 20 us, in clusters of four 13.6).
+// Blocks per tile: as many as there are SMs without a tile, two chunks each at least; eight
+// only where as many clusters of eight fit at once (128 x 16384 bf16, 96 tokens, one tile 14 us, in clusters
+// of four 21; 1792 x 8192, 32 tokens, 14 tiles 10 and 12.5; 2048 x 8192, 16 of which one waits, 22 and 14).
 int blocks_per_tile(int64_t tiles, int64_t chunks) {
   int S = 1;
   while (S < 4 && tiles * 2 * S <= sm_count() && chunks >= 4 * S) S *= 2;
+  if (S == 4 && chunks >= 16 && tiles <= linear_fwd_eights()) S = 8;
   return S;
 }
 
