@@ -69,17 +69,19 @@ Kernel forward_kernel(const LinearArgs& a) {
   }
   if (a.T <= kFewTokens) return kFew;
   if (a.T > kMidTokens) return kMany;
-  // Microseconds by what was measured of the two, the second by the codes, the third by the chunks
-  // of a block, which cost more when they hold more groups (bf16, groups of 128, 64 and 32, second and
-  // third; 32 tokens of 8192 x 8192: 24.9 and 21.0, 30.2 and 23.3, 30.1 and 38.4; 48 tokens of 14336 x 4096:
-  // 25.9 and 19.2, 31.4 and 21.2, 31.6 and 38.0; 48 of 2048 x 8192: 13.3 and 13.6, 16.7 and 14.2, 16.7 and
-  // 17.8; 64 of 1000 x 4096: 9.0 and 9.5, 10.4 and 9.9, 10.4 and 11.7).
+  // About microseconds, the second by the codes and the columns, the third by the chunks of a block, which cost
+  // more when they hold more groups or zero points; fitted to what is faster (11 shapes from 1024 x 1024 to
+  // 8192 x 8192, 128 x 16384 and 14336 x 4096, 17 to 64 tokens, groups of 128, 64 and 32: 12 of 462 calls more than 10 %
+  // from the faster one).  Second and third: 32 tokens of 8192 x 8192 in groups of 128 24.5 and 20.5, 64 29.6 and 22.4,
+  // 32 29.7 and 38.6; 48 tokens of 4096 x 4096 11.6 and 10.8, 13.6 and 10.5, 13.6 and 13.8; of 1000 x 4096
+  // 7.1 and 8.3, 8.3 and 7.5, 8.3 and 9.2.
   const bool narrow = a.w.ng > 1 && a.w.g % 128 != 0;
-  const double codes = 1e-6 * (double)(a.w.mp * a.w.nc * 128);
-  const double mid = a.T <= 32   ? 4.8 + codes * (narrow ? 0.345 : 0.29)
-                     : a.T <= 48 ? 4.5 + codes * (narrow ? 0.52 : 0.39)
-                                 : 6.0 + codes * (narrow ? 0.65 : 0.48);
-  const double many = 6.2 + (double)linear_fwd_steps(a) * (!narrow ? 0.46 : a.w.g % 64 == 0 ? 0.51 : 0.98);
+  const double work = 1e-6 * (double)(a.w.mp * a.w.nc * 128) + 0.28 * (double)a.w.nc;
+  const double mid = a.T <= 32   ? (narrow ? 2.8 + work * 0.275 : 3.5 + work * 0.227)
+                     : a.T <= 48 ? 4.3 + work * (narrow ? 0.44 : 0.27)
+                                 : (narrow ? 7.0 + work * 0.47 : 5.1 + work * 0.353);
+  const double chunk = !narrow ? 0.35 : a.w.g % 64 == 0 ? 0.33 : 0.87;
+  const double many = 6.7 + (double)linear_fwd_steps(a) * chunk * (a.w.zero && a.w.g % 64 == 0 ? 1.25 : 1.0);
   return mid < many ? kMid : kMany;
 }
 

@@ -24,28 +24,31 @@
 // One block per SM, which takes output tiles in turn (or, when there are few, a
 // part of the columns of one, joined over a cluster through distributed shared memory):
 //   warp 0: TMA producer of the activations;
-//   warps 1 and 3: issue the tcgen05.mma (M 128, K 16 each), 128-column chunks in turn;
+//   warps 1 and 3: issue the tcgen05.mma (M 128, K 16 each), 128-column chunks in turn (warp 1
+//     alone where short groups have one set of epilogue warps);
 //   warp 2: allocates and frees TMEM;
 //   warps 4-11: weights, two groups of four (32 rows each) that take the
 //     chunks in turn, codes copied asynchronously kSlots - 1 of their chunks ahead;
 //   the rest: epilogue, each 32 TMEM lanes x NC columns in fp32 registers.  Where units are short, two
-//   sets of them take the units in turn and add their sums at the end of a tile.
+//   sets of them may take the units in turn and add their sums at the end of a tile (cut_of).
 // Activations come by whole chunks, weights pass on by halves of one (32 TMEM columns), so that the
-// second half is unpacked while the first is multiplied.  TMEM: an accumulator of N columns for each
-// issuer (two of them for short groups), then four stages of weights (two where N is above 128, or 64).
+// second half is unpacked while the first is multiplied.  TMEM: an accumulator for each issuer (two of them
+// for short groups) of N columns, twice as many for fp32, then four stages of weights, 64 columns each, where
+// the 512 columns have room for them, else two.
 //
-// Measured: 2048 tokens of 8192 x 8192 bf16 in 174 us in a graph of two weights (1.58 PFLOP/s, 1.62 at
-// 4096 tokens); 48 tokens 22 us, of 14336 x 4096 19; fp32, 1024 tokens of 4096 x 4096 84 us and 2048 of
-// 8192 x 8192 507 us (three products: 1.63 PFLOP/s); experts, 4096 rows over 8 of 28672 x 4096 763 us (1.26
-// PFLOP/s: an expert's last tile is mostly not full), 256 rows over 32 of 1408 x 1024 33 us.  A chunk takes
+// Measured, in graphs: 2048 tokens of 8192 x 8192 bf16 in 174 us (two weights; 1.58 PFLOP/s, 1.62 at
+// 4096 tokens); 48 tokens 22 us, of 14336 x 4096 19; fp32, 1024 tokens of 4096 x 4096 85 us and 2048 of
+// 8192 x 8192 507 us (three products: 1.63 PFLOP/s); experts, 4096 rows over 8 of 28672 x 4096 740 to 763 us (1.26
+// PFLOP/s: an expert's last tile is mostly not full), 256 rows over 32 of 1408 x 1024 25 us (fp32 26), 1024
+// rows over 8 of 4096 x 4096 fp32 110.  A chunk takes
 // 1040 cycles at 192 tokens, of which the tensor core works 816 (at cuBLAS's rate 950): with one issuing
 // warp, whose waits and instructions follow one another, it took 1270 (206 us), with weights passed on
 // by whole chunks 1100.  Few tokens do not make a chunk shorter than about 1000: a warp's instructions follow
 // one another, five or six cycles each, the epilogue's of a unit some 100 and the weights' of a chunk
 // some 300; twice as many weights warps changed nothing, more instructions in the epilogue (scales
 // prefetched into L2, four units ahead, copied to shared memory) made it slower.  Short groups: 2048 tokens
-// of 8192 x 8192 369 us in groups of 64; 1024 of 4096 x 4096 107 us in groups of 32, 64 in groups of 64, 38 in
-// groups of 128.
+// of 8192 x 8192 298 us in groups of 64 (312 with zero points), 555 in groups of 32; 1024 of 4096 x 4096 82 us in
+// groups of 32, 50 in groups of 64, 38 in groups of 128 (fp32: 178, 109, 85).
 //
 // Every mbarrier wait is bounded (clock64 budget); a block whose wait runs
 // out records BAKRON_ERR_TIMEOUT in the device's status word, stops issuing,
@@ -81,7 +84,7 @@ struct FwdArgs {
   int tiles_m;
   int64_t tiles;      // tiles of the output
   int chunks;         // 128-wide K chunks
-  int N;              // tokens per tile, a multiple of 32
+  int N;              // tokens per tile, a multiple of 32 (of 16: fp32, short groups, two sets)
   int stages;
   int wstages;        // 4 where TMEM has room, else 2: a power of two
   int log_acc;        // each issuer has 1 << log_acc accumulators
@@ -370,6 +373,10 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
   return all != 0;
 }
 
+// Warps that issue the products.  Units shorter than a chunk that one set of epilogue warps takes need
+// two accumulators that follow each other within a chunk: one issuer has both.
+constexpr int issuers(int KU, int SETS) { return SETS == 1 && KU < 8 ? 1 : 2; }
+
 // TX: 16-bit terms of the activations; NC: columns per epilogue warp; EW:
 // epilogue warps; KU: accumulation unit in MMA steps of 16 (2, 4 or 8); SETS: sets of
 // epilogue warps that take the units in turn.
@@ -378,6 +385,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
     linear_fwd_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ FwdArgs a) {
   constexpr int THREADS = 32 * (12 + EW);
   constexpr int PARTS = EW / 4 / SETS;       // column parts of the epilogue
+  constexpr int ISSUERS = issuers(KU, SETS);
   // 640 threads start with 96 registers each; the roles share them out
   // (8 x 136 + 8 x 72 + 4 x 64 warps' worth of 20 x 96)
   constexpr bool kSplit = EW == 8;
@@ -413,7 +421,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       mbar_init(smem_u32(&bars.acc_empty[b]), EW / SETS);
     }
     for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&bars.turn[b]), 1);
-    mbar_init(smem_u32(&bars.done), 2);              // the issuers
+    mbar_init(smem_u32(&bars.done), ISSUERS);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) {
@@ -426,7 +434,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t acc_cols = (TX == 1 ? 1u : 2u) * (uint32_t)a.N;
-  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), tmem_a = tmem + (2u << a.log_acc) * acc_cols;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), tmem_a = tmem + ((uint32_t)ISSUERS << a.log_acc) * acc_cols;
   grid_dep_wait();
   grid_dep_launch();
   Tiles<P, FwdArgs> tiles = {a, 0, nullptr, nullptr, 0};
@@ -478,13 +486,13 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
           }
         }
       }
-    } else if (warp == 1 || warp == 3) {
+    } else if (warp == 1 || (ISSUERS == 2 && warp == 3)) {
       // ---------------- MMA issuers, which take the chunks in turn: a warp waits together, one lane
       // issues.  Their own instructions, not the tensor core, bounded a single issuer: what it
       // waited for and issued one after the other.  Each has its accumulators and its stages of
       // weights; the stages of activations are waited for in the order of the chunks (`turn`), so that
       // a use of a stage is never mistaken for the one before.
-      const int me = warp >> 1;
+      const int me = ISSUERS == 2 ? warp >> 1 : 0;
       const uint32_t idesc = idesc_f16<H>(a.N);
       const uint64_t desc_b0 = desc_sw128(ring);
       const uint32_t stage16 = stage_bytes >> 4, half16 = half_bytes >> 4, plane16 = plane_b >> 4;
@@ -500,14 +508,14 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       uint32_t turns = 0;
       Ring rg;
       rg.advance(me, a.stages);
-      for (int64_t seq = me; seq < chunks; seq += 2) {
+      for (int64_t seq = me; seq < chunks; seq += ISSUERS) {
         const uint32_t ws = (uint32_t)seq & last_stage;
-        bool go = seq == 0 || wait_or_abort(my_turn, (turns + (uint32_t)me + 1) & 1, &bars.abort, a.status);
+        bool go = ISSUERS == 1 || seq == 0 || wait_or_abort(my_turn, (turns + (uint32_t)me + 1) & 1, &bars.abort, a.status);
         ++turns;
         go = go && wait_or_abort(fb + 8u * (uint32_t)rg.s, rg.parity, &bars.abort, a.status);
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
-        if (lane == 0) mbar_arrive(other_turn);
+        if (ISSUERS == 2 && lane == 0) mbar_arrive(other_turn);
         const uint64_t db = desc_b0 + (uint32_t)rg.s * stage16;
         const uint32_t ta = tmem_a + ws * 64u;
         // halves of the chunk, each as soon as its weights are there; J steps at a time
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
           if ((j0 + J) % KU == 0) ++u;
         }
         if (!go) break;
-        rg.advance(2, a.stages);
+        rg.advance(ISSUERS, a.stages);
       }
       if (elect_one()) mma_commit(smem_u32(&bars.done));
       __syncwarp();
@@ -563,7 +571,7 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
     uint32_t count = 0;
     const uint32_t tmem_ep = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)set * acc_cols + (uint32_t)col0;
     const uint32_t af_ep = af + 8u * (uint32_t)set, ae_ep = ae + 8u * (uint32_t)set;
-    static_assert(SETS == 2 ? KU < 8 : KU == 8);
+    static_assert(SETS == 1 || KU < 8);
     bool ok = true;
     for (int64_t tile = k.tile; tile < tiles.count() && ok; tile += k.step) {
       const Place at = tiles.at(tile);
@@ -591,8 +599,10 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       }
       uint32_t slot = 0;           // of the accumulator at hand
       auto unit = [&](int u, float s) {
-        // issuer 0's and 1's chunks in turn, a set's units of a chunk one after the other
-        const uint32_t turn = KU == 2 ? count >> 1 : count, use = KU == 2 ? count : count >> 1;
+        // two sets: issuer 0's and 1's chunks in turn, a set's units of a chunk one after the other; one
+        // set: the two accumulators in turn
+        constexpr bool kPairs = SETS == 2 && KU == 2;
+        const uint32_t turn = kPairs ? count >> 1 : count, use = kPairs ? count : count >> 1;
         slot = SETS * (turn & 1);
         ++count;
         ok = wait_or_abort(af_ep + 8u * slot, use & 1, &bars.abort, a.status);
@@ -630,9 +640,9 @@ __global__ void __launch_bounds__(32 * (12 + EW), 1)
       };
       // this set's units: every SETS-th
       float s0 = scale_of(set);
-      if constexpr (SETS == 1) {
+      if constexpr (SETS == 1 && !(TX > 1 && KU == 2)) {
         // scales two units ahead, each in a register of its own (moved, it would be waited for;
-        // for two sets the longer code costs more than it saves)
+        // for two sets, and for fp32 units of 32 columns, the longer code costs more than it saves)
         float s1 = scale_of(1);
         for (int u = 0; u < units && ok; u += 2) {
           unit(u, s0);
@@ -788,9 +798,9 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
   const uint32_t stage = TX * (uint32_t)N * 256u;
   t.stages = (int)std::min<uint32_t>(kMaxStages, (kRing - table) / stage);
   // Short groups change accumulators within a chunk: two for each issuer.
-  t.log_acc = SETS == 2 ? 1 : 0;
+  t.log_acc = KU < 8 ? 1 : 0;
   t.group_mul = (uint32_t)((uint64_t(1) << 31) / (uint64_t)(a.w.g / 32) + 1);
-  t.wstages = (2 << t.log_acc) * (TX == 1 ? 1 : 2) * N + 4 * 64 <= 512 ? 4 : 2;
+  t.wstages = (issuers(KU, SETS) << t.log_acc) * (TX == 1 ? 1 : 2) * N + 4 * 64 <= 512 ? 4 : 2;
   t.epi = a.epi;
   t.offsets = a.offsets;
   t.status = async_status_word();
@@ -833,48 +843,62 @@ cudaError_t run_unit(const LinearArgs& a, int N, cudaStream_t s) {
 
 bool narrow_groups(const LinearArgs& a) { return a.w.ng > 1 && a.w.g % 128 != 0; }
 
-// Tokens per tile, a multiple of `step`: a chunk costs about as much as 500 tokens besides its own.
-int tokens_per_tile(const LinearArgs& a, int most, int step) {
+// How a product is cut: tokens per tile, and the sets of epilogue warps.
+struct Cut {
+  int N, sets;
+};
+
+// The cut that takes the least time: rounds of tiles times a tile's chunks.  A chunk costs about as much as
+// 500 tokens besides its own.  Short groups: a third of a token each besides a fixed cost, and one set of epilogue
+// warps more than two.  But one set leaves TMEM for tiles of 128 tokens (fp32: 64) where two end at 96
+// (48), and ends a tile sooner: it is faster where it saves a round, lets more blocks share a tile, or a tile
+// is short.  Groups of 64 with zero points, two sets and one: 2048 tokens of 8192 x 8192 412 and 312 us, 65
+// 29.7 and 30.1, 512 of 4096 x 4096 45 and 26.5, 128 of 1024 x 1024 8.1 and 6.9; fp32, 1024 of 4096 x 4096 108 and 124.
+Cut cut_of(const LinearArgs& a) {
+  const bool f32 = a.dtype == BAKRON_F32, narrow = narrow_groups(a);
   const int64_t tiles_m = (a.w.m + 127) / 128;
-  int best = most;
+  Cut best = {};
   double cost = 0.0;
-  for (int n = most; n >= step; n -= step) {
-    if (n > a.T + step - 1 && n > step) continue;
-    const int64_t tiles = tiles_m * likely_tiles(a, n);
-    const int S = blocks_per_tile(tiles_m * token_tiles(a, n), a.w.nc);
-    const double rounds = S > 1 ? 1.0 : (double)((tiles + sm_count() - 1) / sm_count());
-    const double c = rounds * (n + 500) / S;
-    if (cost == 0.0 || c < cost) {
-      cost = c;
-      best = n;
+  for (int sets = narrow ? 2 : 1; sets >= 1; --sets) {
+    const int most = !narrow ? (f32 ? 64 : 192) : sets == 2 ? (f32 ? 48 : 96) : (f32 ? 64 : 128);
+    const int step = f32 && sets == 2 ? 16 : 32;
+    for (int n = most; n >= step; n -= step) {
+      if (n > a.T + step - 1 && n > step) continue;
+      const int64_t tiles = tiles_m * likely_tiles(a, n);
+      const int S = blocks_per_tile(tiles_m * token_tiles(a, n), a.w.nc);
+      const double rounds = S > 1 ? 1.0 : (double)((tiles + sm_count() - 1) / sm_count());
+      double c;
+      if (!narrow) c = rounds * (n + 500) / S;
+      else if (sets == 2) c = rounds * ((double)((a.w.nc + S - 1) / S) * (n + 333) + (f32 ? 0 : 333));
+      else c = rounds * (double)((a.w.nc + S - 1) / S) * (n + 333) * (f32 ? 1.2 : 1.08);
+      if (best.N == 0 || c < cost) {
+        cost = c;
+        best = {n, sets};
+      }
     }
   }
   return best;
 }
-inline int most_tokens(const LinearArgs& a) { return narrow_groups(a) ? 96 : 192; }      // of 16-bit x
 
-// Short groups: a unit ends where a group does, after 64 or 32 columns.
-template <typename TO, typename H, int TX, int NC, Product P>
-cudaError_t run_narrow(const LinearArgs& a, int N, cudaStream_t s) {
-  return a.w.g % 64 == 0 ? run_unit<TO, H, TX, NC, 8, 4, 2, P>(a, N, s) : run_unit<TO, H, TX, NC, 8, 2, 2, P>(a, N, s);
-}
-
-template <typename TO, Product P>
-cudaError_t run16(const LinearArgs& a, cudaStream_t s) {
-  const int N = tokens_per_tile(a, most_tokens(a), 32);
-  return narrow_groups(a) ? run_narrow<TO, TO, 1, 96, P>(a, N, s) : run_unit<TO, TO, 1, 96, 8, 8, 1, P>(a, N, s);
+// A unit ends where a group does: 128, 64 or 32 columns.
+template <typename TO, typename H, int TX, Product P>
+cudaError_t run(const LinearArgs& a, cudaStream_t s) {
+  const Cut c = cut_of(a);
+  constexpr int EW = TX == 1 ? 8 : 4;        // epilogue warps of one set
+  if (!narrow_groups(a)) return run_unit<TO, H, TX, TX == 1 ? 96 : 64, EW, 8, 1, P>(a, c.N, s);
+  const bool half = a.w.g % 64 == 0;
+  if (c.sets == 1)
+    return half ? run_unit<TO, H, TX, 64, EW, 4, 1, P>(a, c.N, s) : run_unit<TO, H, TX, 64, EW, 2, 1, P>(a, c.N, s);
+  constexpr int NC = TX == 1 ? 96 : 48;
+  return half ? run_unit<TO, H, TX, NC, 8, 4, 2, P>(a, c.N, s) : run_unit<TO, H, TX, NC, 8, 2, 2, P>(a, c.N, s);
 }
 
 template <Product P>
 cudaError_t forward(const LinearArgs& a, cudaStream_t s) {
   switch (a.dtype) {
-    case BAKRON_F32: {
-      // three terms: few enough tokens for twice the accumulators
-      if (narrow_groups(a)) return run_narrow<float, __nv_bfloat16, 3, 48, P>(a, tokens_per_tile(a, 48, 16), s);
-      return run_unit<float, __nv_bfloat16, 3, 64, 4, 8, 1, P>(a, tokens_per_tile(a, 64, 32), s);
-    }
-    case BAKRON_BF16: return run16<__nv_bfloat16, P>(a, s);
-    default: return run16<__half, P>(a, s);
+    case BAKRON_F32: return run<float, __nv_bfloat16, 3, P>(a, s);     // three terms
+    case BAKRON_BF16: return run<__nv_bfloat16, __nv_bfloat16, 1, P>(a, s);
+    default: return run<__half, __half, 1, P>(a, s);
   }
 }
 
