@@ -281,8 +281,7 @@ def _stream(stream):
 
 
 def _side(stream):
-    """``stream`` as torch knows it when it is another than the current one, else None."""
-    _check_stream(stream)
+    """``stream``, of the current device, as torch knows it when it is another than the current one, else None."""
     torch = _torch()
     if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(_device()):
         return None
@@ -295,7 +294,10 @@ def _empty(shape, dtype, device, stream):
     be handed out again in that stream's order; so another stream gets memory of its own
     pool, which once let go also waits for what the current stream has queued by then."""
     torch = _torch()
-    side = None if stream is None else _side(stream)
+    side = None
+    if stream is not None:
+        _check_stream(stream)
+        side = _side(stream)
     if side is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(side):
