@@ -8,7 +8,8 @@
 // joined in shared memory and go to its row of the workspace, which a second launch adds up in
 // a fixed order (no atomics: the bits do not depend on the run); with one block of rows they
 // are the result.  The activation is chosen once for a thread's rows at hand, not per value.
-// Measured, gated silu of 2048 x 14336 bf16: 31 us (the bytes at 6.80 TB/s: 26), its gradient 48 (43); 37 x 1111
+// Measured, gated silu of 2048 x 14336 bf16: 31 us (the bytes at 6.80 TB/s: 26), its gradient 48 (43); exact gelu, whose
+// erfcf is longer than the bytes, 56 and 69 (not gated 52 and 66; relu 21 and 29); 37 x 1111
 // fp32 gelu 2.6 and with the bias's gradient 3.0 us: launch and latency.  Rows that do not begin on 16 bytes go
 // by pieces of 8, 4 or 2 bytes (2048 x 6144 bf16 silu 12 us; 6148, 6146 and 6145 columns 13, 16 and 24).
 #include <algorithm>

@@ -71,7 +71,7 @@ Kernel forward_kernel(const LinearArgs& a) {
   if (a.T > kMidTokens) return kMany;
   // About microseconds, the second by the codes and the columns, the third by the chunks of a block, which cost
   // more when they hold more groups or zero points; fitted to what is faster (11 shapes from 1024 x 1024 to
-  // 8192 x 8192, 128 x 16384 and 14336 x 4096, 17 to 64 tokens, groups of 128, 64 and 32: 12 of 462 calls more than 10 %
+  // 8192 x 8192, 128 x 16384 and 14336 x 4096, 17 to 64 tokens, groups of 128, 64 and 32: 9 of 462 calls more than 10 %
   // from the faster one).  Second and third: 32 tokens of 8192 x 8192 in groups of 128 24.5 and 20.5, 64 29.6 and 22.4,
   // 32 29.7 and 38.6; 48 tokens of 4096 x 4096 11.6 and 10.8, 13.6 and 10.5, 13.6 and 13.8; of 1000 x 4096
   // 7.1 and 8.3, 8.3 and 7.5, 8.3 and 9.2.
