@@ -288,11 +288,12 @@ def _side(stream):
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, device, stream, out=True):
     """A tensor that a call on ``stream`` (None: the current one) writes.  Memory from the
     current stream's pool may still be read and written by work that is queued there, and would
     be handed out again in that stream's order; so another stream gets memory of its own
-    pool, which once let go also waits for what the current stream has queued by then."""
+    pool.  What is returned (``out``) once let go also waits for what the current stream has
+    queued by then."""
     torch = _torch()
     side = None
     if stream is not None:
@@ -300,10 +301,14 @@ def _empty(shape, dtype, device, stream):
         side = _side(stream)
     if side is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(side):
+    now = torch.cuda.current_stream()
+    torch.cuda.set_stream(side)
+    try:
         t = torch.empty(shape, dtype=dtype, device=device)
-    if t.is_cuda:
-        t.record_stream(torch.cuda.current_stream())
+    finally:
+        torch.cuda.set_stream(now)
+    if out and t.is_cuda:
+        t.record_stream(now)
     return t
 
 
@@ -360,7 +365,7 @@ def _ws(nbytes, workspace, stream):
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError("workspace too small: need %d bytes" % nbytes)
         return workspace
-    return _empty(nbytes, torch.uint8, "cuda", stream)
+    return _empty(nbytes, torch.uint8, "cuda", stream, out=False)
 
 
 def bakron_rowscale(W, qmax, out=None, stream=None):

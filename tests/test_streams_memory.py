@@ -3,7 +3,6 @@ what it was given stays until the call has run.  Memory of the current stream's 
 handed out again in that stream's order, while the call still reads and writes it.  No GPU: tensors,
 streams and a library that say what happens to them."""
 
-import contextlib
 import types
 
 import pytest
@@ -48,21 +47,18 @@ def made(monkeypatch):
     """The tensors that the calls allocate, in order."""
     now, out = [CURRENT], []
 
-    @contextlib.contextmanager
-    def stream(s):
-        now.append(s)
-        yield
-        now.pop()
+    def set_stream(s):
+        now[:] = [s]
 
     def empty(shape, dtype=F32, device=None):
         t = torch.zeros(shape, dtype=dtype).as_subclass(Noted)
-        t.pool = now[-1].cuda_stream
+        t.pool = now[0].cuda_stream
         out.append(t)
         return t
 
     class Torch:
-        cuda = types.SimpleNamespace(Stream=Stream, stream=stream, current_stream=lambda *a: now[-1])
-        _C = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: now[-1].cuda_stream)
+        cuda = types.SimpleNamespace(Stream=Stream, set_stream=set_stream, current_stream=lambda *a: now[0])
+        _C = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: now[0].cuda_stream)
 
         def __getattr__(self, name):
             return empty if name == "empty" else getattr(torch, name)
@@ -140,7 +136,8 @@ def test_memory_of_the_calls_stream(made, name):
     assert made, "nothing was allocated"
     for t in made:
         assert t.pool == SIDE.cuda_stream, "%s came from the current stream's memory" % (tuple(t.shape),)
-        assert CURRENT.cuda_stream in t.users, "the current stream may use what it is given back"
+        if t.dtype != U8 or name in ("plan", "pack"):       # no workspace
+            assert CURRENT.cuda_stream in t.users, "the current stream may use what it is given back"
     for t in inputs:
         assert SIDE.cuda_stream in t.users, "an input may be let go while the call runs"
 
